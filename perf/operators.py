@@ -159,7 +159,7 @@ def _cache(case, g, lens, extra, fill=True):
     scales = torch.rand(S, H, P, 2, generator=g, device=DEV) * 0.02 + 0.02
     tail = _randn(g, S, H, 2, PAGE, D)
     table = torch.rand(S, H, P, generator=g, device=DEV).argsort(dim=-1).to(torch.int32)
-    ctl = torch.zeros(1 + S, dtype=torch.int32, device=DEV)
+    ctl = torch.zeros(1, dtype=torch.int32, device=DEV)
     return dict(codes=codes, scales=scales, sums=sums, tail=tail, table=table, len=lens.clone(), ctl=ctl)
 
 
