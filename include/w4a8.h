@@ -184,6 +184,127 @@ w4a8_status w4a8_matmul_noalloc_check(uint32_t* flags);
 /* Number of K slices S that w4a8_matmul uses for a (K, N) shape (host). */
 int w4a8_matmul_slices(int K, int N);
 
+/* ------------------------------------------------------------------------------
+ * Key/value cache in 8 bits (sequences of any length, beside a session's fp32 cache)
+ *
+ * One w4a8_kv8_cache holds one layer of n_seqs sequences in buffers the caller owns.  A page is
+ * 64 tokens of one (sequence, KV head): int8 codes with one fp32 scale for its keys and one for
+ * its values, made by the rule of w4a8_quantize_rows over the page's 64 * head_dim values
+ *   s = absmax / 127,  c = clamp(rint(x / s), -127, 127);  absmax == 0 -> s = 0, c = 0
+ * (a NaN or an infinity among the values makes s NaN and every c 0: what reads the page gives
+ * NaN).  A sequence of len tokens has len / 64 whole pages; the rows of the page that is
+ * still open stay in fp32 in `tail` until it completes, so tokens are quantised once, with
+ * their page's final scale.  table[s][h] is a permutation of 0..max_pages-1: page p of (s, h)
+ * lies at table[s][h][p], and the entries behind the whole pages are the free ones, so evicting
+ * pages moves table entries and no codes.  Each KV head has its own table; lengths are common.
+ *
+ * codes holds code + 128 in the order in which one warp reads a page as m16n8k16 operands:
+ *   keys:   byte (((((token/16 * D/32 + dim/32) * 8 + token%8) * 4 + dim%32/8) * 2 + dim%8/4) * 2
+ *           + token%16/8) * 4 + dim%4
+ *   values: byte ((((((dim/16 * 2 + token/32) * 8 + dim%8) * 4 + token%8/2) * 2 + token%32/16) * 2
+ *           + dim%16/8) * 2 + token%16/8) * 2 + token%2
+ *
+ * Lengths, counts, tables, masks and lists are read on the device when the kernels run, so a
+ * captured call can be replayed as they change.  What they hold is checked there: a value out
+ * of range makes its sequence (len, counts) or page (table, pages) be left out and sets the
+ * status word ctl (w4a8_kv8_check).  n_seqs 1..4096, n_kv_heads 1..1024, head_dim 64 or 128,
+ * max_pages 1..16384, n_seqs * n_kv_heads * max_pages < 2^31; else W4A8_ERR_SHAPE.  codes 128-byte,
+ * tail, sums and scales 16-byte aligned; else W4A8_ERR_ARG.  Calls that write a cache must be
+ * ordered with the other calls on it.
+ * ---------------------------------------------------------------------------- */
+typedef struct {
+  int n_seqs, n_kv_heads, head_dim, max_pages;
+  uint8_t* codes;   /* [n_seqs][n_kv_heads][max_pages][2 (keys, values)][64 * head_dim] */
+  float* scales;    /* [n_seqs][n_kv_heads][max_pages][2 (keys, values)] */
+  int16_t* sums;    /* [n_seqs][n_kv_heads][max_pages][head_dim]: sums of a page's key codes over its tokens */
+  float* tail;      /* [n_seqs][n_kv_heads][2][64][head_dim]: row i = position 64 * (len / 64) + i */
+  int32_t* table;   /* [n_seqs][n_kv_heads][max_pages] */
+  int32_t* len;     /* [n_seqs], 0 .. 64 * max_pages + 63 */
+  uint32_t* ctl;    /* [1] status word: W4A8_FLAG_* of the calls since it was cleared */
+} w4a8_kv8_cache;
+
+/* A device tensor [n_seqs][n][heads][head_dim] with unit stride along head_dim; strides in elements. */
+typedef struct {
+  void* data;
+  int64_t seq, row, head;
+} w4a8_rows;
+
+enum { W4A8_F32 = 0, W4A8_BF16 = 1 }; /* element types of w4a8_rows */
+
+/* Host.  Bytes of the seven buffers of a cache with these dimensions, in the struct's order. */
+w4a8_status w4a8_kv8_bytes(const w4a8_kv8_cache* c, size_t bytes[7]);
+/* Device.  Empties a cache: len = 0, table = the identity, ctl = 0. */
+w4a8_status w4a8_kv8_reset(const w4a8_kv8_cache* c, void* stream);
+/* Host, synchronous (call after the stream has finished).  *flags = the status word; the call
+ * returns W4A8_ERR_DEVICE_FLAG if it is not 0: W4A8_FLAG_ERR_CAPACITY (a length or count out of
+ * range, or an append beyond max_pages), W4A8_FLAG_ERR_TOKEN (a source row out of range),
+ * W4A8_FLAG_ERR_TREE (a table entry or page list out of range or order), W4A8_FLAG_ERR_TIMEOUT. */
+w4a8_status w4a8_kv8_check(const w4a8_kv8_cache* c, uint32_t* flags);
+
+/* Device.  Commits rows: row j < counts[s] of k and v (n rows, dtype, any order of strides) becomes
+ * position len[s] + j of sequence s; pages that complete are quantised, the rest goes to the tail.
+ * counts: device int32[n_seqs] in 0..n, NULL = n.  index: device int32 [n_seqs][n], NULL = the rows
+ * in order: position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of
+ * a draft tree; the same row may come twice); with it n <= 1024, without it n_src >= n.  The new lengths go to len_out (device int32[n_seqs]);
+ * len_out == c->len advances the cache, which reads the rows from then on.  A sequence that would
+ * pass 64 * max_pages + 63 tokens stays as it was, as does one with a row out of range. */
+w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,
+                            int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);
+/* Device.  Positions first[s] .. first[s] + n - 1 of every sequence as the cache holds them (s * c of
+ * whole pages, one rounding; the fp32 rows of the open page), positions at or behind len[s] as 0, into
+ * k_out and v_out, fp32 [n_seqs][n][n_kv_heads][head_dim] contiguous.  len: NULL = c->len. */
+w4a8_status w4a8_kv8_read(const w4a8_kv8_cache* c, const int32_t* first, const int32_t* len, int n, float* k_out,
+                          float* v_out, void* stream);
+
+/* Attention of n new rows per sequence over its cache and the rows themselves. */
+typedef struct {
+  int n;                 /* rows of every sequence, 1..64 */
+  int n_heads;           /* query heads, n_kv_heads * (1..16); head h uses KV head h / (n_heads / n_kv_heads) */
+  int dtype;             /* of q, k, v and out */
+  float scale;           /* logit = scale * q . k */
+  w4a8_rows q, out;      /* [n_seqs][n][n_heads][head_dim] */
+  w4a8_rows k, v;        /* [n_seqs][n][n_kv_heads][head_dim]; both data NULL: the cache alone is read */
+  const int32_t* counts; /* rows of each sequence, 0..n; NULL = n.  Rows behind them: out is left as it was */
+  const uint64_t* mask;  /* [n_seqs][n]: bit j of row i is set where i sees new row j; NULL: j <= i */
+  const int32_t* pages;  /* [n_seqs][n][n_kv_heads][top_k]: the whole pages that a row reads, ascending, -1 behind
+                            the last (w4a8_kv8_select); NULL: all of them */
+  int top_k;             /* with pages: 1..max_pages */
+  const float* mass;     /* [n_seqs][n_kv_heads][max_pages] */
+  float* mass_out;       /* mass (NULL = 0) + the softmax weight that this call's rows and query heads put on each
+                            whole page; may be mass itself; NULL: not wanted.  Not with pages (W4A8_ERR_UNSUPPORTED) */
+} w4a8_kv8_attn;
+/* Host.  Scratch bytes of w4a8_kv8_attention (the pointers in a are not read, only whether they are NULL). */
+w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, size_t* bytes);
+/* Device.  out[s][i][h] = sum_t w_t v_t with w = softmax over the committed tokens (whole pages s * c, the open
+ * page's fp32 rows) and the visible new rows; a row that sees nothing is 0.  Logits, softmax statistics and sums
+ * are fp32; products of fp32 operands are formed from f16 hi/lo splits (about 2^-21 relative), those of bf16
+ * calls from one f16 factor (weights 2^-11).  A new row has no effect on the rows that do
+ * not see it, whatever it holds (NaN and infinities too), and rows at or behind counts[s] are not read.  The result does not depend on timing; it may depend, in
+ * its last bits, on the other sequences of the call (they share the splits of the long axis).  workspace: 256-byte aligned,
+ * not shared by calls that may overlap; needs no initialisation. */
+w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Device.  For each new row and KV head the top_k whole pages of best score, as an ascending list padded with -1
+ * (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the largest over the head's query group of
+ * q . (sum of the page's keys), in int8 like the pages: the group's queries get codes at one scale
+ * (w4a8_quantize_rows' rule over its heads * head_dim values) and
+ *   score = fl32(key scale * fl32(max_h sum_d code[h][d] * sums[d]))  with the exact integer sum.
+ * The first first_pages and the last last_pages whole pages come before any score, equal scores go to the lowest
+ * page, a NaN score counts as infinity, a group whose absmax is not finite has codes 0.  Rows behind counts get lists of -1.  q as in w4a8_kv8_attn (dtype, n,
+ * n_heads, q and counts of a are used).  workspace: w4a8_kv8_select_workspace_bytes, 256-byte aligned. */
+w4a8_status w4a8_kv8_select_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, size_t* bytes);
+w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, int top_k, int first_pages,
+                            int last_pages, int32_t* pages_out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Device.  Thins every sequence to at most keep whole pages per KV head: the first first_pages and last last_pages
+ * come first, then those of largest mass (ties: the lowest page; NaN counts as infinity).  table_out: kept entries in
+ * order, then dropped ones (free from then on), then the rest; mass_out: the kept masses, 0 behind them; len_out =
+ * len - 64 * (dropped pages per head).  The outputs may be the cache's own table and len, and mass itself. */
+w4a8_status w4a8_kv8_evict(const w4a8_kv8_cache* c, const float* mass, int keep, int first_pages, int last_pages,
+                           int32_t* table_out, float* mass_out, int32_t* len_out, void* stream);
+
 /* ==============================================================================
  * Decoder, session and the GPU-resident speculation loop
  * ============================================================================ */

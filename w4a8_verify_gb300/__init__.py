@@ -54,6 +54,21 @@ class DecodeReport(_c.Structure):
                 ("kernels", _i64)]
 
 
+class KV8CacheDesc(_c.Structure):
+    _fields_ = [("n_seqs", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("max_pages", _i32), ("codes", _vp),
+                ("scales", _vp), ("sums", _vp), ("tail", _vp), ("table", _vp), ("len", _vp), ("ctl", _vp)]
+
+
+class Rows(_c.Structure):
+    _fields_ = [("data", _vp), ("seq", _i64), ("row", _i64), ("head", _i64)]
+
+
+class KV8Attn(_c.Structure):
+    _fields_ = [("n", _i32), ("n_heads", _i32), ("dtype", _i32), ("scale", _f32), ("q", Rows), ("out", Rows),
+                ("k", Rows), ("v", Rows), ("counts", _vp), ("mask", _vp), ("pages", _vp), ("top_k", _i32),
+                ("mass", _vp), ("mass_out", _vp)]
+
+
 FLAG_TERMINATED, FLAG_ERR_CAPACITY, FLAG_ERR_TOKEN, FLAG_ERR_TREE, FLAG_ERR_TIMEOUT = 1, 2, 4, 8, 16
 T_Q, T_K, T_V, T_O, T_GATE, T_UP, T_DOWN, T_EMBED, T_LM_HEAD = range(9)
 
@@ -75,6 +90,17 @@ _SIGNATURES = {
     "w4a8_matmul_check": [_vp, _i32, _i32, _i32, _c.POINTER(_c.c_uint32)],
     "w4a8_matmul_noalloc": [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp],
     "w4a8_matmul_noalloc_check": [_c.POINTER(_c.c_uint32)],
+    "w4a8_kv8_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(_sz)],
+    "w4a8_kv8_reset": [_c.POINTER(KV8CacheDesc), _vp],
+    "w4a8_kv8_check": [_c.POINTER(KV8CacheDesc), _c.POINTER(_c.c_uint32)],
+    "w4a8_kv8_append": [_c.POINTER(KV8CacheDesc), _c.POINTER(Rows), _c.POINTER(Rows), _i32, _i32, _i32, _vp, _vp, _vp,
+                        _vp],
+    "w4a8_kv8_read": [_c.POINTER(KV8CacheDesc), _vp, _vp, _i32, _vp, _vp, _vp],
+    "w4a8_kv8_attention_workspace_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _c.POINTER(_sz)],
+    "w4a8_kv8_attention": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _vp, _sz, _vp],
+    "w4a8_kv8_select_workspace_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _c.POINTER(_sz)],
+    "w4a8_kv8_select": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _i32, _i32, _i32, _vp, _vp, _sz, _vp],
+    "w4a8_kv8_evict": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
     "w4a8_model_create": [_c.POINTER(ModelDesc), _c.POINTER(_vp)],
     "w4a8_model_load_tensor": [_vp, _i32, _i32, _vp, _vp, _vp],
     "w4a8_model_weight_bytes": [_vp, _c.POINTER(_sz)],
@@ -304,6 +330,190 @@ def w4a8_matmul(a_q, a_s, w_t, s_t, N, y=None, workspace=None, stream=None):
     _call("w4a8_matmul", _ptr(a_q), _ptr(a_s), M, K, _ptr(w_t), _ptr(s_t), N, _ptr(y), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
     return y
+
+
+# ------------------------------------------------------------- key/value cache in 8 bits
+
+class KV8Cache:
+    """One layer of ``n_seqs`` sequences' keys and values in 8 bits (w4a8_kv8_cache).
+
+    Holds the cache's tensors, by name in ``tensors`` (``codes``, ``scales``, ``sums``, ``tail``, ``table``,
+    ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
+    fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
+    stream; device state that is out of range is reported by ``check``.
+    """
+
+    _NAMES = (("codes", "uint8"), ("scales", "float32"), ("sums", "int16"), ("tail", "float32"), ("table", "int32"),
+              ("len", "int32"), ("ctl", "int32"))
+
+    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, device="cuda", tensors=None, stream=None):
+        import torch
+        self.desc = KV8CacheDesc(n_seqs, n_kv_heads, head_dim, max_pages)
+        self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
+        need = (_sz * 7)()
+        _call("w4a8_kv8_bytes", _c.byref(self.desc), need)
+        S, H, D, P = self.shape
+        shapes = ((S, H, P, 2, 64 * D), (S, H, P, 2), (S, H, P, D), (S, H, 2, 64, D), (S, H, P), (S,), (1,))
+        self.tensors = {}
+        for (name, dtype), shape, size in zip(self._NAMES, shapes, need):
+            t = torch.empty(shape, dtype=getattr(torch, dtype), device=device) if tensors is None else tensors[name]
+            if t.dtype != getattr(torch, dtype) or t.numel() * t.element_size() != size or not t.is_contiguous():
+                raise ValueError("KV8Cache: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+            self.tensors[name] = t
+            setattr(self.desc, name, t.data_ptr())
+        self.device = self.tensors["codes"].device
+        if any(t.device != self.device for t in self.tensors.values()) or self.device.type != "cuda":
+            raise ValueError("KV8Cache: the tensors must be on one CUDA device")
+        self._ref = _c.byref(self.desc)
+        if tensors is None:
+            self.reset(stream)
+
+    @property
+    def len(self):
+        return self.tensors["len"]
+
+    def _on(self, stream):
+        """The stream of a call, which must be one of the cache's device."""
+        import torch
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError("KV8Cache: the stream is on another device than the cache")
+            return stream.cuda_stream
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _run(self, name, *args):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            _call(name, self._ref, *args)
+        else:
+            with torch.cuda.device(self.device):
+                _call(name, self._ref, *args)
+
+    def _vec(self, t, name, dtype, shape):
+        """Pointer of an optional contiguous tensor of this device, type and shape."""
+        if t is None:
+            return None
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError("KV8Cache: %s must be a contiguous %s tensor %s on the cache's device"
+                             % (name, str(dtype)[6:], list(shape)))
+        return t.data_ptr()
+
+    def _rows(self, t, name, like=None, heads=None, n=None):
+        import torch
+        S, H, D, _ = self.shape
+        if t.dim() != 4 or t.shape[0] != S or t.shape[3] != D or (heads is not None and t.shape[2] != heads) \
+                or (n is not None and t.shape[1] != n):
+            raise ValueError("KV8Cache: %s must be [%d][%s][%s][%d], not %s"
+                             % (name, S, "n" if n is None else n, "heads" if heads is None else heads, D, list(t.shape)))
+        if t.dtype not in (torch.float32, torch.bfloat16) or (like is not None and t.dtype != like.dtype):
+            raise ValueError("KV8Cache: %s has type %s" % (name, t.dtype))
+        a, b, c, d = t.stride()
+        if d != 1 or t.device != self.device:
+            raise ValueError("KV8Cache: %s must have unit stride in its last dimension, on the cache's device" % name)
+        return Rows(t.data_ptr(), a, b, c)
+
+    @staticmethod
+    def _dtype(t):
+        import torch
+        return 0 if t.dtype == torch.float32 else 1
+
+    def reset(self, stream=None):
+        """Empties the cache (w4a8_kv8_reset)."""
+        self._run("w4a8_kv8_reset", self._on(stream))
+
+    def check(self):
+        """The status word (0 = every call's device state was in range); synchronous."""
+        f = _c.c_uint32()
+        st = lib().w4a8_kv8_check(self._ref, _c.byref(f))
+        if st not in (0, 7):
+            raise W4A8Error("w4a8_kv8_check", st)
+        return f.value
+
+    def append(self, k, v, counts=None, index=None, len_out=None, stream=None):
+        """Commits rows of k and v, advancing the cache's lengths, or storing the new ones in ``len_out`` instead
+        (w4a8_kv8_append).  ``index`` [n_seqs][n]: the source row of each new position."""
+        import torch
+        S, H = self.shape[:2]
+        kr = self._rows(k, "k", heads=H)
+        vr = self._rows(v, "v", like=k, heads=H, n=k.shape[1])
+        n = k.shape[1] if index is None else index.shape[1]
+        i32 = torch.int32
+        out = self.desc.len if len_out is None else self._vec(len_out, "len_out", i32, (S,))
+        self._run("w4a8_kv8_append", kr, vr, self._dtype(k), k.shape[1], n, self._vec(counts, "counts", i32, (S,)),
+                  self._vec(index, "index", i32, (S, n)), out, self._on(stream))
+
+    def read(self, first, n, length=None, stream=None):
+        """fp32 keys and values [n_seqs][n][n_kv_heads][head_dim] of positions first[s].. as held (w4a8_kv8_read)."""
+        import torch
+        S, H, D, _ = self.shape
+        k, v = (torch.empty((S, n, H, D), dtype=torch.float32, device=self.device) for _ in range(2))
+        self._run("w4a8_kv8_read", self._vec(first, "first", torch.int32, (S,)),
+                  self._vec(length, "length", torch.int32, (S,)), n, k.data_ptr(), v.data_ptr(), self._on(stream))
+        return k, v
+
+    def _scratch(self, fn, args, workspace):
+        import torch
+        need = _sz()
+        _call(fn, self._ref, _c.byref(args), _c.byref(need))
+        if workspace is None:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
+        return workspace
+
+    def attention(self, q, k=None, v=None, scale=1.0, counts=None, mask=None, pages=None, mass=None, mass_out=None,
+                  out=None, workspace=None, stream=None):
+        """Attention of q's rows over the cache and the new rows k, v (w4a8_kv8_attention); returns ``out``."""
+        import torch
+        S, H, _, P = self.shape
+        qr = self._rows(q, "q")
+        n, heads = q.shape[1], q.shape[2]
+        if (k is None) != (v is None):
+            raise ValueError("KV8Cache: k and v come together")
+        kr = Rows() if k is None else self._rows(k, "k", like=q, heads=H, n=n)
+        vr = Rows() if v is None else self._rows(v, "v", like=q, heads=H, n=n)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        outr = self._rows(out, "out", like=q, heads=heads, n=n)
+        top_k = 0 if pages is None else pages.shape[-1]
+        if mass is not None and mass_out is None:
+            raise ValueError("KV8Cache: mass needs mass_out")
+        a = KV8Attn(n, heads, self._dtype(q), scale, qr, outr, kr, vr, self._vec(counts, "counts", torch.int32, (S,)),
+                    self._vec(mask, "mask", torch.int64, (S, n)),
+                    self._vec(pages, "pages", torch.int32, (S, n, H, top_k)), top_k,
+                    self._vec(mass, "mass", torch.float32, (S, H, P)),
+                    self._vec(mass_out, "mass_out", torch.float32, (S, H, P)))
+        ws = self._scratch("w4a8_kv8_attention_workspace_bytes", a, workspace)
+        self._run("w4a8_kv8_attention", _c.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), self._on(stream))
+        return out
+
+    def select(self, q, top_k, first_pages=0, last_pages=0, counts=None, out=None, workspace=None, stream=None):
+        """The whole pages of best score for every row and KV head, int32 [n_seqs][n][n_kv_heads][top_k], ascending,
+        -1 behind the last (w4a8_kv8_select)."""
+        import torch
+        S, H = self.shape[:2]
+        qr = self._rows(q, "q")
+        n, heads = q.shape[1], q.shape[2]
+        if out is None:
+            out = torch.empty((S, n, H, top_k), dtype=torch.int32, device=self.device)
+        a = KV8Attn(n, heads, self._dtype(q), 1.0, qr)
+        a.counts = self._vec(counts, "counts", torch.int32, (S,))
+        ws = self._scratch("w4a8_kv8_select_workspace_bytes", a, workspace)
+        self._run("w4a8_kv8_select", _c.byref(a), top_k, first_pages, last_pages,
+                  self._vec(out, "out", torch.int32, (S, n, H, top_k)), ws.data_ptr(), ws.numel() * ws.element_size(),
+                  self._on(stream))
+        return out
+
+    def evict(self, mass, keep, first_pages=0, last_pages=0, in_place=False, stream=None):
+        """Keeps at most ``keep`` whole pages per KV head (w4a8_kv8_evict); returns (table, mass, len), new tensors,
+        or the cache's own and ``mass`` itself when ``in_place``."""
+        import torch
+        S, H, _, P = self.shape
+        old = (self.tensors["table"], mass, self.tensors["len"])
+        new = old if in_place else tuple(torch.empty_like(t) for t in old)
+        self._run("w4a8_kv8_evict", self._vec(mass, "mass", torch.float32, (S, H, P)), keep, first_pages, last_pages,
+                  new[0].data_ptr(), new[1].data_ptr(), new[2].data_ptr(), self._on(stream))
+        return new
 
 
 # ------------------------------------------------------------------------ model/session
