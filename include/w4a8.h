@@ -268,7 +268,7 @@ typedef struct {
   const uint64_t* mask;  /* [n_seqs][n]: bit j of row i is set where i sees new row j; NULL: j <= i */
   const int32_t* pages;  /* [n_seqs][n][n_kv_heads][top_k]: the whole pages that a row reads, ascending, -1 behind
                             the last (w4a8_kv8_select); NULL: all of them */
-  int top_k;             /* with pages: 1..max_pages */
+  int top_k;             /* with pages: 1..16384 */
   const float* mass;     /* [n_seqs][n_kv_heads][max_pages] */
   float* mass_out;       /* mass (NULL = 0) + the softmax weight that this call's rows and query heads put on each
                             whole page; may be mass itself; NULL: not wanted.  Not with pages (W4A8_ERR_UNSUPPORTED) */
@@ -285,7 +285,7 @@ w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4
 w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
                                size_t workspace_bytes, void* stream);
 
-/* Device.  For each new row and KV head the top_k whole pages of best score, as an ascending list padded with -1
+/* Device.  For each new row and KV head the top_k (1..16384) whole pages of best score, as an ascending list padded with -1
  * (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the largest over the head's query group of
  * q . (sum of the page's keys), in int8 like the pages: the group's queries get codes at one scale
  * (w4a8_quantize_rows' rule over its heads * head_dim values) and

@@ -374,7 +374,7 @@ def test_out_of_range_state_is_left_out():
 
 @pytest.mark.parametrize("H,G,D,n,dtype", [(2, 4, 128, 1, "fp32"), (1, 7, 64, 3, "bf16"), (3, 1, 64, 2, "fp32"),
                                            (1, 16, 128, 5, "bf16")])
-@pytest.mark.parametrize("top_k,first,last", [(1, 0, 0), (4, 1, 2), (5, 0, 3), (2, 2, 2), (9, 0, 0)])
+@pytest.mark.parametrize("top_k,first,last", [(1, 0, 0), (4, 1, 2), (5, 0, 3), (2, 2, 2), (9, 0, 0), (40, 1, 1)])
 def test_select_and_sparse_attention(H, G, D, n, dtype, top_k, first, last):
     rng = np.random.default_rng(G * n + top_k)
     lens = [0, 63, 64 * 5, 64 * 9 + 10]
@@ -614,4 +614,4 @@ def test_binding_refusals():
     with pytest.raises(W.W4A8Error):
         cache.attention(q, k, k, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")[:0])
     with pytest.raises(W.W4A8Error):
-        cache.select(q, 5)
+        cache.select(q, 16385)

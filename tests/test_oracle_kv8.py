@@ -96,7 +96,7 @@ def test_refusals_without_a_gpu(lib):
         return st or lib.w4a8_kv8_attention(ref(c), ref(a), ws, kw.get("bytes", 0), None)
     assert attn(n=0) == 2 and attn(n=65) == 2 and attn(n_heads=3) == 2 and attn(n_heads=34) == 2
     assert attn(dtype=7) == 1 and attn(k=W.Rows()) == 1             # k and v come together
-    assert attn(pages=0x10000, top_k=0) == 2 and attn(pages=0x10000, top_k=5) == 2
+    assert attn(pages=0x10000, top_k=0) == 2 and attn(pages=0x10000, top_k=16385) == 2
     assert attn(pages=0x10000, top_k=2, mass_out=0x10000) == 3
     assert attn(q=W.Rows()) == 1 and attn(ws=None) == 1 and attn(ws=ctypes.c_void_p(0x10010)) == 1
     assert attn() == 4                                              # a workspace of no bytes
@@ -105,6 +105,6 @@ def test_refusals_without_a_gpu(lib):
     def select(top_k=2, first=0, last=0, out=p, a=a):
         return lib.w4a8_kv8_select(ref(c), ref(a), top_k, first, last, out, p, 0, None)
     assert select(top_k=0) == 1 and select(first=-1) == 1 and select(last=-1) == 1 and select(out=None) == 1
-    assert select(top_k=5) == 2 and select() == 4 and select(a=W.KV8Attn(0, 4, 0, 1.0, rows)) == 2
+    assert select(top_k=16385) == 2 and select() == 4 and select(a=W.KV8Attn(0, 4, 0, 1.0, rows)) == 2
     assert lib.w4a8_kv8_evict(ref(c), None, 1, 0, 0, p, p, p, None) == 1
     assert lib.w4a8_kv8_evict(ref(c), p, -1, 0, 0, p, p, p, None) == 1

@@ -121,7 +121,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   if (ok != W4A8_OK) return ok;
   if (!a || !kv8_dtype(a->dtype) || !a->k.data != !a->v.data) return W4A8_ERR_ARG;
   if (a->n < 1 || a->n > kKv8MaxRows || a->n_heads < 1 || a->n_heads % c->n_kv_heads ||
-      a->n_heads / c->n_kv_heads > kKv8MaxGroup || (a->pages && (a->top_k < 1 || a->top_k > c->max_pages)))
+      a->n_heads / c->n_kv_heads > kKv8MaxGroup || (a->pages && (a->top_k < 1 || a->top_k > kKv8MaxPages)))
     return W4A8_ERR_SHAPE;
   if (a->pages && a->mass_out) return W4A8_ERR_UNSUPPORTED;
   Kv8Geom& g = p->geo;
@@ -132,7 +132,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.RB = sh.TW * sh.WC * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
-  const size_t units = p->segments * ((a->pages ? a->top_k : c->max_pages) + 8);
+  const size_t units = p->segments * ((a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages) + 8);
   if (units >= (size_t)1 << 31) return W4A8_ERR_SHAPE;
   const int ng = kKv8Warps / sh.WC;
   const size_t ctas = (units + ng - 1) / ng;

@@ -10,12 +10,17 @@
 // a 16-row query tile.  A page is stored in the operand's own order (the header documents it), so one 16-byte
 // shared-memory load gives a lane the bytes of two k-steps, and one byte permute turns two codes into two f16:
 // the byte u = code + 128 in the low half of a 16-bit lane is the subnormal u 2^-24, exact, as in the W4A8 matmul.
-// bf16 calls start the accumulators at -128 2^-24 sum(q) (or sum(P)), which takes the 128 out again; fp32 calls
-// subtract it from the operand (exact) so that the sums do not carry it.
+// bf16 calls start the accumulators at -128 2^-24 sum(q) (or sum(P)), which takes the 128 out again.  fp32 calls
+// make whole numbers of the codes (the byte under the exponent of 1024, minus 1152): the tensor core aligns
+// products by their exponents and drops what is below, and subnormal operands cost the sums 2^-20 of the
+// largest product (outputs 1.9e-6 off in the 2-norm at 4096 tokens; 2.4e-7 with whole numbers).
 //
 // fp32 operands are split, q = qh + ql and P = Ph + Pl in f16: hi and lo are neighbouring columns of a tile (four
 // rows to a tile instead of eight), so the accumulator pair of a thread holds both products of one row and adds
-// them there.  Rows of q are scaled by a power of two to use f16's range; P is scaled by 2^15.
+// them there.  Rows of q are scaled by a power of two, to a largest magnitude of at most 2^11; qh is the nearest
+// whole number, so the sums of qh with the codes are whole numbers (times 2^-24) that f32 holds, and the tensor
+// core's truncating additions do not touch them.  (With qh the nearest f16 the logits were off by 3e-7 relative.)
+// P is scaled by 2^15.
 // The transposed P fragments are made with movmatrix: no shared memory in the softmax.
 //
 // Work: every (sequence, KV head, block of rows) is a segment of units, one per page and one per 16 fp32 rows
@@ -87,23 +92,23 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// two f16 operands from bytes 2 i, 2 i + 1 of w: u 2^-24, or (u - 128) 2^-24 if SIGNED
-template <bool SIGNED>
+// Two pairs of f16 operands from the four bytes of w: the subnormals u 2^-24, or the whole numbers u - 128 if WHOLE
+// (1024 + u is the byte under the exponent of 1024).
+template <bool WHOLE>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = __byte_perm(w, 0, 0x4140);
-  hi = __byte_perm(w, 0, 0x4342);
-  if (SIGNED) {
-    const uint32_t bias = 0x00800080u;
-    const __half2 b = *reinterpret_cast<const __half2*>(&bias);
+  lo = __byte_perm(w, WHOLE ? 0x64646464u : 0u, 0x4140);
+  hi = __byte_perm(w, WHOLE ? 0x64646464u : 0u, 0x4342);
+  if (WHOLE) {
+    const __half2 b = __float2half2_rn(1152.0f);
     const __half2 l = __hsub2(*reinterpret_cast<__half2*>(&lo), b), h = __hsub2(*reinterpret_cast<__half2*>(&hi), b);
     lo = *reinterpret_cast<const uint32_t*>(&l);
     hi = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// power of two that takes a largest magnitude into [2^13, 2^14) (1 where it is not finite)
+// power of two that takes a largest magnitude into [2^10, 2^11) (1 where it is not finite)
 __device__ __forceinline__ float f16_scale(float amax) {
   const int ex = (int)(__float_as_uint(amax) >> 23) & 255;
-  return ex == 255 ? 1.0f : __uint_as_float((uint32_t)min(254, 267 - ex) << 23);
+  return ex == 255 ? 1.0f : __uint_as_float((uint32_t)min(254, 264 - ex) << 23);
 }
 
 // ---------------------------------------------------------------------------- the split kernel
@@ -115,15 +120,18 @@ struct Kv8Split {
   static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
   static constexpr int RB = WC * TW * RPT;         // rows of a column block
   static constexpr int NG = kKv8Warps / WC;        // workers of a CTA
-  static constexpr int HALF = kPage * D;           // bytes of a ring entry
+  static constexpr int HALF = kPage * D;           // bytes of a ring entry (kRowTile rows of D floats as well)
   static constexpr int NS = kKv8RingBytes / HALF / NG;  // ring entries of a worker
   static constexpr int BACK = WC == 1 ? 0 : WC;    // entries left unfilled so that the copier does not wait for the slowest warp
   static constexpr int KS = D / 16, DT = D / 16;
+  static constexpr float UNIT = SPLIT ? 1.0f : 16777216.0f;  // codes enter the products divided by this
 };
 
 // What a lane knows of one unit of its worker's range.
+constexpr int kNoUnit = INT_MIN, kNewUnit = INT_MIN + 1, kNewUnits = kKv8MaxRows / kRowTile;
 struct Kv8Unit {
-  int page;     // >= 0: (pair, physical page); -1: nothing; <= -2: row tile -2 - page (tail 0..3, new rows 4..7)
+  int src;      // >= 0: (pair, physical page); kNoUnit: nothing; kNewUnit + f: tile f of the new rows; else
+                // -1 - (4 pair + f): tile f of the open page
   int seg;      // segment
   int u;        // unit inside the segment
   float sk, sv;
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
 
   // The lane's unit x: its segment, page and scales (32 units in parallel, so the table's latency is paid once).
   auto look = [&](int x) -> Kv8Unit {
-    Kv8Unit r{-1, -1, 0, 0.0f, 0.0f};
+    Kv8Unit r{kNoUnit, -1, 0, 0.0f, 0.0f};
     if (x >= u1) return r;
     int lo = 0, hi = S - 1;  // the last sequence whose first unit is at or before x and that has units
     while (lo < hi) {
@@ -199,8 +207,10 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
     const int h = a.pages ? q % H : q / geo.CB;
     r.seg = a.pages ? s * a.n * H + q : s * H * geo.CB + q;
     r.u = u;
+    const size_t pair = kv8_pair(c, s, h);
     if (u >= un.pages) {
-      r.page = -2 - (u < un.pages + un.open ? u - un.pages : 4 + u - un.pages - un.open);
+      const int f = u - un.pages;
+      r.src = f < un.open ? -1 - (int)(pair * 4 + f) : kNewUnit + f - un.open;
       return r;
     }
     int p = u;
@@ -214,11 +224,10 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
         return r;
       }
     }
-    const size_t pair = kv8_pair(c, s, h);
     const int phys = kv8_phys(c, pair, p);
     if (phys < 0) return r;
-    r.page = (int)kv8_page(c, pair, phys);
-    const float2 sc = *reinterpret_cast<const float2*>(c.scales + (size_t)r.page * 2);
+    r.src = (int)kv8_page(c, pair, phys);
+    const float2 sc = *reinterpret_cast<const float2*>(c.scales + (size_t)r.src * 2);
     r.sk = sc.x;
     r.sv = sc.y;
     return r;
@@ -238,8 +247,8 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
   // Copies ahead as far as the ring and the two batches of units allow (one warp of the worker).
   auto copy_ahead = [&](int room) {
     while (in_ring < room && jl < nu && jl < cbase + 64) {
-      const int pg = __shfl_sync(FULL, jl < cbase + 32 ? cur.page : nxt.page, (jl - cbase) & 31);
-      if (pg < 0) {
+      const int from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
+      if (from < kNewUnit + kNewUnits) {  // new rows do not go through the ring
         ++jl;
         continue;
       }
@@ -248,7 +257,11 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
         if (WC > 1 && iph > 0) good = mbar_wait(&empty[is], (iph - 1) & 1);
         if (good) {
           mbar_expect_tx(&full[is], C::HALF);
-          bulk_g2s(ring + (size_t)is * C::HALF, c.codes + ((size_t)pg * 2 + half) * C::HALF, C::HALF, &full[is]);
+          // half a page of codes, or the keys or values of 16 fp32 rows: as many bytes
+          const void* p = from >= 0 ? static_cast<const void*>(c.codes + ((size_t)from * 2 + half) * C::HALF)
+                                    : c.tail + ((size_t)((-1 - from) >> 2) * 2 + half) * (kPage * D) +
+                                          ((-1 - from) & 3) * (kRowTile * D);
+          bulk_g2s(ring + (size_t)is * C::HALF, p, C::HALF, &full[is]);
         }
       }
       good = __shfl_sync(FULL, good, 0);
@@ -279,10 +292,12 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
 
   // ---- state of the segment
   uint32_t qf[TW][KS][2];
-  float O[DT][TW][4], m[TW][NC], l[TW][NC], colfac[TW][NC], seed[TW][2];
+  float O[DT][TW][4], m[TW][NC], l[TW][NC], colfac[TW][NC], collow[TW][NC], seed[TW][2];
   int seg = -1, seg_u = 0, seg_j = 0, s_cur = 0, h_cur = 0, i_cur = 0, cb_cur = 0, cnt_cur = 0, L_cur = 0;
   bool act = false;
-  const float lscale = a.scale * 1.4426950408889634f;
+  // the factor of a column, log2(e) scale UNIT / (power of two of its row), as hi + lo
+  const double lscale = (double)a.scale * 1.4426950408889634 * (double)C::UNIT;
+  const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
   auto row_of = [&](int j, int col) {  // query row (of the segment's R) of column col of the warp's tile j
     return cb_cur * C::RB + (wg * TW + j) * C::RPT + (SPLIT ? col >> 1 : col);
   };
@@ -353,16 +368,18 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           f[e] = v[4 * x + e] * up;
-          if (SPLIT && (g & 1)) f[e] -= __half2float(__float2half_rn(f[e]));
+          if (SPLIT) f[e] = g & 1 ? f[e] - rintf(f[e]) : rintf(f[e]);
           if (!SPLIT) sum += __half2float(__float2half_rn(f[e]));
         }
         qf[j][x][0] = pack_f16(f[0], f[1]);
         qf[j][x][1] = pack_f16(f[2], f[3]);
       }
       // per-column values, from the lanes of column g to the lanes of accumulator columns 2t, 2t + 1
-      const float cf = lscale * 16777216.0f * (1.0f / up);
+      const float down = 1.0f / up;
       if (SPLIT) {
-        colfac[j][0] = __shfl_sync(FULL, cf, 8 * t);
+        const float dn = __shfl_sync(FULL, down, 8 * t);
+        colfac[j][0] = lhi * dn;
+        collow[j][0] = llo * dn;
         seed[j][0] = seed[j][1] = 0.0f;
       } else {
         sum += __shfl_xor_sync(FULL, sum, 1);
@@ -370,7 +387,9 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
         sum *= -128.0f / 16777216.0f;
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
-          colfac[j][x] = __shfl_sync(FULL, cf, 4 * (2 * t + x));
+          const float dn = __shfl_sync(FULL, down, 4 * (2 * t + x));
+          colfac[j][x] = lhi * dn;
+          collow[j][x] = llo * dn;
           seed[j][x] = __shfl_sync(FULL, sum, 4 * (2 * t + x));
         }
       }
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
         const int r = row_of(j, 2 * t + x);
         if (!row_ok(r)) continue;
         if (whole) {
-          const float f = sum == 0.0f ? 0.0f : 16777216.0f / sum;
+          const float f = sum == 0.0f ? 0.0f : C::UNIT / sum;
           T* out = static_cast<T*>(a.out.data) + s_cur * a.out.seq + row_node(r) * a.out.row + row_head(r) * a.out.head;
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
@@ -408,36 +427,47 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
           float* o = ws.o + at * D;
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            o[16 * d + g] = (SPLIT ? O[d][j][0] + O[d][j][1] : O[d][j][x]) * 16777216.0f;
-            o[16 * d + g + 8] = (SPLIT ? O[d][j][2] + O[d][j][3] : O[d][j][x + 2]) * 16777216.0f;
+            o[16 * d + g] = (SPLIT ? O[d][j][0] + O[d][j][1] : O[d][j][x]) * C::UNIT;
+            o[16 * d + g + 8] = (SPLIT ? O[d][j][2] + O[d][j][3] : O[d][j][x + 2]) * C::UNIT;
           }
         }
       }
   };
 
-  // Softmax of MT x 16 tokens: x (log2 units; SPLIT: entries 0 and 2) becomes P 2^15 in place, pf its B fragments,
-  // cc the factor of the old sums, psum the sum over the tokens of a lane's own P (as used by the product).
-  float cc[TW][NC], psum[TW][NC];
-  auto soft = [&](auto mtc, float (&x)[4][TW][4], uint32_t (&pf)[4][TW][2]) {
+  // Softmax of MT x 16 tokens: x (SPLIT: entries 0 and 2) becomes P 2^15 in place, pf its B fragments, cc the factor
+  // of the old sums, psum the sum over the tokens of a lane's own P, rsum that of P as rounded to f16.  PAGE: x are
+  // sums of codes and the logit is x (fh + fl), taken relative to the maximum with one rounding at the size of
+  // the difference: a relative error of a factor is one of the softmax's temperature, which large logits multiply.
+  float cc[TW][NC], psum[TW][NC], rsum[TW][NC];
+  auto soft = [&](auto mtc, auto pagec, float (&x)[4][TW][4], uint32_t (&pf)[4][TW][2], const float (&fh)[TW][NC],
+                  const float (&fl)[TW][NC]) {
     constexpr int MT = decltype(mtc)::value;
+    constexpr bool PAGE = decltype(pagec)::value;
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
 #pragma unroll
       for (int y = 0; y < NC; ++y) {
-        float mx = x[0][j][y];
+        float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) mx = fmaxf(mx, fmaxf(x[i][j][y], x[i][j][y + 2]));
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = y; e < 4; e += 2) mx = fmaxf(mx, PAGE ? x[i][j][e] * fh[j][y] : x[i][j][e]);
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
         const float mn = fmaxf(m[j][y], mx), base = mn == -INFINITY ? 0.0f : mn;
         cc[j][y] = ex2(m[j][y] - base);
         m[j][y] = mn;
-        psum[j][y] = 0.0f;
+        psum[j][y] = rsum[j][y] = 0.0f;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = y; e < 4; e += 2) x[i][j][e] = ex2(x[i][j][e] - base) * 32768.0f;
+          for (int e = y; e < 4; e += 2) {
+            float v = PAGE ? fmaf(x[i][j][e], fh[j][y], -base) : x[i][j][e] - base;
+            if (PAGE) v = fmaf(x[i][j][e], fl[j][y], v);
+            x[i][j][e] = ex2(v) * 32768.0f;
+            psum[j][y] += x[i][j][e];
+          }
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -446,13 +476,12 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
           uint32_t pk;
           if (SPLIT) {
             const float p = x[i][j][2 * e];
-            psum[j][0] += p;
             pk = pack_f16(p, p - __half2float(__float2half_rn(p)));
           } else {
             pk = pack_f16(x[i][j][2 * e], x[i][j][2 * e + 1]);
             const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pk));
-            psum[j][0] += r.x;
-            psum[j][NC - 1] += r.y;
+            rsum[j][0] += r.x;
+            rsum[j][NC - 1] += r.y;
           }
           pf[i][j][e] = movmatrix(pk);
         }
@@ -473,59 +502,67 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
 #pragma unroll
         for (int j = 0; j < TW; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][j][e] = seed[j][e & 1];
+          for (int e = 0; e < 4; ++e) x[i][j][e] = SPLIT ? 0.0f : seed[j][e & 1];
 #pragma unroll
       for (int kp = 0; kp < D / 32; ++kp)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 w = *reinterpret_cast<const uint4*>(kb + ((i * (D / 32) + kp) * 32 + lane) * 16);
-          uint32_t af[4];
-          codes_f16<SPLIT>(w.x, af[0], af[2]);
-          codes_f16<SPLIT>(w.y, af[1], af[3]);
+          uint32_t a0[4], a1[4];
+          codes_f16<SPLIT>(w.x, a0[0], a0[2]);
+          codes_f16<SPLIT>(w.y, a0[1], a0[3]);
+          codes_f16<SPLIT>(w.z, a1[0], a1[2]);
+          codes_f16<SPLIT>(w.w, a1[1], a1[3]);
 #pragma unroll
-          for (int j = 0; j < TW; ++j) mma_f16(x[i][j], af, qf[j][2 * kp][0], qf[j][2 * kp][1]);
-          codes_f16<SPLIT>(w.z, af[0], af[2]);
-          codes_f16<SPLIT>(w.w, af[1], af[3]);
-#pragma unroll
-          for (int j = 0; j < TW; ++j) mma_f16(x[i][j], af, qf[j][2 * kp + 1][0], qf[j][2 * kp + 1][1]);
+          for (int j = 0; j < TW; ++j) {
+            mma_f16(x[i][j], a0, qf[j][2 * kp][0], qf[j][2 * kp][1]);
+            mma_f16(x[i][j], a1, qf[j][2 * kp + 1][0], qf[j][2 * kp + 1][1]);
+          }
         }
     }
     release_half();
     if (act) {
+      if (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < TW; ++j) x[i][j][0] += x[i][j][1], x[i][j][2] += x[i][j][3];  // hi + lo
+      }
+      float fh[TW][NC], fl[TW][NC];
 #pragma unroll
       for (int j = 0; j < TW; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (SPLIT) {
-            const float f = colfac[j][0] * sk;
-            x[i][j][0] = (x[i][j][0] + x[i][j][1]) * f;
-            x[i][j][2] = (x[i][j][2] + x[i][j][3]) * f;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][j][e] *= colfac[j][(e & 1) * (NC - 1)] * sk;
-          }
+        for (int y = 0; y < NC; ++y) {
+          fh[j][y] = colfac[j][y] * sk;
+          fl[j][y] = fmaf(colfac[j][y], sk, -fh[j][y]) + collow[j][y] * sk;
         }
-      soft(std::integral_constant<int, 4>{}, x, pf);
+      soft(std::integral_constant<int, 4>{}, std::true_type{}, x, pf, fh, fl);
     }
     const uint8_t* vb = wait_half();
     if (!ok) return;
     if (act) {
       float ps[TW][2];
-      if (!SPLIT || ws.page) {
 #pragma unroll
-        for (int j = 0; j < TW; ++j)
+      for (int j = 0; j < TW; ++j)
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
+        for (int y = 0; y < NC; ++y) {
+          if (!SPLIT) {
+            float v = rsum[j][y];
+            v += __shfl_xor_sync(FULL, v, 4);
+            v += __shfl_xor_sync(FULL, v, 8);
+            v += __shfl_xor_sync(FULL, v, 16);
+            ps[j][y] = v * (-128.0f / 16777216.0f);
+          }
+          if (ws.page) {
             float v = psum[j][y];
             v += __shfl_xor_sync(FULL, v, 4);
             v += __shfl_xor_sync(FULL, v, 8);
             v += __shfl_xor_sync(FULL, v, 16);
-            if (ws.page && g == 0)
+            if (g == 0)
               ws.page[((size_t)seg * c.max_pages + u) * C::RB + (wg * TW + j) * C::RPT + (SPLIT ? t : 2 * t + y)] =
                   make_float2(m[j][y], v);
-            ps[j][y] = v * (-128.0f / 16777216.0f);
           }
-      }
+        }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         float o[TW][4];
@@ -555,51 +592,68 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
     release_half();
   };
 
-  // Sixteen rows in floating point (open page: fresh = -1; new rows: fresh = their tile), nv of them valid:
-  // keys and values as f16 hi (+ lo) of the value times a power of two, from the tile's largest magnitude.
-  auto rows = [&](auto* kr, int64_t kstep, auto* vr, int64_t vstep, int nv, int fresh, bool vec) {
-    if (!act) return;
-    using E = std::remove_cv_t<std::remove_pointer_t<decltype(kr)>>;
+  // Sixteen rows in floating point, nv of them valid: the open page's from the ring (fresh = -1), or tile `fresh` of
+  // the new rows from memory.  Keys and values as f16 hi (+ lo) of the value times a power of two, from the
+  // tile's largest magnitude.
+  auto rows = [&](int nv, int fresh) {
     float x[4][TW][4];
     uint32_t pf[4][TW][2];
-    auto key8 = [&](int r, int kp, float (&v)[8]) {  // dims 32 kp + 8 t .. + 7 of row r
+    float kv[D / 32][2][8];  // dims 32 kp + 8 t .. + 7 of rows g, g + 8
+    if (fresh < 0) {
+      const float* kb = reinterpret_cast<const float*>(wait_half());
+      if (!ok) return;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      if (r >= nv) return;
-      const E* p = kr + (int64_t)r * kstep + 32 * kp + 8 * t;
-      if (vec) {
-        uint4 w[sizeof(E) / 2];
+      for (int kp = 0; kp < D / 32; ++kp)
 #pragma unroll
-        for (int e = 0; e < (int)sizeof(E) / 2; ++e) w[e] = reinterpret_cast<const uint4*>(p)[e];
-        const E* q = reinterpret_cast<const E*>(w);
+        for (int b = 0; b < 2; ++b) {
+          const float4* p = reinterpret_cast<const float4*>(kb + (g + 8 * b) * D + 32 * kp + 8 * t);
+          const float4 v0 = p[0], v1 = p[1];  // rows behind the last one are read and not used
+          const float w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = kv8_load(q + e);
-      } else {
+          for (int e = 0; e < 8; ++e) kv[kp][b][e] = g + 8 * b < nv ? w[e] : 0.0f;
+        }
+      release_half();
+    } else if (act) {
+      const T* kn = static_cast<const T*>(a.k.data) + s_cur * a.k.seq + h_cur * a.k.head;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = kv8_load(p + e);
+      for (int b = 0; b < 2; ++b) {
+        const int r = fresh * kRowTile + g + 8 * b;
+        const T* p = kn + (int64_t)r * a.k.row + 8 * t;
+#pragma unroll
+        for (int kp = 0; kp < D / 32; ++kp) {
+          if (g + 8 * b >= nv) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kv[kp][b][e] = 0.0f;
+          } else if (geo.vec & 2) {
+            uint4 w[sizeof(T) / 2];
+#pragma unroll
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e) w[e] = reinterpret_cast<const uint4*>(p + 32 * kp)[e];
+            const T* q = reinterpret_cast<const T*>(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kv[kp][b][e] = kv8_load(q + e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kv[kp][b][e] = kv8_load(p + 32 * kp + e);
+          }
+        }
       }
-    };
-    auto value = [&](int r, int d) { return r < nv ? kv8_load(vr + (int64_t)r * vstep + d) : 0.0f; };
+    }
+    if (!act) {
+      if (fresh < 0) {
+        wait_half();
+        if (ok) release_half();
+      }
+      return;
+    }
     float km = 0.0f, vm = 0.0f;
 #pragma unroll
     for (int kp = 0; kp < D / 32; ++kp)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float v[8];
-        key8(g + 8 * b, kp, v);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) km = fabsf(v[e]) <= 3.402823466e38f ? fmaxf(km, fabsf(v[e])) : km;
-      }
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vm = max_nan(vm, fabsf(value(2 * t + (e & 1) + 8 * (e >> 2), 16 * d + g + 8 * ((e >> 1) & 1))));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      km = fmaxf(km, __shfl_xor_sync(FULL, km, o));
-      vm = max_nan(vm, __shfl_xor_sync(FULL, vm, o));
-    }
-    const float kup = f16_scale(km), vup = f16_scale(vm);
+        for (int e = 0; e < 8; ++e) km = fabsf(kv[kp][b][e]) <= 3.402823466e38f ? fmaxf(km, fabsf(kv[kp][b][e])) : km;
+    km = warp_max(km);
+    const float kup = f16_scale(km);
     auto split = [&](float v0, float v1, uint32_t& hi, uint32_t& lo) {
       hi = pack_f16(v0, v1);
       const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
@@ -611,9 +665,8 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
       for (int e = 0; e < 4; ++e) x[0][j][e] = 0.0f;
 #pragma unroll
     for (int kp = 0; kp < D / 32; ++kp) {
-      float v0[8], v1[8];
-      key8(g, kp, v0);
-      key8(g + 8, kp, v1);
+      const float* v0 = kv[kp][0];
+      const float* v1 = kv[kp][1];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         uint32_t hi[4], lo[4];
@@ -629,7 +682,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
       }
     }
     uint32_t vis = 0;  // bit (j NC + y) 2 + e: the row of column y sees token g + 8 e
-    const float kdown = (1.0f / kup) / 16777216.0f;
+    const float kdown = (1.0f / kup) / C::UNIT;
 #pragma unroll
     for (int j = 0; j < TW; ++j)
 #pragma unroll
@@ -643,25 +696,52 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
                                            : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
           bits &= (uint32_t)(mask >> (kRowTile * fresh));
         }
-        const float f = colfac[j][y] * kdown;
+        const float fh = colfac[j][y] * kdown, fl = collow[j][y] * kdown;  // a power of two: exact
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const bool see = bits >> (g + 8 * e) & 1u;
           vis |= (uint32_t)see << ((j * NC + y) * 2 + e);
           const float v = SPLIT ? x[0][j][2 * e] + x[0][j][2 * e + 1] : x[0][j][2 * e + y];
-          x[0][j][2 * e + y] = see ? v * f : -INFINITY;
+          x[0][j][2 * e + y] = see ? fmaf(v, fh, v * fl) : -INFINITY;
         }
       }
-    soft(std::integral_constant<int, 1>{}, x, pf);
+    soft(std::integral_constant<int, 1>{}, std::false_type{}, x, pf, colfac, collow);
+    // entry (e >> 1, e & 1, d): tokens 2t + (e & 1) + 8 (e >> 2), dims 16 d + g + 8 (e >> 1 & 1)
+    float v[DT][8];
+    if (fresh < 0) {
+      const float* vb = reinterpret_cast<const float*>(wait_half());
+      if (!ok) return;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = 2 * t + (e & 1) + 8 * (e >> 2);
+          v[d][e] = r < nv ? vb[r * D + 16 * d + g + 8 * ((e >> 1) & 1)] : 0.0f;
+        }
+    } else {
+      const T* vn = static_cast<const T*>(a.v.data) + s_cur * a.v.seq + h_cur * a.v.head;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = 2 * t + (e & 1) + 8 * (e >> 2);
+          v[d][e] = r < nv ? kv8_load(vn + (int64_t)(fresh * kRowTile + r) * a.v.row + 16 * d + g + 8 * ((e >> 1) & 1)) : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vm = max_nan(vm, fabsf(v[d][e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) vm = max_nan(vm, __shfl_xor_sync(FULL, vm, o));
     if (vm <= 3.402823466e38f) {
-      const float vdown = (1.0f / vup) / 16777216.0f;
+      const float vup = f16_scale(vm), vdown = (1.0f / vup) / C::UNIT;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)  // operand register e: dim g + 8 (e & 1), tokens 2t, 2t + 1, + 8 (e >> 1)
-          split(value(2 * t + 8 * (e >> 1), 16 * d + g + 8 * (e & 1)) * vup,
-                value(2 * t + 1 + 8 * (e >> 1), 16 * d + g + 8 * (e & 1)) * vup, hi[e], lo[e]);
+          split(v[d][(e >> 1) * 4 + (e & 1) * 2] * vup, v[d][(e >> 1) * 4 + (e & 1) * 2 + 1] * vup, hi[e], lo[e]);
 #pragma unroll
         for (int j = 0; j < TW; ++j) {
           float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -671,6 +751,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
           for (int e = 0; e < 4; ++e) O[d][j][e] = fmaf(o[e], vdown, O[d][j][e] * cc[j][(e & 1) * (NC - 1)]);
         }
       }
+      if (fresh < 0) release_half();
       return;
     }
     // A value is not finite: 0 times it would reach rows that do not see it, so each row adds what it sees.
@@ -680,23 +761,28 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
       for (int j = 0; j < TW; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) O[d][j][e] *= cc[j][(e & 1) * (NC - 1)];
+    // entry q of a lane's values (token 2t + (q & 1) + 8 (q >> 1)) is handed to the lanes of the same dims
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
 #pragma unroll 1
-    for (int r = 0; r < nv; ++r)
+      for (int tt = 0; tt < 4; ++tt) {
+        const int r = 2 * tt + (q & 1) + 8 * (q >> 1), src = (r & 7) << 2 | t;
 #pragma unroll
-      for (int j = 0; j < TW; ++j)
+        for (int j = 0; j < TW; ++j)
 #pragma unroll
-        for (int y = 0; y < NC; ++y) {
-          const int src = (r & 7) << 2 | t;
-          const float p0 = __shfl_sync(FULL, x[0][j][y], src), p1 = __shfl_sync(FULL, x[0][j][y + 2], src);
-          const float p = (r < 8 ? p0 : p1) / 16777216.0f;
-          const uint32_t see = __shfl_sync(FULL, vis, src) >> ((j * NC + y) * 2 + (r >> 3)) & 1u;
-          if (!see) continue;
+          for (int y = 0; y < NC; ++y) {
+            const float p = __shfl_sync(FULL, x[0][j][2 * (q >> 1) + y], src) / C::UNIT;
+            const uint32_t see = __shfl_sync(FULL, vis, src) >> ((j * NC + y) * 2 + (q >> 1)) & 1u;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            O[d][j][y] = fmaf(p, value(r, 16 * d + g), O[d][j][y]);
-            O[d][j][y + 2] = fmaf(p, value(r, 16 * d + g + 8), O[d][j][y + 2]);
+            for (int d = 0; d < DT; ++d) {
+              const float v0 = __shfl_sync(FULL, v[d][(q >> 1) * 4 + (q & 1)], g << 2 | tt);
+              const float v1 = __shfl_sync(FULL, v[d][(q >> 1) * 4 + 2 + (q & 1)], g << 2 | tt);
+              if (see) O[d][j][y] = fmaf(p, v0, O[d][j][y]);
+              if (see) O[d][j][y + 2] = fmaf(p, v1, O[d][j][y + 2]);
+            }
           }
-        }
+      }
+    if (fresh < 0) release_half();
   };
 
   // ---- the range
@@ -709,26 +795,20 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
       if (wg == 0) copy_ahead(C::NS - C::BACK);
     }
     const int src = j - cbase;
-    const int pg = __shfl_sync(FULL, cur.page, src), sg = __shfl_sync(FULL, cur.seg, src);
+    const int from = __shfl_sync(FULL, cur.src, src), sg = __shfl_sync(FULL, cur.seg, src);
     const int u = __shfl_sync(FULL, cur.u, src);
     if (sg != seg) {
       if (seg >= 0) flush(last_u + 1);
       begin(sg, u, j);
     }
     last_u = u;
-    if (pg >= 0) {
+    if (from >= 0) {
       page(__shfl_sync(FULL, cur.sk, src), __shfl_sync(FULL, cur.sv, src), u);
-    } else if (pg <= -2) {
-      const int tile = -2 - pg;
-      if (tile < 4) {
-        const float* kt = c.tail + kv8_pair(c, s_cur, h_cur) * 2 * kPage * D + tile * kRowTile * D;
-        rows(kt, D, kt + kPage * D, D, min(kRowTile, L_cur % kPage - tile * kRowTile), -1, true);
-      } else {
-        const int f = tile - 4;
-        const T* kn = static_cast<const T*>(a.k.data) + s_cur * a.k.seq + h_cur * a.k.head + f * kRowTile * a.k.row;
-        const T* vn = static_cast<const T*>(a.v.data) + s_cur * a.v.seq + h_cur * a.v.head + f * kRowTile * a.v.row;
-        rows(kn, a.k.row, vn, a.v.row, min(kRowTile, cnt_cur - f * kRowTile), f, (geo.vec & 2) != 0);
-      }
+    } else if (from >= kNewUnit + kNewUnits) {
+      rows(min(kRowTile, L_cur % kPage - ((-1 - from) & 3) * kRowTile), -1);
+    } else if (from != kNoUnit) {
+      const int f = from - kNewUnit;
+      rows(min(kRowTile, cnt_cur - f * kRowTile), f);
     }
   }
   if (ok) {

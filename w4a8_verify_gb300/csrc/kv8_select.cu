@@ -262,7 +262,7 @@ W4A8_API w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_att
   if (!a->q.data || !aligned(a->q.data, kv8_elem(a->dtype)) || !pages_out || !workspace || !aligned(workspace, 256) ||
       top_k < 1 || first_pages < 0 || last_pages < 0)
     return W4A8_ERR_ARG;
-  if (top_k > c->max_pages) return W4A8_ERR_SHAPE;
+  if (top_k > kKv8MaxPages) return W4A8_ERR_SHAPE;
   if (workspace_bytes < need) return W4A8_ERR_CAPACITY;
   cudaStream_t st = as_stream(stream);
   uint32_t* keys = static_cast<uint32_t*>(workspace);
