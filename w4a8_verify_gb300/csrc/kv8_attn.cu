@@ -134,7 +134,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
   const size_t units = p->segments * ((a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages) + 8);
   if (units >= (size_t)1 << 31) return W4A8_ERR_SHAPE;
-  const int ng = kKv8Warps / sh.WC;
+  const int ng = kv8_warps(sh.TW) / sh.WC;
   const size_t ctas = (units + ng - 1) / ng;
   g.workers = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas) * ng;
   p->prefix = 0;

@@ -36,7 +36,8 @@
 namespace w4a8 {
 
 constexpr int kKv8Ctas = 152;         // one per SM of a GB300
-constexpr int kKv8Warps = 8;          // warps of a CTA, one CTA per SM (registers: 8 warps x 255)
+// Warps of a CTA (one CTA per SM): twelve where a warp holds one tile (168 registers), eight where it holds two.
+__host__ __device__ constexpr int kv8_warps(int TW) { return TW == 1 ? 12 : 8; }
 constexpr int kKv8RingBytes = 196608; // ring of half pages per SM: 24 of 8 KB or 48 of 4 KB
 constexpr int kRowTile = 16;          // fp32 rows of one unit
 
@@ -119,7 +120,8 @@ struct Kv8Split {
   static constexpr int RPT = SPLIT ? 4 : 8;        // rows of an 8-column tile
   static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
   static constexpr int RB = WC * TW * RPT;         // rows of a column block
-  static constexpr int NG = kKv8Warps / WC;        // workers of a CTA
+  static constexpr int WARPS = kv8_warps(TW);
+  static constexpr int NG = WARPS / WC;            // workers of a CTA
   static constexpr int HALF = kPage * D;           // bytes of a ring entry (kRowTile rows of D floats as well)
   static constexpr int NS = kKv8RingBytes / HALF / NG;  // ring entries of a worker
   static constexpr int BACK = WC == 1 ? 0 : WC;    // entries left unfilled so that the copier does not wait for the slowest warp
@@ -138,7 +140,7 @@ struct Kv8Unit {
 };
 
 template <typename T, int D, int TW, int WC>
-__global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
+__global__ void __launch_bounds__(32 * kv8_warps(TW), 1) k_kv8_split(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
                                                                   Kv8Scratch ws) {
   using C = Kv8Split<T, D, TW, WC>;
   constexpr bool SPLIT = C::SPLIT;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
   const int g = lane >> 2, t = lane & 3;
   const int H = c.n_kv_heads, S = c.n_seqs;
 
-  for (int i = tid; i < C::NG * C::NS; i += 32 * kKv8Warps) {
+  for (int i = tid; i < C::NG * C::NS; i += 32 * C::WARPS) {
     mbar_init(&full[i], 1);
     mbar_init(&empty[i], WC);
   }
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
   griddep_enter();
 
   // units before each sequence
-  for (int s = tid; s < S; s += 32 * kKv8Warps) {
+  for (int s = tid; s < S; s += 32 * C::WARPS) {
     const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
     prefix[s + 1] = L < 0 || cnt < 0 ? 0 : kv8_units(a, L, cnt).total() * kv8_segments(c, a, geo, cnt);
   }
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
   }
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int s = tid; s <= S; s += 32 * kKv8Warps) ws.prefix[s] = prefix[s];
+    for (int s = tid; s <= S; s += 32 * C::WARPS) ws.prefix[s] = prefix[s];
 
   const int U = prefix[S];
   const int W = min(geo.workers, U), worker = grp * gridDim.x + blockIdx.x;  // few units spread over the SMs
@@ -435,10 +437,10 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
   };
 
   // Softmax of MT x 16 tokens: x (SPLIT: entries 0 and 2) becomes P 2^15 in place, pf its B fragments, cc the factor
-  // of the old sums, psum the sum over the tokens of a lane's own P, rsum that of P as rounded to f16.  PAGE: x are
+  // of the old sums, psum the sum over the tokens of a lane's own P.  PAGE: x are
   // sums of codes and the logit is x (fh + fl), taken relative to the maximum with one rounding at the size of
   // the difference: a relative error of a factor is one of the softmax's temperature, which large logits multiply.
-  float cc[TW][NC], psum[TW][NC], rsum[TW][NC];
+  float cc[TW][NC], psum[TW][NC];
   auto soft = [&](auto mtc, auto pagec, float (&x)[4][TW][4], uint32_t (&pf)[4][TW][2], const float (&fh)[TW][NC],
                   const float (&fl)[TW][NC]) {
     constexpr int MT = decltype(mtc)::value;
@@ -458,14 +460,18 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
         const float mn = fmaxf(m[j][y], mx), base = mn == -INFINITY ? 0.0f : mn;
         cc[j][y] = ex2(m[j][y] - base);
         m[j][y] = mn;
-        psum[j][y] = rsum[j][y] = 0.0f;
+        psum[j][y] = 0.0f;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = y; e < 4; e += 2) {
-            float v = PAGE ? fmaf(x[i][j][e], fh[j][y], -base) : x[i][j][e] - base;
-            if (PAGE) v = fmaf(x[i][j][e], fl[j][y], v);
-            x[i][j][e] = ex2(v) * 32768.0f;
+            if (SPLIT) {
+              float v = PAGE ? fmaf(x[i][j][e], fh[j][y], -base) : x[i][j][e] - base;
+              if (PAGE) v = fmaf(x[i][j][e], fl[j][y], v);
+              x[i][j][e] = ex2(v) * 32768.0f;
+            } else {
+              x[i][j][e] = ex2(PAGE ? fmaf(x[i][j][e], fh[j][y], 15.0f - base) : x[i][j][e] + (15.0f - base));
+            }
             psum[j][y] += x[i][j][e];
           }
       }
@@ -479,9 +485,6 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
             pk = pack_f16(p, p - __half2float(__float2half_rn(p)));
           } else {
             pk = pack_f16(x[i][j][2 * e], x[i][j][2 * e + 1]);
-            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pk));
-            rsum[j][0] += r.x;
-            rsum[j][NC - 1] += r.y;
           }
           pf[i][j][e] = movmatrix(pk);
         }
@@ -541,19 +544,24 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
     const uint8_t* vb = wait_half();
     if (!ok) return;
     if (act) {
-      float ps[TW][2];
+      // -128 2^-24 sum(P) of the columns, P as the product uses it: a row of constants times P
+      float ps[TW][4];
+      if (!SPLIT) {
+        const uint32_t k = 0x80808080u;  // f16 -128 2^-24 = 0x8080
+        const uint32_t ones[4] = {k, k, k, k};
 #pragma unroll
-      for (int j = 0; j < TW; ++j)
+        for (int j = 0; j < TW; ++j) {
 #pragma unroll
-        for (int y = 0; y < NC; ++y) {
-          if (!SPLIT) {
-            float v = rsum[j][y];
-            v += __shfl_xor_sync(FULL, v, 4);
-            v += __shfl_xor_sync(FULL, v, 8);
-            v += __shfl_xor_sync(FULL, v, 16);
-            ps[j][y] = v * (-128.0f / 16777216.0f);
-          }
-          if (ws.page) {
+          for (int e = 0; e < 4; ++e) ps[j][e] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_f16(ps[j], ones, pf[i][j][0], pf[i][j][1]);
+        }
+      }
+      if (ws.page) {
+#pragma unroll
+        for (int j = 0; j < TW; ++j)
+#pragma unroll
+          for (int y = 0; y < NC; ++y) {
             float v = psum[j][y];
             v += __shfl_xor_sync(FULL, v, 4);
             v += __shfl_xor_sync(FULL, v, 8);
@@ -562,7 +570,20 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
               ws.page[((size_t)seg * c.max_pages + u) * C::RB + (wg * TW + j) * C::RPT + (SPLIT ? t : 2 * t + y)] =
                   make_float2(m[j][y], v);
           }
-        }
+      }
+      bool same = true;  // no row of the warp has a new maximum
+#pragma unroll
+      for (int j = 0; j < TW; ++j)
+#pragma unroll
+        for (int y = 0; y < NC; ++y) same = same && cc[j][y] == 1.0f;
+      if (!__all_sync(FULL, same)) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int j = 0; j < TW; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[d][j][e] *= cc[j][(e & 1) * (NC - 1)];
+      }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         float o[TW][4];
@@ -586,7 +607,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, 1) k_kv8_split(w4a8_kv8_cache 
 #pragma unroll
         for (int j = 0; j < TW; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) O[d][j][e] = fmaf(o[j][e], sv, O[d][j][e] * cc[j][(e & 1) * (NC - 1)]);
+          for (int e = 0; e < 4; ++e) O[d][j][e] = fmaf(o[j][e], sv, O[d][j][e]);
       }
     }
     release_half();
@@ -849,7 +870,7 @@ cudaError_t kv8_split_launch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
   const size_t most = kv8_split_smem(kKv8MaxSeqs, C::NG * C::NS), smem = kv8_split_smem(c.n_seqs, C::NG * C::NS);
   cudaError_t e = cudaFuncSetAttribute(k_kv8_split<T, D, TW, WC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_kv8_split<T, D, TW, WC>, dim3((unsigned)(geo.workers / C::NG)), dim3(32 * kKv8Warps), smem, st, c, a,
+  return launch_pdl(k_kv8_split<T, D, TW, WC>, dim3((unsigned)(geo.workers / C::NG)), dim3(32 * C::WARPS), smem, st, c, a,
                     geo, ws);
 }
 template <typename T, int D>
