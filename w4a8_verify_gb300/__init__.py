@@ -8,7 +8,9 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libw4a8.so")
@@ -93,13 +95,13 @@ _SIGNATURES = {
     "w4a8_kv8_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(_sz)],
     "w4a8_kv8_reset": [_c.POINTER(KV8CacheDesc), _vp],
     "w4a8_kv8_check": [_c.POINTER(KV8CacheDesc), _c.POINTER(_c.c_uint32)],
-    "w4a8_kv8_append": [_c.POINTER(KV8CacheDesc), _c.POINTER(Rows), _c.POINTER(Rows), _i32, _i32, _i32, _vp, _vp, _vp,
+    "w4a8_kv8_append": [_c.POINTER(KV8CacheDesc), _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
                         _vp],
     "w4a8_kv8_read": [_c.POINTER(KV8CacheDesc), _vp, _vp, _i32, _vp, _vp, _vp],
-    "w4a8_kv8_attention_workspace_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _c.POINTER(_sz)],
-    "w4a8_kv8_attention": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _vp, _sz, _vp],
-    "w4a8_kv8_select_workspace_bytes": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _c.POINTER(_sz)],
-    "w4a8_kv8_select": [_c.POINTER(KV8CacheDesc), _c.POINTER(KV8Attn), _i32, _i32, _i32, _vp, _vp, _sz, _vp],
+    "w4a8_kv8_attention_workspace_bytes": [_c.POINTER(KV8CacheDesc), _vp, _c.POINTER(_sz)],
+    "w4a8_kv8_attention": [_c.POINTER(KV8CacheDesc), _vp, _vp, _sz, _vp],
+    "w4a8_kv8_select_workspace_bytes": [_c.POINTER(KV8CacheDesc), _vp, _c.POINTER(_sz)],
+    "w4a8_kv8_select": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp],
     "w4a8_kv8_evict": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
     "w4a8_model_create": [_c.POINTER(ModelDesc), _c.POINTER(_vp)],
     "w4a8_model_load_tensor": [_vp, _i32, _i32, _vp, _vp, _vp],
@@ -334,6 +336,19 @@ def w4a8_matmul(a_q, a_s, w_t, s_t, N, y=None, workspace=None, stream=None):
 
 # ------------------------------------------------------------- key/value cache in 8 bits
 
+def _on_stream(fn):
+    """A method whose ``stream`` argument makes it run (and allocate) with that stream as the current one."""
+    @functools.wraps(fn)
+    def call(self, *args, stream=None, **kw):
+        if stream is None:
+            return fn(self, *args, **kw)
+        if stream.device != self.device:
+            raise ValueError("KV8Cache: the stream is on another device than the cache")
+        with self._torch.cuda.stream(stream):
+            return fn(self, *args, **kw)
+    return call
+
+
 class KV8Cache:
     """One layer of ``n_seqs`` sequences' keys and values in 8 bits (w4a8_kv8_cache).
 
@@ -341,13 +356,21 @@ class KV8Cache:
     ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
     fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
     stream; device state that is out of range is reported by ``check``.
+
+    A decode step is a few microseconds on the device, so the calls marshal their arguments as packed bytes
+    (w4a8_kv8_attn, w4a8_rows) and keep no more than the workspace sizes of the shapes seen.
     """
 
     _NAMES = (("codes", "uint8"), ("scales", "float32"), ("sums", "int16"), ("tail", "float32"), ("table", "int32"),
               ("len", "int32"), ("ctl", "int32"))
+    _ATTN = struct.Struct("@iiif 4q 4q 4q 4q 3q i 2q")   # w4a8_kv8_attn
+    _ROWS = struct.Struct("@4q")                         # w4a8_rows
+    _NONE = (0, 0, 0, 0)
 
-    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, device="cuda", tensors=None, stream=None):
+    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, device="cuda", tensors=None):
         import torch
+        self._torch = torch
+        self._types = {torch.float32: 0, torch.bfloat16: 1}
         self.desc = KV8CacheDesc(n_seqs, n_kv_heads, head_dim, max_pages)
         self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
         need = (_sz * 7)()
@@ -364,62 +387,68 @@ class KV8Cache:
         self.device = self.tensors["codes"].device
         if any(t.device != self.device for t in self.tensors.values()) or self.device.type != "cuda":
             raise ValueError("KV8Cache: the tensors must be on one CUDA device")
+        self._dev = self.device.index
         self._ref = _c.byref(self.desc)
+        self._sizes = {}
         if tensors is None:
-            self.reset(stream)
+            self.reset()
 
     @property
     def len(self):
         return self.tensors["len"]
 
-    def _on(self, stream):
-        """The stream of a call, which must be one of the cache's device."""
-        import torch
-        if stream is not None:
-            if stream.device != self.device:
-                raise ValueError("KV8Cache: the stream is on another device than the cache")
-            return stream.cuda_stream
-        return torch.cuda.current_stream(self.device).cuda_stream
-
     def _run(self, name, *args):
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            _call(name, self._ref, *args)
+        """Calls the entry point with its last argument, the current stream of the cache's device."""
+        torch = self._torch
+        st = torch._C._cuda_getCurrentRawStream(self._dev)
+        fn = getattr(_lib, name)
+        if torch.cuda.current_device() == self._dev:
+            status = fn(self._ref, *args, st)
         else:
             with torch.cuda.device(self.device):
-                _call(name, self._ref, *args)
+                status = fn(self._ref, *args, st)
+        if status:
+            raise W4A8Error(name, status)
 
     def _vec(self, t, name, dtype, shape):
         """Pointer of an optional contiguous tensor of this device, type and shape."""
         if t is None:
-            return None
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            return 0
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._dev:
             raise ValueError("KV8Cache: %s must be a contiguous %s tensor %s on the cache's device"
                              % (name, str(dtype)[6:], list(shape)))
         return t.data_ptr()
 
-    def _rows(self, t, name, like=None, heads=None, n=None):
-        import torch
-        S, H, D, _ = self.shape
-        if t.dim() != 4 or t.shape[0] != S or t.shape[3] != D or (heads is not None and t.shape[2] != heads) \
-                or (n is not None and t.shape[1] != n):
-            raise ValueError("KV8Cache: %s must be [%d][%s][%s][%d], not %s"
-                             % (name, S, "n" if n is None else n, "heads" if heads is None else heads, D, list(t.shape)))
-        if t.dtype not in (torch.float32, torch.bfloat16) or (like is not None and t.dtype != like.dtype):
-            raise ValueError("KV8Cache: %s has type %s" % (name, t.dtype))
+    def _rows(self, t, name, dtype, n, heads):
+        """The fields of a w4a8_rows for t [n_seqs][n][heads][head_dim]."""
+        S, _, D, _ = self.shape
+        if t.shape != (S, n, heads, D):
+            raise ValueError("KV8Cache: %s must be [%d][%d][%d][%d], not %s" % (name, S, n, heads, D, list(t.shape)))
+        if t.dtype is not dtype or dtype not in self._types:
+            raise ValueError("KV8Cache: %s has type %s; fp32 or bf16, the same for all rows" % (name, t.dtype))
         a, b, c, d = t.stride()
-        if d != 1 or t.device != self.device:
+        if d != 1 or t.get_device() != self._dev:
             raise ValueError("KV8Cache: %s must have unit stride in its last dimension, on the cache's device" % name)
-        return Rows(t.data_ptr(), a, b, c)
+        return t.data_ptr(), a, b, c
 
-    @staticmethod
-    def _dtype(t):
-        import torch
-        return 0 if t.dtype == torch.float32 else 1
+    def _scratch(self, fn, key, args, workspace):
+        """(pointer, bytes, tensor) of a call's workspace: the given one, or a new one of the size fn asks for."""
+        if workspace is None:
+            need = self._sizes.get(key)
+            if need is None:
+                n = _sz()
+                _call(fn, self._ref, args, _c.byref(n))
+                need = self._sizes[key] = n.value
+            workspace = self._torch.empty(need, dtype=self._torch.uint8, device=self.device)
+            return workspace.data_ptr(), need, workspace
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
-    def reset(self, stream=None):
+    @_on_stream
+    def reset(self):
         """Empties the cache (w4a8_kv8_reset)."""
-        self._run("w4a8_kv8_reset", self._on(stream))
+        self._run("w4a8_kv8_reset")
 
     def check(self):
         """The status word (0 = every call's device state was in range); synchronous."""
@@ -429,90 +458,99 @@ class KV8Cache:
             raise W4A8Error("w4a8_kv8_check", st)
         return f.value
 
-    def append(self, k, v, counts=None, index=None, len_out=None, stream=None):
+    @_on_stream
+    def append(self, k, v, counts=None, index=None, len_out=None):
         """Commits rows of k and v, advancing the cache's lengths, or storing the new ones in ``len_out`` instead
         (w4a8_kv8_append).  ``index`` [n_seqs][n]: the source row of each new position."""
-        import torch
         S, H = self.shape[:2]
-        kr = self._rows(k, "k", heads=H)
-        vr = self._rows(v, "v", like=k, heads=H, n=k.shape[1])
-        n = k.shape[1] if index is None else index.shape[1]
-        i32 = torch.int32
+        shape = k.shape
+        n_src = shape[1] if len(shape) == 4 else 0
+        dtype, i32 = k.dtype, self._torch.int32
+        kr = self._ROWS.pack(*self._rows(k, "k", dtype, n_src, H))
+        vr = self._ROWS.pack(*self._rows(v, "v", dtype, n_src, H))
+        n = n_src if index is None else index.shape[1]
         out = self.desc.len if len_out is None else self._vec(len_out, "len_out", i32, (S,))
-        self._run("w4a8_kv8_append", kr, vr, self._dtype(k), k.shape[1], n, self._vec(counts, "counts", i32, (S,)),
-                  self._vec(index, "index", i32, (S, n)), out, self._on(stream))
+        self._run("w4a8_kv8_append", kr, vr, self._types[dtype], n_src, n, self._vec(counts, "counts", i32, (S,)),
+                  0 if index is None else self._vec(index, "index", i32, (S, n)), out)
 
-    def read(self, first, n, length=None, stream=None):
+    @_on_stream
+    def read(self, first, n, length=None):
         """fp32 keys and values [n_seqs][n][n_kv_heads][head_dim] of positions first[s].. as held (w4a8_kv8_read)."""
-        import torch
+        torch = self._torch
         S, H, D, _ = self.shape
-        k, v = (torch.empty((S, n, H, D), dtype=torch.float32, device=self.device) for _ in range(2))
+        k = torch.empty((S, n, H, D), dtype=torch.float32, device=self.device)
+        v = torch.empty((S, n, H, D), dtype=torch.float32, device=self.device)
         self._run("w4a8_kv8_read", self._vec(first, "first", torch.int32, (S,)),
-                  self._vec(length, "length", torch.int32, (S,)), n, k.data_ptr(), v.data_ptr(), self._on(stream))
+                  self._vec(length, "length", torch.int32, (S,)), n, k.data_ptr(), v.data_ptr())
         return k, v
 
-    def _scratch(self, fn, args, workspace):
-        import torch
-        need = _sz()
-        _call(fn, self._ref, _c.byref(args), _c.byref(need))
-        if workspace is None:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
-        return workspace
-
+    @_on_stream
     def attention(self, q, k=None, v=None, scale=1.0, counts=None, mask=None, pages=None, mass=None, mass_out=None,
-                  out=None, workspace=None, stream=None):
+                  out=None, workspace=None):
         """Attention of q's rows over the cache and the new rows k, v (w4a8_kv8_attention); returns ``out``."""
-        import torch
+        torch = self._torch
         S, H, _, P = self.shape
-        qr = self._rows(q, "q")
-        n, heads = q.shape[1], q.shape[2]
+        shape, dtype = q.shape, q.dtype
+        if len(shape) != 4:
+            raise ValueError("KV8Cache: q must be [n_seqs][n][heads][head_dim]")
+        n, heads = shape[1], shape[2]
+        qr = self._rows(q, "q", dtype, n, heads)
         if (k is None) != (v is None):
             raise ValueError("KV8Cache: k and v come together")
-        kr = Rows() if k is None else self._rows(k, "k", like=q, heads=H, n=n)
-        vr = Rows() if v is None else self._rows(v, "v", like=q, heads=H, n=n)
+        kr = self._NONE if k is None else self._rows(k, "k", dtype, n, H)
+        vr = self._NONE if v is None else self._rows(v, "v", dtype, n, H)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        outr = self._rows(out, "out", like=q, heads=heads, n=n)
-        top_k = 0 if pages is None else pages.shape[-1]
-        if mass is not None and mass_out is None:
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        outr = self._rows(out, "out", dtype, n, heads)
+        top_k = pp = mi = mo = 0
+        if pages is not None:
+            top_k = pages.shape[-1]
+            pp = self._vec(pages, "pages", torch.int32, (S, n, H, top_k))
+        if mass_out is not None:
+            mi = self._vec(mass, "mass", torch.float32, (S, H, P))
+            mo = self._vec(mass_out, "mass_out", torch.float32, (S, H, P))
+        elif mass is not None:
             raise ValueError("KV8Cache: mass needs mass_out")
-        a = KV8Attn(n, heads, self._dtype(q), scale, qr, outr, kr, vr, self._vec(counts, "counts", torch.int32, (S,)),
-                    self._vec(mask, "mask", torch.int64, (S, n)),
-                    self._vec(pages, "pages", torch.int32, (S, n, H, top_k)), top_k,
-                    self._vec(mass, "mass", torch.float32, (S, H, P)),
-                    self._vec(mass_out, "mass_out", torch.float32, (S, H, P)))
-        ws = self._scratch("w4a8_kv8_attention_workspace_bytes", a, workspace)
-        self._run("w4a8_kv8_attention", _c.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), self._on(stream))
+        a = self._ATTN.pack(n, heads, self._types[dtype], scale, *qr, *outr, *kr, *vr,
+                            0 if counts is None else self._vec(counts, "counts", torch.int32, (S,)),
+                            0 if mask is None else self._vec(mask, "mask", torch.int64, (S, n)), pp, top_k, mi, mo)
+        ws, size, workspace = self._scratch("w4a8_kv8_attention_workspace_bytes",
+                                            (n, heads, dtype, k is None, pages is None, top_k, mo == 0), a, workspace)
+        self._run("w4a8_kv8_attention", a, ws, size)
         return out
 
-    def select(self, q, top_k, first_pages=0, last_pages=0, counts=None, out=None, workspace=None, stream=None):
+    @_on_stream
+    def select(self, q, top_k, first_pages=0, last_pages=0, counts=None, out=None, workspace=None):
         """The whole pages of best score for every row and KV head, int32 [n_seqs][n][n_kv_heads][top_k], ascending,
         -1 behind the last (w4a8_kv8_select)."""
-        import torch
+        torch = self._torch
         S, H = self.shape[:2]
-        qr = self._rows(q, "q")
-        n, heads = q.shape[1], q.shape[2]
+        shape, dtype = q.shape, q.dtype
+        if len(shape) != 4:
+            raise ValueError("KV8Cache: q must be [n_seqs][n][heads][head_dim]")
+        n, heads = shape[1], shape[2]
+        qr = self._rows(q, "q", dtype, n, heads)
         if out is None:
             out = torch.empty((S, n, H, top_k), dtype=torch.int32, device=self.device)
-        a = KV8Attn(n, heads, self._dtype(q), 1.0, qr)
-        a.counts = self._vec(counts, "counts", torch.int32, (S,))
-        ws = self._scratch("w4a8_kv8_select_workspace_bytes", a, workspace)
-        self._run("w4a8_kv8_select", _c.byref(a), top_k, first_pages, last_pages,
-                  self._vec(out, "out", torch.int32, (S, n, H, top_k)), ws.data_ptr(), ws.numel() * ws.element_size(),
-                  self._on(stream))
+        po = self._vec(out, "out", torch.int32, (S, n, H, top_k))
+        none = self._NONE
+        a = self._ATTN.pack(n, heads, self._types[dtype], 1.0, *qr, *none, *none, *none,
+                            0 if counts is None else self._vec(counts, "counts", torch.int32, (S,)), 0, 0, 0, 0, 0)
+        ws, size, workspace = self._scratch("w4a8_kv8_select_workspace_bytes", (n, heads, dtype, top_k), a, workspace)
+        self._run("w4a8_kv8_select", a, top_k, first_pages, last_pages, po, ws, size)
         return out
 
-    def evict(self, mass, keep, first_pages=0, last_pages=0, in_place=False, stream=None):
+    @_on_stream
+    def evict(self, mass, keep, first_pages=0, last_pages=0, in_place=False):
         """Keeps at most ``keep`` whole pages per KV head (w4a8_kv8_evict); returns (table, mass, len), new tensors,
         or the cache's own and ``mass`` itself when ``in_place``."""
-        import torch
+        torch = self._torch
         S, H, _, P = self.shape
+        pm = self._vec(mass, "mass", torch.float32, (S, H, P))
         old = (self.tensors["table"], mass, self.tensors["len"])
         new = old if in_place else tuple(torch.empty_like(t) for t in old)
-        self._run("w4a8_kv8_evict", self._vec(mass, "mass", torch.float32, (S, H, P)), keep, first_pages, last_pages,
-                  new[0].data_ptr(), new[1].data_ptr(), new[2].data_ptr(), self._on(stream))
+        self._run("w4a8_kv8_evict", pm, keep, first_pages, last_pages, new[0].data_ptr(), new[1].data_ptr(),
+                  new[2].data_ptr())
         return new
 
 

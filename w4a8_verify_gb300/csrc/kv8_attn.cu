@@ -7,80 +7,82 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// One CTA per (row of a column block, segment): the parts of a cut segment, a warp takes every eighth of them,
-// eight loads in flight; then the warps' sums.  Order fixed by the parts' places.  Segments of one worker are
-// written already; rows that see nothing (no units) are zero.
-template <typename T, int D>
+// The parts of a segment's rows, first the workers' in their order, then the row tiles': RPC rows to a CTA, a warp
+// takes every (kJoinWarps / RPC)th part of its row, eight loads in flight; then the warps' sums.  No parts: zero.
+template <typename T, int D, int RPC>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
                                                               Kv8Scratch ws) {
   griddep_enter();
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, WPR = kJoinWarps / RPC;
+  using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float sm_l[kJoinWarps];
-  __shared__ float sm_o[kJoinWarps][D];
-  const int H = c.n_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seg = blockIdx.y;
-  int s, h, i, r, q;
-  if (a.pages) {
-    s = seg / H / a.n, h = seg % H, i = seg / H % a.n, r = blockIdx.x, q = seg % (a.n * H);
-  } else {
-    s = seg / geo.CB / H, h = seg / geo.CB % H, r = seg % geo.CB * geo.RB + blockIdx.x, i = r / geo.G;
-    q = seg % (H * geo.CB);
-  }
+  __shared__ __align__(16) float sm_o[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = blockIdx.y;
+  const int rb = blockIdx.x * RPC + warp / WPR, first = warp % WPR;
+  const Kv8Segment sg = kv8_segment(c, a, geo, seg);
+  const int r = sg.cb * geo.RB + rb, i = a.pages ? sg.i : r / geo.G, s = sg.s;
   const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
-  if (L < 0 || r >= geo.R || i >= cnt) return;
-  const int hq = h * geo.G + (a.pages ? r : r % geo.G);
-  T* out = static_cast<T*>(a.out.data) + s * a.out.seq + i * a.out.row + hq * a.out.head;
-  float2* fin = ws.fin ? ws.fin + ((size_t)s * a.n + i) * a.n_heads + hq : nullptr;
-  const int per = kv8_units(a, L, cnt).total();
-  if (per == 0) {
-    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) kv8_store(out + d, 0.0f);
-    if (fin && threadIdx.x == 0) *fin = make_float2(0.0f, 0.0f);
-    return;
-  }
-  const int U = ws.prefix[c.n_seqs], W = min(geo.workers, U), u0 = ws.prefix[s] + q * per;
-  const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + per - 1, W, U) - w0 + 1;
-  if (parts == 1) return;
-  // the first worker's part is its range's last one unless it starts the range
-  const int first = worker_begin(w0, W, U) == u0 ? 0 : 1;
-  auto slot = [&](int p) { return (2 * (size_t)(w0 + p) + (p == 0 ? first : 0)) * geo.RB + blockIdx.x; };
-  float M = -INFINITY;
-  for (int p = lane; p < parts; p += 32) M = fmaxf(M, ws.ml[slot(p)].x);
-  M = warp_max(M);
-  const float base = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f, o[E] = {};
-  constexpr int B = 8;
-  for (int p0 = warp; p0 < parts; p0 += kJoinWarps * B) {
-    float2 ml[B];
-    float v[B][E];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int p = p0 + b * kJoinWarps;
-      ml[b] = p < parts ? ws.ml[slot(p)] : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[b][e] = p < parts ? ws.o[slot(p) * D + e * 32 + lane] : 0.0f;
+  const bool mine = L >= 0 && rb < geo.RB && r < geo.R && i < cnt;
+  float M = -INFINITY, base = 0.0f, l = 0.0f, o[E] = {};
+  if (mine) {
+    const Kv8Units un = kv8_units(a, L, cnt);
+    int w0 = 0, held = 0;
+    if (un.pages > 0) {
+      const int U = ws.prefix[c.n_seqs], W = min(geo.workers, U);
+      const int u0 = ws.prefix[s] + (seg - s * (a.pages ? a.n : geo.CB) * c.n_kv_heads) * un.pages;
+      w0 = worker_of(u0, W, U);
+      held = worker_of(u0 + un.pages - 1, W, U) - w0 + 1;
     }
+    const int parts = held + un.open + un.fresh;
+    // place of a part: those of the workers, then (negative) those of the row tiles
+    const int64_t held0 = ((int64_t)w0 + seg) * geo.RB + rb, tile0 = (int64_t)seg * geo.tiles * geo.RB + rb;
+    auto tile = [&](int p) { return tile0 + (int64_t)(p - held < un.open ? p - held : kPage / kRowTile + p - held - un.open) * geo.RB; };
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, p < held ? ws.ml[held0 + (int64_t)p * geo.RB].x : ws.rml[tile(p)].x);
+    M = warp_max(M);
+    base = M == -INFINITY ? 0.0f : M;
+    constexpr int B = 8;
+    for (int p0 = first; p0 < parts; p0 += WPR * B) {
+      float2 ml[B];
+      Vec v[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const float w = ex2(ml[b].x - base);
-      l = fmaf(ml[b].y, w, l);
+      for (int b = 0; b < B; ++b) {
+        const int p = p0 + b * WPR;
+        ml[b] = make_float2(-INFINITY, 0.0f);
+        v[b] = {};
+        if (p < parts) {
+          const bool h = p < held;
+          const int64_t at = h ? held0 + (int64_t)p * geo.RB : tile(p);
+          ml[b] = (h ? ws.ml : ws.rml)[at];
+          v[b] = *reinterpret_cast<const Vec*>((h ? ws.o : ws.ro) + at * D + E * lane);
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(v[b][e], w, o[e]);
+      for (int b = 0; b < B; ++b) {
+        const float w = ex2(ml[b].x - base);
+        const float* ve = reinterpret_cast<const float*>(&v[b]);
+        l = fmaf(ml[b].y, w, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(ve[e], w, o[e]);
+      }
     }
   }
   if (lane == 0) sm_l[warp] = l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][e * 32 + lane] = o[e];
+  *reinterpret_cast<Vec*>(&sm_o[warp][E * lane]) = *reinterpret_cast<Vec*>(o);
   __syncthreads();
-  float S = 0.0f;
+  if (!mine || first > 0) return;
+  l = 0.0f;
+  float sum[E] = {};
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) S += sm_l[w];
-  if (threadIdx.x < D) {
-    float v = 0.0f;
+  for (int w = 0; w < WPR; ++w) {
+    l += sm_l[warp + w];
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) v += sm_o[w][threadIdx.x];
-    kv8_store(out + threadIdx.x, S == 0.0f ? 0.0f : v / S);
+    for (int e = 0; e < E; ++e) sum[e] += sm_o[warp + w][E * lane + e];
   }
-  if (fin && threadIdx.x == 0) *fin = make_float2(base, S);
+  const int hq = sg.h * geo.G + (a.pages ? r : r % geo.G);
+  T* out = static_cast<T*>(a.out.data) + s * a.out.seq + i * a.out.row + hq * a.out.head + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; ++e) kv8_store(out + e, l == 0.0f ? 0.0f : sum[e] / l);
+  if (ws.fin && lane == 0) ws.fin[((size_t)s * a.n + i) * a.n_heads + hq] = make_float2(base, l);
 }
 
 // Page weights onto the mass: one warp per page, a lane takes every 32nd row, the lanes' sums in a fixed tree.
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(256) k_kv8_mass(w4a8_kv8_cache c, w4a8_kv8_att
 
 struct Plan {
   Kv8Geom geo;
-  size_t segments, prefix, ml, o, fin, page, bytes;  // offsets
+  size_t segments, prefix, ml, o, rml, ro, fin, page, bytes;  // offsets
 };
 
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -128,19 +130,24 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.n = a->n;
   g.G = a->n_heads / c->n_kv_heads;
   g.R = a->pages ? g.G : g.n * g.G;
-  const Kv8Shape sh = kv8_shape(g.R, a->dtype);
-  g.RB = sh.TW * sh.WC * (a->dtype == W4A8_F32 ? 4 : 8);
+  const int wc = kv8_split_warps(g.R, a->dtype);
+  g.RB = wc * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
-  const size_t units = p->segments * ((a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages) + 8);
-  if (units >= (size_t)1 << 31) return W4A8_ERR_SHAPE;
-  const int ng = kv8_warps(sh.TW) / sh.WC;
+  const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
+  if (units >= (size_t)1 << 31 || p->segments > 65535) return W4A8_ERR_SHAPE;
+  const int ng = kKv8Warps / wc;
   const size_t ctas = (units + ng - 1) / ng;
   g.workers = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas) * ng;
   p->prefix = 0;
+  g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);
+  g.segments = (int)p->segments;
+  const size_t slots = g.workers + p->segments, rslots = p->segments * g.tiles, row = (size_t)g.RB * 4;
   p->ml = up256(((size_t)c->n_seqs + 1) * 4);
-  p->o = up256(p->ml + (size_t)2 * g.workers * g.RB * 8);
-  p->fin = up256(p->o + (size_t)2 * g.workers * g.RB * c->head_dim * 4);
+  p->o = up256(p->ml + slots * row * 2);
+  p->rml = up256(p->o + slots * row * c->head_dim);
+  p->ro = up256(p->rml + rslots * row * 2);
+  p->fin = up256(p->ro + rslots * row * c->head_dim);
   p->page = p->bytes = p->fin;
   if (a->mass_out) {
     p->page = up256(p->fin + (size_t)c->n_seqs * a->n * a->n_heads * 8);
@@ -177,22 +184,29 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
       !aligned(a->out.data, el) || !aligned(a->k.data, el) || !aligned(a->v.data, el))
     return W4A8_ERR_ARG;
   if (workspace_bytes < p.bytes) return W4A8_ERR_CAPACITY;
-  if (p.segments > 65535) return W4A8_ERR_SHAPE;
   char* base = static_cast<char*>(workspace);
   Kv8Scratch ws{reinterpret_cast<int*>(base + p.prefix), reinterpret_cast<float2*>(base + p.ml),
-                reinterpret_cast<float*>(base + p.o), a->mass_out ? reinterpret_cast<float2*>(base + p.fin) : nullptr,
+                reinterpret_cast<float*>(base + p.o), reinterpret_cast<float2*>(base + p.rml),
+                reinterpret_cast<float*>(base + p.ro), a->mass_out ? reinterpret_cast<float2*>(base + p.fin) : nullptr,
                 a->mass_out ? reinterpret_cast<float2*>(base + p.page) : nullptr};
-  p.geo.vec = (vec_rows(a->q, a->dtype) ? 1 : 0) | (vec_rows(a->k, a->dtype) ? 2 : 0);
+  p.geo.vec = vec_rows(a->q, a->dtype) ? 1 : 0;
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
   W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
       *c, *a, p.geo, ws, st));
-  const dim3 grid((unsigned)(p.geo.R < p.geo.RB ? p.geo.R : p.geo.RB), (unsigned)p.segments);
-  auto join = [&](auto kern) { return launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, st, *c, *a, p.geo, ws); };
+  // few rows (some CTAs for each SM): eight warps to a row, whose parts may be many; else two
+  const int rows = p.geo.R < p.geo.RB ? p.geo.R : p.geo.RB;
+  auto join = [&](auto one, auto four) {
+    const bool few = (int64_t)rows * (int64_t)p.segments <= 4 * kKv8Ctas;
+    const dim3 grid((unsigned)(few ? rows : (rows + 3) / 4), (unsigned)p.segments);
+    return launch_pdl(few ? one : four, grid, dim3(32 * kJoinWarps), 0, st, *c, *a, p.geo, ws);
+  };
   if (f32)
-    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<float, 64>) : join(k_kv8_join<float, 128>));
+    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<float, 64, 1>, k_kv8_join<float, 64, 4>)
+                      : join(k_kv8_join<float, 128, 1>, k_kv8_join<float, 128, 4>));
   else
-    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<__nv_bfloat16, 64>) : join(k_kv8_join<__nv_bfloat16, 128>));
+    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<__nv_bfloat16, 64, 1>, k_kv8_join<__nv_bfloat16, 64, 4>)
+                      : join(k_kv8_join<__nv_bfloat16, 128, 1>, k_kv8_join<__nv_bfloat16, 128, 4>));
   if (a->mass_out)
     W4A8_CUDA_TRY(launch_pdl(k_kv8_mass,
                              dim3((unsigned)((c->max_pages + 7) / 8), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs),
