@@ -137,7 +137,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
   if (units >= (size_t)1 << 31 || p->segments > 65535) return W4A8_ERR_SHAPE;
   const int ng = kKv8Warps / wc;
-  const size_t ctas = (units + ng - 1) / ng;
+  const size_t ctas = units;  // few pages: spread over the SMs
   g.workers = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas) * ng;
   p->prefix = 0;
   g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);

@@ -2,8 +2,10 @@
 //
 // For query head hq of new row i (KV head h = hq / G), over the tokens t that the row sees
 //   l_t = scale q . k_t,  out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x = l log2(e), m = max x
-// in one pass: per page the running maximum m, sum l and values O of each row become
-//   m' = max(m, max x),  c = 2^(m - m'),  O = O c + s_V (P C_V),  l = l c + sum P,  P = 2^(x - m').
+// in one pass: for each half page the running maximum m, sum l and values O of each row become
+//   m' = max(m, max x),  c = 2^(m - m'),  O = O c + s_V (P C_V),  l = l c + sum P,  P = 2^(x - m'),
+// with m left alone while no x is above m + 8 (P <= 2^8 keeps its f16 range, and most half pages need no
+// reduction over the lanes).
 //
 // Both products run transposed on the tensor cores (m16n8k16, f16): S^T = C_K Q^T and O^T = C_V^T P^T, so the
 // 8-bit codes are the 16-row operand and the few query rows of a KV head fill 8-column tiles, half the padding of
@@ -20,13 +22,14 @@
 // them there.  Rows of q are scaled by a power of two, to a largest magnitude of at most 2^11; qh is the nearest
 // whole number, so the sums of qh with the codes are whole numbers (times 2^-24) that f32 holds, and the tensor
 // core's truncating additions do not touch them.  (With qh the nearest f16 the logits were off by 3e-7 relative.)
-// P is scaled by 2^15.
+// P is scaled by 2^7.
 // The transposed P fragments are made with movmatrix: no shared memory in the softmax.
 //
 // Work: every (sequence, KV head, block of rows) is a segment of pages.  The pages of all segments, end to end, are
 // cut into equal ranges, one for each worker, so ragged batches balance.  A worker is a group of WC warps that share a
-// page and hold different columns; it has its own ring of bulk copies (half a page each) and never waits for
-// another worker.  The fp32 rows (open page, new rows; at most 63 + 64 of a segment) go to one or two further warps
+// page and hold different columns; it has its own ring of bulk copies (a page each) and never waits for
+// another worker.  The code of half a page is a loop of 500 instructions: unrolled over the page (1000) it outran
+// the instruction caches, and twelve warps at different places of it spent a third of their time on fetches.  The fp32 rows (open page, new rows; at most 63 + 64 of a segment) go to one or two further warps
 // of each CTA, 16 rows at a time, in plain fp32: with the tensor-core form of them inside the page loop their code ran
 // a few times per CTA, cold, and one worker's four row tiles took 30 us at the end of a 40 us call.  Each
 // worker's part of a segment and each row tile leaves (maximum, sum, values); k_kv8_join puts them together.
@@ -40,7 +43,8 @@ namespace w4a8 {
 constexpr int kKv8Ctas = 152;         // one per SM of a GB300
 // Warps of a CTA (one CTA per SM, 128 registers): those that take pages and those that take fp32 rows.
 constexpr int kKv8Warps = 12, kKv8RowWarps = 4, kKv8Threads = 32 * (kKv8Warps + kKv8RowWarps);
-constexpr int kKv8RingBytes = 196608; // ring of half pages per SM: 24 of 8 KB or 48 of 4 KB
+constexpr int kKv8RingBytes = 196608; // ring of pages per SM: 12 of 16 KB or 24 of 8 KB
+constexpr float kPScale = 128.0f, kPSlack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
 constexpr int kRowTile = 16;          // fp32 rows of one part
 constexpr int kRowChunk = 4;          // query rows that a row warp takes at a time
 
@@ -137,9 +141,8 @@ struct Kv8Split {
   static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
   static constexpr int RB = WC * RPT;              // rows of a column block
   static constexpr int NG = kKv8Warps / WC;        // workers of a CTA
-  static constexpr int HALF = kPage * D;           // bytes of a ring entry
-  static constexpr int NS = kKv8RingBytes / HALF / NG;  // ring entries of a worker
-  static constexpr int BACK = WC == 1 ? 0 : (WC + 3) / 4;  // entries left unfilled so that the copier does not wait for the slowest warp
+  static constexpr int PAGE = 2 * kPage * D;       // bytes of a ring entry: keys and values of a page
+  static constexpr int NS = kKv8RingBytes / PAGE / NG;  // ring entries of a worker
   static constexpr int KS = D / 16, DT = D / 16;
   static constexpr float UNIT = SPLIT ? 1.0f : 16777216.0f;  // codes enter the products divided by this
 };
@@ -159,7 +162,7 @@ struct Kv8Unit {
 // microseconds, so everything is asked for at once (the values into L2).
 template <typename T, int D>
 __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws,
-                             int seg, int f, int chunk) {
+                             int seg, int f, int chunk, float (*pt)[kRowTile]) {
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int E = D / 32;
   using Vec = std::conditional_t<E == 4, float4, float2>;
@@ -200,31 +203,32 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
     for (int x = 0; x < D * (int)sizeof(float); x += 128)
       if (fresh < 0 || x < D * (int)sizeof(T)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + x));
   }
+  // query row r of the chunk: its place in the column block's rows is r0 + r
+  auto node_of = [&](int r) { return a.pages ? sg.i : (sg.cb * geo.RB + r0 + r) / geo.G; };
+  auto query = [&](int r, float (&q)[E]) {
+    const int rr = sg.cb * geo.RB + r0 + r, hq = sg.h * geo.G + (a.pages ? rr : rr % geo.G);
+    const T* p = static_cast<const T*>(a.q.data) + sg.s * a.q.seq + node_of(r) * a.q.row + hq * a.q.head + E * lane;
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = kv8_load(p + e);
+  };
+  float q[E], next[E];
+  query(0, q);
   load16(kt, kn, a.k.row);
-  int node[kRowChunk], hq[kRowChunk];
-  float q[kRowChunk][E];
-#pragma unroll
-  for (int r = 0; r < kRowChunk; ++r) {
-    const int rr = sg.cb * geo.RB + min(r0 + r, rows - 1);
-    node[r] = a.pages ? sg.i : rr / geo.G;
-    hq[r] = sg.h * geo.G + (a.pages ? rr : rr % geo.G);
-    const T* p = static_cast<const T*>(a.q.data) + sg.s * a.q.seq + node[r] * a.q.row + hq[r] * a.q.head + E * lane;
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[r][e] = kv8_load(p + e);
-  }
   const float qscale = a.scale * 1.4426950408889634f;
   const int tok = lane >> 1;
-  float p[kRowChunk], m[kRowChunk], l[kRowChunk];
-  unsigned seen[kRowChunk];
-#pragma unroll
-  for (int r = 0; r < kRowChunk; ++r) {
+  const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0;
+#pragma unroll 1
+  for (int r = 0; r < nr; ++r) {
+    query(min(r + 1, nr - 1), next);
     float x[kRowTile];
 #pragma unroll
     for (int i = 0; i < kRowTile; ++i) x[i] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+    for (int e = 0; e < E; ++e) {
 #pragma unroll
-      for (int i = 0; i < kRowTile; ++i) x[i] = fmaf(q[r][e], kv[i][e], x[i]);
+      for (int i = 0; i < kRowTile; ++i) x[i] = fmaf(q[e], kv[i][e], x[i]);
+      q[e] = next[e];
+    }
 #pragma unroll
     for (int w = 8; w > 0; w >>= 1) {
       const bool up = lane & (2 * w);
@@ -237,33 +241,32 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
     const float s = (x[0] + __shfl_xor_sync(FULL, x[0], 1)) * qscale;
     bool see = tok < nv;
     if (fresh >= 0) {
-      const int i = node[r];
+      const int i = node_of(r);
       const uint64_t mask = a.mask ? a.mask[(size_t)sg.s * a.n + i] : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
       see = see && (mask >> (fresh * kRowTile + tok) & 1ull);
     }
-    m[r] = warp_max(see ? s : -INFINITY);
-    p[r] = see ? ex2(s - (m[r] == -INFINITY ? 0.0f : m[r])) : 0.0f;
-    seen[r] = __ballot_sync(FULL, see);
-    l[r] = p[r];
+    const float m = warp_max(see ? s : -INFINITY);
+    const float p = see ? ex2(s - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    float l = p;
 #pragma unroll
-    for (int w = 2; w < 32; w <<= 1) l[r] += __shfl_xor_sync(FULL, l[r], w);
+    for (int w = 2; w < 32; w <<= 1) l += __shfl_xor_sync(FULL, l, w);
+    if (lane == 0) ws.rml[at + r] = make_float2(m, l);
+    if (!(lane & 1)) pt[r][tok] = see ? p : -1.0f;
   }
   load16(kt + kPage * D, vn, a.v.row);
-#pragma unroll
-  for (int r = 0; r < kRowChunk; ++r) {
-    if (r >= nr) break;
+  __syncwarp();
+#pragma unroll 1
+  for (int r = 0; r < nr; ++r) {
     float o[E] = {};
 #pragma unroll
     for (int i = 0; i < kRowTile; ++i) {
-      const float pi = __shfl_sync(FULL, p[r], 2 * i);
-      const bool use = seen[r] >> (2 * i) & 1u;
+      const float p = pt[r][i];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = use ? fmaf(pi, kv[i][e], o[e]) : o[e];
+      for (int e = 0; e < E; ++e) o[e] = p != -1.0f ? fmaf(p, kv[i][e], o[e]) : o[e];
     }
-    const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0 + r;
-    if (lane == 0) ws.rml[at] = make_float2(m[r], l[r]);
-    *reinterpret_cast<Vec*>(ws.ro + at * D + E * lane) = *reinterpret_cast<Vec*>(o);
+    *reinterpret_cast<Vec*>(ws.ro + (at + r) * D + E * lane) = *reinterpret_cast<Vec*>(o);
   }
+  __syncwarp();
 }
 
 template <typename T, int D, int WC>
@@ -274,6 +277,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
   constexpr int NC = C::NC, KS = C::KS, DT = C::DT;
   constexpr unsigned FULL = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(16) float row_p[kKv8RowWarps][kRowChunk][kRowTile];
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kKv8RingBytes);
   uint64_t* empty = full + C::NG * C::NS;
   int* prefix = reinterpret_cast<int*>(empty + C::NG * C::NS);
@@ -319,7 +323,8 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const int chunks = (min(geo.R, C::RB) + kRowChunk - 1) / kRowChunk;
     const int parts = geo.segments * geo.tiles * chunks;
     for (int x = (warp - kKv8Warps) * gridDim.x + blockIdx.x; x < parts; x += gridDim.x * kKv8RowWarps)
-      kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks);
+      kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks,
+                         row_p[warp - kKv8Warps]);
     return;
   }
   const int U = prefix[S];
@@ -364,58 +369,15 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     return r;
   };
 
-  uint8_t* ring = sm + (size_t)grp * C::NS * C::HALF;
+  uint8_t* ring = sm + (size_t)grp * C::NS * C::PAGE;
   full += grp * C::NS;
   empty += grp * C::NS;
   Kv8Unit cur = look(u0 + lane), nxt = look(u0 + 32 + lane);
   const int nu = u1 - u0;
-  int jl = 0, half = 0;                 // next unit and half to copy
-  int is = 0, iph = 0, in_ring = 0;     // ring entry, its phase, entries issued and not yet consumed
+  int jl = 0;                           // next unit to copy (one warp of the worker copies)
+  int is = 0, iph = 0, in_ring = 0;     // its ring entry and that one's phase; entries issued and not consumed
   int cs = 0, cph = 0;                  // entry to consume next
   bool ok = true;
-  int cbase = 0;                        // first unit of `cur`
-
-  // Copies ahead as far as the ring and the two batches of units allow (one warp of the worker).
-  auto copy_ahead = [&](int room) {
-    while (in_ring < room && jl < nu && jl < cbase + 64) {
-      const int from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
-      if (from < 0) {
-        ++jl;
-        continue;
-      }
-      bool good = true;
-      if (lane == 0) {
-        if (WC > 1 && iph > 0) good = mbar_wait(&empty[is], (iph - 1) & 1);
-        if (good) {
-          mbar_expect_tx(&full[is], C::HALF);
-          bulk_g2s(ring + (size_t)is * C::HALF, c.codes + ((size_t)from * 2 + half) * C::HALF, C::HALF, &full[is]);
-        }
-      }
-      good = __shfl_sync(FULL, good, 0);
-      if (!good) {
-        ok = false;
-        return;
-      }
-      ++in_ring;
-      if (++is == C::NS) is = 0, ++iph;
-      jl += half;
-      half ^= 1;
-    }
-  };
-  auto wait_half = [&]() -> const uint8_t* {
-    if (!mbar_wait(&full[cs], cph & 1)) ok = false;
-    ok = __all_sync(FULL, ok);
-    return ring + (size_t)cs * C::HALF;
-  };
-  auto release_half = [&]() {
-    __syncwarp();
-    if (WC > 1 && lane == 0) mbar_arrive(&empty[cs]);
-    if (++cs == C::NS) cs = 0, ++cph;
-    --in_ring;
-    if (wg == 0) copy_ahead(C::NS - C::BACK);
-  };
-  // in_ring of a warp that does not copy is not used: only warp 0 counts entries
-  if (wg == 0) copy_ahead(C::NS);
 
   // ---- state of the segment
   uint32_t qf[KS][2];
@@ -507,7 +469,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     }
   };
 
-  // Ends the worker's part of a segment (P carries 2^15, the codes 1 / UNIT).
+  // Ends the worker's part of a segment (P carries kPScale, the codes 1 / UNIT).
   auto flush = [&]() {
     if (!act) return;
     const size_t slot = ((size_t)worker + seg) * C::RB;
@@ -520,168 +482,161 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
       const int r = row_of(2 * t + x);
       if (!row_ok(r)) continue;
       const size_t at = slot + (r - cb_cur * C::RB);
-      if (g == 0) ws.ml[at] = make_float2(m[x], sum / 32768.0f);
+      if (g == 0) ws.ml[at] = make_float2(m[x], sum / kPScale);
       float* o = ws.o + at * D;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        o[16 * d + g] = (SPLIT ? O[d][0] + O[d][1] : O[d][x]) * (C::UNIT / 32768.0f);
-        o[16 * d + g + 8] = (SPLIT ? O[d][2] + O[d][3] : O[d][x + 2]) * (C::UNIT / 32768.0f);
+        o[16 * d + g] = (SPLIT ? O[d][0] + O[d][1] : O[d][x]) * (C::UNIT / kPScale);
+        o[16 * d + g + 8] = (SPLIT ? O[d][2] + O[d][3] : O[d][x + 2]) * (C::UNIT / kPScale);
       }
     }
   };
 
-  // Softmax of a page: x, sums of codes (SPLIT: entries 0 and 2), becomes P 2^15 in place, pf its B fragments, cc the
-  // factor of the old sums, psum the sum over the tokens of a lane's own P.  The logit is x (fh + fl), in fp32 calls
-  // taken relative to the maximum with one rounding at the size of the difference: a relative error of a factor is
-  // one of the softmax's temperature, which large logits multiply.
-  float cc[NC], psum[NC];
-  auto soft = [&](float (&x)[4][4], uint32_t (&pf)[4][2], const float (&fh)[NC], const float (&fl)[NC]) {
+  // A page, half of it (32 tokens) at a time: S^T = C_K Q^T, softmax, O^T += C_V^T P^T.  The logit is x (fh + fl), in
+  // fp32 calls taken relative to the maximum with one rounding at the size of the difference: a relative error of a
+  // factor is one of the softmax's temperature, which large logits multiply.
+  auto page = [&](const uint8_t* pg, float sk, float sv, int u) {
+    float fh[NC], fl[NC], psum[NC];
 #pragma unroll
     for (int y = 0; y < NC; ++y) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = y; e < 4; e += 2) mx = fmaxf(mx, x[i][e] * fh[y]);
-      mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
-      mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-      const float mn = fmaxf(m[y], mx), base = mn == -INFINITY ? 0.0f : mn;
-      cc[y] = ex2(m[y] - base);
-      m[y] = mn;
+      fh[y] = colfac[y] * sk;
+      fl[y] = fmaf(colfac[y], sk, -fh[y]) + collow[y] * sk;
       psum[y] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = y; e < 4; e += 2) {
-          if (SPLIT) {
-            x[i][e] = ex2(fmaf(x[i][e], fl[y], fmaf(x[i][e], fh[y], -base))) * 32768.0f;
-          } else {
-            x[i][e] = ex2(fmaf(x[i][e], fh[y], 15.0f - base));
-          }
-          psum[y] += x[i][e];
-        }
     }
+#pragma unroll 1
+    for (int it = 0; it < 2; ++it) {
+      float x[2][4], x1[2][4];  // two 16-token tiles, even and odd k-steps
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t pk;
-        if (SPLIT) {
-          const float p = x[i][2 * e];
-          pk = pack_f16(p, p - __half2float(__float2half_rn(p)));
-        } else {
-          pk = pack_f16(x[i][2 * e], x[i][2 * e + 1]);
-        }
-        pf[i][e] = movmatrix(pk);
-      }
-#pragma unroll
-    for (int y = 0; y < NC; ++y) l[y] = fmaf(l[y], cc[y], psum[y]);
-  };
-
-  // A page: S^T = C_K Q^T, softmax, O^T += C_V^T P^T.
-  auto page = [&](float sk, float sv, int u) {
-    float x[4][4];
-    uint32_t pf[4][2];
-    const uint8_t* kb = wait_half();
-    if (!ok) return;
-    if (act) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] = SPLIT ? 0.0f : seed[e & 1];
+        for (int e = 0; e < 4; ++e) x[i][e] = SPLIT ? 0.0f : seed[e & 1], x1[i][e] = 0.0f;
+      const uint8_t* kb = pg + (it * (D / 16) * 32 + lane) * 16;
 #pragma unroll
       for (int kp = 0; kp < D / 32; ++kp)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kb + ((i * (D / 32) + kp) * 32 + lane) * 16);
-          uint32_t a0[4], a1[4];
-          codes_f16<SPLIT>(w.x, a0[0], a0[2]);
-          codes_f16<SPLIT>(w.y, a0[1], a0[3]);
-          codes_f16<SPLIT>(w.z, a1[0], a1[2]);
-          codes_f16<SPLIT>(w.w, a1[1], a1[3]);
-          mma_f16(x[i], a0, qf[2 * kp][0], qf[2 * kp][1]);
-          mma_f16(x[i], a1, qf[2 * kp + 1][0], qf[2 * kp + 1][1]);
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(kb + (i * (D / 32) + kp) * 512);
+          uint32_t af[4];
+          codes_f16<SPLIT>(w.x, af[0], af[2]);
+          codes_f16<SPLIT>(w.y, af[1], af[3]);
+          mma_f16(x[i], af, qf[2 * kp][0], qf[2 * kp][1]);
+          codes_f16<SPLIT>(w.z, af[0], af[2]);
+          codes_f16<SPLIT>(w.w, af[1], af[3]);
+          mma_f16(x1[i], af, qf[2 * kp + 1][0], qf[2 * kp + 1][1]);
         }
-    }
-    release_half();
-    if (act) {
-      if (SPLIT) {
+      // logits: entry y + 2 e of tile i is row y of the thread, token g + 8 e of the tile
+      bool high = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i][0] += x[i][1], x[i][2] += x[i][3];  // hi + lo
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] += x1[i][e];
+        if (SPLIT) x[i][0] += x[i][1], x[i][2] += x[i][3];  // hi + lo
+#pragma unroll
+        for (int y = 0; y < NC; ++y) high = high || x[i][y] * fh[y] > m[y] + kPSlack || x[i][y + 2] * fh[y] > m[y] + kPSlack;
       }
-      float fh[NC], fl[NC];
-#pragma unroll
-      for (int y = 0; y < NC; ++y) {
-        fh[y] = colfac[y] * sk;
-        fl[y] = fmaf(colfac[y], sk, -fh[y]) + collow[y] * sk;
-      }
-      soft(x, pf, fh, fl);
-    }
-    const uint8_t* vb = wait_half();
-    if (!ok) return;
-    if (act) {
-      // -128 2^-24 sum(P) of the columns, P as the product uses it: a row of constants times P
-      float ps[4];
-      if (!SPLIT) {
-        const uint32_t k = 0x80808080u;  // f16 -128 2^-24 = 0x8080
-        const uint32_t ones[4] = {k, k, k, k};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ps[e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(ps, ones, pf[i][0], pf[i][1]);
-      }
-      if (ws.page) {
+      if (__any_sync(FULL, high)) {
+        float cc[NC];
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
-          float v = psum[y];
-          v += __shfl_xor_sync(FULL, v, 4);
-          v += __shfl_xor_sync(FULL, v, 8);
-          v += __shfl_xor_sync(FULL, v, 16);
-          if (g == 0)
-            ws.page[((size_t)seg * c.max_pages + u) * C::RB + wg * C::RPT + (SPLIT ? t : 2 * t + y)] =
-                make_float2(m[y], v / 32768.0f);
+          float mx = fmaxf(fmaxf(x[0][y] * fh[y], x[0][y + 2] * fh[y]), fmaxf(x[1][y] * fh[y], x[1][y + 2] * fh[y]));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+          mx = fmaxf(mx, m[y]);
+          cc[y] = mx == -INFINITY ? 1.0f : ex2(m[y] - mx);
+          m[y] = mx;
+          l[y] *= cc[y];
+          psum[y] *= cc[y];
         }
-      }
-      bool same = true;  // no row of the warp has a new maximum
-#pragma unroll
-      for (int y = 0; y < NC; ++y) same = same && cc[y] == 1.0f;
-      if (!__all_sync(FULL, same)) {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int e = 0; e < 4; ++e) O[d][e] *= cc[(e & 1) * (NC - 1)];
       }
+      uint32_t pf[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int y = 0; y < NC; ++y) {
+          const float base = m[y] == -INFINITY ? 0.0f : m[y];
+#pragma unroll
+          for (int e = y; e < 4; e += 2) {
+            x[i][e] = SPLIT ? ex2(fmaf(x[i][e], fl[y], fmaf(x[i][e], fh[y], -base))) * kPScale
+                            : ex2(fmaf(x[i][e], fh[y], 7.0f - base));
+            psum[y] += x[i][e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p = x[i][2 * e];
+          pf[i][e] = movmatrix(SPLIT ? pack_f16(p, p - __half2float(__float2half_rn(p))) : pack_f16(p, x[i][2 * e + 1]));
+        }
+      }
+      // bf16 calls: -128 2^-24 sum(P) of the columns, P as the product uses it, by a row of constants times P
+      float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (!SPLIT) {
+        const uint32_t k = 0x80808080u;  // f16 -128 2^-24 = 0x8080
+        const uint32_t ones[4] = {k, k, k, k};
+        mma_f16(ps, ones, pf[0][0], pf[0][1]);
+        mma_f16(ps, ones, pf[1][0], pf[1][1]);
+      }
+      const uint8_t* vb = pg + kPage * D + (it * 32 + lane) * 16;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        float o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = SPLIT ? 0.0f : ps[e & 1];
-#pragma unroll
-        for (int kp = 0; kp < 2; ++kp) {
-          const uint4 w = *reinterpret_cast<const uint4*>(vb + ((d * 2 + kp) * 32 + lane) * 16);
-          uint32_t af[4];
-          codes_f16<SPLIT>(w.x, af[0], af[2]);
-          codes_f16<SPLIT>(w.y, af[1], af[3]);
-          mma_f16(o, af, pf[2 * kp][0], pf[2 * kp][1]);
-          codes_f16<SPLIT>(w.z, af[0], af[2]);
-          codes_f16<SPLIT>(w.w, af[1], af[3]);
-          mma_f16(o, af, pf[2 * kp + 1][0], pf[2 * kp + 1][1]);
-        }
+        float o[4] = {ps[0], ps[1], ps[2], ps[3]};
+        const uint4 w = *reinterpret_cast<const uint4*>(vb + d * 1024);
+        uint32_t af[4];
+        codes_f16<SPLIT>(w.x, af[0], af[2]);
+        codes_f16<SPLIT>(w.y, af[1], af[3]);
+        mma_f16(o, af, pf[0][0], pf[0][1]);
+        codes_f16<SPLIT>(w.z, af[0], af[2]);
+        codes_f16<SPLIT>(w.w, af[1], af[3]);
+        mma_f16(o, af, pf[1][0], pf[1][1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) O[d][e] = fmaf(o[e], sv, O[d][e]);
       }
     }
-    release_half();
+#pragma unroll
+    for (int y = 0; y < NC; ++y) {
+      l[y] += psum[y];
+      if (ws.page) {
+        float v = psum[y];
+        v += __shfl_xor_sync(FULL, v, 4);
+        v += __shfl_xor_sync(FULL, v, 8);
+        v += __shfl_xor_sync(FULL, v, 16);
+        if (g == 0)
+          ws.page[((size_t)seg * c.max_pages + u) * C::RB + wg * C::RPT + (SPLIT ? t : 2 * t + y)] =
+              make_float2(m[y] == -INFINITY ? 0.0f : m[y], v / kPScale);
+      }
+    }
   };
 
   // ---- the range
-  for (int j = 0; j < nu && ok; ++j) {
+#pragma unroll 1
+  for (int j = 0, cbase = 0; j < nu; ++j) {
     if (j - cbase == 32) {
       cbase += 32;
       cur = nxt;
       nxt = look(u0 + cbase + 32 + lane);
-      if (wg == 0) copy_ahead(C::NS - C::BACK);
+    }
+    if (wg == 0) {  // copy ahead as far as the ring and the two batches of units allow
+      while (in_ring < C::NS && jl < nu && jl < cbase + 64) {
+        const int from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
+        ++jl;
+        if (from < 0) continue;
+        if (lane == 0) {
+          if (WC > 1 && iph > 0) ok = mbar_wait(&empty[is], (iph - 1) & 1);
+          if (ok) {
+            mbar_expect_tx(&full[is], C::PAGE);
+            bulk_g2s(ring + (size_t)is * C::PAGE, c.codes + (size_t)from * C::PAGE, C::PAGE, &full[is]);
+          }
+        }
+        ok = __shfl_sync(FULL, ok, 0);
+        if (!ok) break;
+        ++in_ring;
+        if (++is == C::NS) is = 0, ++iph;
+      }
+      if (!ok) break;
     }
     const int src = j - cbase;
     const int from = __shfl_sync(FULL, cur.src, src), sg = __shfl_sync(FULL, cur.seg, src);
@@ -691,7 +646,14 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     }
     const float sk = __shfl_sync(FULL, cur.sk, src), sv = __shfl_sync(FULL, cur.sv, src);
     const int u = __shfl_sync(FULL, cur.u, src);
-    if (from >= 0) page(sk, sv, u);
+    if (from < 0) continue;
+    ok = __all_sync(FULL, mbar_wait(&full[cs], cph & 1));
+    if (!ok) break;
+    if (act) page(ring + (size_t)cs * C::PAGE, sk, sv, u);
+    __syncwarp();
+    if (WC > 1 && lane == 0) mbar_arrive(&empty[cs]);
+    if (++cs == C::NS) cs = 0, ++cph;
+    --in_ring;
   }
   if (ok) {
     flush();
