@@ -7,7 +7,7 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// The parts of a segment's rows, first the workers' in their order, then the row tiles': RPC rows to a CTA, a warp
+// The parts of a segment's rows, the split kernel's CTAs in their order, then the row tiles': RPC rows to a CTA, a warp
 // takes every (kJoinWarps / RPC)th part of its row, eight loads in flight; then the warps' sums.  No parts: zero.
 template <typename T, int D, int RPC>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
@@ -26,18 +26,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
   float M = -INFINITY, base = 0.0f, l = 0.0f, o[E] = {};
   if (mine) {
     const Kv8Units un = kv8_units(a, L, cnt);
-    int w0 = 0, held = 0;
+    int c0 = 0, held = 0, early = 0;  // CTAs that hold parts, and whether a worker ended it and went on
     if (un.pages > 0) {
-      const int U = ws.prefix[c.n_seqs], W = min(geo.workers, U);
-      const int u0 = ws.prefix[s] + (seg - s * (a.pages ? a.n : geo.CB) * c.n_kv_heads) * un.pages;
-      w0 = worker_of(u0, W, U);
-      held = worker_of(u0 + un.pages - 1, W, U) - w0 + 1;
+      const int U = ws.prefix[c.n_seqs];
+      const Kv8Workers wk = kv8_workers(U, geo.ctas, geo.ng);
+      const int u0 = ws.prefix[s] + (seg - s * (a.pages ? a.n : geo.CB) * c.n_kv_heads) * un.pages, u1 = u0 + un.pages;
+      const int w0 = worker_of(u0, wk.W, U), w1 = worker_of(u1 - 1, wk.W, U);
+      early = worker_begin(w1 + 1, wk.W, U) > u1;
+      c0 = w0 / wk.ng;
+      held = w1 - early < w0 ? 0 : (w1 - early) / wk.ng - c0 + 1;
     }
-    const int parts = held + un.open + un.fresh;
-    // place of a part: those of the workers, then (negative) those of the row tiles
-    const int64_t held0 = ((int64_t)w0 + seg) * geo.RB + rb, tile0 = (int64_t)seg * geo.tiles * geo.RB + rb;
-    auto tile = [&](int p) { return tile0 + (int64_t)(p - held < un.open ? p - held : kPage / kRowTile + p - held - un.open) * geo.RB; };
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, p < held ? ws.ml[held0 + (int64_t)p * geo.RB].x : ws.rml[tile(p)].x);
+    const int tile0 = held + early, parts = tile0 + un.open + un.fresh;
+    // place of part p: of the CTAs, the early one, the row tiles (those beyond the early one: another array)
+    auto place = [&](int p) -> int64_t {
+      if (p < held) return ((int64_t)c0 + p + seg) * geo.RB + rb;
+      if (p < tile0) return ((int64_t)geo.ctas + geo.segments + seg) * geo.RB + rb;
+      const int f = p - tile0 < un.open ? p - tile0 : kPage / kRowTile + p - tile0 - un.open;
+      return ((int64_t)seg * geo.tiles + f) * geo.RB + rb;
+    };
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, (p < tile0 ? ws.ml : ws.rml)[place(p)].x);
     M = warp_max(M);
     base = M == -INFINITY ? 0.0f : M;
     constexpr int B = 8;
@@ -50,10 +57,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
         ml[b] = make_float2(-INFINITY, 0.0f);
         v[b] = {};
         if (p < parts) {
-          const bool h = p < held;
-          const int64_t at = h ? held0 + (int64_t)p * geo.RB : tile(p);
-          ml[b] = (h ? ws.ml : ws.rml)[at];
-          v[b] = *reinterpret_cast<const Vec*>((h ? ws.o : ws.ro) + at * D + E * lane);
+          const int64_t at = place(p);
+          ml[b] = (p < tile0 ? ws.ml : ws.rml)[at];
+          v[b] = *reinterpret_cast<const Vec*>((p < tile0 ? ws.o : ws.ro) + at * D + E * lane);
         }
       }
 #pragma unroll
@@ -136,13 +142,12 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
   const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
   if (units >= (size_t)1 << 31 || p->segments > 65535) return W4A8_ERR_SHAPE;
-  const int ng = kKv8Warps / wc;
-  const size_t ctas = units;  // few pages: spread over the SMs
-  g.workers = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas) * ng;
+  g.ng = kKv8Warps / wc;
+  g.ctas = (int)(units < (size_t)kKv8Ctas ? units : (size_t)kKv8Ctas);
   p->prefix = 0;
   g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);
   g.segments = (int)p->segments;
-  const size_t slots = g.workers + p->segments, rslots = p->segments * g.tiles, row = (size_t)g.RB * 4;
+  const size_t slots = g.ctas + 2 * p->segments, rslots = p->segments * g.tiles, row = (size_t)g.RB * 4;
   p->ml = up256(((size_t)c->n_seqs + 1) * 4);
   p->o = up256(p->ml + slots * row * 2);
   p->rml = up256(p->o + slots * row * c->head_dim);

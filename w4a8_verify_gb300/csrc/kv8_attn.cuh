@@ -32,7 +32,8 @@
 // the instruction caches, and twelve warps at different places of it spent a third of their time on fetches.  The fp32 rows (open page, new rows; at most 63 + 64 of a segment) go to one or two further warps
 // of each CTA, 16 rows at a time, in plain fp32: with the tensor-core form of them inside the page loop their code ran
 // a few times per CTA, cold, and one worker's four row tiles took 30 us at the end of a 40 us call.  Each
-// worker's part of a segment and each row tile leaves (maximum, sum, values); k_kv8_join puts them together.
+// worker's part of a segment and each row tile gives (maximum, sum, values); the workers of a CTA add theirs up where
+// they hold the same segment, and k_kv8_join puts the rest together.
 #pragma once
 #include <type_traits>
 
@@ -51,7 +52,7 @@ constexpr int kRowChunk = 4;          // query rows that a row warp takes at a t
 struct Kv8Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a segment's problem (n G, or G with lists)
   int RB, CB;          // rows of a column block; column blocks
-  int workers;
+  int ctas, ng;        // of the split kernel, and its workers in each at most
   int tiles;           // row tiles of a segment: four of the open page, those of the new rows
   int segments;
   int vec;             // q rows may be read 16 bytes at a time
@@ -59,8 +60,9 @@ struct Kv8Geom {       // of one call, the same for every kernel of it
 
 struct Kv8Scratch {    // workspace pointers
   int* prefix;         // [n_seqs + 1] pages of the segments before each sequence
-  float2* ml;          // [workers + segments][RB] maximum, sum of the part of a (worker, segment): at worker + segment
-  float* o;            // [workers + segments][RB][D] its values
+  float2* ml;          // [ctas + segments][RB] maximum, sum of the part of a (CTA, segment), at CTA + segment; then
+                       // [segments][RB] of the part whose worker went on to another segment
+  float* o;            // [..][RB][D] its values
   float2* rml;         // [segments][tiles][RB] maximum, sum of a row tile
   float* ro;           // [segments][tiles][RB][D] its values
   float2* fin;         // [n_seqs][n][n_heads] maximum, sum of each row (with mass)
@@ -89,6 +91,14 @@ __device__ __forceinline__ Kv8Segment kv8_segment(const w4a8_kv8_cache& c, const
 // Segments of a sequence: (KV head, column block), or (row, KV head) with page lists.
 __device__ __forceinline__ int kv8_segments(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& g, int cnt) {
   return a.pages ? cnt * c.n_kv_heads : cnt > 0 ? c.n_kv_heads * g.CB : 0;
+}
+// Workers of U units: ng for each CTA, W <= U in all.
+struct Kv8Workers {
+  int ng, W;
+};
+__device__ __forceinline__ Kv8Workers kv8_workers(int U, int ctas, int most) {
+  const int ng = min(most, (U + ctas - 1) / ctas);
+  return {ng, min(U, ctas * ng)};
 }
 // First unit of worker w of W <= U over U units, and the worker of unit u.
 __device__ __forceinline__ int worker_begin(int w, int W, int U) { return (int)((int64_t)w * U / W); }
@@ -133,6 +143,9 @@ __device__ __forceinline__ float f16_scale(float amax) {
 }
 
 // ---------------------------------------------------------------------------- the split kernel
+
+// Barrier of the page warps (the first of a CTA).
+__device__ __forceinline__ void page_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kKv8Warps) : "memory"); }
 
 template <typename T, int D, int WC>
 struct Kv8Split {
@@ -328,9 +341,10 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     return;
   }
   const int U = prefix[S];
-  const int W = min(geo.workers, U), worker = grp * gridDim.x + blockIdx.x;  // few units spread over the SMs
-  if (worker >= W) return;
-  const int u0 = worker_begin(worker, W, U), u1 = worker_begin(worker + 1, W, U);
+  const Kv8Workers wk = kv8_workers(U, geo.ctas, C::NG);
+  const int worker = blockIdx.x * wk.ng + grp;
+  const bool has = grp < wk.ng && worker < wk.W;
+  const int u0 = has ? worker_begin(worker, wk.W, U) : 0, u1 = has ? worker_begin(worker + 1, wk.W, U) : 0;
 
   // The lane's unit x: its segment, page and scales (32 units in parallel, so the table's latency is paid once).
   auto look = [&](int x) -> Kv8Unit {
@@ -469,21 +483,19 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     }
   };
 
-  // Ends the worker's part of a segment (P carries kPScale, the codes 1 / UNIT).
-  auto flush = [&]() {
+  // The worker's part of a segment (P carries kPScale, the codes 1 / UNIT) to rows of (ml, o).
+  auto flush = [&](float2* ml, float* out) {
     if (!act) return;
-    const size_t slot = ((size_t)worker + seg) * C::RB;
 #pragma unroll
     for (int x = 0; x < NC; ++x) {
       float sum = l[x];
       sum += __shfl_xor_sync(FULL, sum, 4);
       sum += __shfl_xor_sync(FULL, sum, 8);
       sum += __shfl_xor_sync(FULL, sum, 16);
-      const int r = row_of(2 * t + x);
-      if (!row_ok(r)) continue;
-      const size_t at = slot + (r - cb_cur * C::RB);
-      if (g == 0) ws.ml[at] = make_float2(m[x], sum / kPScale);
-      float* o = ws.o + at * D;
+      const int r = wg * C::RPT + (SPLIT ? t : 2 * t + x);  // of the column block
+      if (!row_ok(cb_cur * C::RB + r)) continue;
+      if (g == 0) ml[r] = make_float2(m[x], sum / kPScale);
+      float* o = out + r * D;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         o[16 * d + g] = (SPLIT ? O[d][0] + O[d][1] : O[d][x]) * (C::UNIT / kPScale);
@@ -641,7 +653,10 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const int src = j - cbase;
     const int from = __shfl_sync(FULL, cur.src, src), sg = __shfl_sync(FULL, cur.seg, src);
     if (sg != seg) {
-      if (seg >= 0) flush();
+      if (seg >= 0) {
+        const size_t at = ((size_t)geo.ctas + geo.segments + seg) * C::RB;
+        flush(ws.ml + at, ws.o + at * D);
+      }
       begin(sg);
     }
     const float sk = __shfl_sync(FULL, cur.sk, src), sv = __shfl_sync(FULL, cur.sv, src);
@@ -655,17 +670,50 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     if (++cs == C::NS) cs = 0, ++cph;
     --in_ring;
   }
-  if (ok) {
-    flush();
-    return;
+  if (!ok) {  // a bounded wait expired: report it, and wait (again bounded) for the copies still in flight
+    if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+    if (wg == 0)
+      for (; in_ring > 0; --in_ring) {
+        (void)mbar_wait(&full[cs], cph & 1);
+        if (++cs == C::NS) cs = 0, ++cph;
+      }
   }
-  // A bounded wait expired: report it, and wait (again bounded) for the copies still in flight.
-  if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
-  if (wg == 0)
-    for (; in_ring > 0; --in_ring) {
-      (void)mbar_wait(&full[cs], cph & 1);
-      if (++cs == C::NS) cs = 0, ++cph;
+  // ---- the workers' last parts, in the ring's place, and of each run of workers on one segment the sum
+  float2* sml = reinterpret_cast<float2*>(sm);                       // [NG][RB]
+  int* sseg = reinterpret_cast<int*>(sml + C::NG * C::RB);           // [NG], -1: none
+  float* so = reinterpret_cast<float*>(sm) + ((C::NG * (2 * C::RB + 1) + 31) & ~31);  // [NG][RB][D]
+  page_warps_sync();
+  if (lane == 0 && wg == 0) sseg[grp] = ok && has ? seg : -1;
+  if (ok && has && seg >= 0) flush(sml + grp * C::RB, so + grp * C::RB * D);
+  page_warps_sync();
+  for (int i0 = 0; i0 < C::NG;) {
+    const int sg = sseg[i0];
+    int i1 = i0 + 1;
+    while (i1 < C::NG && sseg[i1] == sg) ++i1;
+    if (sg >= 0) {
+      const Kv8Segment w = kv8_segment(c, a, geo, sg);
+      const int cnt = a.counts ? a.counts[w.s] : a.n;
+      const int rows = min(C::RB, (a.pages ? geo.G : cnt * geo.G) - w.cb * C::RB);
+      const size_t at = ((size_t)blockIdx.x + sg) * C::RB;
+      for (int x = tid; x < rows * (D / 4); x += 32 * kKv8Warps) {
+        const int r = x / (D / 4), d = x % (D / 4);
+        float M = -INFINITY, L = 0.0f;
+        for (int i = i0; i < i1; ++i) M = fmaxf(M, sml[i * C::RB + r].x);
+        const float base = M == -INFINITY ? 0.0f : M;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = i0; i < i1; ++i) {
+          const float2 ml = sml[i * C::RB + r];
+          const float4 o = reinterpret_cast<const float4*>(so + (i * C::RB + r) * D)[d];
+          const float f = ex2(ml.x - base);
+          L = fmaf(ml.y, f, L);
+          v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+        }
+        reinterpret_cast<float4*>(ws.o + (at + r) * D)[d] = v;
+        if (d == 0) ws.ml[at + r] = make_float2(M, L);
+      }
     }
+    i0 = i1;
+  }
 }
 
 // ---------------------------------------------------------------------------- launch
@@ -690,7 +738,7 @@ cudaError_t kv8_split_launch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
   const size_t most = kv8_split_smem(kKv8MaxSeqs, C::NG * C::NS), smem = kv8_split_smem(c.n_seqs, C::NG * C::NS);
   cudaError_t e = cudaFuncSetAttribute(k_kv8_split<T, D, WC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_kv8_split<T, D, WC>, dim3((unsigned)(geo.workers / C::NG)), dim3(kKv8Threads), smem, st, c, a,
+  return launch_pdl(k_kv8_split<T, D, WC>, dim3((unsigned)geo.ctas), dim3(kKv8Threads), smem, st, c, a,
                     geo, ws);
 }
 template <typename T, int D>
