@@ -252,7 +252,7 @@ w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k, const w
                             int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);
 /* Device.  Positions first[s] .. first[s] + n - 1 of every sequence as the cache holds them (s * c of
  * whole pages, one rounding; the fp32 rows of the open page), positions at or behind len[s] as 0, into
- * k_out and v_out, fp32 [n_seqs][n][n_kv_heads][head_dim] contiguous.  len: NULL = c->len. */
+ * k_out and v_out, fp32 [n_seqs][n][n_kv_heads][head_dim] contiguous, 16-byte aligned.  len: NULL = c->len. */
 w4a8_status w4a8_kv8_read(const w4a8_kv8_cache* c, const int32_t* first, const int32_t* len, int n, float* k_out,
                           float* v_out, void* stream);
 

@@ -36,6 +36,12 @@ inline w4a8_status kv8_valid(const w4a8_kv8_cache* c) {
 inline bool kv8_dtype(int t) { return t == W4A8_F32 || t == W4A8_BF16; }
 inline size_t kv8_elem(int t) { return t == W4A8_F32 ? 4 : 2; }
 
+// Whether groups of eight elements can be read 16 bytes at a time.
+inline bool kv8_vec_rows(const w4a8_rows& r, int dtype) {
+  const int64_t e = 16 / (int64_t)kv8_elem(dtype);
+  return aligned(r.data, 16) && r.seq % e == 0 && r.row % e == 0 && r.head % e == 0;
+}
+
 // (sequence, KV head) pair index and page addresses: 64-bit, a long cache passes 4 GB
 __device__ __forceinline__ size_t kv8_pair(const w4a8_kv8_cache& c, int s, int h) { return (size_t)s * c.n_kv_heads + h; }
 __device__ __forceinline__ size_t kv8_page(const w4a8_kv8_cache& c, size_t pair, int phys) {

@@ -161,12 +161,6 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   return W4A8_OK;
 }
 
-// Whether groups of eight elements can be read 16 bytes at a time.
-bool vec_rows(const w4a8_rows& r, int dtype) {
-  const int64_t e = 16 / (int64_t)kv8_elem(dtype);
-  return aligned(r.data, 16) && r.seq % e == 0 && r.row % e == 0 && r.head % e == 0;
-}
-
 }  // namespace
 
 W4A8_API w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a,
@@ -194,7 +188,7 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
                 reinterpret_cast<float*>(base + p.o), reinterpret_cast<float2*>(base + p.rml),
                 reinterpret_cast<float*>(base + p.ro), a->mass_out ? reinterpret_cast<float2*>(base + p.fin) : nullptr,
                 a->mass_out ? reinterpret_cast<float2*>(base + p.page) : nullptr};
-  p.geo.vec = vec_rows(a->q, a->dtype) ? 1 : 0;
+  p.geo.vec = kv8_vec_rows(a->q, a->dtype) ? 1 : 0;
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
   W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(

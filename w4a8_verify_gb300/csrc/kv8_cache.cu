@@ -34,17 +34,31 @@ __device__ bool append_index_ok(const w4a8_kv8_cache& c, const int32_t* index, i
   return ok;
 }
 
-// One CTA per (page of the call's window, KV head, sequence and keys/values).  A thread owns the
-// 16-byte groups of the page's byte order, so the codes leave in 16-byte stores; the values of a
-// group sit in registers between the absmax and the quantisation (one read of the rows).  The CTA of the
-// window's first page reads the old tail, so it alone writes the new one, afterwards.
+// round(x / s) for |x| <= 127 s, the IEEE quotient's rounding, mostly without the division: q = x (1 / s) is within
+// 2.3e-5 of fl(x / s) (two roundings of at most 127 2^-24 each, and the quotient's own), so only a q that close to a half
+// needs it.  inv is 0 where 1 / s is not a good factor (subnormal s).
+__device__ __forceinline__ int quick_code(float x, float s, float inv) {
+  const float q = x * inv, n = rintf(q);
+  if (inv == 0.0f || fabsf(fabsf(q - n) - 0.5f) < 6e-5f) return kv8_code(x, s);
+  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
+}
+
+constexpr int kVPad = 4;  // bytes between the token rows of a page's value codes in shared memory
+
+// One CTA per (page of the call's window, KV head, sequence and keys/values).  A thread takes eight neighbouring
+// dims of four (D = 128) rows, 16 or 32 bytes at a time where the rows allow it, and keeps them in registers between
+// the absmax and the quantisation: one read of the rows.  Key groups of 16 bytes are whole in a thread; value groups
+// (eight tokens of two dims) are gathered from the codes in shared memory.  The CTA of the window's first page
+// reads the old tail, so it alone writes the new one, afterwards.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c, w4a8_rows kr, w4a8_rows vr, int n_src,
                                                                 int n, const int32_t* counts, const int32_t* index,
-                                                                int32_t* len_out, bool store_len) {
+                                                                int32_t* len_out, bool store_len, int vec) {
   griddep_enter();
+  constexpr int kChunks = kPage * D / 8 / kAppendThreads;
   __shared__ float red[kAppendThreads / 32];
   __shared__ int ksum[D];
+  __shared__ __align__(16) uint8_t vs[kPage * (D + kVPad)];
   const int w = blockIdx.x, h = blockIdx.y, s = blockIdx.z >> 1;
   const bool val = blockIdx.z & 1;
   const int tid = threadIdx.x;
@@ -54,6 +68,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
   if (store_len && w == 0 && h == 0 && !val && tid == 0) len_out[s] = end >= 0 ? end : c.len[s];
   if (end < 0 || end == L) return;
   const w4a8_rows rows = val ? vr : kr;
+  const bool wide = vec >> val & 1;
   const T* src = static_cast<const T*>(rows.data) + (int64_t)s * rows.seq + (int64_t)h * rows.head;
   const size_t pair = kv8_pair(c, s, h);
   float* tail = c.tail + (pair * 2 + val) * kPage * D;
@@ -62,33 +77,50 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     const int j = pos - L;
     return src + (int64_t)(index ? index[(size_t)s * n + j] : j) * rows.row;
   };
-  auto value = [&](int tok, int d) -> float {
-    const int pos = base + tok;
-    return pos < L ? tail[tok * D + d] : kv8_load(row_of(pos) + d);
+  // dims d .. d + 7 (d % 8 == 0) of a position
+  auto load8 = [&](int pos, int d, float (&x)[8]) {
+    if (pos < L) {
+      const float4* p = reinterpret_cast<const float4*>(tail + (pos - base) * D + d);
+      const float4 a = p[0], b = p[1];
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+      return;
+    }
+    const T* p = row_of(pos) + d;
+    if (wide) {
+      uint4 u[sizeof(T) / 2];
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      const T* e = reinterpret_cast<const T*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = kv8_load(e + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = kv8_load(p + i);
+    }
   };
   if (base + kPage <= end) {
     const int phys = kv8_phys(c, pair, page);
-    constexpr int kGroups = 64 * D / 16 / kAppendThreads;  // 16-byte groups of a thread
-    float x[kGroups][16];
+    // chunk i of a thread, keys: group gi = (i / 2) threads + tid of the page's order, its token g + 8 (i & 1);
+    // values: the i-th of the page's eight-dim chunks in rows
+    float x[kChunks][8];
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int gi = i * kAppendThreads + tid, t = gi & 3, g = (gi >> 2) & 7, q = gi >> 5;
-      if (!val) {  // q = (16-token tile, 32-dim chunk): tokens g, g + 8, dims 8t..8t+7
-        const int mt = q / (D / 32), kp = q % (D / 32);
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-          x[i][b] = value(mt * 16 + ((b >> 2) & 1) * 8 + g, kp * 32 + t * 8 + (b >> 3) * 4 + (b & 3));
-      } else {  // q = (16-dim tile, 32-token chunk): dims g, g + 8, tokens 2t, 2t + 1, + 8, + 16, + 24
-        const int dt = q >> 1, kp = q & 1;
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-          x[i][b] = value(kp * 32 + (b >> 3) * 16 + ((b >> 1) & 1) * 8 + t * 2 + (b & 1),
-                          dt * 16 + ((b >> 2) & 1) * 8 + g);
+    for (int i = 0; i < kChunks; ++i) {
+      int tok, d;
+      if (!val) {
+        const int gi = (i >> 1) * kAppendThreads + tid, q = gi >> 5;
+        tok = q / (D / 32) * 16 + (i & 1) * 8 + ((gi >> 2) & 7);
+        d = q % (D / 32) * 32 + (gi & 3) * 8;
+      } else {
+        const int ci = i * kAppendThreads + tid;
+        tok = ci / (D / 8), d = ci % (D / 8) * 8;
       }
-#pragma unroll
-      for (int b = 0; b < 16; ++b) m = max_nan(m, fabsf(x[i][b]));
+      load8(base + tok, d, x[i]);
     }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[i][e]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((tid & 31) == 0) red[tid >> 5] = m;
@@ -98,36 +130,59 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
 #pragma unroll
     for (int i = 1; i < kAppendThreads / 32; ++i) amax = max_nan(amax, red[i]);
     const float sc = kv8_scale(amax);
-    if (phys >= 0) {
-      const size_t pg = kv8_page(c, pair, phys);
-      uint4* out = reinterpret_cast<uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
+    const float inv = sc > 1e-37f ? __fdiv_rn(1.0f, sc) : 0.0f;
+    uint32_t word[kChunks][2];  // code + 128 of four dims each
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int gi = i * kAppendThreads + tid;
-        uint32_t word[4] = {0, 0, 0, 0};
-        int code[16];
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-        for (int b = 0; b < 16; ++b) {
-          code[b] = sc > 0.0f ? kv8_code(x[i][b], sc) : 0;
-          word[b >> 2] |= (uint32_t)(code[b] + 128) << (8 * (b & 3));
-        }
-        out[gi] = make_uint4(word[0], word[1], word[2], word[3]);
-        if (!val) {
-          const int t = gi & 3, kp = (gi >> 5) % (D / 32);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = (uint32_t)((sc > 0.0f ? quick_code(x[i][e], sc, inv) : 0) + 128);
+        if ((e & 3) == 0) word[i][e >> 2] = u;
+        else word[i][e >> 2] |= u << (8 * (e & 3));
+      }
+    const size_t pg = kv8_page(c, pair, phys < 0 ? 0 : phys);
+    uint4* out = reinterpret_cast<uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
+    if (!val) {
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {  // dim 8t + b of the chunk: tokens g and g + 8, then the eight g
-            int v = code[(b >> 2) * 8 + (b & 3)] + code[(b >> 2) * 8 + 4 + (b & 3)];
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[kp * 32 + t * 8 + b], v);  // integers: any order
-          }
+      for (int i = 0; i < kChunks; i += 2) {
+        const int gi = (i >> 1) * kAppendThreads + tid;
+        if (phys >= 0) out[gi] = make_uint4(word[i][0], word[i + 1][0], word[i][1], word[i + 1][1]);
+        const int t = gi & 3, kp = (gi >> 5) % (D / 32);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // dim 8t + e of the chunk: tokens g and g + 8, then the eight g
+          int v = (int)(word[i][e >> 2] >> (8 * (e & 3)) & 255u) + (int)(word[i + 1][e >> 2] >> (8 * (e & 3)) & 255u) - 256;
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
+          if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[kp * 32 + t * 8 + e], v);  // integers: any order
         }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int ci = i * kAppendThreads + tid;
+        uint32_t* p = reinterpret_cast<uint32_t*>(vs + ci / (D / 8) * (D + kVPad) + ci % (D / 8) * 8);
+        p[0] = word[i][0], p[1] = word[i][1];
+      }
+    }
+    __syncthreads();
+    if (phys >= 0) {
       if (tid == 0) c.scales[pg * 2 + val] = sc;
       if (!val) {
-        __syncthreads();
         for (int d = tid; d < D; d += kAppendThreads) c.sums[pg * D + d] = (int16_t)ksum[d];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunks / 2; ++i) {
+          const int gi = i * kAppendThreads + tid, t = gi & 3, g = (gi >> 2) & 7, q = gi >> 5;
+          uint32_t u[4];
+#pragma unroll
+          for (int b = 0; b < 16; ++b) {
+            const int tok = (q & 1) * 32 + (b >> 3) * 16 + ((b >> 1) & 1) * 8 + t * 2 + (b & 1);
+            const uint32_t v = vs[tok * (D + kVPad) + (q >> 1) * 16 + ((b >> 2) & 1) * 8 + g];
+            u[b >> 2] = (b & 3) ? u[b >> 2] | v << (8 * (b & 3)) : v;
+          }
+          out[gi] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
       }
     }
   }
@@ -161,53 +216,82 @@ __global__ void k_kv8_reset(w4a8_kv8_cache c) {
   if (i == 0) *c.ctl = 0;
 }
 
-// One CTA per (page of the window, KV head, sequence and keys/values): 16-byte groups of codes, each value
-// s * c with one rounding; positions of the open page come from the tail.
+// One CTA per (page of the window, KV head, sequence and keys/values): each value s * c with one rounding; positions
+// of the open page come from the tail.  A thread writes eight neighbouring dims of a position, 32 bytes; the codes of
+// value groups (eight tokens of two dims) change places in shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_read(w4a8_kv8_cache c, const int32_t* first, const int32_t* len, int n,
                                                    float* __restrict__ k_out, float* __restrict__ v_out) {
   griddep_enter();
-  const int h = blockIdx.y, s = blockIdx.z >> 1;
+  __shared__ __align__(16) uint8_t vs[kPage * (D + kVPad)];
+  const int h = blockIdx.y, s = blockIdx.z >> 1, tid = threadIdx.x;
   const bool val = blockIdx.z & 1;
   const int F = first[s];
   int L = kv8_len(c, len, s);
   if (F < 0) {
-    if (threadIdx.x == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_CAPACITY);
+    if (tid == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_CAPACITY);
     L = 0;
   }
   if (L < 0) L = 0;
   const int64_t f = F < 0 ? 0 : F;
   const int64_t page = f / kPage + blockIdx.x, base = page * kPage;
+  if (base >= f + n) return;
   const size_t pair = kv8_pair(c, s, h);
-  float* out = val ? v_out : k_out;
-  const size_t rs = (size_t)c.n_kv_heads * D;
-  out += ((size_t)s * n * c.n_kv_heads + h) * D;
-  auto put = [&](int tok, int d, float v) {
+  float* out = (val ? v_out : k_out) + ((size_t)s * n * c.n_kv_heads + h) * D;
+  auto put8 = [&](int tok, int d, const float (&x)[8]) {
     const int64_t j = base + tok - f;
-    if (j >= 0 && j < n) out[(size_t)j * rs + d] = v;
+    if (j < 0 || j >= n) return;
+    float4* p = reinterpret_cast<float4*>(out + (size_t)j * c.n_kv_heads * D + d);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
   };
-  if (base + kPage <= L) {
-    const int phys = kv8_phys(c, pair, (int)page);
-    const size_t pg = kv8_page(c, pair, phys < 0 ? 0 : phys);
-    const float sc = phys < 0 ? 0.0f : c.scales[pg * 2 + val];
-    const uint4* in = reinterpret_cast<const uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
-    for (int gi = threadIdx.x; gi < kPage * D / 16; gi += 256) {
-      const uint4 u = in[gi];
-      const uint32_t word[4] = {u.x, u.y, u.z, u.w};
-      const int t = gi & 3, g = (gi >> 2) & 7, q = gi >> 5;
+  if (base + kPage > L) {
+    const float* tail = c.tail + (pair * 2 + val) * kPage * D;
+    for (int ci = tid; ci < kPage * D / 8; ci += 256) {
+      const int tok = ci / (D / 8), d = ci % (D / 8) * 8;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = base + tok < L ? tail[tok * D + d + e] : 0.0f;
+      put8(tok, d, x);
+    }
+    return;
+  }
+  const int phys = kv8_phys(c, pair, (int)page);
+  const size_t pg = kv8_page(c, pair, phys < 0 ? 0 : phys);
+  const float sc = phys < 0 ? 0.0f : c.scales[pg * 2 + val];
+  const uint4* in = reinterpret_cast<const uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
+  auto value = [&](uint32_t w, int e) { return sc * (float)((int)(w >> (8 * e) & 255u) - 128); };
+#pragma unroll
+  for (int i = 0; i < kPage * D / 16 / 256; ++i) {
+    const int gi = i * 256 + tid, t = gi & 3, g = (gi >> 2) & 7, q = gi >> 5;
+    const uint4 u = __ldg(in + gi);
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+    if (!val) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = value(word[(e >> 2) * 2 + r], e & 3);
+        put8(q / (D / 32) * 16 + r * 8 + g, q % (D / 32) * 32 + t * 8, x);
+      }
+    } else {
 #pragma unroll
       for (int b = 0; b < 16; ++b) {
-        const float x = sc * (float)((int)((word[b >> 2] >> (8 * (b & 3))) & 255u) - 128);
-        if (!val)
-          put((q / (D / 32)) * 16 + ((b >> 2) & 1) * 8 + g, (q % (D / 32)) * 32 + t * 8 + (b >> 3) * 4 + (b & 3), x);
-        else
-          put((q & 1) * 32 + (b >> 3) * 16 + ((b >> 1) & 1) * 8 + t * 2 + (b & 1), (q >> 1) * 16 + ((b >> 2) & 1) * 8 + g,
-              x);
+        const int tok = (q & 1) * 32 + (b >> 3) * 16 + ((b >> 1) & 1) * 8 + t * 2 + (b & 1);
+        vs[tok * (D + kVPad) + (q >> 1) * 16 + ((b >> 2) & 1) * 8 + g] = (uint8_t)(word[b >> 2] >> (8 * (b & 3)));
       }
     }
-  } else {
-    const float* tail = c.tail + (pair * 2 + val) * kPage * D;
-    for (int i = threadIdx.x; i < kPage * D; i += 256) put(i / D, i % D, base + i / D < L ? tail[i] : 0.0f);
+  }
+  if (!val) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPage * D / 8 / 256; ++i) {
+    const int ci = i * 256 + tid, tok = ci / (D / 8), d = ci % (D / 8) * 8;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(vs + tok * (D + kVPad) + d);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = value(p[e >> 2], e & 3);
+    put8(tok, d, x);
   }
 }
 
@@ -256,8 +340,9 @@ W4A8_API w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k
   cudaStream_t st = as_stream(stream);
   const dim3 grid((unsigned)((n + kPage - 1 + kPage - 1) / kPage), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs * 2);
   const bool own = len_out == c->len;
+  const int vec = (kv8_vec_rows(*k, dtype) ? 1 : 0) | (kv8_vec_rows(*v, dtype) ? 2 : 0);
   auto run = [&](auto kern) {
-    return launch_pdl(kern, grid, dim3(kAppendThreads), 0, st, *c, *k, *v, n_src, n, counts, index, len_out, !own);
+    return launch_pdl(kern, grid, dim3(kAppendThreads), 0, st, *c, *k, *v, n_src, n, counts, index, len_out, !own, vec);
   };
   if (dtype == W4A8_F32)
     W4A8_CUDA_TRY(c->head_dim == 64 ? run(k_kv8_append<float, 64>) : run(k_kv8_append<float, 128>));
@@ -273,7 +358,7 @@ W4A8_API w4a8_status w4a8_kv8_read(const w4a8_kv8_cache* c, const int32_t* first
                                    float* k_out, float* v_out, void* stream) {
   const w4a8_status ok = kv8_valid(c);
   if (ok != W4A8_OK) return ok;
-  if (!first || !k_out || !v_out || n < 1) return W4A8_ERR_ARG;
+  if (!first || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || n < 1) return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages + kPage - 1) return W4A8_ERR_CAPACITY;
   const dim3 grid((unsigned)((n + kPage - 1 + kPage - 1) / kPage), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs * 2);
   const int32_t* L = len ? len : c->len;
