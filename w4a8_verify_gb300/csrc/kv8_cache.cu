@@ -34,13 +34,27 @@ __device__ bool append_index_ok(const w4a8_kv8_cache& c, const int32_t* index, i
   return ok;
 }
 
-// round(x / s) for |x| <= 127 s, the IEEE quotient's rounding, mostly without the division: q = x (1 / s) is within
-// 2.3e-5 of fl(x / s) (two roundings of at most 127 2^-24 each, and the quotient's own), so only a q that close to a half
-// needs it.  inv is 0 where 1 / s is not a good factor (subnormal s).
-__device__ __forceinline__ int quick_code(float x, float s, float inv) {
-  const float q = x * inv, n = rintf(q);
-  if (inv == 0.0f || fabsf(fabsf(q - n) - 0.5f) < 6e-5f) return kv8_code(x, s);
-  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
+// Codes + 128 of eight values at scale s > 0 (|x| <= 127 s up to rounding), four to a word: rint of the IEEE quotient,
+// mostly without the division.  q = x (1 / s) is within 2.3e-5 of fl(x / s) (two roundings of at most 127 2^-24 each, and
+// the quotient's own), so only a q that close to a half needs it; adding 1.5 2^23 rounds q to a whole number in the
+// low bits.  inv is 0 where 1 / s is not a good factor (subnormal s).
+__device__ __forceinline__ void codes8(const float (&x)[8], float s, float inv, uint32_t (&word)[2]) {
+  uint32_t n[8];
+  float off = inv == 0.0f ? 1.0f : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = __fmul_rn(x[e], inv), r = q + 12582912.0f;
+    off = fmaxf(off, fabsf(q - (r - 12582912.0f)));
+    n[e] = __float_as_uint(r);
+  }
+  if (off > 0.5f - 6e-5f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n[e] = (uint32_t)kv8_code(x[e], s);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    word[i] = __byte_perm(__byte_perm(n[4 * i], n[4 * i + 1], 0x0040), __byte_perm(n[4 * i + 2], n[4 * i + 3], 0x0040), 0x5410) ^
+              0x80808080u;
 }
 
 constexpr int kVPad = 4;  // bytes between the token rows of a page's value codes in shared memory
@@ -57,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
   griddep_enter();
   constexpr int kChunks = kPage * D / 8 / kAppendThreads;
   __shared__ float red[kAppendThreads / 32];
-  __shared__ int ksum[D];
+  __shared__ uint32_t ksum[D / 2];  // sums of code + 128 of dims 4 i + j and 4 i + j + 2 in entry 2 i + j
   __shared__ __align__(16) uint8_t vs[kPage * (D + kVPad)];
   const int w = blockIdx.x, h = blockIdx.y, s = blockIdx.z >> 1;
   const bool val = blockIdx.z & 1;
@@ -102,11 +116,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     const int phys = kv8_phys(c, pair, page);
     // chunk i of a thread, keys: group gi = (i / 2) threads + tid of the page's order, its token g + 8 (i & 1);
     // values: the i-th of the page's eight-dim chunks in rows
-    float x[kChunks][8];
+    float x[kChunks][8] = {};
     float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      int tok, d;
+    auto place = [&](int i, int& tok, int& d) {
       if (!val) {
         const int gi = (i >> 1) * kAppendThreads + tid, q = gi >> 5;
         tok = q / (D / 32) * 16 + (i & 1) * 8 + ((gi >> 2) & 7);
@@ -115,7 +127,34 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
         const int ci = i * kAppendThreads + tid;
         tok = ci / (D / 8), d = ci % (D / 8) * 8;
       }
-      load8(base + tok, d, x[i]);
+    };
+    if (wide && !index && base >= L) {  // a page of whole new rows: the loads alone, all in flight
+      const T* from = src + (int64_t)(base - L) * rows.row;
+      uint4 u[kChunks][sizeof(T) / 2];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        int tok, d;
+        place(i, tok, d);
+        const uint4* p = reinterpret_cast<const uint4*>(from + tok * rows.row + d);
+#pragma unroll
+        for (int y = 0; y < (int)sizeof(T) / 2; ++y) u[i][y] = __ldg(p + y);
+      }
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = kv8_load(reinterpret_cast<const T*>(u[i]) + e);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kChunks; ++i) {
+        int tok, d;
+        place(i, tok, d);
+        float y[8];
+        load8(base + tok, d, y);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[k][e] = k == i ? y[e] : x[k][e];
+      }
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
@@ -124,7 +163,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((tid & 31) == 0) red[tid >> 5] = m;
-    for (int d = tid; d < D; d += kAppendThreads) ksum[d] = 0;
+    for (int d = tid; d < D / 2; d += kAppendThreads) ksum[d] = 0;
     __syncthreads();
     float amax = red[0];
 #pragma unroll
@@ -133,13 +172,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     const float inv = sc > 1e-37f ? __fdiv_rn(1.0f, sc) : 0.0f;
     uint32_t word[kChunks][2];  // code + 128 of four dims each
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = (uint32_t)((sc > 0.0f ? quick_code(x[i][e], sc, inv) : 0) + 128);
-        if ((e & 3) == 0) word[i][e >> 2] = u;
-        else word[i][e >> 2] |= u << (8 * (e & 3));
-      }
+    for (int i = 0; i < kChunks; ++i) {
+      if (sc > 0.0f) codes8(x[i], sc, inv, word[i]);
+      else word[i][0] = word[i][1] = 0x80808080u;
+    }
     const size_t pg = kv8_page(c, pair, phys < 0 ? 0 : phys);
     uint4* out = reinterpret_cast<uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
     if (!val) {
@@ -149,12 +185,14 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
         if (phys >= 0) out[gi] = make_uint4(word[i][0], word[i + 1][0], word[i][1], word[i + 1][1]);
         const int t = gi & 3, kp = (gi >> 5) % (D / 32);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {  // dim 8t + e of the chunk: tokens g and g + 8, then the eight g
-          int v = (int)(word[i][e >> 2] >> (8 * (e & 3)) & 255u) + (int)(word[i + 1][e >> 2] >> (8 * (e & 3)) & 255u) - 256;
+        for (int e = 0; e < 4; ++e) {  // dims e, e + 2 of a half of the eight: sums of code + 128 in 16 bits each
+          const int sh = 8 * (e & 1), half = e >> 1;
+          uint32_t v = (word[i][half] >> sh & 0x00ff00ffu) + (word[i + 1][half] >> sh & 0x00ff00ffu);
           v += __shfl_xor_sync(0xffffffffu, v, 4);
           v += __shfl_xor_sync(0xffffffffu, v, 8);
           v += __shfl_xor_sync(0xffffffffu, v, 16);
-          if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[kp * 32 + t * 8 + e], v);  // integers: any order
+          // at most 64 * 255 in a half: no carry; integers: any order
+          if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[((kp * 4 + t) * 2 + half) * 2 + (e & 1)], v);
         }
       }
     } else {
@@ -169,19 +207,28 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     if (phys >= 0) {
       if (tid == 0) c.scales[pg * 2 + val] = sc;
       if (!val) {
-        for (int d = tid; d < D; d += kAppendThreads) c.sums[pg * D + d] = (int16_t)ksum[d];
+        for (int d = tid; d < D; d += kAppendThreads)
+          c.sums[pg * D + d] = (int16_t)((int)(ksum[(d >> 2) * 2 + (d & 1)] >> (8 * (d & 2)) & 0xffffu) - 128 * kPage);
       } else {
+        // a thread gathers four groups of one (tile, chunk, t): dims g .. g + 3 and + 8 of eight tokens, as words of
+        // four dims that change places with four tokens
+        for (int x = tid; x < kPage * D / 64; x += kAppendThreads) {
+          const int t = x & 3, g4 = (x >> 2) & 1, q = x >> 3;
+          const uint8_t* from = vs + ((q & 1) * 32 + t * 2) * (D + kVPad) + (q >> 1) * 16 + g4 * 4;
+          uint32_t u[4][4];  // group, word: (ks, dim half): tokens + 16 ks + {0, 1, 8, 9}
 #pragma unroll
-        for (int i = 0; i < kChunks / 2; ++i) {
-          const int gi = i * kAppendThreads + tid, t = gi & 3, g = (gi >> 2) & 7, q = gi >> 5;
-          uint32_t u[4];
+          for (int wd = 0; wd < 4; ++wd) {
+            uint32_t v[4];
 #pragma unroll
-          for (int b = 0; b < 16; ++b) {
-            const int tok = (q & 1) * 32 + (b >> 3) * 16 + ((b >> 1) & 1) * 8 + t * 2 + (b & 1);
-            const uint32_t v = vs[tok * (D + kVPad) + (q >> 1) * 16 + ((b >> 2) & 1) * 8 + g];
-            u[b >> 2] = (b & 3) ? u[b >> 2] | v << (8 * (b & 3)) : v;
+            for (int b = 0; b < 4; ++b)
+              v[b] = *reinterpret_cast<const uint32_t*>(from + ((wd >> 1) * 16 + (b >> 1) * 8 + (b & 1)) * (D + kVPad) + (wd & 1) * 8);
+            const uint32_t a0 = __byte_perm(v[0], v[1], 0x5140), a1 = __byte_perm(v[2], v[3], 0x5140);
+            const uint32_t b0 = __byte_perm(v[0], v[1], 0x7362), b1 = __byte_perm(v[2], v[3], 0x7362);
+            u[0][wd] = __byte_perm(a0, a1, 0x5410), u[1][wd] = __byte_perm(a0, a1, 0x7632);
+            u[2][wd] = __byte_perm(b0, b1, 0x5410), u[3][wd] = __byte_perm(b0, b1, 0x7632);
           }
-          out[gi] = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[(q * 8 + g4 * 4 + i) * 4 + t] = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
         }
       }
     }
