@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <climits>
 
 #include "common.cuh"
@@ -15,6 +16,18 @@ constexpr int kKv8MaxHeads = 1024;
 constexpr int kKv8MaxPages = 16384;    // a million tokens; the selection keeps a head's scores in shared memory
 constexpr int kKv8MaxRows = 64;        // new rows of one sequence in an attention call (one 64-bit mask)
 constexpr int kKv8MaxGroup = 16;       // query heads per KV head
+
+// Lets a kernel use that much dynamic shared memory: once for each device (a host call of a microsecond).
+template <auto Kern>
+inline cudaError_t kv8_smem(size_t bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 inline w4a8_status kv8_dims(const w4a8_kv8_cache* c) {
   if (!c) return W4A8_ERR_ARG;

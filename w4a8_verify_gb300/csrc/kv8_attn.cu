@@ -136,13 +136,14 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.n = a->n;
   g.G = a->n_heads / c->n_kv_heads;
   g.R = a->pages ? g.G : g.n * g.G;
+  const bool wide = kv8_is_wide(*a, g.R);
   const int wc = kv8_split_warps(g.R, a->dtype);
-  g.RB = wc * (a->dtype == W4A8_F32 ? 4 : 8);
+  g.RB = wide ? kWideRows : wc * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
   const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
   if (units >= (size_t)1 << 31 || p->segments > 65535) return W4A8_ERR_SHAPE;
-  g.ng = kKv8Warps / wc;
+  g.ng = wide ? 1 : kKv8Warps / wc;
   g.ctas = (int)(units < (size_t)kKv8Ctas ? units : (size_t)kKv8Ctas);
   p->prefix = 0;
   g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);
@@ -191,7 +192,8 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   p.geo.vec = kv8_vec_rows(a->q, a->dtype) ? 1 : 0;
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
-  W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
+  if (kv8_is_wide(*a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
+  else W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
       *c, *a, p.geo, ws, st));
   // few rows (some CTAs for each SM): eight warps to a row, whose parts may be many; else two
   const int rows = p.geo.R < p.geo.RB ? p.geo.R : p.geo.RB;

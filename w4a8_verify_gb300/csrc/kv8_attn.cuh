@@ -46,6 +46,7 @@ constexpr int kKv8Ctas = 152;         // one per SM of a GB300
 constexpr int kKv8Warps = 12, kKv8RowWarps = 4, kKv8Threads = 32 * (kKv8Warps + kKv8RowWarps);
 constexpr int kKv8RingBytes = 196608; // ring of pages per SM: 12 of 16 KB or 24 of 8 KB
 constexpr float kPScale = 128.0f, kPSlack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
+constexpr int kWideRows = 128;        // query rows of a segment of a wide call (kv8_wide.cu)
 constexpr int kRowTile = 16;          // fp32 rows of one part
 constexpr int kRowChunk = 4;          // query rows that a row warp takes at a time
 
@@ -91,6 +92,30 @@ __device__ __forceinline__ Kv8Segment kv8_segment(const w4a8_kv8_cache& c, const
 // Segments of a sequence: (KV head, column block), or (row, KV head) with page lists.
 __device__ __forceinline__ int kv8_segments(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& g, int cnt) {
   return a.pages ? cnt * c.n_kv_heads : cnt > 0 ? c.n_kv_heads * g.CB : 0;
+}
+// Pages of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be synchronised after it.
+__device__ __forceinline__ void kv8_prefix(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, int* prefix) {
+  const int S = c.n_seqs;
+  for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
+    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : kv8_units(a, L, cnt).pages * kv8_segments(c, a, geo, cnt);
+  }
+  if (threadIdx.x == 0) prefix[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int b = 0; b < S; b += 32) {
+      const int s = b + threadIdx.x;
+      int v = s < S ? prefix[s + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)threadIdx.x >= o) v += x;
+      }
+      if (s < S) prefix[s + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
 }
 // Workers of U units: ng for each CTA, W <= U in all.
 struct Kv8Workers {
@@ -308,26 +333,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   griddep_enter();
 
-  // pages of the segments before each sequence
-  for (int s = tid; s < S; s += kKv8Threads) {
-    const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
-    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : kv8_units(a, L, cnt).pages * kv8_segments(c, a, geo, cnt);
-  }
-  if (tid == 0) prefix[0] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int b = 0; b < S; b += 32) {
-      int v = b + lane < S ? prefix[b + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(FULL, v, o);
-        if (lane >= o) v += x;
-      }
-      if (b + lane < S) prefix[b + lane + 1] = carry + v;
-      carry += __shfl_sync(FULL, v, 31);
-    }
-  }
+  kv8_prefix(c, a, geo, prefix);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int s = tid; s <= S; s += kKv8Threads) ws.prefix[s] = prefix[s];
@@ -736,7 +742,7 @@ cudaError_t kv8_split_launch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
                              cudaStream_t st) {
   using C = Kv8Split<T, D, WC>;
   const size_t most = kv8_split_smem(kKv8MaxSeqs, C::NG * C::NS), smem = kv8_split_smem(c.n_seqs, C::NG * C::NS);
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_split<T, D, WC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  cudaError_t e = kv8_smem<k_kv8_split<T, D, WC>>(most);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_kv8_split<T, D, WC>, dim3((unsigned)geo.ctas), dim3(kKv8Threads), smem, st, c, a,
                     geo, ws);
@@ -753,6 +759,9 @@ cudaError_t kv8_split_dispatch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, 
     default: return kv8_split_launch<T, D, 12>(c, a, geo, ws, st);
   }
 }
+// Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu).
+inline bool kv8_is_wide(const w4a8_kv8_attn& a, int R) { return !a.pages && R >= 32; }
+cudaError_t kv8_wide(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 // one translation unit per head size and element type
 cudaError_t kv8_split_f32_d64(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 cudaError_t kv8_split_f32_d128(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);

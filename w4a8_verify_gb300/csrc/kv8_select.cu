@@ -280,7 +280,7 @@ W4A8_API w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_att
       W4A8_CUDA_TRY(c->head_dim == 64 ? run(k_kv8_score<__nv_bfloat16, 64>) : run(k_kv8_score<__nv_bfloat16, 128>));
   }
   const size_t smem = (size_t)c->max_pages * 4;
-  W4A8_CUDA_TRY(cudaFuncSetAttribute(k_kv8_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8MaxPages * 4));
+  W4A8_CUDA_TRY(kv8_smem<k_kv8_pick>(kKv8MaxPages * 4));
   W4A8_CUDA_TRY(launch_pdl(k_kv8_pick, dim3((unsigned)c->n_kv_heads, (unsigned)(c->n_seqs * n)), dim3(512), smem, st, *c,
                            a->counts, n, top_k, (const uint32_t*)keys, pages_out));
   return W4A8_OK;
@@ -294,7 +294,7 @@ W4A8_API w4a8_status w4a8_kv8_evict(const w4a8_kv8_cache* c, const float* mass, 
   if (!mass || !table_out || !mass_out || !len_out || keep < 0 || first_pages < 0 || last_pages < 0) return W4A8_ERR_ARG;
   cudaStream_t st = as_stream(stream);
   const bool own = len_out == c->len;
-  W4A8_CUDA_TRY(cudaFuncSetAttribute(k_kv8_evict, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8MaxPages * 12));
+  W4A8_CUDA_TRY(kv8_smem<k_kv8_evict>(kKv8MaxPages * 12));
   W4A8_CUDA_TRY(launch_pdl(k_kv8_evict, dim3((unsigned)c->n_kv_heads, (unsigned)c->n_seqs), dim3(512),
                            (size_t)c->max_pages * 12, st, *c, mass, keep, first_pages, last_pages, table_out, mass_out,
                            len_out, !own));

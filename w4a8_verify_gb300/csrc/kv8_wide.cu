@@ -1,0 +1,511 @@
+// Attention over the 8-bit cache for many query rows of a KV head (draft trees, prompt buckets): tcgen05.
+//
+// A segment is 128 query rows of one (sequence, KV head); its pages, end to end over the segments, are cut into equal
+// ranges, one for each CTA.  Per page, in a pipeline of warps:
+//   copy      one bulk copy brings the page's codes (16 KB at D = 128) into a ring of four;
+//   convert   codes become f16 whole numbers, keys [64 tokens][D] and values [D][64 tokens], in the 128-byte-swizzled
+//             K-major layout of the tensor core's B operand.  A 16-byte group of the page's byte order is two 16-byte
+//             chunks of two rows of either tile: one load, eight byte permutes, eight subtractions, two stores;
+//   products  S = Q C_K^T and O' = P C_V^T, tcgen05.mma with A (Q, P) in tensor memory, 128 x 64 x D and 128 x D x 64;
+//   softmax   a thread holds one query row: no exchange between lanes.  P (scaled by 2^7) returns to tensor memory in the
+//             token order of the values' chunks.  The row's maximum moves only when a logit passes it by 8 (log2);
+//   values    O = O c + s_V O' in registers, a thread half a row: the page's scale needs no common factor with the
+//             other pages', and nothing is rescaled in tensor memory.
+// fp32 calls split Q and P into f16 hi + lo and add both products into the same accumulator; qh is the nearest whole
+// number at a largest magnitude of 2^11, so its sums with the codes are exact, as in the split kernel.
+// Why tcgen05 here: the split kernel converts a page once for every eight columns, and mma.sync tops out at a quarter
+// of the dense rate; with 128 rows a page is 2 x 256 cycles of tensor core against 700 of memory traffic.
+#include "kv8_attn.cuh"
+
+namespace w4a8 {
+namespace {
+
+// Warp roles.  Softmax and value warps sit where their number modulo 4 names the tensor-memory lanes they may touch.
+constexpr int kSoftWarps = 4, kSumWarps = 8, kConvWarps = 4;
+constexpr int kSum0 = kSoftWarps, kConv0 = kSum0 + kSumWarps, kMmaWarp = kConv0 + kConvWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kWideThreads = 32 * (kCopyWarp + 1);
+constexpr int kRing = 4;   // pages of codes
+constexpr int kFac = 4;    // rounds of row factors between the softmax and the value warps
+
+template <typename T, int D>
+struct Wide {
+  static constexpr int NQ = sizeof(T) == 4 ? 2 : 1;         // f16 terms of Q and P
+  static constexpr int NO = sizeof(T) == 4 ? 1 : 2;         // buffers of O'
+  static constexpr int PAGE = 2 * kPage * D, TILE = kPage * D * 2;  // bytes of a page of codes, of an f16 tile
+  // tensor memory columns
+  static constexpr int cQ = 0, cS = cQ + NQ * D / 2, cP = cS + 2 * kPage, cO = cP + 2 * NQ * kPage / 2;
+  static_assert(cO + NO * D <= 512, "tensor memory");
+  // shared memory
+  static constexpr int sK = kRing * PAGE, sV = sK + 2 * TILE, sBar = sV + 2 * TILE, sFac = sBar + 256;
+  static constexpr int sPrefix = sFac + kFac * kWideRows * 4 + 64;
+};
+
+struct Bars {  // mbarriers
+  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2];
+};
+static_assert(sizeof(Bars) + 4 <= 256, "barriers");
+
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// D[128][N] (+)= A (tensor memory) B (shared memory), one k-step of 16
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// f16 x f16 -> f32, both operands K-major, M = 128
+__host__ __device__ constexpr uint32_t tc_idesc(int N) { return 1u << 4 | (uint32_t)(N / 8) << 17 | (128u / 16) << 24; }
+// K-major rows of 128 bytes, 128-byte swizzle, eight rows 1024 bytes apart
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+  return (uint64_t)(addr >> 4 & 0x3fffu) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+#define W4A8_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define W4A8_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+// 32 columns of the warp's 32 lanes
+__device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;\n"
+      : W4A8_R8(v, 0), W4A8_R8(v, 8), W4A8_R8(v, 16), W4A8_R8(v, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_load16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
+      : W4A8_R8(v, 0), W4A8_R8(v, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::W4A8_I8(
+                   v, 0),
+               W4A8_I8(v, 8), "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A position in a ring of mbarriers: entry and phase parity.
+template <int N>
+struct Turn {
+  int i = 0, ph = 0;
+  __device__ void next() {
+    if (++i == N) i = 0, ph ^= 1;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+  using C = Wide<T, D>;
+  constexpr int NQ = C::NQ, NO = C::NO;
+  constexpr unsigned FULL = 0xffffffffu;
+  extern __shared__ __align__(16) uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);  // swizzle atoms start at multiples of 1024
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::sBar + sizeof(Bars));
+  Bars& bar = *reinterpret_cast<Bars*>(sm + C::sBar);
+  float* fac = reinterpret_cast<float*>(sm + C::sFac);          // [kFac][rows] factor of the old values
+  int* moved = reinterpret_cast<int*>(fac + kFac * kWideRows);  // [kFac][softmax warp] whether one is not 1
+  int* prefix = reinterpret_cast<int*>(sm + C::sPrefix);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int S = c.n_seqs;
+
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&bar.code_full[i], 1), mbar_init(&bar.code_empty[i], kConvWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], kConvWarps), mbar_init(&bar.v_full[i], kConvWarps);
+      mbar_init(&bar.s_done[i], 1), mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&bar.s_empty[i], kSoftWarps), mbar_init(&bar.p_full[i], kSoftWarps);
+      mbar_init(&bar.o_empty[i], kSumWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  }
+  griddep_enter();
+  kv8_prefix(c, a, geo, prefix);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (blockIdx.x == 0)
+    for (int s = tid; s <= S; s += kWideThreads) ws.prefix[s] = prefix[s];
+  const uint32_t tmem = s_tmem;
+  const int U = prefix[S];
+  const Kv8Workers wk = kv8_workers(U, geo.ctas, 1);
+  const int worker = blockIdx.x;
+  const bool has = worker < wk.W;
+  const int u0 = has ? worker_begin(worker, wk.W, U) : 0, u1 = has ? worker_begin(worker + 1, wk.W, U) : 0;
+
+  // every role walks the range in the same way: runs of pages of one segment
+  struct Run {
+    int seg, first, pages;  // segment, its first page here, how many
+    bool ends;              // whether the range goes on behind the run
+    size_t pair;
+    Kv8Segment sg;
+    int cnt;
+  };
+  auto run_at = [&](int x) {
+    Run r;
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    r.cnt = a.counts ? a.counts[lo] : a.n;
+    const int per = c.len[lo] / kPage, q = (x - prefix[lo]) / per;
+    r.first = (x - prefix[lo]) % per;
+    r.seg = lo * c.n_kv_heads * geo.CB + q;
+    r.pages = min(per - r.first, u1 - x);
+    r.ends = x + r.pages < u1;
+    r.sg = kv8_segment(c, a, geo, r.seg);
+    r.pair = kv8_pair(c, r.sg.s, r.sg.h);
+    return r;
+  };
+  // physical page of page p of a run, or -1: read as an empty page
+  auto phys_of = [&](const Run& r, int p) {
+    const int v = c.table[r.pair * c.max_pages + p];
+    return v >= 0 && v < c.max_pages ? v : -1;
+  };
+  bool ok = true;
+  auto wait = [&](uint64_t* b, int parity) {
+    ok = ok && __all_sync(FULL, mbar_wait(b, (unsigned)parity));
+    return ok;
+  };
+
+  if (warp == kCopyWarp) {
+    Turn<kRing> e;
+    int n = 0;
+    for (int x = u0; x < u1 && ok;) {
+      const Run r = run_at(x);
+      for (int p = 0; p < r.pages && ok; ++p, ++n, e.next()) {
+        if (n >= kRing && !wait(&bar.code_empty[e.i], e.ph ^ 1)) break;
+        int phys = phys_of(r, r.first + p);
+        if (phys < 0) {
+          if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TREE);
+          phys = 0;
+        }
+        if (lane == 0) {
+          mbar_expect_tx(&bar.code_full[e.i], C::PAGE);
+          bulk_g2s(sm + e.i * C::PAGE, c.codes + kv8_page(c, r.pair, phys) * C::PAGE, C::PAGE, &bar.code_full[e.i]);
+        }
+        __syncwarp();
+      }
+      x += r.pages;
+    }
+    // no copy in flight when the CTA ends
+    for (int i = max(0, n - kRing); i < n; ++i) (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
+  } else if (warp >= kConv0 && warp < kMmaWarp) {
+    const int ct = tid - kConv0 * 32;  // 0..127
+    Turn<kRing> e;
+    Turn<2> b;
+    for (int i = 0; i < u1 - u0 && ok; ++i, e.next(), b.next()) {
+      if (!wait(&bar.code_full[e.i], e.ph)) break;
+      const uint8_t* pg = sm + e.i * C::PAGE;
+#pragma unroll 1
+      for (int v = 0; v < 2 && ok; ++v) {
+        // the tile's last readers: the products of two pages ago
+        if (i >= 2 && !wait(v ? &bar.pv_done[b.i] : &bar.s_done[b.i], b.ph ^ 1)) break;
+        uint8_t* tile = sm + (v ? C::sV : C::sK) + b.i * C::TILE;
+        const uint8_t* from = pg + v * kPage * D;
+        constexpr int kChunks = D / 32;  // keys: 32-dim chunks of a 16-token tile; values: two 32-token chunks of a 16-dim tile
+#pragma unroll
+        for (int k = 0; k < kPage * D / 16 / 128; ++k) {
+          const int gi = k * 128 + ct, t = gi & 3, g = (gi >> 2) & 7;
+          int q = gi >> 5;
+          // neighbouring rows of a store phase take the other half of a row's 128 bytes: no bank conflict
+          q ^= g & 1;
+          const uint4 w = *reinterpret_cast<const uint4*>(from + (q * 32 + (gi & 31)) * 16);
+          const int tile16 = v ? q >> 1 : q / kChunks, chunk = (v ? q & 1 : q % kChunks) * 4 + t, row = tile16 * 16 + g;
+          uint4 lo, hi;
+          codes_f16<true>(w.x, lo.x, lo.y);
+          codes_f16<true>(w.z, lo.z, lo.w);
+          codes_f16<true>(w.y, hi.x, hi.y);
+          codes_f16<true>(w.w, hi.z, hi.w);
+          // keys of D = 128 are two tiles of 64 dims
+          uint8_t* to = tile + (v ? 0 : (chunk >> 3) * (kPage * 128)) + row * 128 + (((chunk & 7) ^ g) << 4);
+          *reinterpret_cast<uint4*>(to) = lo;
+          *reinterpret_cast<uint4*>(to + 8 * 128) = hi;
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v ? &bar.v_full[b.i] : &bar.k_full[b.i]);
+      }
+      if (lane == 0) mbar_arrive(&bar.code_empty[e.i]);
+    }
+  } else if (warp == kMmaWarp) {
+    Turn<2> b, pb;
+    Turn<NO> ob;
+    int n = 0;  // pages whose S is issued
+    auto values = [&](int i) {  // O' of page i (the one before the newest S)
+      if (!wait(&bar.p_full[pb.i], pb.ph) || !wait(&bar.v_full[pb.i], pb.ph)) return;
+      if (i >= NO && !wait(&bar.o_empty[ob.i], ob.ph ^ 1)) return;
+      tc_after();
+      if (lane == 0) {
+        const uint32_t v = smem_u32(sm + C::sV + pb.i * C::TILE);
+        for (int x = 0; x < NQ; ++x)
+          for (int k = 0; k < kPage / 16; ++k)
+            tc_mma(tmem + C::cO + ob.i * D, tmem + C::cP + (pb.i * NQ + x) * (kPage / 2) + k * 8, tc_desc(v + k * 32), tc_idesc(D),
+                   x + k > 0);
+        tc_commit(&bar.pv_done[pb.i]);
+      }
+      __syncwarp();
+      pb.next();
+      ob.next();
+    };
+    for (int x = u0; x < u1 && ok;) {
+      const Run r = run_at(x);
+      for (int p = 0; p < r.pages && ok; ++p, ++n, b.next()) {
+        // the softmax warps wait for a run's last products before they bring the next run's Q, and release s_empty
+        // of both buffers when it is there
+        if (!wait(&bar.k_full[b.i], b.ph) || !wait(&bar.s_empty[b.i], b.ph)) break;
+        tc_after();
+        if (lane == 0) {
+          const uint32_t k0 = smem_u32(sm + C::sK + b.i * C::TILE);
+          for (int x2 = 0; x2 < NQ; ++x2)
+            for (int k = 0; k < D / 16; ++k)
+              tc_mma(tmem + C::cS + b.i * kPage, tmem + C::cQ + x2 * (D / 2) + k * 8,
+                     tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32), tc_idesc(kPage), x2 + k > 0);
+          tc_commit(&bar.s_done[b.i]);
+        }
+        __syncwarp();
+        if (p > 0) values(n - 1);
+      }
+      if (ok && r.pages > 0) values(n - 1);
+      x += r.pages;
+    }
+  } else if (warp < kSoftWarps) {
+    const int row = tid;  // 0..127
+    const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
+    Turn<2> b;
+    Turn<kFac> fb;
+    int n = 0, freed = 0;  // pages done; S buffers released to the products (page n needs n + 1 of them)
+    const double lscale = (double)a.scale * 1.4426950408889634;
+    const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
+    for (int x = u0; x < u1 && ok;) {
+      const Run r = run_at(x);
+      const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      // Q of the run: the products of the run before are done (its last O' was waited for)
+      float colfac, collow, m = -INFINITY, l = 0.0f;
+      {
+        const int rr = r.sg.cb * kWideRows + row;
+        const T* q = static_cast<const T*>(a.q.data) + r.sg.s * a.q.seq + (rr / geo.G) * a.q.row +
+                     (r.sg.h * geo.G + rr % geo.G) * a.q.head;
+        float am = 0.0f;
+        auto load8 = [&](int d, float (&v)[8]) {
+          if (row >= rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+          } else if (geo.vec) {
+            uint4 w[sizeof(T) / 2];
+#pragma unroll
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e) w[e] = reinterpret_cast<const uint4*>(q + d)[e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = kv8_load(reinterpret_cast<const T*>(w) + e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = kv8_load(q + d + e);
+          }
+        };
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          float v[8];
+          load8(d, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) am = max_nan(am, fabsf(v[e]));
+        }
+        const float up = f16_scale(am), down = 1.0f / up;
+        colfac = lhi * down;
+        collow = llo * down;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float v[8];
+            load8(d + 8 * y, v);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float f0 = v[e] * up, f1 = v[e + 1] * up;
+              if (NQ == 2) {
+                hi[4 * y + e / 2] = pack_f16(rintf(f0), rintf(f1));
+                lo[4 * y + e / 2] = pack_f16(f0 - rintf(f0), f1 - rintf(f1));
+              } else {
+                hi[4 * y + e / 2] = pack_f16(f0, f1);
+              }
+            }
+          }
+          tc_store16(mine + C::cQ + d / 2, hi);
+          if (NQ == 2) tc_store16(mine + C::cQ + D / 2 + d / 2, lo);
+        }
+        tc_store_wait();
+      }
+      tc_before();
+      __syncwarp();
+      for (int y = 0; y < 2 && freed < n + r.pages; ++y, ++freed)
+        if (lane == 0) mbar_arrive(&bar.s_empty[freed & 1]);
+      for (int p = 0; p < r.pages && ok; ++p, ++n, b.next(), fb.next()) {
+        const int phys = phys_of(r, r.first + p);
+        const float sk = phys < 0 ? 0.0f : c.scales[kv8_page(c, r.pair, phys) * 2];
+        const float fh = colfac * sk, fl = fmaf(colfac, sk, -fh) + collow * sk;
+        if (!wait(&bar.s_done[b.i], b.ph)) break;
+        tc_after();
+        const uint32_t sa = mine + C::cS + b.i * kPage;
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[32];
+          tc_load32(sa + 32 * y, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]) * fh);
+        }
+        float f = 1.0f;
+        if (phys >= 0 && mx > m + kPSlack) {
+          f = ex2(m - mx);
+          m = mx;
+          l *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        // P's last readers; and the value warps are past page n - 4, whose row factors these replace
+        if (n >= 2 && !wait(&bar.pv_done[b.i], b.ph ^ 1)) break;
+        fac[fb.i * kWideRows + row] = f;
+        const bool any = __any_sync(FULL, f != 1.0f);
+        if (lane == 0) moved[fb.i * kSoftWarps + warp] = any;
+        float ps = 0.0f;
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[32], hi[16], lo[16];
+          tc_load32(sa + 32 * y, v);
+          // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
+#pragma unroll
+          for (int z = 0; z < 16; ++z) {
+            const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
+            float e[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float s = __uint_as_float(v[tok + w]);
+              e[w] = NQ == 2 ? ex2(fmaf(s, fl, fmaf(s, fh, -base))) * kPScale : ex2(fmaf(s, fh, 7.0f - base));
+              if (phys < 0) e[w] = 0.0f;
+              ps += e[w];
+            }
+            hi[z] = pack_f16(e[0], e[1]);
+            if (NQ == 2) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[z]));
+              lo[z] = pack_f16(e[0] - h.x, e[1] - h.y);
+            }
+          }
+          tc_store16(mine + C::cP + b.i * NQ * (kPage / 2) + 16 * y, hi);
+          if (NQ == 2) tc_store16(mine + C::cP + (b.i * NQ + 1) * (kPage / 2) + 16 * y, lo);
+        }
+        l += ps;
+        tc_store_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.p_full[b.i]);
+          if (freed < n + r.pages - p) mbar_arrive(&bar.s_empty[b.i]);
+        }
+        if (freed < n + r.pages - p) ++freed;
+        if (ws.page && row < rows)
+          ws.page[((size_t)r.seg * c.max_pages + r.first + p) * kWideRows + row] =
+              make_float2(m == -INFINITY ? 0.0f : m, ps / kPScale);
+      }
+      // the run's last products are done before the next run's Q takes the place of this one
+      if (!ok || !wait(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
+      tc_after();
+      if (row < rows) {
+        const size_t at = r.ends ? (size_t)geo.ctas + geo.segments + r.seg : (size_t)blockIdx.x + r.seg;
+        ws.ml[at * kWideRows + row] = make_float2(m, l / kPScale);
+      }
+      x += r.pages;
+    }
+  } else {
+    // values: quadrant of lanes, half of the columns
+    const int quad = warp & 3, half = (warp - kSum0) >> 2, row = quad * 32 + lane;
+    constexpr int DH = D / 2;
+    const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + C::cO + half * DH;
+    Turn<2> b;
+    Turn<NO> ob;
+    Turn<kFac> fb;
+    for (int x = u0; x < u1 && ok;) {
+      const Run r = run_at(x);
+      const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      float O[DH];
+#pragma unroll
+      for (int d = 0; d < DH; ++d) O[d] = 0.0f;
+      for (int p = 0; p < r.pages && ok; ++p, b.next(), ob.next(), fb.next()) {
+        const int phys = phys_of(r, r.first + p);
+        const float sv = phys < 0 ? 0.0f : c.scales[kv8_page(c, r.pair, phys) * 2 + 1];
+        if (!wait(&bar.p_full[b.i], b.ph) || !wait(&bar.pv_done[b.i], b.ph)) break;
+        tc_after();
+        if (moved[fb.i * kSoftWarps + quad]) {
+          const float f = fac[fb.i * kWideRows + row];
+#pragma unroll
+          for (int d = 0; d < DH; ++d) O[d] *= f;
+        }
+#pragma unroll
+        for (int d = 0; d < DH; d += 16) {
+          uint32_t v[16];
+          tc_load16(mine + ob.i * D + d, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) O[d + e] = fmaf(__uint_as_float(v[e]), sv, O[d + e]);
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.o_empty[ob.i]);
+      }
+      if (ok && row < rows) {
+        const size_t at = r.ends ? (size_t)geo.ctas + geo.segments + r.seg : (size_t)blockIdx.x + r.seg;
+        float4* o = reinterpret_cast<float4*>(ws.o + (at * kWideRows + row) * D + half * DH);
+#pragma unroll
+        for (int d = 0; d < DH; d += 4)
+          o[d / 4] = make_float4(O[d] / kPScale, O[d + 1] / kPScale, O[d + 2] / kPScale, O[d + 3] / kPScale);
+      }
+      x += r.pages;
+    }
+  }
+  if (!ok && lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// The fp32 rows of wide calls: a warp a part.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+  griddep_enter();
+  __shared__ __align__(16) float row_p[4][kRowChunk][kRowTile];
+  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
+  const int x = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (x < geo.segments * geo.tiles * chunks)
+    kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[threadIdx.x >> 5]);
+}
+
+template <typename T, int D>
+cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
+  using C = Wide<T, D>;
+  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
+  const int64_t parts = (int64_t)geo.segments * geo.tiles * chunks;
+  cudaError_t e = launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)((parts + 3) / 4)), dim3(128), 0, st, c, a, geo, ws);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 1024 + C::sPrefix + 4 * ((size_t)c.n_seqs + 1);
+  e = kv8_smem<k_kv8_wide<T, D>>(1024 + C::sPrefix + 4 * (kKv8MaxSeqs + 1));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
+}
+
+}  // namespace
+
+cudaError_t kv8_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
+  if (a.dtype == W4A8_F32) return c.head_dim == 64 ? wide_run<float, 64>(c, a, geo, ws, st) : wide_run<float, 128>(c, a, geo, ws, st);
+  return c.head_dim == 64 ? wide_run<__nv_bfloat16, 64>(c, a, geo, ws, st) : wide_run<__nv_bfloat16, 128>(c, a, geo, ws, st);
+}
+
+}  // namespace w4a8
