@@ -8,9 +8,9 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
+import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libw4a8.so")
@@ -336,29 +336,18 @@ def w4a8_matmul(a_q, a_s, w_t, s_t, N, y=None, workspace=None, stream=None):
 
 # ------------------------------------------------------------- key/value cache in 8 bits
 
-def _on_stream(fn):
-    """A method whose ``stream`` argument makes it run (and allocate) with that stream as the current one."""
-    @functools.wraps(fn)
-    def call(self, *args, stream=None, **kw):
-        if stream is None:
-            return fn(self, *args, **kw)
-        if stream.device != self.device:
-            raise ValueError("KV8Cache: the stream is on another device than the cache")
-        with self._torch.cuda.stream(stream):
-            return fn(self, *args, **kw)
-    return call
-
-
 class KV8Cache:
     """One layer of ``n_seqs`` sequences' keys and values in 8 bits (w4a8_kv8_cache).
 
     Holds the cache's tensors, by name in ``tensors`` (``codes``, ``scales``, ``sums``, ``tail``, ``table``,
     ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
     fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
-    stream; device state that is out of range is reported by ``check``.
+    stream of the cache's device, or on ``stream`` (outputs and workspaces are then allocated on it); device state
+    that is out of range is reported by ``check``.
 
-    A decode step is a few microseconds on the device, so the calls marshal their arguments as packed bytes
-    (w4a8_kv8_attn, w4a8_rows) and keep no more than the workspace sizes of the shapes seen.
+    A decode step is about ten microseconds on the device, so the calls are written out: arguments are marshalled as
+    packed bytes (w4a8_kv8_attn, w4a8_rows); the workspace sizes of the shapes seen and one workspace for each
+    stream are kept.
     """
 
     _NAMES = (("codes", "uint8"), ("scales", "float32"), ("sums", "int16"), ("tail", "float32"), ("table", "int32"),
@@ -379,8 +368,9 @@ class KV8Cache:
         shapes = ((S, H, P, 2, 64 * D), (S, H, P, 2), (S, H, P, D), (S, H, 2, 64, D), (S, H, P), (S,), (1,))
         self.tensors = {}
         for (name, dtype), shape, size in zip(self._NAMES, shapes, need):
-            t = torch.empty(shape, dtype=getattr(torch, dtype), device=device) if tensors is None else tensors[name]
-            if t.dtype != getattr(torch, dtype) or t.numel() * t.element_size() != size or not t.is_contiguous():
+            dtype = getattr(torch, dtype)
+            t = torch.empty(shape, dtype=dtype, device=device) if tensors is None else tensors[name]
+            if t.dtype != dtype or t.numel() * t.element_size() != size or not t.is_contiguous():
                 raise ValueError("KV8Cache: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
             self.tensors[name] = t
             setattr(self.desc, name, t.data_ptr())
@@ -389,7 +379,9 @@ class KV8Cache:
             raise ValueError("KV8Cache: the tensors must be on one CUDA device")
         self._dev = self.device.index
         self._ref = _c.byref(self.desc)
-        self._sizes = {}
+        self._sizes, self._kept, self._lock = {}, {}, threading.Lock()
+        self._attention, self._select, self._evict = lib().w4a8_kv8_attention, lib().w4a8_kv8_select, lib().w4a8_kv8_evict
+        self._append, self._read = lib().w4a8_kv8_append, lib().w4a8_kv8_read
         if tensors is None:
             self.reset()
 
@@ -397,58 +389,82 @@ class KV8Cache:
     def len(self):
         return self.tensors["len"]
 
-    def _run(self, name, *args):
-        """Calls the entry point with its last argument, the current stream of the cache's device."""
+    def _elsewhere(self, stream, method, args):
+        """The call with ``stream`` as the current one."""
+        if stream.device != self.device:
+            raise ValueError("KV8Cache: the stream is on another device than the cache")
+        with self._torch.cuda.stream(stream):
+            return method(*args)
+
+    def _run(self, fn, *args):
+        """Calls fn(cache, *args, the current stream of the cache's device)."""
         torch = self._torch
-        st = torch._C._cuda_getCurrentRawStream(self._dev)
-        fn = getattr(_lib, name)
         if torch.cuda.current_device() == self._dev:
-            status = fn(self._ref, *args, st)
+            status = fn(self._ref, *args, torch._C._cuda_getCurrentRawStream(self._dev))
         else:
-            with torch.cuda.device(self.device):
-                status = fn(self._ref, *args, st)
+            with torch.cuda.device(self._dev):
+                status = fn(self._ref, *args, torch._C._cuda_getCurrentRawStream(self._dev))
         if status:
-            raise W4A8Error(name, status)
+            raise W4A8Error(fn.__name__, status)
 
     def _vec(self, t, name, dtype, shape):
-        """Pointer of an optional contiguous tensor of this device, type and shape."""
-        if t is None:
-            return 0
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._dev:
+        """Pointer of a contiguous tensor of this device, type and shape."""
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._dev or not t.is_contiguous():
             raise ValueError("KV8Cache: %s must be a contiguous %s tensor %s on the cache's device"
                              % (name, str(dtype)[6:], list(shape)))
         return t.data_ptr()
 
-    def _rows(self, t, name, dtype, n, heads):
-        """The fields of a w4a8_rows for t [n_seqs][n][heads][head_dim]."""
-        S, _, D, _ = self.shape
-        if t.shape != (S, n, heads, D):
-            raise ValueError("KV8Cache: %s must be [%d][%d][%d][%d], not %s" % (name, S, n, heads, D, list(t.shape)))
-        if t.dtype is not dtype or dtype not in self._types:
-            raise ValueError("KV8Cache: %s has type %s; fp32 or bf16, the same for all rows" % (name, t.dtype))
-        a, b, c, d = t.stride()
-        if d != 1 or t.get_device() != self._dev:
-            raise ValueError("KV8Cache: %s must have unit stride in its last dimension, on the cache's device" % name)
+    def _rows(self, t, name, dtype, shape):
+        """The fields of a w4a8_rows for t of that shape, [n_seqs][n][heads][head_dim]."""
+        a, b, c, d = t.stride() if t.shape == shape else (0, 0, 0, 0)
+        if d != 1 or t.dtype is not dtype or t.get_device() != self._dev:
+            raise ValueError("KV8Cache: %s must be %s %s with unit stride in the last dimension, on the cache's device"
+                             % (name, str(dtype)[6:], list(shape)))
         return t.data_ptr(), a, b, c
 
-    def _scratch(self, fn, key, args, workspace):
-        """(pointer, bytes, tensor) of a call's workspace: the given one, or a new one of the size fn asks for."""
-        if workspace is None:
-            need = self._sizes.get(key)
-            if need is None:
-                n = _sz()
-                _call(fn, self._ref, args, _c.byref(n))
-                need = self._sizes[key] = n.value
-            workspace = self._torch.empty(need, dtype=self._torch.uint8, device=self.device)
-            return workspace.data_ptr(), need, workspace
-        if workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    def _query(self, q):
+        """(fields, type number, n, heads) of a tensor of query rows."""
+        S, _, D, _ = self.shape
+        shape, dtype = q.shape, q.dtype
+        kind = self._types.get(dtype)
+        if kind is None or len(shape) != 4 or shape[0] != S or shape[3] != D:
+            raise ValueError("KV8Cache: q must be fp32 or bf16 [%d][n][heads][%d], not %s %s"
+                             % (S, D, str(dtype)[6:], list(shape)))
+        return self._rows(q, "q", dtype, shape), kind, shape[1], shape[2]
 
-    @_on_stream
-    def reset(self):
+    def _launch(self, fn, size_fn, key, args, workspace, *more):
+        """fn(cache, args, *more, workspace, its bytes, stream).  Without a workspace of the caller's: the one that the
+        cache keeps for the current stream (calls on one stream run in order; the lock keeps the launches of two
+        threads' calls apart), or a new one where that does not hold or would stay large: in a capture, whose graph may
+        be replayed beside other work, with another device current, above 32 MB."""
+        torch = self._torch
+        if workspace is not None:
+            if workspace.device != self.device or not workspace.is_contiguous():
+                raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
+            return self._run(fn, args, *more, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        need = self._sizes.get(key)
+        if need is None:
+            n = _sz()
+            _call(size_fn, self._ref, args, _c.byref(n))
+            need = self._sizes[key] = n.value
+        if need > 32 << 20 or torch.cuda.current_device() != self._dev or torch._C._cuda_isCurrentStreamCapturing():
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            return self._run(fn, args, *more, workspace.data_ptr(), need)
+        stream = torch._C._cuda_getCurrentRawStream(self._dev)
+        with self._lock:
+            ptr, size, _ = self._kept.get(stream, (0, -1, None))
+            if size < need:
+                t = torch.empty(need, dtype=torch.uint8, device=self.device)
+                ptr, size, _ = self._kept[stream] = (t.data_ptr(), need, t)
+            status = fn(self._ref, args, *more, ptr, size, stream)
+        if status:
+            raise W4A8Error(fn.__name__, status)
+
+    def reset(self, stream=None):
         """Empties the cache (w4a8_kv8_reset)."""
-        self._run("w4a8_kv8_reset")
+        if stream is not None:
+            return self._elsewhere(stream, self.reset, ())
+        self._run(lib().w4a8_kv8_reset)
 
     def check(self):
         """The status word (0 = every call's device state was in range); synchronous."""
@@ -458,100 +474,107 @@ class KV8Cache:
             raise W4A8Error("w4a8_kv8_check", st)
         return f.value
 
-    @_on_stream
-    def append(self, k, v, counts=None, index=None, len_out=None):
+    def append(self, k, v, counts=None, index=None, len_out=None, stream=None):
         """Commits rows of k and v, advancing the cache's lengths, or storing the new ones in ``len_out`` instead
         (w4a8_kv8_append).  ``index`` [n_seqs][n]: the source row of each new position."""
-        S, H = self.shape[:2]
-        shape = k.shape
-        n_src = shape[1] if len(shape) == 4 else 0
+        if stream is not None:
+            return self._elsewhere(stream, self.append, (k, v, counts, index, len_out))
+        S, H, D, _ = self.shape
         dtype, i32 = k.dtype, self._torch.int32
-        kr = self._ROWS.pack(*self._rows(k, "k", dtype, n_src, H))
-        vr = self._ROWS.pack(*self._rows(v, "v", dtype, n_src, H))
+        kind = self._types.get(dtype)
+        if kind is None or k.dim() != 4:
+            raise ValueError("KV8Cache: k must be fp32 or bf16 [n_seqs][n][n_kv_heads][head_dim]")
+        n_src = k.shape[1]
+        shape = (S, n_src, H, D)
+        kr = self._ROWS.pack(*self._rows(k, "k", dtype, shape))
+        vr = self._ROWS.pack(*self._rows(v, "v", dtype, shape))
         n = n_src if index is None else index.shape[1]
-        out = self.desc.len if len_out is None else self._vec(len_out, "len_out", i32, (S,))
-        self._run("w4a8_kv8_append", kr, vr, self._types[dtype], n_src, n, self._vec(counts, "counts", i32, (S,)),
-                  0 if index is None else self._vec(index, "index", i32, (S, n)), out)
+        self._run(self._append, kr, vr, kind, n_src, n, 0 if counts is None else self._vec(counts, "counts", i32, (S,)),
+                  0 if index is None else self._vec(index, "index", i32, (S, n)),
+                  self.desc.len if len_out is None else self._vec(len_out, "len_out", i32, (S,)))
 
-    @_on_stream
-    def read(self, first, n, length=None):
+    def read(self, first, n, length=None, stream=None):
         """fp32 keys and values [n_seqs][n][n_kv_heads][head_dim] of positions first[s].. as held (w4a8_kv8_read)."""
+        if stream is not None:
+            return self._elsewhere(stream, self.read, (first, n, length))
         torch = self._torch
         S, H, D, _ = self.shape
         k = torch.empty((S, n, H, D), dtype=torch.float32, device=self.device)
-        v = torch.empty((S, n, H, D), dtype=torch.float32, device=self.device)
-        self._run("w4a8_kv8_read", self._vec(first, "first", torch.int32, (S,)),
-                  self._vec(length, "length", torch.int32, (S,)), n, k.data_ptr(), v.data_ptr())
+        v = torch.empty_like(k)
+        self._run(self._read, self._vec(first, "first", torch.int32, (S,)),
+                  0 if length is None else self._vec(length, "length", torch.int32, (S,)), n, k.data_ptr(), v.data_ptr())
         return k, v
 
-    @_on_stream
     def attention(self, q, k=None, v=None, scale=1.0, counts=None, mask=None, pages=None, mass=None, mass_out=None,
-                  out=None, workspace=None):
+                  out=None, workspace=None, stream=None):
         """Attention of q's rows over the cache and the new rows k, v (w4a8_kv8_attention); returns ``out``."""
+        if stream is not None:
+            return self._elsewhere(stream, self.attention,
+                                   (q, k, v, scale, counts, mask, pages, mass, mass_out, out, workspace))
         torch = self._torch
-        S, H, _, P = self.shape
-        shape, dtype = q.shape, q.dtype
-        if len(shape) != 4:
-            raise ValueError("KV8Cache: q must be [n_seqs][n][heads][head_dim]")
-        n, heads = shape[1], shape[2]
-        qr = self._rows(q, "q", dtype, n, heads)
-        if (k is None) != (v is None):
+        S, H, D, P = self.shape
+        qr, kind, n, heads = self._query(q)
+        dtype = q.dtype
+        if k is None and v is None:
+            kr = vr = self._NONE
+        elif k is None or v is None:
             raise ValueError("KV8Cache: k and v come together")
-        kr = self._NONE if k is None else self._rows(k, "k", dtype, n, H)
-        vr = self._NONE if v is None else self._rows(v, "v", dtype, n, H)
+        else:
+            kr, vr = self._rows(k, "k", dtype, (S, n, H, D)), self._rows(v, "v", dtype, (S, n, H, D))
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
-        outr = self._rows(out, "out", dtype, n, heads)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            outr = (out.data_ptr(), n * heads * D, heads * D, D)
+        else:
+            outr = self._rows(out, "out", dtype, (S, n, heads, D))
         top_k = pp = mi = mo = 0
         if pages is not None:
             top_k = pages.shape[-1]
             pp = self._vec(pages, "pages", torch.int32, (S, n, H, top_k))
         if mass_out is not None:
-            mi = self._vec(mass, "mass", torch.float32, (S, H, P))
+            mi = 0 if mass is None else self._vec(mass, "mass", torch.float32, (S, H, P))
             mo = self._vec(mass_out, "mass_out", torch.float32, (S, H, P))
         elif mass is not None:
             raise ValueError("KV8Cache: mass needs mass_out")
-        a = self._ATTN.pack(n, heads, self._types[dtype], scale, *qr, *outr, *kr, *vr,
+        a = self._ATTN.pack(n, heads, kind, scale, *qr, *outr, *kr, *vr,
                             0 if counts is None else self._vec(counts, "counts", torch.int32, (S,)),
                             0 if mask is None else self._vec(mask, "mask", torch.int64, (S, n)), pp, top_k, mi, mo)
-        ws, size, workspace = self._scratch("w4a8_kv8_attention_workspace_bytes",
-                                            (n, heads, dtype, k is None, pages is None, top_k, mo == 0), a, workspace)
-        self._run("w4a8_kv8_attention", a, ws, size)
+        self._launch(self._attention, "w4a8_kv8_attention_workspace_bytes",
+                     (n, heads, kind, k is None, pages is None, top_k, mo == 0), a, workspace)
         return out
 
-    @_on_stream
-    def select(self, q, top_k, first_pages=0, last_pages=0, counts=None, out=None, workspace=None):
+    def select(self, q, top_k, first_pages=0, last_pages=0, counts=None, out=None, workspace=None, stream=None):
         """The whole pages of best score for every row and KV head, int32 [n_seqs][n][n_kv_heads][top_k], ascending,
         -1 behind the last (w4a8_kv8_select)."""
+        if stream is not None:
+            return self._elsewhere(stream, self.select, (q, top_k, first_pages, last_pages, counts, out, workspace))
         torch = self._torch
         S, H = self.shape[:2]
-        shape, dtype = q.shape, q.dtype
-        if len(shape) != 4:
-            raise ValueError("KV8Cache: q must be [n_seqs][n][heads][head_dim]")
-        n, heads = shape[1], shape[2]
-        qr = self._rows(q, "q", dtype, n, heads)
+        qr, kind, n, heads = self._query(q)
         if out is None:
             out = torch.empty((S, n, H, top_k), dtype=torch.int32, device=self.device)
-        po = self._vec(out, "out", torch.int32, (S, n, H, top_k))
+            po = out.data_ptr()
+        else:
+            po = self._vec(out, "out", torch.int32, (S, n, H, top_k))
         none = self._NONE
-        a = self._ATTN.pack(n, heads, self._types[dtype], 1.0, *qr, *none, *none, *none,
+        a = self._ATTN.pack(n, heads, kind, 1.0, *qr, *none, *none, *none,
                             0 if counts is None else self._vec(counts, "counts", torch.int32, (S,)), 0, 0, 0, 0, 0)
-        ws, size, workspace = self._scratch("w4a8_kv8_select_workspace_bytes", (n, heads, dtype, top_k), a, workspace)
-        self._run("w4a8_kv8_select", a, top_k, first_pages, last_pages, po, ws, size)
+        self._launch(self._select, "w4a8_kv8_select_workspace_bytes", (n, heads, kind), a, workspace, top_k, first_pages,
+                     last_pages, po)
         return out
 
-    @_on_stream
-    def evict(self, mass, keep, first_pages=0, last_pages=0, in_place=False):
+    def evict(self, mass, keep, first_pages=0, last_pages=0, in_place=False, stream=None):
         """Keeps at most ``keep`` whole pages per KV head (w4a8_kv8_evict); returns (table, mass, len), new tensors,
         or the cache's own and ``mass`` itself when ``in_place``."""
+        if stream is not None:
+            return self._elsewhere(stream, self.evict, (mass, keep, first_pages, last_pages, in_place))
         torch = self._torch
         S, H, _, P = self.shape
         pm = self._vec(mass, "mass", torch.float32, (S, H, P))
-        old = (self.tensors["table"], mass, self.tensors["len"])
-        new = old if in_place else tuple(torch.empty_like(t) for t in old)
-        self._run("w4a8_kv8_evict", pm, keep, first_pages, last_pages, new[0].data_ptr(), new[1].data_ptr(),
-                  new[2].data_ptr())
-        return new
+        table, length = self.tensors["table"], self.tensors["len"]
+        if not in_place:
+            table, mass, length = torch.empty_like(table), torch.empty_like(mass), torch.empty_like(length)
+        self._run(self._evict, pm, keep, first_pages, last_pages, table.data_ptr(), mass.data_ptr(), length.data_ptr())
+        return table, mass, length
 
 
 # ------------------------------------------------------------------------ model/session

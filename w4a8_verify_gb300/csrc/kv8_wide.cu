@@ -11,8 +11,10 @@
 //             token order of the values' chunks.  The row's maximum moves only when a logit passes it by 8 (log2);
 //   values    O = O c + s_V O' in registers, a thread half a row: the page's scale needs no common factor with the
 //             other pages', and nothing is rescaled in tensor memory.
-// fp32 calls split Q and P into f16 hi + lo and add both products into the same accumulator; qh is the nearest whole
-// number at a largest magnitude of 2^11, so its sums with the codes are exact, as in the split kernel.
+// fp32 calls split Q and P into f16 hi + lo and add both products into the same accumulator.  The hi terms are the
+// nearest whole numbers at a largest magnitude of 2^11 (P <= 1 there: the maximum moves at once), so their sums with the
+// codes are whole numbers below 2^24, which the tensor core's truncating additions leave exact; with hi the nearest
+// f16 of P outputs were off by 1.8e-6 in the 2-norm at 4096 tokens, against 0.3e-6.
 // Why tcgen05 here: the split kernel converts a page once for every eight columns, and mma.sync tops out at a quarter
 // of the dense rate; with 128 rows a page is 2 x 256 cycles of tensor core against 700 of memory traffic.
 #include "kv8_attn.cuh"
@@ -32,8 +34,14 @@ struct Wide {
   static constexpr int NQ = sizeof(T) == 4 ? 2 : 1;         // f16 terms of Q and P
   static constexpr int NO = sizeof(T) == 4 ? 1 : 2;         // buffers of O'
   static constexpr int PAGE = 2 * kPage * D, TILE = kPage * D * 2;  // bytes of a page of codes, of an f16 tile
-  // tensor memory columns
-  static constexpr int cQ = 0, cS = cQ + NQ * D / 2, cP = cS + 2 * kPage, cO = cP + 2 * NQ * kPage / 2;
+  // scale of P, and how far (log2) a logit may pass its row's maximum before that moves
+  static constexpr float PSCALE = NQ == 2 ? 1024.0f : kPScale, SLACK = NQ == 2 ? 0.0f : kPSlack;
+  // buffers of P
+  static constexpr int NP = NQ == 2 ? 1 : 2;
+  // tensor memory columns: Q, S twice, the product with the lo term of Q (apart: a sum of whole numbers that
+  // fractions are added to is truncated each time), P, O'
+  static constexpr int cQ = 0, cS = cQ + NQ * D / 2, cL = cS + 2 * kPage, cP = cL + (NQ - 1) * kPage,
+                       cO = cP + NP * NQ * kPage / 2;
   static_assert(cO + NO * D <= 512, "tensor memory");
   // shared memory
   static constexpr int sK = kRing * PAGE, sV = sK + 2 * TILE, sBar = sV + 2 * TILE, sFac = sBar + 256;
@@ -41,7 +49,7 @@ struct Wide {
 };
 
 struct Bars {  // mbarriers
-  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2];
+  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], lo_empty;
 };
 static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
@@ -125,6 +133,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       mbar_init(&bar.s_empty[i], kSoftWarps), mbar_init(&bar.p_full[i], kSoftWarps);
       mbar_init(&bar.o_empty[i], kSumWarps);
     }
+    mbar_init(&bar.lo_empty, kSoftWarps);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
@@ -168,10 +177,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     r.pair = kv8_pair(c, r.sg.s, r.sg.h);
     return r;
   };
-  // physical page of page p of a run, or -1: read as an empty page
-  auto phys_of = [&](const Run& r, int p) {
-    const int v = c.table[r.pair * c.max_pages + p];
-    return v >= 0 && v < c.max_pages ? v : -1;
+  // 32 pages of a run, one for each lane: physical page (-1: left out, as an empty one) and one of its scales
+  struct Batch {
+    int phys;
+    float scale;
+  };
+  auto batch_at = [&](const Run& r, int p, int which) {
+    Batch t{-1, 0.0f};
+    if (p + lane < r.pages) {
+      const int v = c.table[r.pair * c.max_pages + r.first + p + lane];
+      if (v >= 0 && v < c.max_pages) t.phys = v, t.scale = c.scales[kv8_page(c, r.pair, v) * 2 + which];
+    }
+    return t;
   };
   bool ok = true;
   auto wait = [&](uint64_t* b, int parity) {
@@ -184,9 +201,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     int n = 0;
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
+      Batch now{}, then = batch_at(r, 0, 0);
       for (int p = 0; p < r.pages && ok; ++p, ++n, e.next()) {
+        if ((p & 31) == 0) now = then, then = batch_at(r, p + 32, 0);
         if (n >= kRing && !wait(&bar.code_empty[e.i], e.ph ^ 1)) break;
-        int phys = phys_of(r, r.first + p);
+        int phys = __shfl_sync(FULL, now.phys, p & 31);
         if (phys < 0) {
           if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TREE);
           phys = 0;
@@ -251,7 +270,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         const uint32_t v = smem_u32(sm + C::sV + pb.i * C::TILE);
         for (int x = 0; x < NQ; ++x)
           for (int k = 0; k < kPage / 16; ++k)
-            tc_mma(tmem + C::cO + ob.i * D, tmem + C::cP + (pb.i * NQ + x) * (kPage / 2) + k * 8, tc_desc(v + k * 32), tc_idesc(D),
+            tc_mma(tmem + C::cO + ob.i * D, tmem + C::cP + (pb.i % C::NP * NQ + x) * (kPage / 2) + k * 8, tc_desc(v + k * 32), tc_idesc(D),
                    x + k > 0);
         tc_commit(&bar.pv_done[pb.i]);
       }
@@ -268,10 +287,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         tc_after();
         if (lane == 0) {
           const uint32_t k0 = smem_u32(sm + C::sK + b.i * C::TILE);
-          for (int x2 = 0; x2 < NQ; ++x2)
-            for (int k = 0; k < D / 16; ++k)
-              tc_mma(tmem + C::cS + b.i * kPage, tmem + C::cQ + x2 * (D / 2) + k * 8,
-                     tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32), tc_idesc(kPage), x2 + k > 0);
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma(tmem + C::cS + b.i * kPage, tmem + C::cQ + k * 8, tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32),
+                   tc_idesc(kPage), k > 0);
+        }
+        __syncwarp();
+        if (NQ == 2) {
+          if (!wait(&bar.lo_empty, n & 1)) break;
+          tc_after();
+        }
+        if (lane == 0) {
+          const uint32_t k0 = smem_u32(sm + C::sK + b.i * C::TILE);
+          for (int k = 0; k < D / 16 && NQ == 2; ++k)
+            tc_mma(tmem + C::cL, tmem + C::cQ + D / 2 + k * 8, tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32),
+                   tc_idesc(kPage), k > 0);
           tc_commit(&bar.s_done[b.i]);
         }
         __syncwarp();
@@ -286,11 +315,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     Turn<2> b;
     Turn<kFac> fb;
     int n = 0, freed = 0;  // pages done; S buffers released to the products (page n needs n + 1 of them)
-    const double lscale = (double)a.scale * 1.4426950408889634;
+    // the logit's factor is not negative (Q takes the scale's sign), so the largest logit is the largest S
+    const double lscale = fabs((double)a.scale) * 1.4426950408889634;
     const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
       const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      Batch now{}, then = batch_at(r, 0, 0);
       // Q of the run: the products of the run before are done (its last O' was waited for)
       float colfac, collow, m = -INFINITY, l = 0.0f;
       {
@@ -320,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
 #pragma unroll
           for (int e = 0; e < 8; ++e) am = max_nan(am, fabsf(v[e]));
         }
-        const float up = f16_scale(am), down = 1.0f / up;
+        const float up = a.scale < 0.0f ? -f16_scale(am) : f16_scale(am), down = 1.0f / f16_scale(am);
         colfac = lhi * down;
         collow = llo * down;
 #pragma unroll 1
@@ -350,9 +381,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       __syncwarp();
       for (int y = 0; y < 2 && freed < n + r.pages; ++y, ++freed)
         if (lane == 0) mbar_arrive(&bar.s_empty[freed & 1]);
+      if (NQ == 2 && lane == 0) mbar_arrive(&bar.lo_empty);
       for (int p = 0; p < r.pages && ok; ++p, ++n, b.next(), fb.next()) {
-        const int phys = phys_of(r, r.first + p);
-        const float sk = phys < 0 ? 0.0f : c.scales[kv8_page(c, r.pair, phys) * 2];
+        if ((p & 31) == 0) now = then, then = batch_at(r, p + 32, 0);
+        const int phys = __shfl_sync(FULL, now.phys, p & 31);
+        const float sk = __shfl_sync(FULL, now.scale, p & 31);
         const float fh = colfac * sk, fl = fmaf(colfac, sk, -fh) + collow * sk;
         if (!wait(&bar.s_done[b.i], b.ph)) break;
         tc_after();
@@ -362,18 +395,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         for (int y = 0; y < 2; ++y) {
           uint32_t v[32];
           tc_load32(sa + 32 * y, v);
+          float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]) * fh);
+          for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(v[e]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
+        mx *= fh;
         float f = 1.0f;
-        if (phys >= 0 && mx > m + kPSlack) {
+        if (phys >= 0 && mx > m + C::SLACK) {
           f = ex2(m - mx);
           m = mx;
           l *= f;
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        // a page that is not there: 2^-inf
+        const float base = phys < 0 ? INFINITY : m == -INFINITY ? 0.0f : m;
         // P's last readers; and the value warps are past page n - 4, whose row factors these replace
-        if (n >= 2 && !wait(&bar.pv_done[b.i], b.ph ^ 1)) break;
+        if (n >= C::NP && !wait(&bar.pv_done[(n - C::NP) & 1], (n - C::NP) >> 1 & 1)) break;
         fac[fb.i * kWideRows + row] = f;
         const bool any = __any_sync(FULL, f != 1.0f);
         if (lane == 0) moved[fb.i * kSoftWarps + warp] = any;
@@ -382,7 +419,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         for (int y = 0; y < 2; ++y) {
           uint32_t v[32], hi[16], lo[16];
           tc_load32(sa + 32 * y, v);
+          if (NQ == 2) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t w[16];
+              tc_load16(mine + C::cL + 32 * y + 16 * z, w);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                v[16 * z + e] = __float_as_uint(__uint_as_float(v[16 * z + e]) + __uint_as_float(w[e]));
+            }
+          }
           // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
+          float sum[2] = {0.0f, 0.0f};
 #pragma unroll
           for (int z = 0; z < 16; ++z) {
             const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
@@ -390,18 +438,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float s = __uint_as_float(v[tok + w]);
-              e[w] = NQ == 2 ? ex2(fmaf(s, fl, fmaf(s, fh, -base))) * kPScale : ex2(fmaf(s, fh, 7.0f - base));
-              if (phys < 0) e[w] = 0.0f;
-              ps += e[w];
+              e[w] = NQ == 2 ? ex2(fmaf(s, fl, fmaf(s, fh, -base))) * C::PSCALE : ex2(fmaf(s, fh, 7.0f - base));
+              sum[w] += e[w];
             }
-            hi[z] = pack_f16(e[0], e[1]);
             if (NQ == 2) {
-              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[z]));
-              lo[z] = pack_f16(e[0] - h.x, e[1] - h.y);
+              hi[z] = pack_f16(rintf(e[0]), rintf(e[1]));
+              lo[z] = pack_f16(e[0] - rintf(e[0]), e[1] - rintf(e[1]));
+            } else {
+              hi[z] = pack_f16(e[0], e[1]);
             }
           }
-          tc_store16(mine + C::cP + b.i * NQ * (kPage / 2) + 16 * y, hi);
-          if (NQ == 2) tc_store16(mine + C::cP + (b.i * NQ + 1) * (kPage / 2) + 16 * y, lo);
+          ps += sum[0] + sum[1];
+          tc_store16(mine + C::cP + b.i % C::NP * NQ * (kPage / 2) + 16 * y, hi);
+          if (NQ == 2) tc_store16(mine + C::cP + kPage / 2 + 16 * y, lo);
         }
         l += ps;
         tc_store_wait();
@@ -410,18 +459,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         if (lane == 0) {
           mbar_arrive(&bar.p_full[b.i]);
           if (freed < n + r.pages - p) mbar_arrive(&bar.s_empty[b.i]);
+          if (NQ == 2 && p + 1 < r.pages) mbar_arrive(&bar.lo_empty);
         }
         if (freed < n + r.pages - p) ++freed;
         if (ws.page && row < rows)
           ws.page[((size_t)r.seg * c.max_pages + r.first + p) * kWideRows + row] =
-              make_float2(m == -INFINITY ? 0.0f : m, ps / kPScale);
+              make_float2(m == -INFINITY ? 0.0f : m, ps / C::PSCALE);
       }
       // the run's last products are done before the next run's Q takes the place of this one
       if (!ok || !wait(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
       tc_after();
       if (row < rows) {
         const size_t at = r.ends ? (size_t)geo.ctas + geo.segments + r.seg : (size_t)blockIdx.x + r.seg;
-        ws.ml[at * kWideRows + row] = make_float2(m, l / kPScale);
+        ws.ml[at * kWideRows + row] = make_float2(m, l / C::PSCALE);
       }
       x += r.pages;
     }
@@ -436,12 +486,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
       const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      Batch now{}, then = batch_at(r, 0, 1);
       float O[DH];
 #pragma unroll
       for (int d = 0; d < DH; ++d) O[d] = 0.0f;
       for (int p = 0; p < r.pages && ok; ++p, b.next(), ob.next(), fb.next()) {
-        const int phys = phys_of(r, r.first + p);
-        const float sv = phys < 0 ? 0.0f : c.scales[kv8_page(c, r.pair, phys) * 2 + 1];
+        if ((p & 31) == 0) now = then, then = batch_at(r, p + 32, 1);
+        const float sv = __shfl_sync(FULL, now.scale, p & 31);
         if (!wait(&bar.p_full[b.i], b.ph) || !wait(&bar.pv_done[b.i], b.ph)) break;
         tc_after();
         if (moved[fb.i * kSoftWarps + quad]) {
@@ -465,7 +516,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         float4* o = reinterpret_cast<float4*>(ws.o + (at * kWideRows + row) * D + half * DH);
 #pragma unroll
         for (int d = 0; d < DH; d += 4)
-          o[d / 4] = make_float4(O[d] / kPScale, O[d + 1] / kPScale, O[d + 2] / kPScale, O[d + 3] / kPScale);
+          o[d / 4] = make_float4(O[d] / C::PSCALE, O[d + 1] / C::PSCALE, O[d + 2] / C::PSCALE, O[d + 3] / C::PSCALE);
       }
       x += r.pages;
     }
@@ -477,28 +528,33 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The fp32 rows of wide calls: a warp a part.
+// The fp32 rows of wide calls, a warp a part: launched behind the wide kernel and run beside it (64 threads of 128
+// registers are what it leaves of an SM).  It reads what the wide kernel waited for before it let this one start, so
+// the wait for that kernel comes last, for the join that follows.
+constexpr int kRowsWarps = 2;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
-  griddep_enter();
-  __shared__ __align__(16) float row_p[4][kRowChunk][kRowTile];
+__global__ void __launch_bounds__(32 * kRowsWarps) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+  griddep_launch();
+  __shared__ __align__(16) float row_p[kRowsWarps][kRowChunk][kRowTile];
   const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
-  const int x = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, x = blockIdx.x * kRowsWarps + warp;
   if (x < geo.segments * geo.tiles * chunks)
-    kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[threadIdx.x >> 5]);
+    kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[warp]);
+  griddep_wait();
 }
 
 template <typename T, int D>
 cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
   using C = Wide<T, D>;
+  const size_t smem = 1024 + C::sPrefix + 4 * ((size_t)c.n_seqs + 1);
+  cudaError_t e = kv8_smem<k_kv8_wide<T, D>>(1024 + C::sPrefix + 4 * (kKv8MaxSeqs + 1));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
+  if (e != cudaSuccess) return e;
   const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
   const int64_t parts = (int64_t)geo.segments * geo.tiles * chunks;
-  cudaError_t e = launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)((parts + 3) / 4)), dim3(128), 0, st, c, a, geo, ws);
-  if (e != cudaSuccess) return e;
-  const size_t smem = 1024 + C::sPrefix + 4 * ((size_t)c.n_seqs + 1);
-  e = kv8_smem<k_kv8_wide<T, D>>(1024 + C::sPrefix + 4 * (kKv8MaxSeqs + 1));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
+  return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)((parts + kRowsWarps - 1) / kRowsWarps)), dim3(32 * kRowsWarps), 0, st, c,
+                    a, geo, ws);
 }
 
 }  // namespace
