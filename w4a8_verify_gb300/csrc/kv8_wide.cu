@@ -8,13 +8,15 @@
 //             chunks of two rows of either tile: one load, eight byte permutes, eight subtractions, two stores;
 //   products  S = Q C_K^T and O' = P C_V^T, tcgen05.mma with A (Q, P) in tensor memory, 128 x 64 x D and 128 x D x 64;
 //   softmax   a thread holds one query row: no exchange between lanes.  P (scaled by 2^7) returns to tensor memory in the
-//             token order of the values' chunks.  The row's maximum moves only when a logit passes it by 8 (log2);
+//             token order of the values' chunks.  A page is tried with the row's old maximum, and done again with
+//             its own when a logit passes that by 8 (log2);
 //   values    O = O c + s_V O' in registers, a thread half a row: the page's scale needs no common factor with the
 //             other pages', and nothing is rescaled in tensor memory.
 // fp32 calls split Q and P into f16 hi + lo and add both products into the same accumulator.  The hi terms are the
-// nearest whole numbers at a largest magnitude of 2^11 (P <= 1 there: the maximum moves at once), so their sums with the
-// codes are whole numbers below 2^24, which the tensor core's truncating additions leave exact; with hi the nearest
-// f16 of P outputs were off by 1.8e-6 in the 2-norm at 4096 tokens, against 0.3e-6.
+// nearest whole numbers at a largest magnitude of 2^11 (P: scaled by 2^10, with the maximum of its own page),
+// so their sums with the codes are whole numbers below 2^24, which the tensor core's truncating additions leave exact.
+// With hi the nearest f16, and Q's lo product in the accumulator of its hi product, outputs were off by 1.8e-6 in the
+// 2-norm at 4096 tokens, against 0.6e-6.
 // Why tcgen05 here: the split kernel converts a page once for every eight columns, and mma.sync tops out at a quarter
 // of the dense rate; with 128 rows a page is 2 x 256 cycles of tensor core against 700 of memory traffic.
 #include "kv8_attn.cuh"
@@ -35,7 +37,7 @@ struct Wide {
   static constexpr int NO = sizeof(T) == 4 ? 1 : 2;         // buffers of O'
   static constexpr int PAGE = 2 * kPage * D, TILE = kPage * D * 2;  // bytes of a page of codes, of an f16 tile
   // scale of P, and how far (log2) a logit may pass its row's maximum before that moves
-  static constexpr float PSCALE = NQ == 2 ? 1024.0f : kPScale, SLACK = NQ == 2 ? 0.0f : kPSlack;
+  static constexpr float PSCALE = NQ == 2 ? 1024.0f : kPScale, SLACK = NQ == 2 ? 0.9f : kPSlack;
   // buffers of P
   static constexpr int NP = NQ == 2 ? 1 : 2;
   // tensor memory columns: Q, S twice, the product with the lo term of Q (apart: a sum of whole numbers that
@@ -55,21 +57,31 @@ static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-// D[128][N] (+)= A (tensor memory) B (shared memory), one k-step of 16
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
 // f16 x f16 -> f32, both operands K-major, M = 128
 __host__ __device__ constexpr uint32_t tc_idesc(int N) { return 1u << 4 | (uint32_t)(N / 8) << 17 | (128u / 16) << 24; }
-// K-major rows of 128 bytes, 128-byte swizzle, eight rows 1024 bytes apart
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
-  return (uint64_t)(addr >> 4 & 0x3fffu) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Shared-memory operand, low word: K-major rows of 128 bytes; high word: eight rows 1024 bytes apart, 128-byte swizzle
+__device__ __forceinline__ uint32_t tc_desc(uint32_t addr) { return (addr >> 4 & 0x3fffu) | 1u << 16; }
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+// D[128][N] (+)= A (tensor memory) B (shared memory), one k-step of 16, by one thread of a converged warp: the operands
+// are uniform values, and no branch around the instruction keeps the compiler from holding them as such
+template <int N>
+__device__ __forceinline__ void tc_mma(uint32_t leader, uint32_t d, uint32_t a, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %0, 0;\n mov.b64 b, {%3, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %5, p;\n}\n" ::"r"(leader), "r"(d), "r"(a), "r"(desc),
+      "r"((uint32_t)add), "r"(tc_idesc(N)), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(leader), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
 #define W4A8_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
 #define W4A8_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
@@ -128,7 +140,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&bar.code_full[i], 1), mbar_init(&bar.code_empty[i], kConvWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], kConvWarps), mbar_init(&bar.v_full[i], kConvWarps);
+      mbar_init(&bar.k_full[i], kConvWarps / 2), mbar_init(&bar.v_full[i], kConvWarps / 2);
       mbar_init(&bar.s_done[i], 1), mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.s_empty[i], kSoftWarps), mbar_init(&bar.p_full[i], kSoftWarps);
       mbar_init(&bar.o_empty[i], kSumWarps);
@@ -221,60 +233,56 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     // no copy in flight when the CTA ends
     for (int i = max(0, n - kRing); i < n; ++i) (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
   } else if (warp >= kConv0 && warp < kMmaWarp) {
-    const int ct = tid - kConv0 * 32;  // 0..127
+    // the first half of the warps takes the keys, the second the values
+    constexpr int kHalf = kConvWarps / 2;
+    const int v = (warp - kConv0) / kHalf, ct = (tid - kConv0 * 32) % (32 * kHalf);
     Turn<kRing> e;
     Turn<2> b;
     for (int i = 0; i < u1 - u0 && ok; ++i, e.next(), b.next()) {
+      // the tile's last readers: the products of two pages ago
+      if (i >= 2 && !wait(v ? &bar.pv_done[b.i] : &bar.s_done[b.i], b.ph ^ 1)) break;
       if (!wait(&bar.code_full[e.i], e.ph)) break;
-      const uint8_t* pg = sm + e.i * C::PAGE;
-#pragma unroll 1
-      for (int v = 0; v < 2 && ok; ++v) {
-        // the tile's last readers: the products of two pages ago
-        if (i >= 2 && !wait(v ? &bar.pv_done[b.i] : &bar.s_done[b.i], b.ph ^ 1)) break;
-        uint8_t* tile = sm + (v ? C::sV : C::sK) + b.i * C::TILE;
-        const uint8_t* from = pg + v * kPage * D;
-        constexpr int kChunks = D / 32;  // keys: 32-dim chunks of a 16-token tile; values: two 32-token chunks of a 16-dim tile
-#pragma unroll
-        for (int k = 0; k < kPage * D / 16 / 128; ++k) {
-          const int gi = k * 128 + ct, t = gi & 3, g = (gi >> 2) & 7;
-          int q = gi >> 5;
-          // neighbouring rows of a store phase take the other half of a row's 128 bytes: no bank conflict
-          q ^= g & 1;
-          const uint4 w = *reinterpret_cast<const uint4*>(from + (q * 32 + (gi & 31)) * 16);
-          const int tile16 = v ? q >> 1 : q / kChunks, chunk = (v ? q & 1 : q % kChunks) * 4 + t, row = tile16 * 16 + g;
-          uint4 lo, hi;
-          codes_f16<true>(w.x, lo.x, lo.y);
-          codes_f16<true>(w.z, lo.z, lo.w);
-          codes_f16<true>(w.y, hi.x, hi.y);
-          codes_f16<true>(w.w, hi.z, hi.w);
-          // keys of D = 128 are two tiles of 64 dims
-          uint8_t* to = tile + (v ? 0 : (chunk >> 3) * (kPage * 128)) + row * 128 + (((chunk & 7) ^ g) << 4);
-          *reinterpret_cast<uint4*>(to) = lo;
-          *reinterpret_cast<uint4*>(to + 8 * 128) = hi;
-        }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v ? &bar.v_full[b.i] : &bar.k_full[b.i]);
+      uint8_t* tile = sm + (v ? C::sV : C::sK) + b.i * C::TILE;
+      const uint8_t* from = sm + e.i * C::PAGE + v * kPage * D;
+      constexpr int kChunks = D / 32;  // keys: 32-dim chunks of a 16-token tile; values: two 32-token chunks of a 16-dim tile
+#pragma unroll 4
+      for (int k = 0; k < kPage * D / 16 / (32 * kHalf); ++k) {
+        const int gi = k * (32 * kHalf) + ct, t = gi & 3, g = (gi >> 2) & 7;
+        // neighbouring rows of a store phase take the other half of a row's 128 bytes: no bank conflict
+        const int q = (gi >> 5) ^ (g & 1);
+        const uint4 w = *reinterpret_cast<const uint4*>(from + (q * 32 + (gi & 31)) * 16);
+        const int tile16 = v ? q >> 1 : q / kChunks, chunk = (v ? q & 1 : q % kChunks) * 4 + t, row = tile16 * 16 + g;
+        uint4 lo, hi;
+        codes_f16<true>(w.x, lo.x, lo.y);
+        codes_f16<true>(w.z, lo.z, lo.w);
+        codes_f16<true>(w.y, hi.x, hi.y);
+        codes_f16<true>(w.w, hi.z, hi.w);
+        // keys of D = 128 are two tiles of 64 dims
+        uint8_t* to = tile + (v ? 0 : (chunk >> 3) * (kPage * 128)) + row * 128 + (((chunk & 7) ^ g) << 4);
+        *reinterpret_cast<uint4*>(to) = lo;
+        *reinterpret_cast<uint4*>(to + 8 * 128) = hi;
       }
-      if (lane == 0) mbar_arrive(&bar.code_empty[e.i]);
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.code_empty[e.i]);
+        mbar_arrive(v ? &bar.v_full[b.i] : &bar.k_full[b.i]);
+      }
     }
   } else if (warp == kMmaWarp) {
     Turn<2> b, pb;
     Turn<NO> ob;
     int n = 0;  // pages whose S is issued
+    const uint32_t one = elect_one();
     auto values = [&](int i) {  // O' of page i (the one before the newest S)
       if (!wait(&bar.p_full[pb.i], pb.ph) || !wait(&bar.v_full[pb.i], pb.ph)) return;
       if (i >= NO && !wait(&bar.o_empty[ob.i], ob.ph ^ 1)) return;
       tc_after();
-      if (lane == 0) {
-        const uint32_t v = smem_u32(sm + C::sV + pb.i * C::TILE);
-        for (int x = 0; x < NQ; ++x)
-          for (int k = 0; k < kPage / 16; ++k)
-            tc_mma(tmem + C::cO + ob.i * D, tmem + C::cP + (pb.i % C::NP * NQ + x) * (kPage / 2) + k * 8, tc_desc(v + k * 32), tc_idesc(D),
-                   x + k > 0);
-        tc_commit(&bar.pv_done[pb.i]);
-      }
-      __syncwarp();
+      const uint32_t v = tc_desc(smem_u32(sm + C::sV + pb.i * C::TILE)), o = tmem + C::cO + ob.i * D;
+      const uint32_t pa = tmem + C::cP + pb.i % C::NP * NQ * (kPage / 2);
+#pragma unroll
+      for (int k = 0; k < NQ * kPage / 16; ++k) tc_mma<D>(one, o, pa + k * 8, v + (k & 3) * 2, k > 0);
+      tc_commit(one, &bar.pv_done[pb.i]);
       pb.next();
       ob.next();
     };
@@ -285,25 +293,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         // of both buffers when it is there
         if (!wait(&bar.k_full[b.i], b.ph) || !wait(&bar.s_empty[b.i], b.ph)) break;
         tc_after();
-        if (lane == 0) {
-          const uint32_t k0 = smem_u32(sm + C::sK + b.i * C::TILE);
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma(tmem + C::cS + b.i * kPage, tmem + C::cQ + k * 8, tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32),
-                   tc_idesc(kPage), k > 0);
-        }
-        __syncwarp();
+        // 16 dims are 32 bytes of a row; dims 64 .. 127 are another tile
+        const uint32_t k0 = tc_desc(smem_u32(sm + C::sK + b.i * C::TILE));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma<kPage>(one, tmem + C::cS + b.i * kPage, tmem + C::cQ + k * 8, k0 + (k >> 2) * (kPage * 128 / 16) + (k & 3) * 2, k > 0);
         if (NQ == 2) {
           if (!wait(&bar.lo_empty, n & 1)) break;
           tc_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma<kPage>(one, tmem + C::cL, tmem + C::cQ + D / 2 + k * 8, k0 + (k >> 2) * (kPage * 128 / 16) + (k & 3) * 2, k > 0);
         }
-        if (lane == 0) {
-          const uint32_t k0 = smem_u32(sm + C::sK + b.i * C::TILE);
-          for (int k = 0; k < D / 16 && NQ == 2; ++k)
-            tc_mma(tmem + C::cL, tmem + C::cQ + D / 2 + k * 8, tc_desc(k0 + (k >> 2) * (kPage * 128) + (k & 3) * 32),
-                   tc_idesc(kPage), k > 0);
-          tc_commit(&bar.s_done[b.i]);
-        }
-        __syncwarp();
+        tc_commit(one, &bar.s_done[b.i]);
         if (p > 0) values(n - 1);
       }
       if (ok && r.pages > 0) values(n - 1);
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
             for (int e = 0; e < 8; ++e) v[e] = kv8_load(q + d + e);
           }
         };
-#pragma unroll 4
+#pragma unroll 8
         for (int d = 0; d < D; d += 8) {
           float v[8];
           load8(d, v);
@@ -390,68 +392,82 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         if (!wait(&bar.s_done[b.i], b.ph)) break;
         tc_after();
         const uint32_t sa = mine + C::cS + b.i * kPage;
-        float mx = -INFINITY;
+        float f = 1.0f, ps, mx;
+        // the run's first maximum; bf16 calls try later pages with the old one
+        if (p == 0 || NQ == 2) {
+          mx = -INFINITY;
 #pragma unroll 1
-        for (int y = 0; y < 2; ++y) {
-          uint32_t v[32];
-          tc_load32(sa + 32 * y, v);
-          float m4[4] = {mx, mx, mx, mx};
+          for (int y = 0; y < 2; ++y) {
+            uint32_t v[32];
+            tc_load32(sa + 32 * y, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(v[e]));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+          }
+          if (phys >= 0 && mx * fh > m) {
+            f = ex2(m - mx * fh);
+            m = mx * fh;
+            l *= f;
+          }
         }
-        mx *= fh;
-        float f = 1.0f;
-        if (phys >= 0 && mx > m + C::SLACK) {
-          f = ex2(m - mx);
-          m = mx;
-          l *= f;
-        }
-        // a page that is not there: 2^-inf
-        const float base = phys < 0 ? INFINITY : m == -INFINITY ? 0.0f : m;
         // P's last readers; and the value warps are past page n - 4, whose row factors these replace
         if (n >= C::NP && !wait(&bar.pv_done[(n - C::NP) & 1], (n - C::NP) >> 1 & 1)) break;
+#pragma unroll 1
+        for (int again = 0;; ++again) {
+          // a page that is not there: 2^-inf
+          const float base = phys < 0 ? INFINITY : m == -INFINITY ? 0.0f : m;
+          ps = 0.0f, mx = -INFINITY;
+#pragma unroll 1
+          for (int y = 0; y < 2; ++y) {
+            uint32_t v[32], hi[16], lo[16];
+            tc_load32(sa + 32 * y, v);
+            if (NQ == 2) {
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                uint32_t w[16];
+                tc_load16(mine + C::cL + 32 * y + 16 * z, w);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  v[16 * z + e] = __float_as_uint(__uint_as_float(v[16 * z + e]) + __uint_as_float(w[e]));
+              }
+            }
+            // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
+            float sum[2] = {0.0f, 0.0f}, top[2] = {mx, mx};
+#pragma unroll
+            for (int z = 0; z < 16; ++z) {
+              const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
+              float e[2];
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const float s = __uint_as_float(v[tok + w]);
+                top[w] = fmaxf(top[w], s);
+                e[w] = NQ == 2 ? ex2(fmaf(s, fl, fmaf(s, fh, -base))) * C::PSCALE : ex2(fmaf(s, fh, 7.0f - base));
+                sum[w] += e[w];
+              }
+              if (NQ == 2) {
+                hi[z] = pack_f16(rintf(e[0]), rintf(e[1]));
+                lo[z] = pack_f16(e[0] - rintf(e[0]), e[1] - rintf(e[1]));
+              } else {
+                hi[z] = pack_f16(e[0], e[1]);
+              }
+            }
+            mx = fmaxf(top[0], top[1]);
+            ps += sum[0] + sum[1];
+            tc_store16(mine + C::cP + b.i % C::NP * NQ * (kPage / 2) + 16 * y, hi);
+            if (NQ == 2) tc_store16(mine + C::cP + kPage / 2 + 16 * y, lo);
+          }
+          mx *= fh;
+          const bool move = phys >= 0 && mx > m + C::SLACK;
+          if (again || !__any_sync(FULL, move)) break;
+          if (move) {
+            const float g = ex2(m - mx);
+            f *= g;
+            m = mx;
+            l *= g;
+          }
+        }
         fac[fb.i * kWideRows + row] = f;
         const bool any = __any_sync(FULL, f != 1.0f);
         if (lane == 0) moved[fb.i * kSoftWarps + warp] = any;
-        float ps = 0.0f;
-#pragma unroll 1
-        for (int y = 0; y < 2; ++y) {
-          uint32_t v[32], hi[16], lo[16];
-          tc_load32(sa + 32 * y, v);
-          if (NQ == 2) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              uint32_t w[16];
-              tc_load16(mine + C::cL + 32 * y + 16 * z, w);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                v[16 * z + e] = __float_as_uint(__uint_as_float(v[16 * z + e]) + __uint_as_float(w[e]));
-            }
-          }
-          // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
-          float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int z = 0; z < 16; ++z) {
-            const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
-            float e[2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const float s = __uint_as_float(v[tok + w]);
-              e[w] = NQ == 2 ? ex2(fmaf(s, fl, fmaf(s, fh, -base))) * C::PSCALE : ex2(fmaf(s, fh, 7.0f - base));
-              sum[w] += e[w];
-            }
-            if (NQ == 2) {
-              hi[z] = pack_f16(rintf(e[0]), rintf(e[1]));
-              lo[z] = pack_f16(e[0] - rintf(e[0]), e[1] - rintf(e[1]));
-            } else {
-              hi[z] = pack_f16(e[0], e[1]);
-            }
-          }
-          ps += sum[0] + sum[1];
-          tc_store16(mine + C::cP + b.i % C::NP * NQ * (kPage / 2) + 16 * y, hi);
-          if (NQ == 2) tc_store16(mine + C::cP + kPage / 2 + 16 * y, lo);
-        }
         l += ps;
         tc_store_wait();
         tc_before();
