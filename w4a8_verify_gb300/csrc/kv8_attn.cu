@@ -12,10 +12,9 @@ constexpr int kJoinWarps = 8;
 template <typename T, int D, int RPC>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
                                                               Kv8Scratch ws) {
-  griddep_enter();
   constexpr int E = D / 32, WPR = kJoinWarps / RPC;
   using Vec = std::conditional_t<E == 4, float4, float2>;
-  __shared__ float sm_l[kJoinWarps];
+  __shared__ float2 sm_ml[kJoinWarps];
   __shared__ __align__(16) float sm_o[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = blockIdx.y;
   const int rb = blockIdx.x * RPC + warp / WPR, first = warp % WPR;
@@ -23,7 +22,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
   const int r = sg.cb * geo.RB + rb, i = a.pages ? sg.i : r / geo.G, s = sg.s;
   const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
   const bool mine = L >= 0 && rb < geo.RB && r < geo.R && i < cnt;
-  float M = -INFINITY, base = 0.0f, l = 0.0f, o[E] = {};
+  // lengths and counts are older than the split kernel; its parts are waited for
+  griddep_enter();
+  float m = -INFINITY, l = 0.0f, o[E] = {};
   if (mine) {
     const Kv8Units un = kv8_units(a, L, cnt);
     int c0 = 0, held = 0, early = 0;  // CTAs that hold parts, and whether a worker ended it and went on
@@ -44,9 +45,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
       const int f = p - tile0 < un.open ? p - tile0 : kPage / kRowTile + p - tile0 - un.open;
       return ((int64_t)seg * geo.tiles + f) * geo.RB + rb;
     };
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, (p < tile0 ? ws.ml : ws.rml)[place(p)].x);
-    M = warp_max(M);
-    base = M == -INFINITY ? 0.0f : M;
     constexpr int B = 8;
     for (int p0 = first; p0 < parts; p0 += WPR * B) {
       float2 ml[B];
@@ -62,6 +60,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
           v[b] = *reinterpret_cast<const Vec*>((p < tile0 ? ws.o : ws.ro) + at * D + E * lane);
         }
       }
+      float mx = m;
+#pragma unroll
+      for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
+      const float base = mx == -INFINITY ? 0.0f : mx, f = ex2(m - base);
+      m = mx;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const float w = ex2(ml[b].x - base);
@@ -72,17 +78,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
       }
     }
   }
-  if (lane == 0) sm_l[warp] = l;
+  if (lane == 0) sm_ml[warp] = make_float2(m, l);
   *reinterpret_cast<Vec*>(&sm_o[warp][E * lane]) = *reinterpret_cast<Vec*>(o);
   __syncthreads();
   if (!mine || first > 0) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) M = fmaxf(M, sm_ml[warp + w].x);
+  const float base = M == -INFINITY ? 0.0f : M;
   l = 0.0f;
   float sum[E] = {};
 #pragma unroll
   for (int w = 0; w < WPR; ++w) {
-    l += sm_l[warp + w];
+    const float2 ml = sm_ml[warp + w];
+    const float f = ex2(ml.x - base);
+    l = fmaf(ml.y, f, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] += sm_o[warp + w][E * lane + e];
+    for (int e = 0; e < E; ++e) sum[e] = fmaf(sm_o[warp + w][E * lane + e], f, sum[e]);
   }
   const int hq = sg.h * geo.G + (a.pages ? r : r % geo.G);
   T* out = static_cast<T*>(a.out.data) + s * a.out.seq + i * a.out.row + hq * a.out.head + E * lane;
@@ -136,7 +148,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.n = a->n;
   g.G = a->n_heads / c->n_kv_heads;
   g.R = a->pages ? g.G : g.n * g.G;
-  const bool wide = kv8_is_wide(*a, g.R);
+  const bool wide = kv8_is_wide(*c, *a, g.R);
   const int wc = kv8_split_warps(g.R, a->dtype);
   g.RB = wide ? kWideRows : wc * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
@@ -192,7 +204,7 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   p.geo.vec = kv8_vec_rows(a->q, a->dtype) ? 1 : 0;
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
-  if (kv8_is_wide(*a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
+  if (kv8_is_wide(*c, *a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
   else W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
       *c, *a, p.geo, ws, st));
   // few rows (some CTAs for each SM): eight warps to a row, whose parts may be many; else two

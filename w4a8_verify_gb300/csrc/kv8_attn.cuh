@@ -759,8 +759,16 @@ cudaError_t kv8_split_dispatch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, 
     default: return kv8_split_launch<T, D, 12>(c, a, geo, ws, st);
   }
 }
-// Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu).
-inline bool kv8_is_wide(const w4a8_kv8_attn& a, int R) { return !a.pages && R >= 32; }
+// Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu): more than 128 rows, or at least eight tiles
+// and 16384 tile-pages of room (the lengths are not known here).  Measured with full caches of 8 KV heads of 128, split
+// kernel / wide kernel, us: fp32, 64 rows, 4096 tokens 29.9 / 32.3 and 16384 tokens 64.7 / 50.0; 128 rows 38.9 / 37.2
+// and 111 / 55; bf16, 128 rows, 4096 tokens 27.8 / 31.8 and 16384 tokens 58.9 / 41.5; 256 rows, 1024 tokens 49.9 / 34.8;
+// 32 rows, 32768 tokens 60.6 / 65.4 (fp32) and 35.2 / 45.8 (bf16).
+inline bool kv8_is_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, int R) {
+  if (a.pages) return false;
+  const int tiles = (R + 3) / (a.dtype == W4A8_F32 ? 4 : 8);
+  return R > kWideRows || (tiles >= 8 && (int64_t)tiles * c.n_seqs * c.n_kv_heads * c.max_pages >= 16384);
+}
 cudaError_t kv8_wide(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 // one translation unit per head size and element type
 cudaError_t kv8_split_f32_d64(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);

@@ -14,19 +14,42 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 constexpr uint32_t kForcedKey = 0xff800000u;  // the key of infinity
 
-// The k-th largest of P keys (0 < k <= P) by four passes over their bytes: *T is that key and *ties how
-// many of the keys equal to it belong to the k largest.  keys in shared memory; hist: 256 words.
+// The keys of the k largest of P (0 < k < P) are those above *T and *ties of those equal to it.  Forced pages and
+// infinities are counted first; the others are looked for by their distance from the smallest, eight bits at a
+// time from the highest that differs (the leading bits of scores are much alike: bins of whole bytes would put most keys
+// into two or three of them, one atomic after the other).  keys in shared memory; hist: 256 words.
 __device__ void kth_largest(const uint32_t* keys, int P, int k, uint32_t* hist, uint32_t* T, int* ties) {
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
-  uint32_t prefix = 0;
-  int left = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
+  __shared__ uint32_t s_low, s_high, s_bin;
+  __shared__ int s_top, s_left, s_bins;
+  if (threadIdx.x == 0) s_low = ~0u, s_high = 0u, s_top = 0;
+  __syncthreads();
+  uint32_t low = ~0u, high = 0u;
+  int top = 0;
+  for (int i = threadIdx.x; i < P; i += blockDim.x) {
+    const uint32_t x = keys[i];
+    if (x >= kForcedKey) ++top;
+    else low = min(low, x), high = max(high, x);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  top = __reduce_add_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) atomicMin(&s_low, low), atomicMax(&s_high, high), atomicAdd(&s_top, top);
+  __syncthreads();
+  low = s_low, high = s_high, top = s_top;
+  if (top >= k) {  // no key is above infinity's
+    *T = kForcedKey, *ties = k;
+    return;
+  }
+  int left = k - top, bits = high > low ? 32 - __clz(high - low) : 0;
+  uint32_t prefix = 0;  // of the distance of the key looked for: its bits above `bits`
+  while (bits > 0) {
+    const int lo = max(bits - 8, 0);
     for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
     __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = threadIdx.x; i < P; i += blockDim.x)
-      if ((keys[i] & mask) == prefix) atomicAdd(&hist[(keys[i] >> shift) & 255u], 1u);
+    for (int i = threadIdx.x; i < P; i += blockDim.x) {
+      const uint32_t x = keys[i], d = x - low;
+      if (x < kForcedKey && (bits == 32 ? 0u : d >> bits) == prefix) atomicAdd(&hist[(d >> lo) & ((1u << (bits - lo)) - 1u)], 1u);
+    }
     __syncthreads();
     if (threadIdx.x < 32) {  // lane l: bins 255 - 8l .. 248 - 8l, from the top
       const int lane = threadIdx.x;
@@ -43,16 +66,22 @@ __device__ void kth_largest(const uint32_t* keys, int P, int k, uint32_t* hist, 
       if (above < left && above + sum >= left) {
         int i = 0;
         while (above + c[i] < left) above += c[i++];
-        s_prefix = prefix | (uint32_t)(255 - 8 * lane - i) << shift;
+        s_bin = (uint32_t)(255 - 8 * lane - i);
         s_left = left - above;
+        s_bins = c[i];
       }
     }
     __syncthreads();
-    prefix = s_prefix;
+    prefix = prefix << (bits - lo) | s_bin;
     left = s_left;
+    bits = lo;
+    const int in_bin = s_bins;
+    __syncthreads();
+    if (in_bin == left) break;  // the whole bin belongs to them: above anything below it
   }
-  *T = prefix;
-  *ties = left;
+  // bits > 0: every key at or above the bin's first one
+  *T = low + (prefix << bits) - (bits > 0 ? 1u : 0u);
+  *ties = bits > 0 ? 0 : left;
 }
 
 // Calls put(i, kept, rank) for every i in [0, P): kept where key i is among the k largest (ties to the lowest i),

@@ -109,6 +109,9 @@ __device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void tc_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The nearest whole number of |x| < 2^22 (NaN stays)
+__device__ __forceinline__ float whole(float x) { return __fadd_rn(__fadd_rn(x, 12582912.0f), -12582912.0f); }
+
 // A position in a ring of mbarriers: entry and phase parity.
 template <int N>
 struct Turn {
@@ -367,8 +370,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
             for (int e = 0; e < 8; e += 2) {
               const float f0 = v[e] * up, f1 = v[e + 1] * up;
               if (NQ == 2) {
-                hi[4 * y + e / 2] = pack_f16(rintf(f0), rintf(f1));
-                lo[4 * y + e / 2] = pack_f16(f0 - rintf(f0), f1 - rintf(f1));
+                const float w0 = whole(f0), w1 = whole(f1);
+                hi[4 * y + e / 2] = pack_f16(w0, w1);
+                lo[4 * y + e / 2] = pack_f16(f0 - w0, f1 - w1);
               } else {
                 hi[4 * y + e / 2] = pack_f16(f0, f1);
               }
@@ -444,8 +448,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
                 sum[w] += e[w];
               }
               if (NQ == 2) {
-                hi[z] = pack_f16(rintf(e[0]), rintf(e[1]));
-                lo[z] = pack_f16(e[0] - rintf(e[0]), e[1] - rintf(e[1]));
+                const float w0 = whole(e[0]), w1 = whole(e[1]);
+                hi[z] = pack_f16(w0, w1);
+                lo[z] = pack_f16(e[0] - w0, e[1] - w1);
               } else {
                 hi[z] = pack_f16(e[0], e[1]);
               }
