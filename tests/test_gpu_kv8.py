@@ -615,3 +615,193 @@ def test_binding_refusals():
         cache.attention(q, k, k, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")[:0])
     with pytest.raises(W.W4A8Error):
         cache.select(q, 16385)
+
+
+# ------------------------------------------------------------------------------- long ranges
+
+def _random_cache(seed, lens, H, D, max_pages=None):
+    """A cache of random codes, scales, tail rows and tables (code sums to match)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    S, P = len(lens), max_pages or max(lens) // 64 + 1
+    c = W.KV8Cache(S, H, D, P)
+    t = c.tensors
+    t["codes"].random_(1, 256, generator=g)
+    t["scales"].uniform_(0.01, 0.03, generator=g)
+    t["tail"].normal_(0, 1, generator=g)
+    t["table"].copy_(torch.rand(S, H, P, generator=g, device="cuda").argsort(dim=-1))
+    t["len"].copy_(_i32(list(lens)))
+    at = torch.from_numpy(O.byte_order(D, O.key_byte)).cuda()
+    if P * S * H < 1 << 16:
+        for s in range(S):
+            t["sums"][s] = (t["codes"][s, :, :, 0][..., at.reshape(-1)].view(H, P, 64, D).int() - 128).sum(2)
+    return c
+
+
+def _held64(c, s, h, pages=None):
+    """fp64 keys and values of the whole pages (or of those listed), then of the open page."""
+    D, L, t = c.shape[2], int(c.len[s]), c.tensors
+    at = [torch.from_numpy(O.byte_order(D, b)).cuda().reshape(-1) for b in (O.key_byte, O.value_byte)]
+    phys = t["table"][s, h, :L // 64].long()
+    phys = phys if pages is None else phys[pages]
+    out = []
+    for i in range(2):
+        x = (t["codes"][s, h, phys, i][:, at[i]].double() - 128) * t["scales"][s, h, phys, i].double()[:, None]
+        out.append(torch.cat([x.view(-1, D), t["tail"][s, h, i, :L % 64].double()]))
+    return out
+
+
+def _long_check(c, q, k, v, scale, out, heads, seqs, mass=None, mass_out=None, pages=None):
+    """Rows of some heads and sequences against fp64 on the device (new rows causal), with the bounds of this file."""
+    n, G, D = q.shape[1], q.shape[2] // c.shape[1], q.shape[3]
+    bf = q.dtype == torch.bfloat16
+    num = den = 0.0
+    for s in seqs:
+        for h in heads:
+            for i in (range(n) if pages is not None else (None,)):
+                lst = None if pages is None else pages[s, i, h][pages[s, i, h] >= 0].long()
+                K, V = _held64(c, s, h, lst)
+                held = len(K)
+                K, V = torch.cat([K, k[s, :, h].double()]), torch.cat([V, v[s, :, h].double()])
+                rows = slice(0, n) if i is None else slice(i, i + 1)
+                Q = q[s, rows, h * G:(h + 1) * G].double().reshape(-1, D)
+                logits = Q @ K.T * scale
+                A = float((Q.abs() @ K.abs().T).max()) * abs(scale)
+                node = torch.arange(n, device="cuda")[rows].repeat_interleave(G)
+                hide = torch.arange(n, device="cuda")[None] > node[:, None]
+                logits[:, held:][hide] = -float("inf")
+                w = torch.softmax(logits, -1)
+                ref = w @ V
+                got = out[s, rows, h * G:(h + 1) * G].double().reshape(-1, D)
+                d = (2.0 ** -10 if bf else 2.0 ** -19) * A
+                tol = float(V.abs().max()) * (2 * d + (2.0 ** -9 if bf else 2.0 ** -17)) + (2.0 ** -8 * ref.abs() if bf else 0)
+                assert ((got - ref).abs() <= tol).all(), (s, h, i, float((got - ref).abs().max()))
+                num, den = num + float(((got - ref) ** 2).sum()), den + float((ref ** 2).sum())
+                if mass is not None:
+                    full = int(c.len[s]) // 64
+                    add = w[:, :64 * full].sum(0).view(full, 64).sum(1)
+                    have = (mass_out[s, h] - mass[s, h]).double()
+                    slack = 2 * d + (2.0 ** -9 if bf else 2.0 ** -17)
+                    assert ((have[:full] - add).abs() <= slack * add + 2.0 ** -20 * mass_out[s, h, :full].abs()).all()
+                    assert not have[full:].any()
+    assert (num / den) ** 0.5 <= (4e-3 if bf else 2e-6)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("S,H,G,D,n,L,mass", [
+    (24, 2, 4, 128, 1, 6000, True),       # ragged batch: many segments for a worker
+    (48, 4, 7, 64, 1, 9000, False),       # two warps on a page, rings of several pages
+    (3, 2, 4, 128, 16, 5000, True),       # a tree's rows on two and four warps a page
+    (2, 1, 12, 64, 8, 4000, False),       # twelve warps on a page
+    (3, 2, 8, 128, 17, 9000, True),       # tcgen05: runs of several segments in a CTA, the ring of codes in turns
+    (2, 3, 16, 64, 9, 12000, False),
+])
+def test_long_ragged_ranges(dtype, S, H, G, D, n, L, mass):
+    rng = np.random.default_rng(S + n)
+    lens = [L] + [int(x) for x in rng.integers(0, L, S - 1)]
+    c = _random_cache(S * n, lens, H, D)
+    q = _rows(rng, S, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    old = torch.rand(S, H, c.shape[3], device="cuda") if mass else None
+    new = torch.empty_like(old) if mass else None
+    for scale in (D ** -0.5, -0.05):
+        out = c.attention(q, k, v, scale=scale, mass=old, mass_out=new)
+        _long_check(c, q, k, v, scale, out, range(H), sorted({0, 1, S - 1}), old, new)
+        assert torch.equal(out, c.attention(q, k, v, scale=scale, mass=old, mass_out=new))   # no dependence on timing
+    assert c.check() == 0
+
+
+def test_a_million_tokens_past_four_gigabytes():
+    """Twenty heads of 2^20 tokens of 128: page addresses beyond 32 bits, hundreds of pages for a worker, every
+    length the format allows; attention, selection and a sparse read of the last head."""
+    L = 64 * 16384 + 63
+    rng = np.random.default_rng(0)
+    H, D = 20, 128
+    c = _random_cache(3, [L], H, D, max_pages=16384)
+    assert c.tensors["codes"].numel() > 1 << 32
+    q, k = _rows(rng, 1, 1, H, D, "fp32", 2.0), _rows(rng, 1, 1, H, D, "fp32")
+    out = c.attention(q, k, k, scale=D ** -0.5)
+    _long_check(c, q, k, k, D ** -0.5, out, [0, H - 1], [0])
+    c.tensors["sums"].random_(-500, 500)
+    pages = c.select(q, 50, first_pages=1, last_pages=1)
+    h, t = H - 1, c.tensors
+    phys = t["table"][0, h].long()
+    code, _ = O.quantize_page(_np(q)[0, 0, h:h + 1])
+    dot = (t["sums"][0, h, phys].double() @ torch.from_numpy(code).double().cuda().T).amax(1).float()
+    score = (t["scales"][0, h, phys, 0] * dot).cpu().numpy()
+    score[0] = score[-1] = np.inf
+    want = np.sort(np.argsort(-score, kind="stable")[:50])
+    assert pages[0, 0, h].tolist() == want.tolist()
+    out = c.attention(q, k, k, scale=D ** -0.5, pages=pages)
+    _long_check(c, q, k, k, D ** -0.5, out, [0, H - 1], [0], pages=pages)
+    assert c.check() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_long_sparse_reads(dtype):
+    rng = np.random.default_rng(5)
+    S, H, G, D, n = 6, 2, 4, 128, 5
+    c = _random_cache(9, [20000, 0, 64 * 40, 64 * 39 + 5, 12345, 19999], H, D)
+    q = _rows(rng, S, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    pages = c.select(q, 40, last_pages=1)
+    out = c.attention(q, k, v, scale=0.1, pages=pages)
+    _long_check(c, q, k, v, 0.1, out, range(H), range(S), pages=pages)
+
+
+def test_wide_calls_in_a_graph_and_with_empty_sequences():
+    """tcgen05 calls captured and replayed with other lengths, counts of zero, an empty cache, a page out of range."""
+    rng = np.random.default_rng(71)
+    S, H, G, D, n = 3, 1, 16, 64, 12                       # 192 query rows
+    c = _random_cache(4, [700, 0, 1300], H, D, max_pages=24)
+    q, k, v = _rows(rng, S, n, H * G, D, "bf16"), _rows(rng, S, n, H, D, "bf16"), _rows(rng, S, n, H, D, "bf16")
+    counts = _i32([n, n, n])
+    out, mass = torch.empty_like(q), torch.zeros(S, H, 24, device="cuda")
+    zero = torch.zeros_like(mass)
+    c.attention(q, k, v, scale=0.1, counts=counts, out=out, mass=zero, mass_out=mass)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.attention(q, k, v, scale=0.1, counts=counts, out=out, mass=zero, mass_out=mass)
+    for lens, cnt in (([700, 0, 1300], [n] * 3), ([64, 1000, 63], [n, 0, n]), ([1535, 1, 5], [1, n, 7]), ([0, 0, 0], [n, 1, n])):
+        c.len.copy_(_i32(lens))
+        counts.copy_(_i32(cnt))
+        out.fill_(9.0)
+        graph.replay()
+        want, m2 = torch.full_like(out, 9.0), torch.empty_like(mass)
+        c.attention(q, k, v, scale=0.1, counts=counts, out=want, mass=zero, mass_out=m2)
+        assert torch.equal(out, want) and torch.equal(mass, m2)
+        for s in range(S):
+            assert (out[s, cnt[s]:] == 9.0).all()
+            if cnt[s] == n:
+                _long_check(c, q, k, v, 0.1, out, [0], [s], zero, mass)
+    assert c.check() == 0
+    c.len.copy_(_i32([700, 0, 1300]))
+    c.tensors["table"][0, 0, 3] = 24
+    c.attention(q, k, v, scale=0.1, out=out)
+    assert c.check() == W.FLAG_ERR_TREE
+    assert torch.equal(out[1:], c.attention(q, k, v, scale=0.1)[1:])
+
+
+def test_threads_and_a_given_stream():
+    """Two threads on one stream share the workspace that the cache keeps; a call on another stream has its own."""
+    import threading
+    rng = np.random.default_rng(81)
+    c = _random_cache(6, [3000, 900], 2, 128)
+    jobs = []
+    for n in (1, 24):
+        q, k = _rows(rng, 2, n, 8, 128, "fp32"), _rows(rng, 2, n, 2, 128, "fp32")
+        jobs.append((q, k, c.attention(q, k, k, scale=0.1)))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    bad = []
+
+    def work(j, stream):
+        q, k, want = jobs[j]
+        outs = [c.attention(q, k, k, scale=0.1, stream=stream) for _ in range(40)]
+        torch.cuda.synchronize()
+        bad.extend(1 for o in outs if not torch.equal(o, want))
+    threads = [threading.Thread(target=work, args=(j % 2, side if j == 3 else None)) for j in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
