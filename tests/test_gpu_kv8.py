@@ -267,7 +267,7 @@ def test_trees_chains_and_counts(n, H, G, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("n", [4, 16])
+@pytest.mark.parametrize("n", [4, 16, 40])
 def test_masked_rows_with_nan_and_infinities(dtype, n):
     """A new row that a row does not see has no effect on it; rows that see nothing are 0; padded rows are not read."""
     rng = np.random.default_rng(n)
@@ -290,17 +290,18 @@ def test_masked_rows_with_nan_and_infinities(dtype, n):
     assert bad[:, 2, :, 5].all() and not bad[:, :2].any() and not bad[:, 3:].any()
 
 
-def test_non_finite_queries_and_pages():
+@pytest.mark.parametrize("dtype,n", [("fp32", 2), ("bf16", 2), ("fp32", 40), ("bf16", 40)])
+def test_non_finite_queries_and_pages(dtype, n):
     rng = np.random.default_rng(11)
     H, G, D = 1, 4, 64
     cache, ref = _filled(rng, 2, H, D, [130, 130])
     bad = _rows(rng, 2, 1, H, D, "fp32")
     bad[0] = float("inf")
     cache.append(bad.expand(2, 62, H, D), bad.expand(2, 62, H, D))      # completes page 2 of both, with infinities in 0's
-    q = _rows(rng, 2, 2, H * G, D, "fp32")
+    q = _rows(rng, 2, n, H * G, D, dtype)
     q[1, 0, 2, 7] = float("nan")
     q[1, 1, 0, 0] = float("inf")
-    k = _rows(rng, 2, 2, H, D, "fp32")
+    k = _rows(rng, 2, n, H, D, dtype)
     out = cache.attention(q, k, k, scale=0.1)
     assert torch.isnan(out[0]).all()
     nan = torch.isnan(out[1])
@@ -392,6 +393,23 @@ def test_select_and_sparse_attention(H, G, D, n, dtype, top_k, first, last):
     mask = [_tree_mask(rng, n) for _ in range(4)]
     _attend(cache, ref, q, k, v, D ** -0.5, counts=counts, mask=mask, pages=got.tolist())
     assert cache.check() == 0
+
+
+def test_more_rows_than_a_grid_dimension():
+    """4096 sequences (65536 lists and 131072 segments): every limit of the grids that only the first dimension lifts."""
+    rng = np.random.default_rng(23)
+    S, H, D, n = 4096, 2, 64, 16
+    c = _random_cache(2, [130 if s % 7 == 0 else 200 for s in range(S)], H, D, max_pages=3)
+    q, k = _rows(rng, S, n, H, D, "bf16"), _rows(rng, S, n, H, D, "bf16")
+    pages = c.select(q, 2)
+    out = c.attention(q, k, k, scale=0.1, pages=pages)
+    at = [0, 1, 7, S - 2, S - 1]
+    small = W.KV8Cache(len(at), H, D, 3, tensors={x: (t if x == "ctl" else t[at].contiguous()) for x, t in c.tensors.items()})
+    assert torch.equal(pages[at], small.select(q[at].contiguous(), 2))
+    _long_check(c, q, k, k, 0.1, out, range(H), at, pages=pages)
+    out = c.attention(q[:, :1], k[:, :1], k[:, :1], scale=0.1)
+    _long_check(c, q[:, :1], k[:, :1], k[:, :1], 0.1, out, range(H), at)
+    assert c.check() == 0
 
 
 def test_select_ties_zero_queries_and_nan_scales():

@@ -99,6 +99,7 @@ def test_refusals_without_a_gpu(lib):
     assert attn(pages=0x10000, top_k=0) == 2 and attn(pages=0x10000, top_k=16385) == 2
     assert attn(pages=0x10000, top_k=2, mass_out=0x10000) == 3
     assert attn(q=W.Rows()) == 1 and attn(ws=None) == 1 and attn(ws=ctypes.c_void_p(0x10010)) == 1
+    assert attn(out=W.Rows(0x10000, 1, 0, 1)) == 1                  # rows on one another
     assert attn() == 4                                              # a workspace of no bytes
     a = W.KV8Attn(4, 4, 0, 1.0, rows)
 

@@ -360,29 +360,28 @@ class KV8Cache:
         import torch
         self._torch = torch
         self._types = {torch.float32: 0, torch.bfloat16: 1}
-        self.desc = KV8CacheDesc(n_seqs, n_kv_heads, head_dim, max_pages)
-        self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
-        need = (_sz * 7)()
-        _call("w4a8_kv8_bytes", _c.byref(self.desc), need)
-        S, H, D, P = self.shape
+        S, H, D, P = self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
+        self.desc = KV8CacheDesc(S, H, D, P)
+        _call("w4a8_kv8_bytes", _c.byref(self.desc), (_sz * 7)())     # refuses dimensions out of range
         shapes = ((S, H, P, 2, 64 * D), (S, H, P, 2), (S, H, P, D), (S, H, 2, 64, D), (S, H, P), (S,), (1,))
-        self.tensors = {}
-        for (name, dtype), shape, size in zip(self._NAMES, shapes, need):
+        own, got = tensors is None, {}
+        for (name, dtype), shape in zip(self._NAMES, shapes):
             dtype = getattr(torch, dtype)
-            t = torch.empty(shape, dtype=dtype, device=device) if tensors is None else tensors[name]
-            if t.dtype != dtype or t.numel() * t.element_size() != size or not t.is_contiguous():
+            t = got[name] = torch.empty(shape, dtype=dtype, device=device) if own else tensors[name]
+            if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
                 raise ValueError("KV8Cache: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
-            self.tensors[name] = t
-            setattr(self.desc, name, t.data_ptr())
-        self.device = self.tensors["codes"].device
-        if any(t.device != self.device for t in self.tensors.values()) or self.device.type != "cuda":
+        self.tensors = got
+        self.device = got["codes"].device
+        self._dev = got["codes"].get_device()
+        if self._dev < 0 or any(t.get_device() != self._dev for t in got.values()):
             raise ValueError("KV8Cache: the tensors must be on one CUDA device")
-        self._dev = self.device.index
+        self.desc = KV8CacheDesc(S, H, D, P, *[t.data_ptr() for t in got.values()])
         self._ref = _c.byref(self.desc)
         self._sizes, self._kept, self._lock = {}, {}, threading.Lock()
-        self._attention, self._select, self._evict = lib().w4a8_kv8_attention, lib().w4a8_kv8_select, lib().w4a8_kv8_evict
-        self._append, self._read = lib().w4a8_kv8_append, lib().w4a8_kv8_read
-        if tensors is None:
+        L = lib()
+        self._attention, self._select, self._evict = L.w4a8_kv8_attention, L.w4a8_kv8_select, L.w4a8_kv8_evict
+        self._append, self._read = L.w4a8_kv8_append, L.w4a8_kv8_read
+        if own:
             self.reset()
 
     @property

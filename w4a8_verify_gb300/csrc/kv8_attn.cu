@@ -16,8 +16,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
   using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float2 sm_ml[kJoinWarps];
   __shared__ __align__(16) float sm_o[kJoinWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = blockIdx.y;
-  const int rb = blockIdx.x * RPC + warp / WPR, first = warp % WPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = blockIdx.x;
+  const int rb = blockIdx.y * RPC + warp / WPR, first = warp % WPR;
   const Kv8Segment sg = kv8_segment(c, a, geo, seg);
   const int r = sg.cb * geo.RB + rb, i = a.pages ? sg.i : r / geo.G, s = sg.s;
   const int L = kv8_len(c, c.len, s), cnt = kv8_count(c, a.counts, s, a.n);
@@ -154,7 +154,7 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.CB = (g.R + g.RB - 1) / g.RB;
   p->segments = (size_t)c->n_seqs * c->n_kv_heads * (a->pages ? g.n : g.CB);
   const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
-  if (units >= (size_t)1 << 31 || p->segments > 65535) return W4A8_ERR_SHAPE;
+  if (units >= (size_t)1 << 31 || p->segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.ng = wide ? 1 : kKv8Warps / wc;
   g.ctas = (int)(units < (size_t)kKv8Ctas ? units : (size_t)kKv8Ctas);
   p->prefix = 0;
@@ -192,6 +192,8 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   if (ok == W4A8_OK) ok = plan_of(c, a, &p);
   if (ok != W4A8_OK) return ok;
   const size_t el = kv8_elem(a->dtype);
+  // rows of out that lie on one another would be written in any order
+  if ((c->n_seqs > 1 && !a->out.seq) || (a->n > 1 && !a->out.row) || (a->n_heads > 1 && !a->out.head)) return W4A8_ERR_ARG;
   if (!a->q.data || !a->out.data || !workspace || !aligned(workspace, 256) || !aligned(a->q.data, el) ||
       !aligned(a->out.data, el) || !aligned(a->k.data, el) || !aligned(a->v.data, el))
     return W4A8_ERR_ARG;
@@ -211,7 +213,7 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   const int rows = p.geo.R < p.geo.RB ? p.geo.R : p.geo.RB;
   auto join = [&](auto one, auto four) {
     const bool few = (int64_t)rows * (int64_t)p.segments <= 4 * kKv8Ctas;
-    const dim3 grid((unsigned)(few ? rows : (rows + 3) / 4), (unsigned)p.segments);
+    const dim3 grid((unsigned)p.segments, (unsigned)(few ? rows : (rows + 3) / 4));
     return launch_pdl(few ? one : four, grid, dim3(32 * kJoinWarps), 0, st, *c, *a, p.geo, ws);
   };
   if (f32)

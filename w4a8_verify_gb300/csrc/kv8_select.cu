@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(w4a8_kv8_cache c, w
   constexpr int DL = D / 8;  // dims of a lane
   __shared__ float red[kScoreThreads / 32];
   __shared__ __align__(16) int8_t codes[kKv8MaxGroup * D];
-  const int h = blockIdx.y, s = blockIdx.z / n, i = blockIdx.z % n;
+  const int h = blockIdx.y, s = blockIdx.x / n, i = blockIdx.x % n;
   const int L = kv8_len(c, c.len, s);
   const int cnt = kv8_count(c, counts, s, n);
   const int whole = L < 0 ? 0 : L / kPage;
-  if (i >= cnt || whole <= top_k || (int)blockIdx.x * kScorePages >= whole) return;  // nothing to choose between
+  if (i >= cnt || whole <= top_k || (int)blockIdx.z * kScorePages >= whole) return;  // nothing to choose between
   const T* q = static_cast<const T*>(qr.data) + (int64_t)s * qr.seq + (int64_t)i * qr.row + (int64_t)h * G * qr.head;
   float m = 0.0f;
   for (int e = threadIdx.x; e < G * D; e += kScoreThreads) m = max_nan(m, fabsf(kv8_load(q + (e / D) * qr.head + e % D)));
@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(w4a8_kv8_cache c, w
   __syncthreads();
   const int lane8 = threadIdx.x & 7;
   const size_t pair = kv8_pair(c, s, h);
-  uint32_t* out = keys + ((size_t)blockIdx.z * c.n_kv_heads + h) * c.max_pages;
-  const int p1 = min(whole, ((int)blockIdx.x + 1) * kScorePages);
-  for (int p0 = blockIdx.x * kScorePages; p0 < p1; p0 += kScoreThreads / 8) {  // uniform: the shuffles need every lane
+  uint32_t* out = keys + ((size_t)blockIdx.x * c.n_kv_heads + h) * c.max_pages;
+  const int p1 = min(whole, ((int)blockIdx.z + 1) * kScorePages);
+  for (int p0 = blockIdx.z * kScorePages; p0 < p1; p0 += kScoreThreads / 8) {  // uniform: the shuffles need every lane
     const int p = p0 + (threadIdx.x >> 3);
     const int phys = p < p1 ? kv8_phys(c, pair, p) : -1;
     const size_t pg = kv8_page(c, pair, max(phys, 0));
@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(512) k_kv8_pick(w4a8_kv8_cache c, const int32_
   griddep_enter();
   extern __shared__ uint32_t sm[];
   __shared__ uint32_t hist[256];
-  const int h = blockIdx.x, s = blockIdx.y / n, i = blockIdx.y % n;
+  const int h = blockIdx.y, s = blockIdx.x / n, i = blockIdx.x % n;
   const int L = kv8_len(c, c.len, s);
   const int cnt = kv8_count(c, counts, s, n);
   const int whole = L < 0 || i >= cnt ? 0 : L / kPage;
-  const size_t at = (size_t)blockIdx.y * c.n_kv_heads + h;
+  const size_t at = (size_t)blockIdx.x * c.n_kv_heads + h;
   int32_t* out = pages + at * top_k;
   const int kept = min(whole, top_k);
   for (int j = kept + threadIdx.x; j < top_k; j += blockDim.x) out[j] = -1;
@@ -268,7 +268,7 @@ static w4a8_status select_args(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a) 
   if (ok != W4A8_OK) return ok;
   if (!a || !kv8_dtype(a->dtype)) return W4A8_ERR_ARG;
   if (a->n < 1 || a->n > kKv8MaxRows || a->n_heads < 1 || a->n_heads % c->n_kv_heads ||
-      a->n_heads / c->n_kv_heads > kKv8MaxGroup || (int64_t)c->n_seqs * a->n > 65535)
+      a->n_heads / c->n_kv_heads > kKv8MaxGroup)
     return W4A8_ERR_SHAPE;
   return W4A8_OK;
 }
@@ -297,8 +297,8 @@ W4A8_API w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_att
   uint32_t* keys = static_cast<uint32_t*>(workspace);
   const int G = a->n_heads / c->n_kv_heads, n = a->n;
   if (c->max_pages > top_k) {
-    const dim3 grid((unsigned)((c->max_pages + kScorePages - 1) / kScorePages), (unsigned)c->n_kv_heads,
-                    (unsigned)(c->n_seqs * n));
+    const dim3 grid((unsigned)(c->n_seqs * n), (unsigned)c->n_kv_heads,
+                    (unsigned)((c->max_pages + kScorePages - 1) / kScorePages));
     auto run = [&](auto kern) {
       return launch_pdl(kern, grid, dim3(kScoreThreads), 0, st, *c, a->q, a->counts, n, G, top_k, first_pages, last_pages,
                         keys);
@@ -310,7 +310,7 @@ W4A8_API w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_att
   }
   const size_t smem = (size_t)c->max_pages * 4;
   W4A8_CUDA_TRY(kv8_smem<k_kv8_pick>(kKv8MaxPages * 4));
-  W4A8_CUDA_TRY(launch_pdl(k_kv8_pick, dim3((unsigned)c->n_kv_heads, (unsigned)(c->n_seqs * n)), dim3(512), smem, st, *c,
+  W4A8_CUDA_TRY(launch_pdl(k_kv8_pick, dim3((unsigned)(c->n_seqs * n), (unsigned)c->n_kv_heads), dim3(512), smem, st, *c,
                            a->counts, n, top_k, (const uint32_t*)keys, pages_out));
   return W4A8_OK;
 }
