@@ -48,7 +48,9 @@ constexpr int kKv8RingBytes = 196608; // ring of pages per SM: 12 of 16 KB or 24
 constexpr float kPScale = 128.0f, kPSlack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
 constexpr int kWideRows = 128;        // query rows of a segment of a wide call (kv8_wide.cu)
 constexpr int kRowTile = 16;          // fp32 rows of one part
-constexpr int kRowChunk = 4;          // query rows that a row warp takes at a time
+// Query rows that a row warp takes at a time: few where warps are many (beside the page warps), more where a call has
+// many rows for the same keys.
+constexpr int kRowChunk = 4, kWideRowChunk = 8;
 
 struct Kv8Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a segment's problem (n G, or G with lists)
@@ -193,12 +195,12 @@ struct Kv8Unit {
   float sk, sv;
 };
 
-// One part in plain fp32: the 16 (or fewer) fp32 rows of tile f of a segment for kRowChunk of its query rows, by one
+// One part in plain fp32: the 16 (or fewer) fp32 rows of tile f of a segment for CHUNK of its query rows, by one
 // warp.  A lane holds its dims of the 16 keys, then of the 16 values, in registers, and its dims of the query rows; the
 // 16 dot products of a row are summed over the lanes in 16 exchanges that leave token lane / 2 in each lane.  A
 // token that a row does not see is left out of its sums, whatever it holds.  Beside the page warps a load takes
 // microseconds, so everything is asked for at once (the values into L2).
-template <typename T, int D>
+template <typename T, int D, int CHUNK>
 __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws,
                              int seg, int f, int chunk, float (*pt)[kRowTile]) {
   constexpr unsigned FULL = 0xffffffffu;
@@ -211,7 +213,7 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
   const int fresh = f - kPage / kRowTile;
   const int nv = min(kRowTile, fresh < 0 ? L % kPage - f * kRowTile : a.k.data ? cnt - fresh * kRowTile : 0);
   const int rows = min(geo.RB, (a.pages ? geo.G : cnt * geo.G) - sg.cb * geo.RB);  // of this column block
-  const int r0 = chunk * kRowChunk, nr = min(rows - r0, kRowChunk);
+  const int r0 = chunk * CHUNK, nr = min(rows - r0, CHUNK);
   if (nv <= 0 || nr <= 0) return;
   const float* kt = c.tail + kv8_pair(c, sg.s, sg.h) * 2 * kPage * D + f * kRowTile * D + E * lane;
   const T* kn = static_cast<const T*>(a.k.data) + sg.s * a.k.seq + sg.h * a.k.head + (int64_t)fresh * kRowTile * a.k.row + E * lane;
@@ -249,47 +251,69 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
 #pragma unroll
     for (int e = 0; e < E; ++e) q[e] = kv8_load(p + e);
   };
-  float q[E], next[E];
-  query(0, q);
+  // two rows at a time, the next two on their way: a row's chain of exchanges leaves room for another's
+  float q[2][E], next[2][E];
+  query(0, q[0]);
+  query(min(1, nr - 1), q[1]);
   load16(kt, kn, a.k.row);
   const float qscale = a.scale * 1.4426950408889634f;
   const int tok = lane >> 1;
   const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0;
 #pragma unroll 1
-  for (int r = 0; r < nr; ++r) {
-    query(min(r + 1, nr - 1), next);
-    float x[kRowTile];
+  for (int r = 0; r < nr; r += 2) {
+    query(min(r + 2, nr - 1), next[0]);
+    query(min(r + 3, nr - 1), next[1]);
+    float x[2][kRowTile];
 #pragma unroll
-    for (int i = 0; i < kRowTile; ++i) x[i] = 0.0f;
+    for (int y = 0; y < 2; ++y) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+      for (int i = 0; i < kRowTile; ++i) x[y][i] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kRowTile; ++i) x[i] = fmaf(q[e], kv[i][e], x[i]);
-      q[e] = next[e];
+      for (int e = 0; e < E; ++e) {
+#pragma unroll
+        for (int i = 0; i < kRowTile; ++i) x[y][i] = fmaf(q[y][e], kv[i][e], x[y][i]);
+        q[y][e] = next[y][e];
+      }
     }
 #pragma unroll
     for (int w = 8; w > 0; w >>= 1) {
       const bool up = lane & (2 * w);
 #pragma unroll
-      for (int i = 0; i < w; ++i) {
-        const float keep = up ? x[i + w] : x[i], give = up ? x[i] : x[i + w];
-        x[i] = keep + __shfl_xor_sync(FULL, give, 2 * w);
-      }
-    }
-    const float s = (x[0] + __shfl_xor_sync(FULL, x[0], 1)) * qscale;
-    bool see = tok < nv;
-    if (fresh >= 0) {
-      const int i = node_of(r);
-      const uint64_t mask = a.mask ? a.mask[(size_t)sg.s * a.n + i] : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
-      see = see && (mask >> (fresh * kRowTile + tok) & 1ull);
-    }
-    const float m = warp_max(see ? s : -INFINITY);
-    const float p = see ? ex2(s - (m == -INFINITY ? 0.0f : m)) : 0.0f;
-    float l = p;
+      for (int i = 0; i < w; ++i)
 #pragma unroll
-    for (int w = 2; w < 32; w <<= 1) l += __shfl_xor_sync(FULL, l, w);
-    if (lane == 0) ws.rml[at + r] = make_float2(m, l);
-    if (!(lane & 1)) pt[r][tok] = see ? p : -1.0f;
+        for (int y = 0; y < 2; ++y) {
+          const float keep = up ? x[y][i + w] : x[y][i], give = up ? x[y][i] : x[y][i + w];
+          x[y][i] = keep + __shfl_xor_sync(FULL, give, 2 * w);
+        }
+    }
+    float s[2], m[2], l[2];
+    bool see[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      s[y] = (x[y][0] + __shfl_xor_sync(FULL, x[y][0], 1)) * qscale;
+      see[y] = tok < nv;
+      if (fresh >= 0) {
+        const int i = node_of(min(r + y, nr - 1));
+        const uint64_t mask = a.mask ? a.mask[(size_t)sg.s * a.n + i] : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
+        see[y] = see[y] && (mask >> (fresh * kRowTile + tok) & 1ull);
+      }
+      m[y] = see[y] ? s[y] : -INFINITY;
+    }
+#pragma unroll
+    for (int w = 16; w > 1; w >>= 1)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) m[y] = fmaxf(m[y], __shfl_xor_sync(FULL, m[y], w));
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const float p = see[y] ? ex2(s[y] - (m[y] == -INFINITY ? 0.0f : m[y])) : 0.0f;
+      l[y] = p;
+      if (!(lane & 1) && r + y < nr) pt[r + y][tok] = see[y] ? p : -1.0f;
+    }
+#pragma unroll
+    for (int w = 2; w < 32; w <<= 1)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) l[y] += __shfl_xor_sync(FULL, l[y], w);
+    if (lane < 2 && r + lane < nr) ws.rml[at + r + lane] = lane ? make_float2(m[1], l[1]) : make_float2(m[0], l[0]);
   }
   load16(kt + kPage * D, vn, a.v.row);
   __syncwarp();
@@ -342,7 +366,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const int chunks = (min(geo.R, C::RB) + kRowChunk - 1) / kRowChunk;
     const int parts = geo.segments * geo.tiles * chunks;
     for (int x = (warp - kKv8Warps) * gridDim.x + blockIdx.x; x < parts; x += gridDim.x * kKv8RowWarps)
-      kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks,
+      kv8_row_part<T, D, kRowChunk>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks,
                          row_p[warp - kKv8Warps]);
     return;
   }
@@ -759,15 +783,16 @@ cudaError_t kv8_split_dispatch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, 
     default: return kv8_split_launch<T, D, 12>(c, a, geo, ws, st);
   }
 }
-// Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu): more than 128 rows, or at least eight tiles
-// and 16384 tile-pages of room (the lengths are not known here).  Measured with full caches of 8 KV heads of 128, split
-// kernel / wide kernel, us: fp32, 64 rows, 4096 tokens 29.9 / 32.3 and 16384 tokens 64.7 / 50.0; 128 rows 38.9 / 37.2
-// and 111 / 55; bf16, 128 rows, 4096 tokens 27.8 / 31.8 and 16384 tokens 58.9 / 41.5; 256 rows, 1024 tokens 49.9 / 34.8;
-// 32 rows, 32768 tokens 60.6 / 65.4 (fp32) and 35.2 / 45.8 (bf16).
+// Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu): more than 128 rows, or more than 32 and
+// 2^21 tile-page-dims of room (the lengths are not known here).  Measured with full caches of 8 KV heads of 128, split
+// kernel / wide kernel, us: fp32, 64 rows, 4096 tokens 29.9 / 32.3 and 16384 tokens 64.7 / 48.8; 128 rows 38.9 / 35.9
+// and 111 / 53.6; bf16, 128 rows, 4096 tokens 27.8 / 31.8 and 16384 tokens 58.9 / 42.4; 256 rows, 1024 tokens 49.9 / 35;
+// 32 rows, 32768 tokens 60.6 / 64.5 (fp32) and 35.2 / 45.8 (bf16).  Heads of 64: 64 rows, 8192 tokens 27.5 / 28.7 and
+// 16384 tokens 41.5 / 38.6 (fp32), 28.0 / 32.8 (bf16).
 inline bool kv8_is_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, int R) {
   if (a.pages) return false;
-  const int tiles = (R + 3) / (a.dtype == W4A8_F32 ? 4 : 8);
-  return R > kWideRows || (tiles >= 8 && (int64_t)tiles * c.n_seqs * c.n_kv_heads * c.max_pages >= 16384);
+  const int64_t tiles = (R + 3) / (a.dtype == W4A8_F32 ? 4 : 8);
+  return R > kWideRows || (R > 32 && tiles * c.n_seqs * c.n_kv_heads * c.max_pages * c.head_dim >= 1 << 21);
 }
 cudaError_t kv8_wide(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 // one translation unit per head size and element type

@@ -47,11 +47,13 @@ struct Wide {
   static_assert(cO + NO * D <= 512, "tensor memory");
   // shared memory
   static constexpr int sK = kRing * PAGE, sV = sK + 2 * TILE, sBar = sV + 2 * TILE, sFac = sBar + 256;
-  static constexpr int sPrefix = sFac + kFac * kWideRows * 4 + 64;
+  static constexpr int QROW = D * (int)sizeof(T) + 16;  // a staged query row: 16 bytes on, so that lanes of a row each do not collide
+  static constexpr int sQ = sFac + kFac * kWideRows * 4 + 64;
+  static constexpr int sPrefix = sQ + kWideRows * QROW;
 };
 
 struct Bars {  // mbarriers
-  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], lo_empty;
+  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], lo_empty, q_full, q_empty;
 };
 static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       mbar_init(&bar.o_empty[i], kSumWarps);
     }
     mbar_init(&bar.lo_empty, kSoftWarps);
+    mbar_init(&bar.q_full, 1), mbar_init(&bar.q_empty, kSoftWarps);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
@@ -211,11 +214,26 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     return ok;
   };
 
+  // query row of the run's row `row`
+  auto query_row = [&](const Run& r, int row) {
+    const int rr = r.sg.cb * kWideRows + row;
+    return static_cast<const T*>(a.q.data) + r.sg.s * a.q.seq + (rr / geo.G) * a.q.row + (r.sg.h * geo.G + rr % geo.G) * a.q.head;
+  };
+  auto rows_of = [&](const Run& r) { return max(0, min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows)); };
   if (warp == kCopyWarp) {
     Turn<kRing> e;
-    int n = 0;
-    for (int x = u0; x < u1 && ok;) {
+    int n = 0, runs = 0;
+    for (int x = u0; x < u1 && ok; ++runs) {
       const Run r = run_at(x);
+      if (geo.vec) {  // the run's query rows
+        const int rows = rows_of(r);
+        if (runs > 0 && !wait(&bar.q_empty, (runs - 1) & 1)) break;
+        if (lane == 0) mbar_expect_tx(&bar.q_full, rows * D * sizeof(T));
+        __syncwarp();
+        for (int row = lane; row < rows; row += 32)
+          bulk_g2s(sm + C::sQ + row * C::QROW, query_row(r, row), D * sizeof(T), &bar.q_full);
+        __syncwarp();
+      }
       Batch now{}, then = batch_at(r, 0, 0);
       for (int p = 0; p < r.pages && ok; ++p, ++n, e.next()) {
         if ((p & 31) == 0) now = then, then = batch_at(r, p + 32, 0);
@@ -235,6 +253,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     }
     // no copy in flight when the CTA ends
     for (int i = max(0, n - kRing); i < n; ++i) (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
+    if (geo.vec && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1);
   } else if (warp >= kConv0 && warp < kMmaWarp) {
     // the first half of the warps takes the keys, the second the values
     constexpr int kHalf = kConvWarps / 2;
@@ -319,20 +338,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
     Turn<2> b;
     Turn<kFac> fb;
-    int n = 0, freed = 0;  // pages done; S buffers released to the products (page n needs n + 1 of them)
+    int n = 0, runs = 0, freed = 0;  // pages and runs done; S buffers released to the products (page n needs n + 1 of them)
     // the logit's factor is not negative (Q takes the scale's sign), so the largest logit is the largest S
     const double lscale = fabs((double)a.scale) * 1.4426950408889634;
     const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
-      const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      const int rows = rows_of(r);
       Batch now{}, then = batch_at(r, 0, 0);
       // Q of the run: the products of the run before are done (its last O' was waited for)
       float colfac, collow, m = -INFINITY, l = 0.0f;
       {
-        const int rr = r.sg.cb * kWideRows + row;
-        const T* q = static_cast<const T*>(a.q.data) + r.sg.s * a.q.seq + (rr / geo.G) * a.q.row +
-                     (r.sg.h * geo.G + rr % geo.G) * a.q.head;
+        const T* q = geo.vec ? reinterpret_cast<const T*>(sm + C::sQ + row * C::QROW) : query_row(r, min(row, max(rows - 1, 0)));
+        if (geo.vec && !wait(&bar.q_full, runs & 1)) break;
         float am = 0.0f;
         auto load8 = [&](int d, float (&v)[8]) {
           if (row >= rows) {
@@ -385,6 +403,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       }
       tc_before();
       __syncwarp();
+      if (geo.vec && lane == 0) mbar_arrive(&bar.q_empty);
       for (int y = 0; y < 2 && freed < n + r.pages; ++y, ++freed)
         if (lane == 0) mbar_arrive(&bar.s_empty[freed & 1]);
       if (NQ == 2 && lane == 0) mbar_arrive(&bar.lo_empty);
@@ -495,6 +514,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         ws.ml[at * kWideRows + row] = make_float2(m, l / C::PSCALE);
       }
       x += r.pages;
+      ++runs;
     }
   } else {
     // values: quadrant of lanes, half of the columns
@@ -506,7 +526,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     Turn<kFac> fb;
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
-      const int rows = min(kWideRows, r.cnt * geo.G - r.sg.cb * kWideRows);
+      const int rows = rows_of(r);
       Batch now{}, then = batch_at(r, 0, 1);
       float O[DH];
 #pragma unroll
@@ -554,13 +574,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
 // the wait for that kernel comes last, for the join that follows.
 constexpr int kRowsWarps = 2;
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kRowsWarps) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+__global__ void __launch_bounds__(32 * kRowsWarps, 8) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
   griddep_launch();
-  __shared__ __align__(16) float row_p[kRowsWarps][kRowChunk][kRowTile];
-  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
+  __shared__ __align__(16) float row_p[kRowsWarps][kWideRowChunk][kRowTile];
+  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kWideRowChunk - 1) / kWideRowChunk;
   const int warp = threadIdx.x >> 5, x = blockIdx.x * kRowsWarps + warp;
   if (x < geo.segments * geo.tiles * chunks)
-    kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[warp]);
+    kv8_row_part<T, D, kWideRowChunk>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[warp]);
   griddep_wait();
 }
 
@@ -572,7 +592,7 @@ cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8G
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
   if (e != cudaSuccess) return e;
-  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kRowChunk - 1) / kRowChunk;
+  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kWideRowChunk - 1) / kWideRowChunk;
   const int64_t parts = (int64_t)geo.segments * geo.tiles * chunks;
   return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)((parts + kRowsWarps - 1) / kRowsWarps)), dim3(32 * kRowsWarps), 0, st, c,
                     a, geo, ws);
