@@ -245,9 +245,10 @@ w4a8_status w4a8_kv8_check(const w4a8_kv8_cache* c, uint32_t* flags);
  * position len[s] + j of sequence s; pages that complete are quantised, the rest goes to the tail.
  * counts: device int32[n_seqs] in 0..n, NULL = n.  index: device int32 [n_seqs][n], NULL = the rows
  * in order: position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of
- * a draft tree; the same row may come twice); with it n <= 1024, without it n_src >= n.  The new lengths go to len_out (device int32[n_seqs]);
- * len_out == c->len advances the cache, which reads the rows from then on.  A sequence that would
- * pass 64 * max_pages + 63 tokens stays as it was, as does one with a row out of range. */
+ * a draft tree; the same row may come twice); with it n <= 1024, without it n_src >= n (W4A8_ERR_SHAPE).  The new
+ * lengths go to len_out (device int32[n_seqs]); len_out == c->len advances the cache, which reads the
+ * rows from then on.  A sequence that would pass 64 * max_pages + 63 tokens stays as it was, as does
+ * one with a row out of range; an n beyond that is W4A8_ERR_CAPACITY. */
 w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,
                             int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);
 /* Device.  Positions first[s] .. first[s] + n - 1 of every sequence as the cache holds them (s * c of
@@ -276,23 +277,28 @@ typedef struct {
 /* Host.  Scratch bytes of w4a8_kv8_attention (the pointers in a are not read, only whether they are NULL). */
 w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, size_t* bytes);
 /* Device.  out[s][i][h] = sum_t w_t v_t with w = softmax over the committed tokens (whole pages s * c, the open
- * page's fp32 rows) and the visible new rows; a row that sees nothing is 0.  Logits, softmax statistics and sums
- * are fp32; products of fp32 operands are formed from f16 hi/lo splits (about 2^-21 relative), those of bf16
- * calls from one f16 factor (weights 2^-11).  A new row has no effect on the rows that do
- * not see it, whatever it holds (NaN and infinities too), and rows at or behind counts[s] are not read.  The result does not depend on timing; it may depend, in
- * its last bits, on the other sequences of the call (they share the splits of the long axis).  workspace: 256-byte aligned,
- * not shared by calls that may overlap; needs no initialisation. */
+ * page's fp32 rows) and the visible new rows; a row that sees nothing is 0.  Logits, softmax
+ * statistics and sums are fp32.  The products with the fp32 rows are plain fp32; those with the
+ * pages' codes use f16 hi/lo pairs of q and of the weights in fp32 calls (about 2^-21 relative) and
+ * one f16 factor each in bf16 calls (2^-11).  A new row has no effect on the rows that do not see
+ * it, whatever it holds (NaN and infinities too), and rows at or behind counts[s] are not read.
+ * The result does not depend on timing; it may depend, in its last bits, on the other sequences of
+ * the call (they share the splits of the long axis).  out's strides must not be 0 where that axis
+ * has more than one entry (W4A8_ERR_ARG).  A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
+ * n_kv_heads * B < 2^22, and times the pages that a row reads < 2^31, with B = n (with pages), else
+ * the blocks of at most 128 and at least 12 query rows (n * heads of a KV head) it is cut into.
+ * workspace: 256-byte aligned, not shared by calls that may overlap; needs no initialisation. */
 w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
                                size_t workspace_bytes, void* stream);
 
-/* Device.  For each new row and KV head the top_k (1..16384) whole pages of best score, as an ascending list padded with -1
- * (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the largest over the head's query group of
+/* Device.  For each new row and KV head the top_k (1..16384) whole pages of best score, as an
+ * ascending list padded with -1 (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the largest over the head's query group of
  * q . (sum of the page's keys), in int8 like the pages: the group's queries get codes at one scale
  * (w4a8_quantize_rows' rule over its heads * head_dim values) and
  *   score = fl32(key scale * fl32(max_h sum_d code[h][d] * sums[d]))  with the exact integer sum.
  * The first first_pages and the last last_pages whole pages come before any score, equal scores go to the lowest
- * page, a NaN score counts as infinity, a group whose absmax is not finite has codes 0.  Rows behind counts get lists of -1.  q as in w4a8_kv8_attn (dtype, n,
- * n_heads, q and counts of a are used).  workspace: w4a8_kv8_select_workspace_bytes, 256-byte aligned. */
+ * page, a NaN score counts as infinity, a group whose absmax is not finite has codes 0.  Rows behind
+ * counts get lists of -1.  q as in w4a8_kv8_attn (dtype, n, n_heads, q and counts of a are used).  workspace: w4a8_kv8_select_workspace_bytes, 256-byte aligned. */
 w4a8_status w4a8_kv8_select_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, size_t* bytes);
 w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, int top_k, int first_pages,
                             int last_pages, int32_t* pages_out, void* workspace, size_t workspace_bytes,

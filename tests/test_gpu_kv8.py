@@ -266,6 +266,21 @@ def test_trees_chains_and_counts(n, H, G, D, dtype):
         _attend(cache, ref, q, k, v, D ** -0.5, counts=[n - 1, 0, n], mass=torch.rand(3, H, cache.shape[3], device="cuda"))
 
 
+@pytest.mark.parametrize("n,H,G,D,dtype", [(64, 2, 4, 128, "fp32"), (64, 2, 2, 64, "bf16"), (48, 1, 16, 64, "fp32"),
+                                           (20, 3, 5, 128, "bf16")])
+def test_padded_batches(n, H, G, D, dtype):
+    """Sequences of few rows between full ones: blocks of rows that nobody has take no part."""
+    rng = np.random.default_rng(n + D)
+    lens = [200, 330, 64, 129, 500]
+    cache, ref = _filled(rng, 5, H, D, lens, dtype)
+    q = _rows(rng, 5, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, 5, n, H, D, dtype), _rows(rng, 5, n, H, D, dtype)
+    for counts in ([1, n, 3, n, 2], [n, 0, n - 1, 1, n], [0, 1, n // 2 + 1, 0, n // 4 + 1]):
+        _attend(cache, ref, q, k, v, D ** -0.5, counts=counts)
+        _attend(cache, ref, q, k, v, D ** -0.5, counts=counts, mass=torch.rand(5, H, cache.shape[3], device="cuda"))
+    assert cache.check() == 0
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("n", [4, 16, 40])
 def test_masked_rows_with_nan_and_infinities(dtype, n):

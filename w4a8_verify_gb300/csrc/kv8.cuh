@@ -61,19 +61,9 @@ __device__ __forceinline__ size_t kv8_page(const w4a8_kv8_cache& c, size_t pair,
   return pair * c.max_pages + phys;
 }
 
-// Byte of (token, dim) inside a page's keys or values (the order the header documents).
-__device__ __forceinline__ int kv8_key_byte(int D, int tok, int d) {
-  return (((((tok >> 4) * (D >> 5) + (d >> 5)) * 8 + (tok & 7)) * 4 + ((d >> 3) & 3)) * 2 + ((d >> 2) & 1)) * 8 +
-         ((tok >> 3) & 1) * 4 + (d & 3);
-}
-__device__ __forceinline__ int kv8_val_byte(int tok, int d) {
-  return ((((((d >> 4) * 2 + (tok >> 5)) * 8 + (d & 7)) * 4 + ((tok & 7) >> 1)) * 2 + ((tok >> 4) & 1)) * 2 +
-          ((d >> 3) & 1)) * 4 + ((tok >> 3) & 1) * 2 + (tok & 1);
-}
-
 // Committed length of sequence s, or -1 (and the status bit) where it is out of range.
 __device__ __forceinline__ int kv8_len(const w4a8_kv8_cache& c, const int32_t* len, int s) {
-  const int L = len[s];
+  const int L = __ldcg(len + s);  // from L2: a kernel that starts early reads it before it waits for the last one
   if (L < 0 || L > kPage * c.max_pages + kPage - 1) {
     atomicOr(c.ctl, (unsigned)FLAG_ERR_CAPACITY);
     return -1;
@@ -83,7 +73,7 @@ __device__ __forceinline__ int kv8_len(const w4a8_kv8_cache& c, const int32_t* l
 // Rows of sequence s in a call of n, or -1 (and the status bit) where the count is out of range.
 __device__ __forceinline__ int kv8_count(const w4a8_kv8_cache& c, const int32_t* counts, int s, int n) {
   if (!counts) return n;
-  const int v = counts[s];
+  const int v = __ldcg(counts + s);
   if (v < 0 || v > n) {
     atomicOr(c.ctl, (unsigned)FLAG_ERR_CAPACITY);
     return -1;
@@ -100,15 +90,11 @@ __device__ __forceinline__ int kv8_phys(const w4a8_kv8_cache& c, size_t pair, in
   return v;
 }
 
+__device__ __forceinline__ float kv8_float(float v) { return v; }
+__device__ __forceinline__ float kv8_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T>
-__device__ __forceinline__ float kv8_load(const T* p);
-template <>
-__device__ __forceinline__ float kv8_load<float>(const float* p) {
-  return *p;
-}
-template <>
-__device__ __forceinline__ float kv8_load<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return __bfloat162float(*p);
+__device__ __forceinline__ float kv8_load(const T* p) {
+  return kv8_float(*p);
 }
 template <typename T>
 __device__ __forceinline__ void kv8_store(T* p, float v);

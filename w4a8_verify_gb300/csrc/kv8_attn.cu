@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
     if (un.pages > 0) {
       const int U = ws.prefix[c.n_seqs];
       const Kv8Workers wk = kv8_workers(U, geo.ctas, geo.ng);
-      const int u0 = ws.prefix[s] + (seg - s * (a.pages ? a.n : geo.CB) * c.n_kv_heads) * un.pages, u1 = u0 + un.pages;
+      const int of = a.pages ? sg.i * c.n_kv_heads + sg.h : sg.h * kv8_blocks(geo, cnt) + sg.cb;  // segment of the sequence
+      const int u0 = ws.prefix[s] + of * un.pages, u1 = u0 + un.pages;
       const int w0 = worker_of(u0, wk.W, U), w1 = worker_of(u1 - 1, wk.W, U);
       early = worker_begin(w1 + 1, wk.W, U) > u1;
       c0 = w0 / wk.ng;
@@ -156,9 +157,12 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   const size_t units = p->segments * (a->pages && a->top_k < c->max_pages ? a->top_k : c->max_pages);
   if (units >= (size_t)1 << 31 || p->segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.ng = wide ? 1 : kKv8Warps / wc;
-  g.ctas = (int)(units < (size_t)kKv8Ctas ? units : (size_t)kKv8Ctas);
-  p->prefix = 0;
   g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);
+  // CTAs for the pages, or (split kernel) for a round of its row warps' parts
+  const size_t parts = wide ? 0 : p->segments * g.tiles * ((g.R < g.RB ? g.R : g.RB) + kRowChunk - 1) / kRowChunk;
+  const size_t ctas = units > parts / kKv8RowWarps ? units : parts / kKv8RowWarps;
+  g.ctas = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas);
+  p->prefix = 0;
   g.segments = (int)p->segments;
   const size_t slots = g.ctas + 2 * p->segments, rslots = p->segments * g.tiles, row = (size_t)g.RB * 4;
   p->ml = up256(((size_t)c->n_seqs + 1) * 4);
@@ -203,7 +207,7 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
                 reinterpret_cast<float*>(base + p.o), reinterpret_cast<float2*>(base + p.rml),
                 reinterpret_cast<float*>(base + p.ro), a->mass_out ? reinterpret_cast<float2*>(base + p.fin) : nullptr,
                 a->mass_out ? reinterpret_cast<float2*>(base + p.page) : nullptr};
-  p.geo.vec = kv8_vec_rows(a->q, a->dtype) ? 1 : 0;
+  p.geo.vec = (kv8_vec_rows(a->q, a->dtype) ? 1 : 0) | (kv8_vec_rows(a->k, a->dtype) ? 2 : 0) | (kv8_vec_rows(a->v, a->dtype) ? 4 : 0);
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
   if (kv8_is_wide(*c, *a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));

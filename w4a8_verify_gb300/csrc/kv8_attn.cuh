@@ -48,9 +48,7 @@ constexpr int kKv8RingBytes = 196608; // ring of pages per SM: 12 of 16 KB or 24
 constexpr float kPScale = 128.0f, kPSlack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
 constexpr int kWideRows = 128;        // query rows of a segment of a wide call (kv8_wide.cu)
 constexpr int kRowTile = 16;          // fp32 rows of one part
-// Query rows that a row warp takes at a time: few where warps are many (beside the page warps), more where a call has
-// many rows for the same keys.
-constexpr int kRowChunk = 4, kWideRowChunk = 8;
+constexpr int kRowChunk = 4;          // query rows that a row warp takes at a time
 
 struct Kv8Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a segment's problem (n G, or G with lists)
@@ -58,7 +56,7 @@ struct Kv8Geom {       // of one call, the same for every kernel of it
   int ctas, ng;        // of the split kernel, and its workers in each at most
   int tiles;           // row tiles of a segment: four of the open page, those of the new rows
   int segments;
-  int vec;             // q rows may be read 16 bytes at a time
+  int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
 };
 
 struct Kv8Scratch {    // workspace pointers
@@ -91,9 +89,11 @@ __device__ __forceinline__ Kv8Segment kv8_segment(const w4a8_kv8_cache& c, const
   if (a.pages) return {seg / H / a.n, seg % H, seg / H % a.n, 0};
   return {seg / g.CB / H, seg / g.CB % H, 0, seg % g.CB};
 }
-// Segments of a sequence: (KV head, column block), or (row, KV head) with page lists.
+// Column blocks that hold rows of a sequence of cnt rows: a padded batch reads no pages for the others.
+__device__ __forceinline__ int kv8_blocks(const Kv8Geom& g, int cnt) { return (cnt * g.G + g.RB - 1) / g.RB; }
+// Segments of a sequence that have rows: (KV head, column block), or (row, KV head) with page lists.
 __device__ __forceinline__ int kv8_segments(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& g, int cnt) {
-  return a.pages ? cnt * c.n_kv_heads : cnt > 0 ? c.n_kv_heads * g.CB : 0;
+  return c.n_kv_heads * (a.pages ? cnt : kv8_blocks(g, cnt));
 }
 // Pages of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be synchronised after it.
 __device__ __forceinline__ void kv8_prefix(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, int* prefix) {
@@ -195,12 +195,12 @@ struct Kv8Unit {
   float sk, sv;
 };
 
-// One part in plain fp32: the 16 (or fewer) fp32 rows of tile f of a segment for CHUNK of its query rows, by one
+// One part in plain fp32: the 16 (or fewer) fp32 rows of tile f of a segment for kRowChunk of its query rows, by one
 // warp.  A lane holds its dims of the 16 keys, then of the 16 values, in registers, and its dims of the query rows; the
 // 16 dot products of a row are summed over the lanes in 16 exchanges that leave token lane / 2 in each lane.  A
 // token that a row does not see is left out of its sums, whatever it holds.  Beside the page warps a load takes
-// microseconds, so everything is asked for at once (the values into L2).
-template <typename T, int D, int CHUNK>
+// microseconds, so everything is asked for at once (the values into L2).  
+template <typename T, int D>
 __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws,
                              int seg, int f, int chunk, float (*pt)[kRowTile]) {
   constexpr unsigned FULL = 0xffffffffu;
@@ -208,12 +208,12 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
   using Vec = std::conditional_t<E == 4, float4, float2>;
   const int lane = threadIdx.x & 31;
   const Kv8Segment sg = kv8_segment(c, a, geo, seg);
-  const int L = c.len[sg.s], cnt = a.counts ? a.counts[sg.s] : a.n;
+  const int L = __ldcg(c.len + sg.s), cnt = a.counts ? __ldcg(a.counts + sg.s) : a.n;
   if (L < 0 || L > kPage * c.max_pages + kPage - 1 || cnt <= 0 || cnt > a.n || (a.pages && sg.i >= cnt)) return;
   const int fresh = f - kPage / kRowTile;
   const int nv = min(kRowTile, fresh < 0 ? L % kPage - f * kRowTile : a.k.data ? cnt - fresh * kRowTile : 0);
   const int rows = min(geo.RB, (a.pages ? geo.G : cnt * geo.G) - sg.cb * geo.RB);  // of this column block
-  const int r0 = chunk * CHUNK, nr = min(rows - r0, CHUNK);
+  const int r0 = chunk * kRowChunk, nr = min(rows - r0, kRowChunk);
   if (nv <= 0 || nr <= 0) return;
   const float* kt = c.tail + kv8_pair(c, sg.s, sg.h) * 2 * kPage * D + f * kRowTile * D + E * lane;
   const T* kn = static_cast<const T*>(a.k.data) + sg.s * a.k.seq + sg.h * a.k.head + (int64_t)fresh * kRowTile * a.k.row + E * lane;
@@ -226,10 +226,10 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
       float* ve = reinterpret_cast<float*>(&v);
       if (i < nv) {
         if (fresh < 0) {
-          v = *reinterpret_cast<const Vec*>(tail + i * D);
+          v = __ldcg(reinterpret_cast<const Vec*>(tail + i * D));
         } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) ve[e] = kv8_load(rows16 + (int64_t)i * step + e);
+          for (int e = 0; e < E; ++e) ve[e] = kv8_float(__ldcg(rows16 + (int64_t)i * step + e));
         }
       }
 #pragma unroll
@@ -249,7 +249,7 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
     const int rr = sg.cb * geo.RB + r0 + r, hq = sg.h * geo.G + (a.pages ? rr : rr % geo.G);
     const T* p = static_cast<const T*>(a.q.data) + sg.s * a.q.seq + node_of(r) * a.q.row + hq * a.q.head + E * lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = kv8_load(p + e);
+    for (int e = 0; e < E; ++e) q[e] = kv8_float(__ldcg(p + e));
   };
   // two rows at a time, the next two on their way: a row's chain of exchanges leaves room for another's
   float q[2][E], next[2][E];
@@ -294,7 +294,7 @@ __device__ void kv8_row_part(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, co
       see[y] = tok < nv;
       if (fresh >= 0) {
         const int i = node_of(min(r + y, nr - 1));
-        const uint64_t mask = a.mask ? a.mask[(size_t)sg.s * a.n + i] : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
+        const uint64_t mask = a.mask ? __ldcg(a.mask + (size_t)sg.s * a.n + i) : (i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
         see[y] = see[y] && (mask >> (fresh * kRowTile + tok) & 1ull);
       }
       m[y] = see[y] ? s[y] : -INFINITY;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const int chunks = (min(geo.R, C::RB) + kRowChunk - 1) / kRowChunk;
     const int parts = geo.segments * geo.tiles * chunks;
     for (int x = (warp - kKv8Warps) * gridDim.x + blockIdx.x; x < parts; x += gridDim.x * kKv8RowWarps)
-      kv8_row_part<T, D, kRowChunk>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks,
+      kv8_row_part<T, D>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks,
                          row_p[warp - kKv8Warps]);
     return;
   }
@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const int s = lo, cnt = a.counts ? a.counts[s] : a.n;
     const Kv8Units un = kv8_units(a, c.len[s], cnt);
     const int per = un.pages, q = (x - prefix[s]) / per, u = (x - prefix[s]) % per;
-    const int h = a.pages ? q % H : q / geo.CB;
-    r.seg = a.pages ? s * a.n * H + q : s * H * geo.CB + q;
+    const int blocks = kv8_blocks(geo, cnt), h = a.pages ? q % H : q / blocks;
+    r.seg = a.pages ? s * a.n * H + q : (s * H + h) * geo.CB + q % blocks;
     r.u = u;
     const size_t pair = kv8_pair(c, s, h);
     int p = u;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
 #pragma unroll
       for (int kp = 0; kp < D / 32; ++kp) {
         const T* p = q + 32 * kp + 8 * t;
-        if (geo.vec) {
+        if (geo.vec & 1) {
           uint4 w[sizeof(T) / 2];
 #pragma unroll
           for (int x = 0; x < (int)sizeof(T) / 2; ++x) w[x] = reinterpret_cast<const uint4*>(p)[x];
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
 inline int kv8_split_warps(int R, int dtype) {
   const int rpt = dtype == W4A8_F32 ? 4 : 8, tiles = (R + rpt - 1) / rpt;
   int best = 1;
-  for (int wc : {2, 3, 4, 6, 12})
+  for (int wc : {2, 3, 4})
     if ((tiles + wc - 1) / wc * wc <= (tiles + best - 1) / best * best) best = wc;
   return best;
 }

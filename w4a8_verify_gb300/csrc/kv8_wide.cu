@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     r.cnt = a.counts ? a.counts[lo] : a.n;
     const int per = c.len[lo] / kPage, q = (x - prefix[lo]) / per;
     r.first = (x - prefix[lo]) % per;
-    r.seg = lo * c.n_kv_heads * geo.CB + q;
+    const int blocks = kv8_blocks(geo, r.cnt);
+    r.seg = (lo * c.n_kv_heads + q / blocks) * geo.CB + q % blocks;
     r.pages = min(per - r.first, u1 - x);
     r.ends = x + r.pages < u1;
     r.sg = kv8_segment(c, a, geo, r.seg);
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     int n = 0, runs = 0;
     for (int x = u0; x < u1 && ok; ++runs) {
       const Run r = run_at(x);
-      if (geo.vec) {  // the run's query rows
+      if (geo.vec & 1) {  // the run's query rows
         const int rows = rows_of(r);
         if (runs > 0 && !wait(&bar.q_empty, (runs - 1) & 1)) break;
         if (lane == 0) mbar_expect_tx(&bar.q_full, rows * D * sizeof(T));
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     }
     // no copy in flight when the CTA ends
     for (int i = max(0, n - kRing); i < n; ++i) (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
-    if (geo.vec && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1);
+    if ((geo.vec & 1) && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1);
   } else if (warp >= kConv0 && warp < kMmaWarp) {
     // the first half of the warps takes the keys, the second the values
     constexpr int kHalf = kConvWarps / 2;
@@ -349,14 +350,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       // Q of the run: the products of the run before are done (its last O' was waited for)
       float colfac, collow, m = -INFINITY, l = 0.0f;
       {
-        const T* q = geo.vec ? reinterpret_cast<const T*>(sm + C::sQ + row * C::QROW) : query_row(r, min(row, max(rows - 1, 0)));
-        if (geo.vec && !wait(&bar.q_full, runs & 1)) break;
+        const T* q = geo.vec & 1 ? reinterpret_cast<const T*>(sm + C::sQ + row * C::QROW) : query_row(r, min(row, max(rows - 1, 0)));
+        if ((geo.vec & 1) && !wait(&bar.q_full, runs & 1)) break;
         float am = 0.0f;
         auto load8 = [&](int d, float (&v)[8]) {
           if (row >= rows) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-          } else if (geo.vec) {
+          } else if (geo.vec & 1) {
             uint4 w[sizeof(T) / 2];
 #pragma unroll
             for (int e = 0; e < (int)sizeof(T) / 2; ++e) w[e] = reinterpret_cast<const uint4*>(q + d)[e];
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       }
       tc_before();
       __syncwarp();
-      if (geo.vec && lane == 0) mbar_arrive(&bar.q_empty);
+      if ((geo.vec & 1) && lane == 0) mbar_arrive(&bar.q_empty);
       for (int y = 0; y < 2 && freed < n + r.pages; ++y, ++freed)
         if (lane == 0) mbar_arrive(&bar.s_empty[freed & 1]);
       if (NQ == 2 && lane == 0) mbar_arrive(&bar.lo_empty);
@@ -569,18 +570,151 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The fp32 rows of wide calls, a warp a part: launched behind the wide kernel and run beside it (64 threads of 128
-// registers are what it leaves of an SM).  It reads what the wide kernel waited for before it let this one start, so
-// the wait for that kernel comes last, for the join that follows.
-constexpr int kRowsWarps = 2;
+// The fp32 rows of wide calls: 64 query rows by 16 tokens to a CTA of 128 threads, both products in registers: a thread
+// holds the logits of four rows and two tokens, then D / 8 values of the four rows.  Rows 16 apart and tokens 8 apart
+// belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice: 6 reads for 32
+// fused multiply-adds, 20 for 256.  Plain fp32.
+// Launched behind the wide kernel and run beside it where an SM has room: it reads (from L2) what the wide kernel
+// waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
+constexpr int kRowsThreads = 128, kRowsRows = 64;
+template <int D>
+struct RowsSmem {
+  float q[kRowsRows][D + 4], k[kRowTile][D + 4], v[kRowTile][D], p[kRowsRows][kRowTile + 4];
+  uint32_t see[kRowsRows];
+};
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kRowsWarps, 8) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+__global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
   griddep_launch();
-  __shared__ __align__(16) float row_p[kRowsWarps][kWideRowChunk][kRowTile];
-  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kWideRowChunk - 1) / kWideRowChunk;
-  const int warp = threadIdx.x >> 5, x = blockIdx.x * kRowsWarps + warp;
-  if (x < geo.segments * geo.tiles * chunks)
-    kv8_row_part<T, D, kWideRowChunk>(c, a, geo, ws, x / chunks / geo.tiles, x / chunks % geo.tiles, x % chunks, row_p[warp]);
+  extern __shared__ __align__(16) uint8_t sm_raw[];
+  RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(sm_raw);
+  constexpr int kBlocks = kWideRows / kRowsRows, V = D / 8;  // of a segment; vectors of eight elements in a row
+  const int tid = threadIdx.x, rg = tid >> 3, tg = tid & 7;
+  const int x = blockIdx.x / kBlocks, seg = x / geo.tiles, f = x % geo.tiles, fresh = f - kPage / kRowTile;
+  const Kv8Segment sg = kv8_segment(c, a, geo, seg);
+  const int L = __ldcg(c.len + sg.s), cnt = a.counts ? __ldcg(a.counts + sg.s) : a.n;
+  const int r0 = blockIdx.x % kBlocks * kRowsRows, first = sg.cb * kWideRows + r0;  // of the segment; of the KV head
+  int nv = 0, rows = 0;
+  if (L >= 0 && L <= kPage * c.max_pages + kPage - 1 && cnt > 0 && cnt <= a.n) {
+    nv = min(kRowTile, fresh < 0 ? L % kPage - f * kRowTile : a.k.data ? cnt - fresh * kRowTile : 0);
+    rows = min(kRowsRows, cnt * geo.G - first);
+  }
+  if (nv > 0 && rows > 0) {  // the same for the whole block
+    const float* tail = c.tail + kv8_pair(c, sg.s, sg.h) * 2 * kPage * D + f * kRowTile * D;
+    const T* kn = static_cast<const T*>(a.k.data) + sg.s * a.k.seq + sg.h * a.k.head + (int64_t)fresh * kRowTile * a.k.row;
+    const T* vn = static_cast<const T*>(a.v.data) + sg.s * a.v.seq + sg.h * a.v.head + (int64_t)fresh * kRowTile * a.v.row;
+    // eight elements of a row of T; all of a loop's rows on their way
+    auto load8 = [&](const T* p, int vec, float (&e)[8]) {
+      if (vec) {
+        uint4 w[sizeof(T) / 2];
+#pragma unroll
+        for (int y = 0; y < (int)sizeof(T) / 2; ++y) w[y] = __ldcg(reinterpret_cast<const uint4*>(p) + y);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = kv8_load(reinterpret_cast<const T*>(w) + y);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = kv8_float(__ldcg(p + y));
+      }
+    };
+    bool bad = false;  // a value that is not finite
+#pragma unroll
+    for (int y = tid; y < 2 * kRowTile * V; y += kRowsThreads) {
+      const int t = y / V % kRowTile, d = y % V * 8;
+      const bool val = y >= kRowTile * V;
+      float e[8] = {};
+      if (t < nv) {
+        if (fresh < 0) {
+          const float4* p = reinterpret_cast<const float4*>(tail + (val ? kPage * D : 0) + t * D + d);
+          *reinterpret_cast<float4*>(e) = __ldcg(p), *reinterpret_cast<float4*>(e + 4) = __ldcg(p + 1);
+        } else {
+          load8(val ? vn + (int64_t)t * a.v.row + d : kn + (int64_t)t * a.k.row + d, geo.vec & (val ? 4 : 2), e);
+        }
+      }
+      float* to = val ? &sm.v[t][d] : &sm.k[t][d];
+      *reinterpret_cast<float4*>(to) = *reinterpret_cast<float4*>(e);
+      *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<float4*>(e + 4);
+#pragma unroll
+      for (int z = 0; z < 8; ++z) bad = bad || (val && !(fabsf(e[z]) <= 3.402823466e38f));
+    }
+#pragma unroll 4
+    for (int y = tid; y < kRowsRows * V; y += kRowsThreads) {
+      const int r = y / V, d = y % V * 8, rr = first + min(r, rows - 1);
+      float e[8];
+      load8(static_cast<const T*>(a.q.data) + sg.s * a.q.seq + (rr / geo.G) * a.q.row +
+                (sg.h * geo.G + rr % geo.G) * a.q.head + d, geo.vec & 1, e);
+      *reinterpret_cast<float4*>(&sm.q[r][d]) = *reinterpret_cast<float4*>(e);
+      *reinterpret_cast<float4*>(&sm.q[r][d + 4]) = *reinterpret_cast<float4*>(e + 4);
+    }
+    if (tid < kRowsRows) {  // tokens that a row sees
+      const int node = (first + min(tid, rows - 1)) / geo.G;
+      uint32_t see = (1u << nv) - 1u;
+      if (fresh >= 0) {
+        const uint64_t mask = a.mask ? __ldcg(a.mask + (size_t)sg.s * a.n + node) : (node >= 63 ? ~0ull : (1ull << (node + 1)) - 1ull);
+        see &= (uint32_t)(mask >> (fresh * kRowTile));
+      }
+      sm.see[tid] = see;
+    }
+    bad = __syncthreads_or(bad);
+    float s[4][2] = {};
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 k[2], q[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.k[8 * j + tg][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[16 * i + rg][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
+    }
+    const float qscale = a.scale * 1.4426950408889634f;
+    const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * i + rg;
+      const uint32_t see = sm.see[r] >> tg;
+      const float s0 = see & 1u ? s[i][0] * qscale : -INFINITY, s1 = see & 256u ? s[i][1] * qscale : -INFINITY;
+      float m = fmaxf(s0, s1);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.0f : m;
+      const float p0 = see & 1u ? ex2(s0 - base) : 0.0f, p1 = see & 256u ? ex2(s1 - base) : 0.0f;
+      float l = p0 + p1;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      sm.p[r][tg] = p0, sm.p[r][8 + tg] = p1;
+      if (tg == 0 && r < rows) ws.rml[at + r] = make_float2(m, l);
+    }
+    __syncwarp();  // a row's weights come from the lanes that read them
+    float4 o[4][D / 32] = {};
+#pragma unroll 1
+    for (int t = 0; t < kRowTile; t += 4) {
+      float p[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(&sm.p[16 * i + rg][t]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float4 v[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = *reinterpret_cast<const float4*>(&sm.v[t + y][32 * e + 4 * tg]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (bad && !(sm.see[16 * i + rg] >> (t + y) & 1u)) continue;  // 0 times it would not be 0
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            o[i][e].x = fmaf(p[i][y], v[e].x, o[i][e].x), o[i][e].y = fmaf(p[i][y], v[e].y, o[i][e].y);
+            o[i][e].z = fmaf(p[i][y], v[e].z, o[i][e].z), o[i][e].w = fmaf(p[i][y], v[e].w, o[i][e].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (16 * i + rg < rows)
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) *reinterpret_cast<float4*>(ws.ro + (at + 16 * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
+  }
   griddep_wait();
 }
 
@@ -592,10 +726,10 @@ cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8G
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
   if (e != cudaSuccess) return e;
-  const int chunks = ((geo.R < geo.RB ? geo.R : geo.RB) + kWideRowChunk - 1) / kWideRowChunk;
-  const int64_t parts = (int64_t)geo.segments * geo.tiles * chunks;
-  return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)((parts + kRowsWarps - 1) / kRowsWarps)), dim3(32 * kRowsWarps), 0, st, c,
-                    a, geo, ws);
+  e = kv8_smem<k_kv8_rows<T, D>>(sizeof(RowsSmem<D>));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)(geo.segments * geo.tiles * (kWideRows / kRowsRows))), dim3(kRowsThreads),
+                    sizeof(RowsSmem<D>), st, c, a, geo, ws);
 }
 
 }  // namespace
