@@ -8,7 +8,7 @@ namespace {
 constexpr int kJoinWarps = 8;
 
 // The parts of a segment's rows, the split kernel's CTAs in their order, then the row tiles': RPC rows to a CTA, a warp
-// takes every (kJoinWarps / RPC)th part of its row, eight loads in flight; then the warps' sums.  No parts: zero.
+// takes every (kJoinWarps / RPC)th part of its row, B loads in flight; then the warps' sums.  No parts: zero.
 template <typename T, int D, int RPC>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
                                                               Kv8Scratch ws) {
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, 
       const int f = p - tile0 < un.open ? p - tile0 : kPage / kRowTile + p - tile0 - un.open;
       return ((int64_t)seg * geo.tiles + f) * geo.RB + rb;
     };
-    constexpr int B = 8;
+    constexpr int B = WPR == 1 ? 4 : 8;
     for (int p0 = first; p0 < parts; p0 += WPR * B) {
       float2 ml[B];
       Vec v[B];
@@ -213,19 +213,19 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   if (kv8_is_wide(*c, *a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
   else W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
       *c, *a, p.geo, ws, st));
-  // few rows (some CTAs for each SM): eight warps to a row, whose parts may be many; else two
+  // Warps of a row: all eight of a CTA where rows are few (some CTAs for each SM) and parts may be many; one where
+  // segments are so many that each has a few parts (64 sequences of 8 heads: 2.4 us less than with two); else two (one
+  // sequence with 128 rows to a head: 2 us less than with one).
   const int rows = p.geo.R < p.geo.RB ? p.geo.R : p.geo.RB;
-  auto join = [&](auto one, auto four) {
-    const bool few = (int64_t)rows * (int64_t)p.segments <= 4 * kKv8Ctas;
-    const dim3 grid((unsigned)p.segments, (unsigned)(few ? rows : (rows + 3) / 4));
-    return launch_pdl(few ? one : four, grid, dim3(32 * kJoinWarps), 0, st, *c, *a, p.geo, ws);
+  const int rpc = (int64_t)rows * (int64_t)p.segments <= 4 * kKv8Ctas ? 1 : p.segments < (size_t)kKv8Ctas ? 4 : 8;
+  auto join = [&](auto one, auto four, auto eight) {
+    const dim3 grid((unsigned)p.segments, (unsigned)((rows + rpc - 1) / rpc));
+    return launch_pdl(rpc == 1 ? one : rpc == 4 ? four : eight, grid, dim3(32 * kJoinWarps), 0, st, *c, *a, p.geo, ws);
   };
-  if (f32)
-    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<float, 64, 1>, k_kv8_join<float, 64, 4>)
-                      : join(k_kv8_join<float, 128, 1>, k_kv8_join<float, 128, 4>));
-  else
-    W4A8_CUDA_TRY(d64 ? join(k_kv8_join<__nv_bfloat16, 64, 1>, k_kv8_join<__nv_bfloat16, 64, 4>)
-                      : join(k_kv8_join<__nv_bfloat16, 128, 1>, k_kv8_join<__nv_bfloat16, 128, 4>));
+#define W4A8_JOIN(T, D) join(k_kv8_join<T, D, 1>, k_kv8_join<T, D, 4>, k_kv8_join<T, D, 8>)
+  W4A8_CUDA_TRY(f32 ? (d64 ? W4A8_JOIN(float, 64) : W4A8_JOIN(float, 128))
+                    : (d64 ? W4A8_JOIN(__nv_bfloat16, 64) : W4A8_JOIN(__nv_bfloat16, 128)));
+#undef W4A8_JOIN
   if (a->mass_out)
     W4A8_CUDA_TRY(launch_pdl(k_kv8_mass,
                              dim3((unsigned)((c->max_pages + 7) / 8), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs),

@@ -570,20 +570,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The fp32 rows of wide calls: 64 query rows by 16 tokens to a CTA of 128 threads, both products in registers: a thread
-// holds the logits of four rows and two tokens, then D / 8 values of the four rows.  Rows 16 apart and tokens 8 apart
-// belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice: 6 reads for 32
-// fused multiply-adds, 20 for 256.  Plain fp32.
+// The fp32 rows of wide calls: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
+// holds the logits of two rows and two tokens, then D / 8 values of the two rows.  Rows 32 apart and tokens 8 apart
+// belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice.  Plain fp32.
 // Launched behind the wide kernel and run beside it where an SM has room: it reads (from L2) what the wide kernel
 // waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
-constexpr int kRowsThreads = 128, kRowsRows = 64;
+constexpr int kRowsThreads = 256, kRowsRows = 64, kRT = 8 * kRowsRows / kRowsThreads;  // kRT rows of a thread
 template <int D>
 struct RowsSmem {
   float q[kRowsRows][D + 4], k[kRowTile][D + 4], v[kRowTile][D], p[kRowsRows][kRowTile + 4];
   uint32_t see[kRowsRows];
 };
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
+__global__ void __launch_bounds__(kRowsThreads, 3) k_kv8_rows(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo, Kv8Scratch ws) {
   griddep_launch();
   extern __shared__ __align__(16) uint8_t sm_raw[];
   RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(sm_raw);
@@ -654,16 +653,16 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, 
       sm.see[tid] = see;
     }
     bad = __syncthreads_or(bad);
-    float s[4][2] = {};
+    float s[kRT][2] = {};
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      float4 k[2], q[4];
+      float4 k[2], q[kRT];
 #pragma unroll
       for (int j = 0; j < 2; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.k[8 * j + tg][d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[16 * i + rg][d]);
+      for (int i = 0; i < kRT; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[kRowsRows / kRT * i + rg][d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kRT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
@@ -671,8 +670,8 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, 
     const float qscale = a.scale * 1.4426950408889634f;
     const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 16 * i + rg;
+    for (int i = 0; i < kRT; ++i) {
+      const int r = kRowsRows / kRT * i + rg;
       const uint32_t see = sm.see[r] >> tg;
       const float s0 = see & 1u ? s[i][0] * qscale : -INFINITY, s1 = see & 256u ? s[i][1] * qscale : -INFINITY;
       float m = fmaxf(s0, s1);
@@ -687,20 +686,20 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, 
       if (tg == 0 && r < rows) ws.rml[at + r] = make_float2(m, l);
     }
     __syncwarp();  // a row's weights come from the lanes that read them
-    float4 o[4][D / 32] = {};
+    float4 o[kRT][D / 32] = {};
 #pragma unroll 1
     for (int t = 0; t < kRowTile; t += 4) {
-      float p[4][4];
+      float p[kRT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(&sm.p[16 * i + rg][t]);
+      for (int i = 0; i < kRT; ++i) *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(&sm.p[kRowsRows / kRT * i + rg][t]);
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         float4 v[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) v[e] = *reinterpret_cast<const float4*>(&sm.v[t + y][32 * e + 4 * tg]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (bad && !(sm.see[16 * i + rg] >> (t + y) & 1u)) continue;  // 0 times it would not be 0
+        for (int i = 0; i < kRT; ++i) {
+          if (bad && !(sm.see[kRowsRows / kRT * i + rg] >> (t + y) & 1u)) continue;  // 0 times it would not be 0
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) {
             o[i][e].x = fmaf(p[i][y], v[e].x, o[i][e].x), o[i][e].y = fmaf(p[i][y], v[e].y, o[i][e].y);
@@ -710,12 +709,13 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_kv8_rows(w4a8_kv8_cache c, 
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (16 * i + rg < rows)
+    for (int i = 0; i < kRT; ++i)
+      if (kRowsRows / kRT * i + rg < rows)
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) *reinterpret_cast<float4*>(ws.ro + (at + 16 * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
+        for (int e = 0; e < D / 32; ++e) *reinterpret_cast<float4*>(ws.ro + (at + kRowsRows / kRT * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
   }
-  griddep_wait();
+  // the grid has not ended before the wide kernel has; only one CTA keeps its place for that
+  if (blockIdx.x == 0) griddep_wait();
 }
 
 template <typename T, int D>
