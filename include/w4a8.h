@@ -292,13 +292,14 @@ w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, 
                                size_t workspace_bytes, void* stream);
 
 /* Device.  For each new row and KV head the top_k (1..16384) whole pages of best score, as an
- * ascending list padded with -1 (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the largest over the head's query group of
- * q . (sum of the page's keys), in int8 like the pages: the group's queries get codes at one scale
- * (w4a8_quantize_rows' rule over its heads * head_dim values) and
+ * ascending list padded with -1 (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the
+ * largest over the head's query group of q . (sum of the page's keys), in int8 like the pages: the
+ * group's queries get codes at one scale (w4a8_quantize_rows' rule over its heads * head_dim values) and
  *   score = fl32(key scale * fl32(max_h sum_d code[h][d] * sums[d]))  with the exact integer sum.
- * The first first_pages and the last last_pages whole pages come before any score, equal scores go to the lowest
- * page, a NaN score counts as infinity, a group whose absmax is not finite has codes 0.  Rows behind
- * counts get lists of -1.  q as in w4a8_kv8_attn (dtype, n, n_heads, q and counts of a are used).  workspace: w4a8_kv8_select_workspace_bytes, 256-byte aligned. */
+ * The first first_pages and the last last_pages whole pages come before any score, equal scores go to
+ * the lowest page, a NaN score counts as infinity, a group whose absmax is not finite has codes 0.  Rows
+ * behind counts get lists of -1.  q as in w4a8_kv8_attn (dtype, n, n_heads, q and counts of a are used).
+ * workspace: w4a8_kv8_select_workspace_bytes, 256-byte aligned, not shared by calls that may overlap. */
 w4a8_status w4a8_kv8_select_workspace_bytes(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, size_t* bytes);
 w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, int top_k, int first_pages,
                             int last_pages, int32_t* pages_out, void* workspace, size_t workspace_bytes,

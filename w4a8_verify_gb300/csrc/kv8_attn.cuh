@@ -29,11 +29,17 @@
 // cut into equal ranges, one for each worker, so ragged batches balance.  A worker is a group of WC warps that share a
 // page and hold different columns; it has its own ring of bulk copies (a page each) and never waits for
 // another worker.  The code of half a page is a loop of 500 instructions: unrolled over the page (1000) it outran
-// the instruction caches, and twelve warps at different places of it spent a third of their time on fetches.  The fp32 rows (open page, new rows; at most 63 + 64 of a segment) go to one or two further warps
-// of each CTA, 16 rows at a time, in plain fp32: with the tensor-core form of them inside the page loop their code ran
-// a few times per CTA, cold, and one worker's four row tiles took 30 us at the end of a 40 us call.  Each
-// worker's part of a segment and each row tile gives (maximum, sum, values); the workers of a CTA add theirs up where
-// they hold the same segment, and k_kv8_join puts the rest together.
+// the instruction caches, and twelve warps at different places of it spent a third of their time on fetches.
+// The fp32 rows (open page, new rows; at most 63 + 64 of a segment) go to four further warps of each CTA, 16 tokens of
+// four query rows at a time, in plain fp32: with the tensor-core form of them inside the page loop their code ran a few
+// times per CTA, cold, and one worker's four row tiles took 30 us at the end of a 40 us call.  Each worker's part
+// of a segment and each row tile gives (maximum, sum, values); the workers of a CTA add theirs up where they hold the
+// same segment, and k_kv8_join puts the rest together.
+//
+// Bound: the codes once from memory when rows are few, the instructions of the conversion and the softmax when they
+// are many.  Measured (join included): one row of 131071 tokens, 8 KV heads of 128, 4 query heads each, bf16, 269 MB:
+// 53.3 us, 5.0 TB/s; 64 such rows of 2048 to 8191 tokens each, 572 MB: 106 us, 5.4 TB/s; a tree of 16 fp32 rows over 4096 tokens:
+// 27.7 us, of which 13 remain at 64 tokens (launches, rows, join).
 #pragma once
 #include <type_traits>
 
@@ -748,9 +754,10 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
 
 // ---------------------------------------------------------------------------- launch
 
-// Warps on a page for R query rows of a problem, a tile each (four rows of fp32, eight of bf16): the number, of those
-// that divide the CTA's warps, that leaves the fewest idle over the column blocks; the largest of equals (fewer
-// reads of a page).
+// Warps on a page for R query rows of a problem, a tile each (four rows of fp32, eight of bf16): the number up to four
+// that leaves the fewest idle over the column blocks; the largest of equals (fewer reads of a page).  With six and
+// twelve allowed as well, 96 bf16 rows at 2048 tokens took 28.5 us instead of 18.4 (few workers, each with pages of two
+// segments one after the other), and no length gained.
 inline int kv8_split_warps(int R, int dtype) {
   const int rpt = dtype == W4A8_F32 ? 4 : 8, tiles = (R + rpt - 1) / rpt;
   int best = 1;
@@ -778,17 +785,16 @@ cudaError_t kv8_split_dispatch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, 
     case 1: return kv8_split_launch<T, D, 1>(c, a, geo, ws, st);
     case 2: return kv8_split_launch<T, D, 2>(c, a, geo, ws, st);
     case 3: return kv8_split_launch<T, D, 3>(c, a, geo, ws, st);
-    case 4: return kv8_split_launch<T, D, 4>(c, a, geo, ws, st);
-    case 6: return kv8_split_launch<T, D, 6>(c, a, geo, ws, st);
-    default: return kv8_split_launch<T, D, 12>(c, a, geo, ws, st);
+    default: return kv8_split_launch<T, D, 4>(c, a, geo, ws, st);
   }
 }
 // Calls whose KV heads have many query rows run on tcgen05 (kv8_wide.cu): more than 128 rows, or more than 32 and
-// 2^21 tile-page-dims of room (the lengths are not known here).  Measured with full caches of 8 KV heads of 128, split
-// kernel / wide kernel, us: fp32, 64 rows, 4096 tokens 29.9 / 32.3 and 16384 tokens 64.7 / 48.8; 128 rows 38.9 / 35.9
-// and 111 / 53.6; bf16, 128 rows, 4096 tokens 27.8 / 31.8 and 16384 tokens 58.9 / 42.4; 256 rows, 1024 tokens 49.9 / 35;
-// 32 rows, 32768 tokens 60.6 / 64.5 (fp32) and 35.2 / 45.8 (bf16).  Heads of 64: 64 rows, 8192 tokens 27.5 / 28.7 and
-// 16384 tokens 41.5 / 38.6 (fp32), 28.0 / 32.8 (bf16).
+// 2^21 tile-page-dims of room (the lengths are not known here).  Measured with full caches of 8 KV heads, split / wide
+// kernel, us.  Heads of 128, fp32: 32 rows, 32768 tokens 59.6 / 65.0; 64 rows, 4096 tokens 28.2 / 28.4 and 8192 tokens
+// 39.1 / 33.6; 128 rows, 2048 tokens 26.6 / 34.7, 4096 tokens 37.9 / 37.6 and 16384 tokens 110 / 55.5; 144 rows, 2048
+// tokens 28.9 / 33.1 and 8192 tokens 68.5 / 50.7.  bf16: 96 rows, 8192 tokens 30.6 / 34.7 and 16384 tokens 47.3 / 41.2;
+// 128 rows, 8192 tokens 37.4 / 36.7; 144 rows, 512 tokens 29.5 / 25.3 and 8192 tokens 40.1 / 38.6.  Heads of 64, fp32, 64
+// rows: 8192 tokens 26.6 / 26.3 and 16384 tokens 40.8 / 36.0.
 inline bool kv8_is_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, int R) {
   if (a.pages) return false;
   const int64_t tiles = (R + 3) / (a.dtype == W4A8_F32 ? 4 : 8);

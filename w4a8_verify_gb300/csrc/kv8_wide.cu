@@ -12,13 +12,16 @@
 //             its own when a logit passes that by 8 (log2);
 //   values    O = O c + s_V O' in registers, a thread half a row: the page's scale needs no common factor with the
 //             other pages', and nothing is rescaled in tensor memory.
-// fp32 calls split Q and P into f16 hi + lo and add both products into the same accumulator.  The hi terms are the
-// nearest whole numbers at a largest magnitude of 2^11 (P: scaled by 2^10, with the maximum of its own page),
+// fp32 calls split Q and P into f16 hi + lo; the products of P's share an accumulator, those of Q's have one each.  The
+// hi terms are the nearest whole numbers at a largest magnitude of 2^11 (P: scaled by 2^10, with the maximum of its own page),
 // so their sums with the codes are whole numbers below 2^24, which the tensor core's truncating additions leave exact.
 // With hi the nearest f16, and Q's lo product in the accumulator of its hi product, outputs were off by 1.8e-6 in the
 // 2-norm at 4096 tokens, against 0.6e-6.
 // Why tcgen05 here: the split kernel converts a page once for every eight columns, and mma.sync tops out at a quarter
 // of the dense rate; with 128 rows a page is 2 x 256 cycles of tensor core against 700 of memory traffic.
+// Measured: 128 rows to each of 8 KV heads of 128, 32768 tokens: 56.0 us bf16, 79.7 us fp32 (0.97 and 1.8 us for a page of a
+// CTA, whose products take a quarter of that); 256 rows with the pages' mass, 32000 tokens, bf16: 91.6 us.  Bound by
+// the latency of the softmax warps (one to a scheduler; more of them leave too few registers for the values).
 #include "kv8_attn.cuh"
 
 namespace w4a8 {
@@ -573,6 +576,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
 // The fp32 rows of wide calls: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
 // holds the logits of two rows and two tokens, then D / 8 values of the two rows.  Rows 32 apart and tokens 8 apart
 // belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice.  Plain fp32.
+// One warp to four rows (the split kernel's form, 16 exchanges between lanes a row) took 49 us for 512 rows of each of 8
+// heads and 64 new tokens, with nothing else to do; this takes 25 (whole calls).
 // Launched behind the wide kernel and run beside it where an SM has room: it reads (from L2) what the wide kernel
 // waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
 constexpr int kRowsThreads = 256, kRowsRows = 64, kRT = 8 * kRowsRows / kRowsThreads;  // kRT rows of a thread
