@@ -35,16 +35,16 @@ __device__ bool append_index_ok(const w4a8_kv8_cache& c, const int32_t* index, i
 }
 
 // Codes + 128 of eight values at scale s > 0 (|x| <= 127 s up to rounding), four to a word: rint of the IEEE quotient,
-// mostly without the division.  q = x (1 / s) is within 2.3e-5 of fl(x / s) (two roundings of at most 127 2^-24 each, and
-// the quotient's own), so only a q that close to a half needs it; adding 1.5 2^23 rounds q to a whole number in the
-// low bits.  inv is 0 where 1 / s is not a good factor (subnormal s).
+// mostly without the division.  x fl(1 / s) is within 1.2e-5 of fl(x / s) (127 2^-24 of the reciprocal's rounding, half of
+// that of the quotient's), so only one that close to a half needs it; added to 1.5 2^23 in one rounding it becomes a whole
+// number in the low bits.  inv is 0 where 1 / s is not a good factor (subnormal s).
 __device__ __forceinline__ void codes8(const float (&x)[8], float s, float inv, uint32_t (&word)[2]) {
   uint32_t n[8];
   float off = inv == 0.0f ? 1.0f : 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float q = __fmul_rn(x[e], inv), r = q + 12582912.0f;
-    off = fmaxf(off, fabsf(q - (r - 12582912.0f)));
+    const float r = fmaf(x[e], inv, 12582912.0f);
+    off = fmaxf(off, fabsf(fmaf(x[e], inv, -__fadd_rn(r, -12582912.0f))));
     n[e] = __float_as_uint(r);
   }
   if (off > 0.5f - 6e-5f) {
@@ -60,15 +60,16 @@ __device__ __forceinline__ void codes8(const float (&x)[8], float s, float inv, 
 constexpr int kVPad = 4;  // bytes between the token rows of a page's value codes in shared memory
 
 // One CTA per (page of the call's window, KV head, sequence and keys/values).  A thread takes eight neighbouring
-// dims of four (D = 128) rows, 16 or 32 bytes at a time where the rows allow it, and keeps them in registers between
-// the absmax and the quantisation: one read of the rows.  Key groups of 16 bytes are whole in a thread; value groups
-// (eight tokens of two dims) are gathered from the codes in shared memory.  The CTA of the window's first page
-// reads the old tail, so it alone writes the new one, afterwards.
-// Bound by instructions (absmax, rounding and packing: 63% of the issue slots): 32768 bf16 rows of 8 heads of 128, 134 MB
-// in and 67 MB out, 63 us cold (3.2 TB/s).  With four pages a CTA and the next one's loads in flight (120 registers) append
-// and read together took 10 us more.
+// dims of four (D = 128) rows, 16 or 32 bytes at a time where the rows allow it.  A page of whole new rows is read once,
+// all loads in flight, and held in registers between the absmax and the quantisation; other pages (rows of the
+// tail, of a list, unaligned) are read twice.  Key groups of 16 bytes are whole in a thread; value groups (eight tokens of
+// two dims) are gathered from the codes in shared memory.  The CTA of the window's first page reads the old tail, so
+// it alone writes the new one, afterwards.
+// Bound by instructions (20 a value: absmax, rounding, packing, sums; 72% of the issue slots) and by the loads in flight:
+// 32768 bf16 rows of 8 heads of 128, 134 MB in and 67 MB out, 57 us cold (3.5 TB/s) with six CTAs on an SM, 63 with four.
+// Four pages a CTA with the next one's loads in flight (120 registers): 10 us more.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c, w4a8_rows kr, w4a8_rows vr, int n_src,
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 5) k_kv8_append(w4a8_kv8_cache c, w4a8_rows kr, w4a8_rows vr, int n_src,
                                                                 int n, const int32_t* counts, const int32_t* index,
                                                                 int32_t* len_out, bool store_len, int vec) {
   griddep_enter();
@@ -119,8 +120,6 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     const int phys = kv8_phys(c, pair, page);
     // chunk i of a thread, keys: group gi = (i / 2) threads + tid of the page's order, its token g + 8 (i & 1);
     // values: the i-th of the page's eight-dim chunks in rows
-    float x[kChunks][8] = {};
-    float m = 0.0f;
     auto place = [&](int i, int& tok, int& d) {
       if (!val) {
         const int gi = (i >> 1) * kAppendThreads + tid, q = gi >> 5;
@@ -131,9 +130,24 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
         tok = ci / (D / 8), d = ci % (D / 8) * 8;
       }
     };
-    if (wide && !index && base >= L) {  // a page of whole new rows: the loads alone, all in flight
+    const bool whole = wide && !index && base >= L;  // a page of whole new rows: the loads alone, all in flight
+    uint4 u[kChunks][sizeof(T) / 2];
+    float m = 0.0f;
+    auto held = [&](int i, float (&y)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = kv8_load(reinterpret_cast<const T*>(u[i]) + e);
+    };
+    auto again = [&](int i, float (&y)[8]) {
+      int tok, d;
+      place(i, tok, d);
+      load8(base + tok, d, y);
+    };
+    auto largest = [&](const float (&y)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
+    };
+    if (whole) {
       const T* from = src + (int64_t)(base - L) * rows.row;
-      uint4 u[kChunks][sizeof(T) / 2];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         int tok, d;
@@ -142,27 +156,29 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
 #pragma unroll
         for (int y = 0; y < (int)sizeof(T) / 2; ++y) u[i][y] = __ldg(p + y);
       }
+      if constexpr (sizeof(T) == 2) {  // of pairs
+        __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
+        for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = kv8_load(reinterpret_cast<const T*>(u[i]) + e);
+          for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(reinterpret_cast<const __nv_bfloat162*>(u[i])[e]));
+        m = max_nan(__low2float(top), __high2float(top));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          float y[8];
+          held(i, y);
+          largest(y);
+        }
+      }
     } else {
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < kChunks; ++i) {
-        int tok, d;
-        place(i, tok, d);
         float y[8];
-        load8(base + tok, d, y);
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][e] = k == i ? y[e] : x[k][e];
+        again(i, y);
+        largest(y);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[i][e]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((tid & 31) == 0) red[tid >> 5] = m;
@@ -175,28 +191,48 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(w4a8_kv8_cache c,
     const float inv = sc > 1e-37f ? __fdiv_rn(1.0f, sc) : 0.0f;
     uint32_t word[kChunks][2];  // code + 128 of four dims each
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (sc > 0.0f) codes8(x[i], sc, inv, word[i]);
-      else word[i][0] = word[i][1] = 0x80808080u;
+    for (int i = 0; i < kChunks; ++i) word[i][0] = word[i][1] = 0x80808080u;
+    if (sc > 0.0f && whole) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        float y[8];
+        held(i, y);
+        codes8(y, sc, inv, word[i]);
+      }
+    } else if (sc > 0.0f) {
+#pragma unroll 1
+      for (int i = 0; i < kChunks; ++i) {
+        float y[8];
+        uint32_t w[2];
+        again(i, y);
+        codes8(y, sc, inv, w);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) word[k][0] = k == i ? w[0] : word[k][0], word[k][1] = k == i ? w[1] : word[k][1];
+      }
     }
     const size_t pg = kv8_page(c, pair, phys < 0 ? 0 : phys);
     uint4* out = reinterpret_cast<uint4*>(c.codes + (pg * 2 + val) * (size_t)(kPage * D));
     if (!val) {
+      uint32_t sum[4] = {};  // dims e, e + 2 of a half of the thread's eight: sums of code + 128 in 16 bits each
 #pragma unroll
       for (int i = 0; i < kChunks; i += 2) {
-        const int gi = (i >> 1) * kAppendThreads + tid;
-        if (phys >= 0) out[gi] = make_uint4(word[i][0], word[i + 1][0], word[i][1], word[i + 1][1]);
-        const int t = gi & 3, kp = (gi >> 5) % (D / 32);
+        if (phys >= 0) out[(i >> 1) * kAppendThreads + tid] = make_uint4(word[i][0], word[i + 1][0], word[i][1], word[i + 1][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // dims e, e + 2 of a half of the eight: sums of code + 128 in 16 bits each
+        for (int e = 0; e < 4; ++e) {
           const int sh = 8 * (e & 1), half = e >> 1;
-          uint32_t v = (word[i][half] >> sh & 0x00ff00ffu) + (word[i + 1][half] >> sh & 0x00ff00ffu);
-          v += __shfl_xor_sync(0xffffffffu, v, 4);
-          v += __shfl_xor_sync(0xffffffffu, v, 8);
-          v += __shfl_xor_sync(0xffffffffu, v, 16);
-          // at most 64 * 255 in a half: no carry; integers: any order
-          if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[((kp * 4 + t) * 2 + half) * 2 + (e & 1)], v);
+          sum[e] += (word[i][half] >> sh & 0x00ff00ffu) + (word[i + 1][half] >> sh & 0x00ff00ffu);
         }
+      }
+      // a thread's chunks are of the same dims: its groups are 8 (a multiple of D / 32) dim blocks apart
+      const int t = tid & 3, kp = (tid >> 5) % (D / 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t v = sum[e];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        // at most 64 * 255 in a half: no carry; integers: any order
+        if (((tid >> 2) & 7) == 0) atomicAdd(&ksum[((kp * 4 + t) * 2 + (e >> 1)) * 2 + (e & 1)], v);
       }
     } else {
 #pragma unroll
