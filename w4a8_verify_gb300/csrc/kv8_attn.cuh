@@ -38,7 +38,7 @@
 //
 // Bound: the codes once from memory when rows are few, the instructions of the conversion and the softmax when they
 // are many.  Measured (join included): one row of 131071 tokens, 8 KV heads of 128, 4 query heads each, bf16, 269 MB:
-// 53.3 us, 5.0 TB/s; 64 such rows of 2048 to 8191 tokens each, 572 MB: 106 us, 5.4 TB/s; a tree of 16 fp32 rows over 4096 tokens:
+// 53.3 us, 5.0 TB/s; 64 sequences of up to 8191 tokens, 646 MB: 117 us cold, 5.6 TB/s; a tree of 16 fp32 rows over 4096 tokens:
 // 27.7 us, of which 13 remain at 64 tokens (launches, rows, join).
 #pragma once
 #include <type_traits>
