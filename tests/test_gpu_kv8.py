@@ -281,6 +281,23 @@ def test_padded_batches(n, H, G, D, dtype):
     assert cache.check() == 0
 
 
+@pytest.mark.parametrize("S,n,H,G,D,dtype", [(38, 7, 2, 7, 64, "fp32"), (40, 14, 2, 5, 128, "bf16"), (20, 33, 3, 3, 64, "bf16"),
+                                             (21, 16, 4, 4, 128, "fp32")])
+def test_many_sequences_of_several_rows(S, n, H, G, D, dtype):
+    """Many parts of fp32 rows, with all pages and with lists of them."""
+    rng = np.random.default_rng(S + n)
+    lens = [int(x) for x in rng.integers(0, 210, S)]
+    cache, ref = _filled(rng, S, H, D, lens, dtype)
+    q = _rows(rng, S, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    mask = [_tree_mask(rng, n) for _ in range(S)]
+    counts = [int(x) for x in rng.integers(0, n + 1, S)]
+    _attend(cache, ref, q, k, v, D ** -0.5, mask=mask, counts=counts)
+    pages = cache.select(q, 2, first_pages=1, counts=_i32(counts))
+    _attend(cache, ref, q, k, v, D ** -0.5, mask=mask, counts=counts, pages=pages.tolist())
+    assert cache.check() == 0
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("n", [4, 16, 40])
 def test_masked_rows_with_nan_and_infinities(dtype, n):

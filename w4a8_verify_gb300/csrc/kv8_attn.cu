@@ -161,7 +161,12 @@ w4a8_status plan_of(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, Plan* p) {
   g.ng = wide ? 1 : kKv8Warps / wc;
   g.tiles = kPage / kRowTile + (a->k.data ? (g.n + kRowTile - 1) / kRowTile : 0);
   // CTAs for the pages, or (split kernel) for a round of its row warps' parts
-  const size_t parts = wide ? 0 : p->segments * g.tiles * ((g.R < g.RB ? g.R : g.RB) + kRowChunk - 1) / kRowChunk;
+  const size_t chunks = p->segments * ((g.R < g.RB ? g.R : g.RB) + kRowChunk - 1) / kRowChunk;
+  // the fp32 rows by a kernel of their own where the row warps would take more than about two rounds (with half of an
+  // open page): 38 sequences of 27 tokens, 7 fp32 rows, 2 heads of 64, 7 query heads each 30.1 -> 16.1 us; below that its
+  // launch costs more
+  g.apart = !wide && g.n * g.G > kRowsApart && chunks * (g.tiles - 2) > 2 * kKv8Ctas * kKv8RowWarps;
+  const size_t parts = wide || g.apart ? 0 : chunks * g.tiles;
   const size_t ctas = units > parts / kKv8RowWarps ? units : parts / kKv8RowWarps;
   g.ctas = (int)(ctas < (size_t)kKv8Ctas ? ctas : (size_t)kKv8Ctas);
   p->prefix = 0;
@@ -215,6 +220,7 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
   if (kv8_is_wide(*c, *a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
   else W4A8_CUDA_TRY((f32 ? d64 ? kv8_split_f32_d64 : kv8_split_f32_d128 : d64 ? kv8_split_bf16_d64 : kv8_split_bf16_d128)(
       *c, *a, p.geo, ws, st));
+  if (p.geo.apart) W4A8_CUDA_TRY(kv8_rows(*c, *a, p.geo, ws, st));
   // Warps of a row: all eight of a CTA where rows are few (some CTAs for each SM) and parts may be many; one where
   // segments are so many that each has a few parts (64 sequences of 8 heads: 2.4 us less than with two); else two (one
   // sequence with 128 rows to a head: 2 us less than with one).

@@ -55,6 +55,7 @@ constexpr float kPScale = 128.0f, kPSlack = 8.0f;  // scale of P; how far (log2)
 constexpr int kWideRows = 128;        // query rows of a segment of a wide call (kv8_wide.cu)
 constexpr int kRowTile = 16;          // fp32 rows of one part
 constexpr int kRowChunk = 4;          // query rows that a row warp takes at a time
+constexpr int kRowsApart = 16;        // rows of a KV head above which many parts go to a kernel of their own
 
 struct Kv8Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a segment's problem (n G, or G with lists)
@@ -62,6 +63,7 @@ struct Kv8Geom {       // of one call, the same for every kernel of it
   int ctas, ng;        // of the split kernel, and its workers in each at most
   int tiles;           // row tiles of a segment: four of the open page, those of the new rows
   int segments;
+  int apart;           // whether k_kv8_rows takes the fp32 rows, not the split kernel's row warps
   int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
 };
 
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     for (int s = tid; s <= S; s += kKv8Threads) ws.prefix[s] = prefix[s];
 
   if (warp >= kKv8Warps) {  // fp32 rows: parts dealt over the row warps of all CTAs
+    if (geo.apart) return;
     const int chunks = (min(geo.R, C::RB) + kRowChunk - 1) / kRowChunk;
     const int parts = geo.segments * geo.tiles * chunks;
     for (int x = (warp - kKv8Warps) * gridDim.x + blockIdx.x; x < parts; x += gridDim.x * kKv8RowWarps)
@@ -801,6 +804,7 @@ inline bool kv8_is_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, int R) 
   return R > kWideRows || (R > 32 && tiles * c.n_seqs * c.n_kv_heads * c.max_pages * c.head_dim >= 1 << 21);
 }
 cudaError_t kv8_wide(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
+cudaError_t kv8_rows(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 // one translation unit per head size and element type
 cudaError_t kv8_split_f32_d64(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
 cudaError_t kv8_split_f32_d128(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);

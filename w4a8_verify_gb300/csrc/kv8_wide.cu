@@ -573,13 +573,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The fp32 rows of wide calls: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
+// The fp32 rows of wide calls, and of others with many: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
 // holds the logits of two rows and two tokens, then D / 8 values of the two rows.  Rows 32 apart and tokens 8 apart
 // belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice.  Plain fp32.
 // One warp to four rows (the split kernel's form, 16 exchanges between lanes a row) took 49 us for 512 rows of each of 8
 // heads and 64 new tokens, with nothing else to do; this takes 25 (whole calls).
-// Launched behind the wide kernel and run beside it where an SM has room: it reads (from L2) what the wide kernel
-// waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
+// Launched behind the wide or the split kernel and run beside it where an SM has room: it reads (from L2) what that
+// kernel waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
 constexpr int kRowsThreads = 256, kRowsRows = 64, kRT = 8 * kRowsRows / kRowsThreads;  // kRT rows of a thread
 template <int D>
 struct RowsSmem {
@@ -591,12 +591,21 @@ __global__ void __launch_bounds__(kRowsThreads, 3) k_kv8_rows(w4a8_kv8_cache c, 
   griddep_launch();
   extern __shared__ __align__(16) uint8_t sm_raw[];
   RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(sm_raw);
-  constexpr int kBlocks = kWideRows / kRowsRows, V = D / 8;  // of a segment; vectors of eight elements in a row
+  constexpr int V = D / 8;  // vectors of eight elements in a row
   const int tid = threadIdx.x, rg = tid >> 3, tg = tid & 7;
-  const int x = blockIdx.x / kBlocks, seg = x / geo.tiles, f = x % geo.tiles, fresh = f - kPage / kRowTile;
-  const Kv8Segment sg = kv8_segment(c, a, geo, seg);
+  // blocks of a KV head's rows (with page lists too: their segments differ in the pages alone)
+  const int blocks = (a.n * geo.G + kRowsRows - 1) / kRowsRows, x = blockIdx.x / blocks;
+  const int f = x % geo.tiles, fresh = f - kPage / kRowTile, pair = x / geo.tiles;
+  const struct { int s, h; } sg = {pair / c.n_kv_heads, pair % c.n_kv_heads};
   const int L = __ldcg(c.len + sg.s), cnt = a.counts ? __ldcg(a.counts + sg.s) : a.n;
-  const int r0 = blockIdx.x % kBlocks * kRowsRows, first = sg.cb * kWideRows + r0;  // of the segment; of the KV head
+  const int first = blockIdx.x % blocks * kRowsRows;
+  auto slot = [&](int r) {  // of row first + r of the KV head
+    if (a.pages) {
+      const size_t seg = ((size_t)sg.s * a.n + (first + r) / geo.G) * c.n_kv_heads + sg.h;
+      return (seg * geo.tiles + f) * geo.RB + (first + r) % geo.G;
+    }
+    return (((size_t)pair * geo.CB + (first + r) / geo.RB) * geo.tiles + f) * geo.RB + (first + r) % geo.RB;
+  };
   int nv = 0, rows = 0;
   if (L >= 0 && L <= kPage * c.max_pages + kPage - 1 && cnt > 0 && cnt <= a.n) {
     nv = min(kRowTile, fresh < 0 ? L % kPage - f * kRowTile : a.k.data ? cnt - fresh * kRowTile : 0);
@@ -673,7 +682,6 @@ __global__ void __launch_bounds__(kRowsThreads, 3) k_kv8_rows(w4a8_kv8_cache c, 
           s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
     }
     const float qscale = a.scale * 1.4426950408889634f;
-    const size_t at = ((size_t)seg * geo.tiles + f) * geo.RB + r0;
 #pragma unroll
     for (int i = 0; i < kRT; ++i) {
       const int r = kRowsRows / kRT * i + rg;
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3) k_kv8_rows(w4a8_kv8_cache c, 
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       sm.p[r][tg] = p0, sm.p[r][8 + tg] = p1;
-      if (tg == 0 && r < rows) ws.rml[at + r] = make_float2(m, l);
+      if (tg == 0 && r < rows) ws.rml[slot(r)] = make_float2(m, l);
     }
     __syncwarp();  // a row's weights come from the lanes that read them
     float4 o[kRT][D / 32] = {};
@@ -717,10 +725,20 @@ __global__ void __launch_bounds__(kRowsThreads, 3) k_kv8_rows(w4a8_kv8_cache c, 
     for (int i = 0; i < kRT; ++i)
       if (kRowsRows / kRT * i + rg < rows)
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) *reinterpret_cast<float4*>(ws.ro + (at + kRowsRows / kRT * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
+        for (int e = 0; e < D / 32; ++e)
+          *reinterpret_cast<float4*>(ws.ro + slot(kRowsRows / kRT * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
   }
-  // the grid has not ended before the wide kernel has; only one CTA keeps its place for that
+  // the grid has not ended before the kernel in front has; only one CTA keeps its place for that
   if (blockIdx.x == 0) griddep_wait();
+}
+
+template <typename T, int D>
+cudaError_t rows_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
+  cudaError_t e = kv8_smem<k_kv8_rows<T, D>>(sizeof(RowsSmem<D>));
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (a.n * geo.G + kRowsRows - 1) / kRowsRows;
+  return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)(blocks * geo.tiles * c.n_seqs * c.n_kv_heads)), dim3(kRowsThreads),
+                    sizeof(RowsSmem<D>), st, c, a, geo, ws);
 }
 
 template <typename T, int D>
@@ -731,10 +749,7 @@ cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8G
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_kv8_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
   if (e != cudaSuccess) return e;
-  e = kv8_smem<k_kv8_rows<T, D>>(sizeof(RowsSmem<D>));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_kv8_rows<T, D>, dim3((unsigned)(geo.segments * geo.tiles * (kWideRows / kRowsRows))), dim3(kRowsThreads),
-                    sizeof(RowsSmem<D>), st, c, a, geo, ws);
+  return rows_run<T, D>(c, a, geo, ws, st);
 }
 
 }  // namespace
@@ -742,6 +757,11 @@ cudaError_t wide_run(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8G
 cudaError_t kv8_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
   if (a.dtype == W4A8_F32) return c.head_dim == 64 ? wide_run<float, 64>(c, a, geo, ws, st) : wide_run<float, 128>(c, a, geo, ws, st);
   return c.head_dim == 64 ? wide_run<__nv_bfloat16, 64>(c, a, geo, ws, st) : wide_run<__nv_bfloat16, 128>(c, a, geo, ws, st);
+}
+
+cudaError_t kv8_rows(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, const Kv8Geom& geo, const Kv8Scratch& ws, cudaStream_t st) {
+  if (a.dtype == W4A8_F32) return c.head_dim == 64 ? rows_run<float, 64>(c, a, geo, ws, st) : rows_run<float, 128>(c, a, geo, ws, st);
+  return c.head_dim == 64 ? rows_run<__nv_bfloat16, 64>(c, a, geo, ws, st) : rows_run<__nv_bfloat16, 128>(c, a, geo, ws, st);
 }
 
 }  // namespace w4a8
