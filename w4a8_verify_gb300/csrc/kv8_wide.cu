@@ -32,7 +32,7 @@ constexpr int kSoftWarps = 4, kSumWarps = 8, kConvWarps = 4;
 constexpr int kSum0 = kSoftWarps, kConv0 = kSum0 + kSumWarps, kMmaWarp = kConv0 + kConvWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kWideThreads = 32 * (kCopyWarp + 1);
 constexpr int kRing = 4;   // pages of codes
-constexpr int kFac = 4;    // rounds of row factors between the softmax and the value warps
+constexpr int kFac = 4;    // pages whose P and row factors may be on their way from the softmax to the value warps
 
 template <typename T, int D>
 struct Wide {
@@ -55,8 +55,17 @@ struct Wide {
   static constexpr int sPrefix = sQ + kWideRows * QROW;
 };
 
-struct Bars {  // mbarriers
-  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[2], pv_done[2], o_empty[2], lo_empty, q_full, q_empty;
+// mbarriers.  A wait knows its phase by parity alone, so the phase after it must not complete before every warp has passed
+// the wait.  Use n of an entry of depth d is waited for before use n + d can complete because that one needs, from the waiting warp:
+//   code_full  code_empty(n)                                   code_empty  the copy of page n + kRing
+//   k_full, v_full  S(n), O'(n), issued behind the wait        s_done, pv_done  k_full(n + 2), v_full(n + 2) (converters),
+//   s_empty    S(n), lo_empty: L(n), issued behind the wait      p_full(n + 1) or p_full(n + 2) (softmax), o_empty(n) (values)
+//   p_full     o_empty(n), by way of O'(n + 2), S(n + 4)       o_empty     O'(n + NO), issued behind the wait
+//   q_full     q_empty of the run                              q_empty     the next run's copies
+// p_full has kFac entries: with two, bf16 calls (two buffers of P and of O') let the softmax warps complete p_full(n) and
+// p_full(n + 2) while a value warp was still at page n - 1; it then waited for p_full(n + 4), which needs its own o_empty(n).
+struct Bars {
+  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[kFac], pv_done[2], o_empty[2], lo_empty, q_full, q_empty;
 };
 static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
@@ -117,10 +126,11 @@ __device__ __forceinline__ void tc_store_wait() { asm volatile("tcgen05.wait::st
 // The nearest whole number of |x| < 2^22 (NaN stays)
 __device__ __forceinline__ float whole(float x) { return __fadd_rn(__fadd_rn(x, 12582912.0f), -12582912.0f); }
 
-// A position in a ring of mbarriers: entry and phase parity.
+// Use n of a ring of mbarriers: entry and phase parity.
 template <int N>
 struct Turn {
-  int i = 0, ph = 0;
+  int i, ph;
+  __device__ explicit Turn(unsigned n = 0) : i((int)(n % N)), ph((int)(n / N & 1u)) {}
   __device__ void next() {
     if (++i == N) i = 0, ph ^= 1;
   }
@@ -150,9 +160,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], kConvWarps / 2), mbar_init(&bar.v_full[i], kConvWarps / 2);
       mbar_init(&bar.s_done[i], 1), mbar_init(&bar.pv_done[i], 1);
-      mbar_init(&bar.s_empty[i], kSoftWarps), mbar_init(&bar.p_full[i], kSoftWarps);
+      mbar_init(&bar.s_empty[i], kSoftWarps);
       mbar_init(&bar.o_empty[i], kSumWarps);
     }
+    for (int i = 0; i < kFac; ++i) mbar_init(&bar.p_full[i], kSoftWarps);
     mbar_init(&bar.lo_empty, kSoftWarps);
     mbar_init(&bar.q_full, 1), mbar_init(&bar.q_empty, kSoftWarps);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -296,12 +307,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       }
     }
   } else if (warp == kMmaWarp) {
-    Turn<2> b, pb;
-    Turn<NO> ob;
+    Turn<2> b;
     int n = 0;  // pages whose S is issued
     const uint32_t one = elect_one();
     auto values = [&](int i) {  // O' of page i (the one before the newest S)
-      if (!wait(&bar.p_full[pb.i], pb.ph) || !wait(&bar.v_full[pb.i], pb.ph)) return;
+      const Turn<2> pb(i);
+      const Turn<NO> ob(i);
+      const Turn<kFac> pf(i);
+      if (!wait(&bar.p_full[pf.i], pf.ph) || !wait(&bar.v_full[pb.i], pb.ph)) return;
       if (i >= NO && !wait(&bar.o_empty[ob.i], ob.ph ^ 1)) return;
       tc_after();
       const uint32_t v = tc_desc(smem_u32(sm + C::sV + pb.i * C::TILE)), o = tmem + C::cO + ob.i * D;
@@ -309,8 +322,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
 #pragma unroll
       for (int k = 0; k < NQ * kPage / 16; ++k) tc_mma<D>(one, o, pa + k * 8, v + (k & 3) * 2, k > 0);
       tc_commit(one, &bar.pv_done[pb.i]);
-      pb.next();
-      ob.next();
     };
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         tc_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bar.p_full[b.i]);
+          mbar_arrive(&bar.p_full[fb.i]);
           if (freed < n + r.pages - p) mbar_arrive(&bar.s_empty[b.i]);
           if (NQ == 2 && p + 1 < r.pages) mbar_arrive(&bar.lo_empty);
         }
@@ -538,7 +549,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
       for (int p = 0; p < r.pages && ok; ++p, b.next(), ob.next(), fb.next()) {
         if ((p & 31) == 0) now = then, then = batch_at(r, p + 32, 1);
         const float sv = __shfl_sync(FULL, now.scale, p & 31);
-        if (!wait(&bar.p_full[b.i], b.ph) || !wait(&bar.pv_done[b.i], b.ph)) break;
+        if (!wait(&bar.p_full[fb.i], fb.ph) || !wait(&bar.pv_done[b.i], b.ph)) break;
         tc_after();
         if (moved[fb.i * kSoftWarps + quad]) {
           const float f = fac[fb.i * kWideRows + row];
