@@ -36,6 +36,7 @@ class Model:
     def __init__(self, counts):
         self.counts = counts                     # arrivals of a phase, by barrier
         self.steps = {}                          # role -> [(kind, ...)]
+        self.ends = []                           # (role, role that has to be done by its end)
 
     def add(self, role, *step):
         self.steps.setdefault(role, []).append(step)
@@ -87,6 +88,9 @@ class Model:
             for r, i in who:
                 if all(c.get(r, -1) < i for _, _, c in after):
                     bad.append("%s: phase %d of %s may complete before its wait for phase %d" % (r, phase + 1, what, phase))
+        for r, last in self.ends:                # what has to be done when a role ends
+            if clock[r].get(last, -1) < len(self.steps[last]) - 1:
+                bad.append("%s ends before %s" % (r, last))
         return bad
 
 
@@ -99,7 +103,7 @@ def wide_model(text, runs, fp32, vec):
     convs = ["conv%d" % w for w in range(k["kConvWarps"])]
     half = len(convs) // 2
     m = Model(dict(code_full=1, code_empty=len(convs), k_full=half, v_full=half, s_done=1, pv_done=1, s_empty=len(soft),
-                   p_full=len(soft), o_empty=len(sums), lo_empty=len(soft), q_full=1, q_empty=len(soft), issue=1))
+                   p_full=len(soft), o_empty=len(sums), lo_empty=len(soft), q_full=1, q_empty=len(soft), issue=1, drained=1))
     depth = dict(bars, o_empty=no)               # the products use NO of its entries
 
     def ev(role, kind, name, n):                 # the n-th use of a barrier: entry and phase
@@ -181,6 +185,7 @@ def wide_model(text, runs, fp32, vec):
                 values(n - 1)
             n += 1
         values(n - 1)
+    give_up(m, text, issued)
     for q, r in enumerate(soft):                 # softmax
         n = freed = 0
         for i, pages in enumerate(runs):
@@ -223,6 +228,16 @@ def wide_model(text, runs, fp32, vec):
     return m
 
 
+def give_up(m, text, issued):
+    """The product warp's end, after its last wait or the first that ran out: the tensor core has to be done."""
+    m.ends.append(("mma", "tensor"))
+    if re.search(r"tc_commit\(elect_one\(\), &bar\.drained\);[^;]*mbar_wait\(&bar\.drained, 0\)[^;]*;\s*asm volatile\(\"tcgen05\.dealloc", text):
+        m.add("mma", "arrive", ("issue", issued[0]), 0)
+        m.add("tensor", "wait", ("issue", issued[0]), 0)
+        m.add("tensor", "arrive", ("drained", 0), 0)
+        m.add("mma", "wait", ("drained", 0), 0)
+
+
 RUNS = [[1], [2], [3], [4], [5], [10], [2, 4], [1, 3], [1, 1, 1, 1, 1, 1], [3, 1, 2, 1, 4], [35, 1, 9], [40]]
 
 
@@ -261,3 +276,28 @@ def test_the_model_sees_a_ring_that_is_too_short():
     assert not wide_model(short, [10], True, True).check()
     short = re.sub(r"kFac = \d+", "kFac = 1", text)
     assert any("fac" in x for x in wide_model(short, [6], False, False).check())
+
+
+@pytest.mark.parametrize("fp32", [True, False])
+@pytest.mark.parametrize("left", range(0, 60, 7))
+def test_no_product_is_under_way_when_a_wait_has_run_out(fp32, left):
+    """The product warp stops at its `left`th wait, the others where that leaves them; the tensor core is done at its end."""
+    m = wide_model(_source(), [9], fp32, True)
+    keep, issued, n = [], [0], 0
+    for step in m.steps["mma"]:
+        if step[0] == "wait":
+            if n == left or step[1][0] == "drained":
+                break
+            n += 1
+        keep.append(step)
+    stopped = Model(m.counts)
+    stopped.steps = {r: list(s) for r, s in m.steps.items()}
+    issued[0] = sum(s[0] == "arrive" for s in keep)
+    stopped.steps["mma"] = keep
+    steps, stopped.steps["tensor"] = m.steps["tensor"], []
+    for step in steps:
+        if step[0] == "wait" and step[1][1] == issued[0]:
+            break
+        stopped.steps["tensor"].append(step)
+    give_up(stopped, _source(), issued)
+    assert not [x for x in stopped.check() if "ends before" in x]

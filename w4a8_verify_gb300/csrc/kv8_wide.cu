@@ -65,7 +65,7 @@ struct Wide {
 // p_full has kFac entries: with two, bf16 calls (two buffers of P and of O') let the softmax warps complete p_full(n) and
 // p_full(n + 2) while a value warp was still at page n - 1; it then waited for p_full(n + 4), which needs its own o_empty(n).
 struct Bars {
-  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[kFac], pv_done[2], o_empty[2], lo_empty, q_full, q_empty;
+  uint64_t code_full[kRing], code_empty[kRing], k_full[2], v_full[2], s_done[2], s_empty[2], p_full[kFac], pv_done[2], o_empty[2], lo_empty, q_full, q_empty, drained;
 };
 static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     }
     for (int i = 0; i < kFac; ++i) mbar_init(&bar.p_full[i], kSoftWarps);
     mbar_init(&bar.lo_empty, kSoftWarps);
-    mbar_init(&bar.q_full, 1), mbar_init(&bar.q_empty, kSoftWarps);
+    mbar_init(&bar.q_full, 1), mbar_init(&bar.q_empty, kSoftWarps), mbar_init(&bar.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
@@ -581,7 +581,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == kMmaWarp) {
+    // tensor memory is given back and the CTA ends: no product is under way then, also where a wait ran out
+    tc_commit(elect_one(), &bar.drained);
+    if (!__all_sync(FULL, mbar_wait(&bar.drained, 0)) && lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
 }
 
 // The fp32 rows of wide calls, and of others with many: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
