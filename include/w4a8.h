@@ -284,12 +284,19 @@ w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4
  * it, whatever it holds (NaN and infinities too), and rows at or behind counts[s] are not read.
  * The result does not depend on timing; it may depend, in its last bits, on the other sequences of
  * the call (they share the splits of the long axis).  out's strides must not be 0 where that axis
- * has more than one entry (W4A8_ERR_ARG).  A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
+ * has more than one entry (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one that runs out sets
+ * W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN, as is the mass of their pages.  A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
  * n_kv_heads * B < 2^22, and times the pages that a row reads < 2^31, with B = n (with pages), else
  * the blocks of at most 128 and at least 12 query rows (n * heads of a KV head) it is cut into.
  * workspace: 256-byte aligned, not shared by calls that may overlap; needs no initialisation. */
 w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
                                size_t workspace_bytes, void* stream);
+/* Device, test-only: w4a8_kv8_attention in which CTA number cta of the kernel over the pages issues none of its copies
+ * and waits are limited to 20 ms, so that its waits run out: ctl gets W4A8_FLAG_ERR_TIMEOUT, the rows that miss its part
+ * (and the mass of their pages) are NaN, the others are as ever.  Nothing hangs or faults, no copy is left in
+ * flight, and later calls work. */
+w4a8_status w4a8_kv8_attention_inject_timeout(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
+                                              size_t workspace_bytes, int cta, void* stream);
 
 /* Device.  For each new row and KV head the top_k (1..16384) whole pages of best score, as an
  * ascending list padded with -1 (pages_out, int32 [n_seqs][n][n_kv_heads][top_k]).  The score is the

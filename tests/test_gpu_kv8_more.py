@@ -54,3 +54,62 @@ def test_wide_calls_again_and_again(dtype, S, H, G, D, n, L, calls):
     torch.cuda.synchronize()
     assert int(wrong) == 0
     assert [j[0].check() for j in jobs] == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,H,G,D,n,cta", [
+    ([3000, 40, 700, 5000], 2, 4, 128, 1, 3),          # a page and a worker a warp
+    ([3000, 40, 700, 5000], 2, 4, 64, 12, 150),        # several warps to a page, one of the last CTAs, if it has pages
+    ([64, 0, 127], 1, 4, 128, 2, 0),                   # three rows of one page each: one CTA has all or one
+    ([20000, 63, 9000], 2, 8, 128, 40, 60),            # tcgen05, runs of several segments
+    ([9000, 63, 5000], 2, 16, 64, 9, 0),
+])
+def test_a_wait_that_runs_out_shows(dtype, lens, H, G, D, n, cta):
+    """One CTA's copies are withheld (w4a8_kv8_attention_inject_timeout): the rows that miss its part are NaN, the others
+    and the pages' mass as ever, the status word says so, and the next call on the same workspace is right."""
+    rng = np.random.default_rng(n)
+    S = len(lens)
+    c = _random_cache(n, lens, H, D)
+    q = _rows(rng, S, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    old, mass = torch.rand(S, H, c.shape[3], device="cuda"), torch.empty(S, H, c.shape[3], device="cuda")
+    want = c.attention(q, k, v, scale=0.1, mass=old, mass_out=mass)
+    pages = c.select(q, 6, last_pages=1)
+    sparse = c.attention(q, k, v, scale=0.1, pages=pages)
+    assert c.check() == 0
+    real = c._attention
+    f = W.lib().w4a8_kv8_attention_inject_timeout
+
+    def cut_short(ref, a, workspace, size, stream):
+        return f(ref, a, workspace, size, cta, stream)
+    for lists in (False, True):
+        c._attention = cut_short
+        m2 = torch.zeros_like(mass)
+        if lists:
+            got, ref = c.attention(q, k, v, scale=0.1, pages=pages), sparse
+        else:
+            got, ref = c.attention(q, k, v, scale=0.1, mass=old, mass_out=m2), want
+        c._attention = real
+        nan = torch.isnan(got)
+        rows = nan.all(-1)
+        assert torch.equal(nan.any(-1), rows)
+        assert torch.equal(got[~rows], ref[~rows])
+        if cta == 150 and not rows.any():                              # a call of few pages: none for this CTA
+            assert c.check() == 0
+            continue
+        assert rows.any()
+        short = [s for s in range(S) if lens[s] < 64]
+        assert not rows[short].any()                                   # no pages: nothing of theirs is missing
+        if max(lens) > 1000:
+            assert int(rows.sum()) < rows.numel() // 2
+        if not lists:
+            lost = rows.view(S, n, H, G).any(dim=3).any(dim=1)         # [S][H]
+            full = torch.tensor([[x // 64 for _ in range(H)] for x in lens], device="cuda")
+            held = torch.arange(c.shape[3], device="cuda") < full[..., None]
+            assert torch.equal(torch.isnan(m2), held & lost[..., None])
+            assert torch.equal(m2[~lost], mass[~lost])
+        assert c.check() == W.FLAG_ERR_TIMEOUT
+        c.tensors["ctl"].zero_()
+    assert torch.equal(c.attention(q, k, v, scale=0.1, pages=pages), sparse)
+    assert torch.equal(c.attention(q, k, v, scale=0.1, mass=old, mass_out=m2), want) and torch.equal(m2, mass)
+    assert c.check() == 0

@@ -231,7 +231,7 @@ def wide_model(text, runs, fp32, vec):
 def give_up(m, text, issued):
     """The product warp's end, after its last wait or the first that ran out: the tensor core has to be done."""
     m.ends.append(("mma", "tensor"))
-    if re.search(r"tc_commit\(elect_one\(\), &bar\.drained\);[^;]*mbar_wait\(&bar\.drained, 0\)[^;]*;\s*asm volatile\(\"tcgen05\.dealloc", text):
+    if re.search(r"tc_commit\(elect_one\(\), &bar\.drained\);[^;]*mbar_wait\(&bar\.drained, 0[,)][^;]*;\s*asm volatile\(\"tcgen05\.dealloc", text):
         m.add("mma", "arrive", ("issue", issued[0]), 0)
         m.add("tensor", "wait", ("issue", issued[0]), 0)
         m.add("tensor", "arrive", ("drained", 0), 0)

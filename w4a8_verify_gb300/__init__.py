@@ -100,6 +100,7 @@ _SIGNATURES = {
     "w4a8_kv8_read": [_c.POINTER(KV8CacheDesc), _vp, _vp, _i32, _vp, _vp, _vp],
     "w4a8_kv8_attention_workspace_bytes": [_c.POINTER(KV8CacheDesc), _vp, _c.POINTER(_sz)],
     "w4a8_kv8_attention": [_c.POINTER(KV8CacheDesc), _vp, _vp, _sz, _vp],
+    "w4a8_kv8_attention_inject_timeout": [_c.POINTER(KV8CacheDesc), _vp, _vp, _sz, _i32, _vp],
     "w4a8_kv8_select_workspace_bytes": [_c.POINTER(KV8CacheDesc), _vp, _c.POINTER(_sz)],
     "w4a8_kv8_select": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp],
     "w4a8_kv8_evict": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp],

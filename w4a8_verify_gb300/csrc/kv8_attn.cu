@@ -8,7 +8,8 @@ namespace {
 constexpr int kJoinWarps = 8;
 
 // The parts of a segment's rows, the split kernel's CTAs in their order, then the row tiles': RPC rows to a CTA, a warp
-// takes every (kJoinWarps / RPC)th part of its row, B loads in flight; then the warps' sums.  No parts: zero.
+// takes every (kJoinWarps / RPC)th part of its row, B loads in flight; then the warps' sums.  No parts: zero.  The
+// sum of a part that is not there, where a CTA's wait ran out, is NaN, and so is the row.
 // Bound by latency: 32 rows of 28 parts 6.6 us cold, 4096 rows 8 us.
 template <typename T, int D, int RPC>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_kv8_join(w4a8_kv8_cache c, w4a8_kv8_attn a, Kv8Geom geo,
@@ -196,8 +197,9 @@ W4A8_API w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c,
   return ok;
 }
 
-W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
-                                        size_t workspace_bytes, void* stream) {
+// withheld, wait_ns: see Kv8Geom.
+static w4a8_status attend(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace, size_t workspace_bytes,
+                          void* stream, int withheld, uint64_t wait_ns) {
   Plan p;
   w4a8_status ok = kv8_valid(c);
   if (ok == W4A8_OK) ok = plan_of(c, a, &p);
@@ -215,6 +217,8 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
                 reinterpret_cast<float*>(base + p.ro), a->mass_out ? reinterpret_cast<float2*>(base + p.fin) : nullptr,
                 a->mass_out ? reinterpret_cast<float2*>(base + p.page) : nullptr};
   p.geo.vec = (kv8_vec_rows(a->q, a->dtype) ? 1 : 0) | (kv8_vec_rows(a->k, a->dtype) ? 2 : 0) | (kv8_vec_rows(a->v, a->dtype) ? 4 : 0);
+  p.geo.withheld = withheld;
+  p.geo.wait_ns = wait_ns;
   cudaStream_t st = as_stream(stream);
   const bool f32 = a->dtype == W4A8_F32, d64 = c->head_dim == 64;
   if (kv8_is_wide(*c, *a, p.geo.R)) W4A8_CUDA_TRY(kv8_wide(*c, *a, p.geo, ws, st));
@@ -239,4 +243,15 @@ W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_
                              dim3((unsigned)((c->max_pages + 7) / 8), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs),
                              dim3(256), 0, st, *c, *a, p.geo, ws));
   return W4A8_OK;
+}
+
+W4A8_API w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  return attend(c, a, workspace, workspace_bytes, stream, -1, kWaitLimitNs);
+}
+
+W4A8_API w4a8_status w4a8_kv8_attention_inject_timeout(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
+                                                       size_t workspace_bytes, int cta, void* stream) {
+  if (cta < 0) return W4A8_ERR_ARG;
+  return attend(c, a, workspace, workspace_bytes, stream, cta, 20000000ull);
 }

@@ -65,6 +65,8 @@ struct Kv8Geom {       // of one call, the same for every kernel of it
   int segments;
   int apart;           // whether k_kv8_rows takes the fp32 rows, not the split kernel's row warps
   int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
+  int withheld;        // CTA whose pages are not copied (w4a8_kv8_attention_inject_timeout), -1: none
+  uint64_t wait_ns;    // limit of the kernels' waits
 };
 
 struct Kv8Scratch {    // workspace pointers
@@ -348,6 +350,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
   constexpr unsigned FULL = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(16) float row_p[kKv8RowWarps][kRowChunk][kRowTile];
+  __shared__ int cut;  // whether a wait of the CTA ran out
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kKv8RingBytes);
   uint64_t* empty = full + C::NG * C::NS;
   int* prefix = reinterpret_cast<int*>(empty + C::NG * C::NS);
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
   const int g = lane >> 2, t = lane & 3;
   const int H = c.n_kv_heads, S = c.n_seqs;
 
+  if (tid == 0) cut = 0;
   for (int i = tid; i < C::NG * C::NS; i += kKv8Threads) {
     mbar_init(&full[i], 1);
     mbar_init(&empty[i], WC);
@@ -676,10 +680,11 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
         ++jl;
         if (from < 0) continue;
         if (lane == 0) {
-          if (WC > 1 && iph > 0) ok = mbar_wait(&empty[is], (iph - 1) & 1);
+          if (WC > 1 && iph > 0) ok = mbar_wait(&empty[is], (iph - 1) & 1, geo.wait_ns);
           if (ok) {
             mbar_expect_tx(&full[is], C::PAGE);
-            bulk_g2s(ring + (size_t)is * C::PAGE, c.codes + (size_t)from * C::PAGE, C::PAGE, &full[is]);
+            if (geo.withheld != (int)blockIdx.x)
+              bulk_g2s(ring + (size_t)is * C::PAGE, c.codes + (size_t)from * C::PAGE, C::PAGE, &full[is]);
           }
         }
         ok = __shfl_sync(FULL, ok, 0);
@@ -701,7 +706,7 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     const float sk = __shfl_sync(FULL, cur.sk, src), sv = __shfl_sync(FULL, cur.sv, src);
     const int u = __shfl_sync(FULL, cur.u, src);
     if (from < 0) continue;
-    ok = __all_sync(FULL, mbar_wait(&full[cs], cph & 1));
+    ok = __all_sync(FULL, mbar_wait(&full[cs], cph & 1, geo.wait_ns));
     if (!ok) break;
     if (act) page(ring + (size_t)cs * C::PAGE, sk, sv, u);
     __syncwarp();
@@ -710,10 +715,10 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
     --in_ring;
   }
   if (!ok) {  // a bounded wait expired: report it, and wait (again bounded) for the copies still in flight
-    if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+    if (lane == 0) cut = 1, atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
     if (wg == 0)
       for (; in_ring > 0; --in_ring) {
-        (void)mbar_wait(&full[cs], cph & 1);
+        (void)mbar_wait(&full[cs], cph & 1, geo.wait_ns);
         if (++cs == C::NS) cs = 0, ++cph;
       }
   }
@@ -752,6 +757,15 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
       }
     }
     i0 = i1;
+  }
+  if (cut) {  // the CTA's parts are not what they should be: NaN, for the join to pass on
+    page_warps_sync();
+    const int last = u1 > u0 ? look(u1 - 1).seg : -1;
+    for (int x = u0 + lane; x < u1; x += 32) {
+      const int sg = look(x).seg;
+      const size_t at = ((size_t)sg + (sg == last ? blockIdx.x : (size_t)geo.ctas + geo.segments)) * C::RB;
+      for (int r = 0; r < C::RB; ++r) ws.ml[at + r] = make_float2(NAN, NAN);
+    }
   }
 }
 

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   };
   bool ok = true;
   auto wait = [&](uint64_t* b, int parity) {
-    ok = ok && __all_sync(FULL, mbar_wait(b, (unsigned)parity));
+    ok = ok && __all_sync(FULL, mbar_wait(b, (unsigned)parity, geo.wait_ns));
     return ok;
   };
 
@@ -260,15 +260,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
         }
         if (lane == 0) {
           mbar_expect_tx(&bar.code_full[e.i], C::PAGE);
-          bulk_g2s(sm + e.i * C::PAGE, c.codes + kv8_page(c, r.pair, phys) * C::PAGE, C::PAGE, &bar.code_full[e.i]);
+          if (geo.withheld != (int)blockIdx.x)
+            bulk_g2s(sm + e.i * C::PAGE, c.codes + kv8_page(c, r.pair, phys) * C::PAGE, C::PAGE, &bar.code_full[e.i]);
         }
         __syncwarp();
       }
       x += r.pages;
     }
     // no copy in flight when the CTA ends
-    for (int i = max(0, n - kRing); i < n; ++i) (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
-    if ((geo.vec & 1) && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1);
+    for (int i = max(0, n - kRing); i < n; ++i)
+      (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1), geo.wait_ns);
+    if ((geo.vec & 1) && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1, geo.wait_ns);
   } else if (warp >= kConv0 && warp < kMmaWarp) {
     // the first half of the warps takes the keys, the second the values
     constexpr int kHalf = kConvWarps / 2;
@@ -579,12 +581,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   }
   if (!ok && lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
   tc_before();
-  __syncthreads();
+  const int cut = __syncthreads_or(!ok);
   tc_after();
+  if (cut)  // the CTA's parts are not what they should be: NaN, for the join to pass on
+    for (int x = u0; x < u1;) {
+      const Run r = run_at(x);
+      const size_t at = r.ends ? (size_t)geo.ctas + geo.segments + r.seg : (size_t)blockIdx.x + r.seg;
+      if (tid < kWideRows) ws.ml[at * kWideRows + tid] = make_float2(NAN, NAN);
+      x += r.pages;
+    }
   if (warp == kMmaWarp) {
     // tensor memory is given back and the CTA ends: no product is under way then, also where a wait ran out
     tc_commit(elect_one(), &bar.drained);
-    if (!__all_sync(FULL, mbar_wait(&bar.drained, 0)) && lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+    if (!__all_sync(FULL, mbar_wait(&bar.drained, 0, geo.wait_ns)) && lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
