@@ -93,16 +93,18 @@ def select(cache, s, h, q, top_k, first, last):
     for p, (ck, sk, _, _) in enumerate(take):
         best = max(int(ck.sum(axis=0) @ c) for c in code)
         x = np.float32(sk) * np.float32(best)
-        forced = p < first or p >= len(take) - last
-        score.append(np.inf if forced or np.isnan(x) else x)
-    order = sorted(range(len(take)), key=lambda p: (-score[p], p))
-    return sorted(order[:top_k])
+        score.append(np.inf if np.isnan(x) else x)
+    return _best(score, top_k, first, last)
+
+
+def _best(score, k, first, last):
+    """The k best pages, ascending: the first and last ones whatever their score, then by score; equals by the lowest page."""
+    n = len(score)
+    order = sorted(range(n), key=lambda p: (1, -score[p], p) if first <= p < n - last else (0, 0, p))
+    return sorted(order[:k])
 
 
 def evict(mass, keep, first, last):
     """mass [whole pages] -> (kept pages, dropped pages), both ascending."""
-    n = len(mass)
-    score = [np.inf if p < first or p >= n - last or np.isnan(m) else m for p, m in enumerate(mass)]
-    order = sorted(range(n), key=lambda p: (-score[p], p))
-    kept = sorted(order[:keep])
-    return kept, sorted(set(range(n)) - set(kept))
+    kept = _best([np.inf if np.isnan(m) else m for m in mass], keep, first, last)
+    return kept, sorted(set(range(len(mass))) - set(kept))

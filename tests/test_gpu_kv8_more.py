@@ -8,6 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import w4a8_verify_gb300 as W
+from oracle import kv8 as O
 from test_gpu_kv8 import _i32, _long_check, _random_cache, _rows
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +114,27 @@ def test_a_wait_that_runs_out_shows(dtype, lens, H, G, D, n, cta):
     assert torch.equal(c.attention(q, k, v, scale=0.1, pages=pages), sparse)
     assert torch.equal(c.attention(q, k, v, scale=0.1, mass=old, mass_out=m2), want) and torch.equal(m2, mass)
     assert c.check() == 0
+
+
+@pytest.mark.parametrize("first,last,k", [(1, 2, 4), (1, 2, 2), (0, 3, 3), (0, 1, 1), (2, 2, 9), (0, 0, 4)])
+def test_first_and_last_pages_come_before_infinite_scores(first, last, k):
+    """Pages of NaN and of infinite score or mass in front of the last pages: those stay all the same."""
+    D, P = 64, 30
+    cache, ref = W.KV8Cache(1, 1, D, P), O.Cache(1, 1, D, P)
+    x = torch.from_numpy(np.random.default_rng(k).standard_normal((1, 64 * P, 1, D)).astype(np.float32)).cuda()
+    x[:, 64 * 2:64 * 6] = float("nan")
+    cache.append(x, torch.ones_like(x))
+    ref.append(0, x[0].cpu().numpy(), np.ones((64 * P, 1, D), np.float32))
+    q = torch.ones(1, 1, 2, D, device="cuda")
+    got = cache.select(q, k, first_pages=first, last_pages=last)[0, 0, 0].tolist()
+    assert got == O.select(ref, 0, 0, np.ones((2, D), np.float32), k, first, last)
+    must = [p for p in range(P) if p < first or p >= P - last]
+    assert set(must[:k]) <= set(got)
+    mass = torch.rand(1, 1, P, device="cuda")
+    mass[0, 0, 3:7], mass[0, 0, 9:12] = float("inf"), float("nan")
+    held = cache.tensors["table"][0, 0].tolist()
+    kept, gone = O.evict(mass[0, 0].tolist(), k, first, last)
+    assert set(must[:k]) <= set(kept)
+    table, left, length = cache.evict(mass, k, first_pages=first, last_pages=last)
+    assert table[0, 0].tolist() == [held[p] for p in kept + gone] and int(length[0]) == 64 * k
+    assert torch.equal(left[0, 0, :k].nan_to_num(nan=-1.0), mass[0, 0, kept].nan_to_num(nan=-1.0))

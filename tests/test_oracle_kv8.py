@@ -109,3 +109,15 @@ def test_refusals_without_a_gpu(lib):
     assert select(top_k=16385) == 2 and select() == 4 and select(a=W.KV8Attn(0, 4, 0, 1.0, rows)) == 2
     assert lib.w4a8_kv8_evict(ref(c), None, 1, 0, 0, p, p, p, None) == 1
     assert lib.w4a8_kv8_evict(ref(c), p, -1, 0, 0, p, p, p, None) == 1
+
+
+def test_first_and_last_pages_come_before_infinities():
+    inf, nan = float("inf"), float("nan")
+    assert O.evict([inf, nan, 1.0, 0.0], 1, 0, 1) == ([3], [0, 1, 2])
+    assert O.evict([inf, nan, 1.0, 0.0], 3, 0, 1) == ([0, 1, 3], [2])
+    assert O.evict([0.0, inf, inf, 0.0], 2, 2, 1) == ([0, 1], [2, 3])
+    c = O.Cache(1, 1, 64, 8)
+    x = np.ones((64 * 6, 1, 64))
+    x[:64 * 3] = nan
+    c.append(0, x, x)
+    assert O.select(c, 0, 0, np.ones((2, 64), np.float32), 2, 0, 1) == [0, 5]

@@ -12,7 +12,8 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-constexpr uint32_t kForcedKey = 0xff800000u;  // the key of infinity
+constexpr uint32_t kInfKey = 0xff800000u;     // the key of infinity
+constexpr uint32_t kForcedKey = 0xffffffffu;  // of the first and last pages: above any score's
 
 // The keys of the k largest of P (0 < k < P) are those above *T and *ties of those equal to it.  Forced pages and
 // infinities are counted first; the others are looked for by their distance from the smallest, eight bits at a
@@ -24,10 +25,10 @@ __device__ void kth_largest(const uint32_t* keys, int P, int k, uint32_t* hist, 
   if (threadIdx.x == 0) s_low = ~0u, s_high = 0u, s_top = 0;
   __syncthreads();
   uint32_t low = ~0u, high = 0u;
-  int top = 0;
+  int top = 0;  // forced pages and infinities, and in the upper half the forced ones (at most 16384 of either)
   for (int i = threadIdx.x; i < P; i += blockDim.x) {
     const uint32_t x = keys[i];
-    if (x >= kForcedKey) ++top;
+    if (x >= kInfKey) top += x == kForcedKey ? 0x10001 : 1;
     else low = min(low, x), high = max(high, x);
   }
   low = __reduce_min_sync(0xffffffffu, low);
@@ -35,9 +36,11 @@ __device__ void kth_largest(const uint32_t* keys, int P, int k, uint32_t* hist, 
   top = __reduce_add_sync(0xffffffffu, top);
   if ((threadIdx.x & 31) == 0) atomicMin(&s_low, low), atomicMax(&s_high, high), atomicAdd(&s_top, top);
   __syncthreads();
-  low = s_low, high = s_high, top = s_top;
-  if (top >= k) {  // no key is above infinity's
-    *T = kForcedKey, *ties = k;
+  low = s_low, high = s_high, top = s_top & 0xffff;
+  const int forced = s_top >> 16;
+  if (top >= k) {  // the forced pages, and infinities if they leave room
+    *T = forced >= k ? kForcedKey : kInfKey;
+    *ties = forced >= k ? k : k - forced;
     return;
   }
   int left = k - top, bits = high > low ? 32 - __clz(high - low) : 0;
@@ -48,7 +51,7 @@ __device__ void kth_largest(const uint32_t* keys, int P, int k, uint32_t* hist, 
     __syncthreads();
     for (int i = threadIdx.x; i < P; i += blockDim.x) {
       const uint32_t x = keys[i], d = x - low;
-      if (x < kForcedKey && (bits == 32 ? 0u : d >> bits) == prefix) atomicAdd(&hist[(d >> lo) & ((1u << (bits - lo)) - 1u)], 1u);
+      if (x < kInfKey && (bits == 32 ? 0u : d >> bits) == prefix) atomicAdd(&hist[(d >> lo) & ((1u << (bits - lo)) - 1u)], 1u);
     }
     __syncthreads();
     if (threadIdx.x < 32) {  // lane l: bins 255 - 8l .. 248 - 8l, from the top
