@@ -138,3 +138,40 @@ def test_first_and_last_pages_come_before_infinite_scores(first, last, k):
     table, left, length = cache.evict(mass, k, first_pages=first, last_pages=last)
     assert table[0, 0].tolist() == [held[p] for p in kept + gone] and int(length[0]) == 64 * k
     assert torch.equal(left[0, 0, :k].nan_to_num(nan=-1.0), mass[0, 0, kept].nan_to_num(nan=-1.0))
+
+
+def test_tensors_of_a_call_on_a_given_stream_may_be_dropped():
+    """The caller's last references to the rows, the cache's to its pages, go while the given stream is still busy with
+    something else: their memory is not handed out again before the call has read it."""
+    lens, H, D = [500, 77], 2, 64
+
+    def case():
+        r = np.random.default_rng(92)
+        return _random_cache(8, lens, H, D), _rows(r, 2, 3, 4 * H, D, "fp32"), _rows(r, 2, 3, H, D, "fp32")
+    c, q, k = case()
+    want = c.attention(q, k, k, scale=0.1)
+    before = c.tensors["codes"].numel()
+    c.append(k, k)
+    held = c.read(_i32([480, 60]), 30)
+    side = torch.cuda.Stream()
+    for what in ("rows", "cache", "append"):
+        c, q, k = case()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)                     # tens of milliseconds
+        if what == "append":
+            c.append(k, k, stream=side)
+        else:
+            got = c.attention(q, k, k, scale=0.1, stream=side)
+        sizes = (q.shape, k.shape) if what != "cache" else [t.shape for t in c.tensors.values() if t.dtype == torch.float32]
+        if what == "cache":
+            c = None
+        q = k = None
+        junk = [torch.full(s, float("nan"), device="cuda") for s in sizes for _ in range(3)]
+        junk.append(torch.full((before,), 255, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        if what == "append":
+            assert all(torch.equal(a, b) for a, b in zip(c.read(_i32([480, 60]), 30), held))
+        else:
+            assert torch.equal(got, want)
+        del junk

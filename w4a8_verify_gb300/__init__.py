@@ -343,8 +343,9 @@ class KV8Cache:
     Holds the cache's tensors, by name in ``tensors`` (``codes``, ``scales``, ``sums``, ``tail``, ``table``,
     ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
     fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
-    stream of the cache's device, or on ``stream`` (outputs and workspaces are then allocated on it); device state
-    that is out of range is reported by ``check``.
+    stream of the cache's device, or on ``stream`` (outputs and workspaces are then allocated on it, and the memory of
+    the call's tensors is not given to others before it is through with them; work of other streams on them is the
+    caller's to order); device state that is out of range is reported by ``check``.
 
     A decode step is about ten microseconds on the device, so the calls are written out: arguments are marshalled as
     packed bytes (w4a8_kv8_attn, w4a8_rows); the workspace sizes of the shapes seen and one workspace for each
@@ -378,7 +379,7 @@ class KV8Cache:
             raise ValueError("KV8Cache: the tensors must be on one CUDA device")
         self.desc = KV8CacheDesc(S, H, D, P, *[t.data_ptr() for t in got.values()])
         self._ref = _c.byref(self.desc)
-        self._sizes, self._kept, self._lock = {}, {}, threading.Lock()
+        self._sizes, self._kept, self._lock, self._streams = {}, {}, threading.Lock(), set()
         L = lib()
         self._attention, self._select, self._evict = L.w4a8_kv8_attention, L.w4a8_kv8_select, L.w4a8_kv8_evict
         self._append, self._read = L.w4a8_kv8_append, L.w4a8_kv8_read
@@ -390,11 +391,20 @@ class KV8Cache:
         return self.tensors["len"]
 
     def _elsewhere(self, stream, method, args):
-        """The call with ``stream`` as the current one."""
+        """The call with ``stream`` as the current one; tensors of other streams are marked as in use on it."""
+        torch = self._torch
         if stream.device != self.device:
             raise ValueError("KV8Cache: the stream is on another device than the cache")
-        with self._torch.cuda.stream(stream):
-            return method(*args)
+        with torch.cuda.stream(stream):
+            result = method(*args)
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+        if stream.cuda_stream not in self._streams:      # the cache's own: once for each stream
+            self._streams.add(stream.cuda_stream)
+            for t in self.tensors.values():
+                t.record_stream(stream)
+        return result
 
     def _run(self, fn, *args):
         """Calls fn(cache, *args, the current stream of the cache's device)."""
