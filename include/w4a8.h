@@ -283,9 +283,10 @@ w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4
  * one f16 factor each in bf16 calls (2^-11).  A new row has no effect on the rows that do not see
  * it, whatever it holds (NaN and infinities too), and rows at or behind counts[s] are not read.
  * The result does not depend on timing; it may depend, in its last bits, on the other sequences of
- * the call (they share the splits of the long axis).  out's strides must not be 0 where that axis
- * has more than one entry (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one that runs out sets
- * W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN, as is the mass of their pages.  A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
+ * the call (they share the splits of the long axis).  Rows of out must not lie on one another
+ * (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one that runs out sets
+ * W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN, as is the mass of their pages.
+ * A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
  * n_kv_heads * B < 2^22, and times the pages that a row reads < 2^31, with B = n (with pages), else
  * the blocks of at most 128 and at least 12 query rows (n * heads of a KV head) it is cut into.
  * workspace: 256-byte aligned, not shared by calls that may overlap; needs no initialisation. */

@@ -175,3 +175,21 @@ def test_tensors_of_a_call_on_a_given_stream_may_be_dropped():
         else:
             assert torch.equal(got, want)
         del junk
+
+
+@pytest.mark.parametrize("seq,row,head", [(64 * 3, 64 * 12, 64 * 2), (64 * 2, 64 * 9, 64 * 36), (64 * 24, 64 * 4 + 1, 64), (65, 65 * 3, 65 * 6)])
+def test_outputs_in_any_layout_without_overlap(seq, row, head):
+    """Rows of out between one another (strides that do not nest), in any order: each where it belongs, nothing else."""
+    rng = np.random.default_rng(seq)
+    S, H, G, D, n = 3, 1, 4, 64, 2
+    if seq == 64 * 3:
+        S = 2                                                  # 0, 3 rows and 0, 2, 4, 6: no two alike
+    c = _random_cache(5, [300, 64, 90][:S], H, D)
+    q, k = _rows(rng, S, n, H * G, D, "fp32"), _rows(rng, S, n, H, D, "fp32")
+    want = c.attention(q, k, k, scale=0.1)
+    buf = torch.full((64 * 200,), 5.0, device="cuda")
+    out = buf.as_strided((S, n, H * G, D), (seq, row, head, 1))
+    c.attention(q, k, k, scale=0.1, out=out)
+    assert torch.equal(out, want)
+    out.fill_(5.0)
+    assert (buf == 5.0).all()

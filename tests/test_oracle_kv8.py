@@ -121,3 +121,25 @@ def test_first_and_last_pages_come_before_infinities():
     x[:64 * 3] = nan
     c.append(0, x, x)
     assert O.select(c, 0, 0, np.ones((2, 64), np.float32), 2, 0, 1) == [0, 5]
+
+
+def _overlap(seq, row, head, S, n, heads, D):
+    """Whether two rows of D elements share one, element by element."""
+    at = (np.arange(S)[:, None, None] * seq + np.arange(n)[:, None] * row + np.arange(heads) * head).reshape(-1)
+    return len(np.unique(at[:, None] + np.arange(D))) < at.size * D
+
+
+LAYOUTS = [(64 * 8 - 1, 128, 64), (64 * 6, 64, 65), (64, 64 * 4, 63), (64 * 8, 64 * 4 - 1, 64), (4096, 64, 64 * 2 - 1),
+           (64 * 3, 64 * 5, 64 * 4 + 1), (-64 * 7, 64 * 2, 64), (130, 64 * 3, 64 * 6), (1 << 62, 1, 64), (64, -64, 1 << 40)]
+
+
+@pytest.mark.parametrize("seq,row,head", LAYOUTS, ids=str)
+def test_overlapping_output_rows_are_refused(lib, seq, row, head):
+    """Rows of out that share elements, by any of their strides (3 sequences, 2 rows, 4 heads of 64)."""
+    if pytest.importorskip("torch").cuda.is_available():
+        pytest.skip("the pointers of an accepted call would be read")
+    assert abs(seq) > 1 << 30 or abs(head) > 1 << 30 or _overlap(seq, row, head, 3, 2, 4, 64)
+    rows = W.Rows(0x100000, 4096, 512, 64)
+    a = W.KV8Attn(2, 4, 0, 1.0, rows, W.Rows(0x100000, seq, row, head))
+    p = ctypes.c_void_p(0x100000)
+    assert lib.w4a8_kv8_attention(ctypes.byref(_desc(3, 2, 64, 4)), ctypes.byref(a), p, 1 << 40, None) == 1
