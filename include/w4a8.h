@@ -288,7 +288,7 @@ w4a8_status w4a8_kv8_attention_workspace_bytes(const w4a8_kv8_cache* c, const w4
  * W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN, as is the mass of their pages.
  * A call of too many rows is W4A8_ERR_SHAPE: n_seqs *
  * n_kv_heads * B < 2^22, and times the pages that a row reads < 2^31, with B = n (with pages), else
- * the blocks of at most 128 and at least 12 query rows (n * heads of a KV head) it is cut into.
+ * the blocks of at most 128 and at least 4 (fp32) or 8 (bf16) query rows (n * heads of a KV head) it is cut into.
  * workspace: 256-byte aligned, not shared by calls that may overlap; needs no initialisation. */
 w4a8_status w4a8_kv8_attention(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -143,3 +143,22 @@ def test_overlapping_output_rows_are_refused(lib, seq, row, head):
     a = W.KV8Attn(2, 4, 0, 1.0, rows, W.Rows(0x100000, seq, row, head))
     p = ctypes.c_void_p(0x100000)
     assert lib.w4a8_kv8_attention(ctypes.byref(_desc(3, 2, 64, 4)), ctypes.byref(a), p, 1 << 40, None) == 1
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_size_limit_of_the_header(lib, dtype):
+    """n_seqs * n_kv_heads * B < 2^22 with B blocks of at least the header's rows: such calls are accepted, whatever the number
+    of rows; so is B * pages of a row up to 2^31."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "w4a8.h")).read()
+    least = int(re.search(r"at least (\d+) \(fp32\) or (\d+) \(bf16\)\s+(?:\* )?query rows", text).group(1 + dtype))
+    rows, sz = W.Rows(0x100000, 4096, 512, 64), ctypes.c_size_t()
+    for G in (1, 4, 7, 16):
+        for n in range(1, 65):
+            B = -(-n * G // least)
+            H = min(1024, ((1 << 22) - 1) // (4096 * B))
+            a = W.KV8Attn(n, H * G, dtype, 1.0, rows, rows)
+            size = lib.w4a8_kv8_attention_workspace_bytes
+            for pages in (1, min(511, ((1 << 31) - 1) // (4096 * H * B))):
+                assert size(ctypes.byref(_desc(4096, H, 64, pages)), ctypes.byref(a), ctypes.byref(sz)) == 0, (G, n, H, pages)

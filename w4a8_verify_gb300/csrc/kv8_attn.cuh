@@ -772,9 +772,13 @@ __global__ void __launch_bounds__(kKv8Threads, 1) k_kv8_split(w4a8_kv8_cache c, 
 // ---------------------------------------------------------------------------- launch
 
 // Warps on a page for R query rows of a problem, a tile each (four rows of fp32, eight of bf16): the number up to four
-// that leaves the fewest idle over the column blocks; the largest of equals (fewer reads of a page).  With six and
+// that leaves none idle over the column blocks; the largest of them (fewer reads of a page).  With six and
 // twelve allowed as well, 96 bf16 rows at 2048 tokens took 28.5 us instead of 18.4 (few workers, each with pages of two
-// segments one after the other), and no length gained.
+// segments one after the other), and no length gained.  Where only one divides the tiles, the fewer blocks of three or four
+// warps, some idle, win as often as they lose; fp32, 8 KV heads of 128, one warp / the best of three and four, us:
+//   20 rows: 1024 tokens 13.0 / 13.5, 16384 tokens 25.6 / 26.7; 16 sequences of up to 1024 39.5 / 36.4, of 16384 158 / 155
+//   28 rows: 1024 tokens 13.7 / 14.1, 16384 tokens 30.7 / 33.1; 16 sequences of up to 1024 45.4 / 41.3, of 16384 220 / 208
+//   44 rows: 1024 tokens 14.0 / 14.4, 4096 tokens 21.5 / 19.5;  16 sequences of up to 1024 53.6 / 49.2, of 4096 99.5 / 99.2
 inline int kv8_split_warps(int R, int dtype) {
   const int rpt = dtype == W4A8_F32 ? 4 : 8, tiles = (R + rpt - 1) / rpt;
   int best = 1;
