@@ -162,3 +162,20 @@ def test_size_limit_of_the_header(lib, dtype):
             size = lib.w4a8_kv8_attention_workspace_bytes
             for pages in (1, min(511, ((1 << 31) - 1) // (4096 * H * B))):
                 assert size(ctypes.byref(_desc(4096, H, 64, pages)), ctypes.byref(a), ctypes.byref(sz)) == 0, (G, n, H, pages)
+
+
+@pytest.mark.parametrize("dtype,rows", [(0, 4), (1, 8)])
+def test_the_kernel_of_a_call_goes_by_its_tiles(lib, dtype, rows):
+    """Row counts of the same tiles take the same kernel (seen in the scratch they need), at every length near the crossover
+    of 2^21 tile-page-dims: head size 128, one KV head, no new rows."""
+    r, sz = W.Rows(0x100000, 4096, 512, 64), ctypes.c_size_t()
+
+    def scratch(n, pages):
+        a = W.KV8Attn(n, 1, dtype, 1.0, r, r)
+        assert lib.w4a8_kv8_attention_workspace_bytes(ctypes.byref(_desc(1, 1, 128, pages)), ctypes.byref(a), ctypes.byref(sz)) == 0
+        return sz.value
+    for tiles in range(32 // rows + 1, 64 // rows + 1):
+        at = -(-(1 << 21) // (tiles * 128))                     # the first length of the wide kernel
+        for pages in (at - 1, at):
+            assert len({scratch(n, pages) for n in range((tiles - 1) * rows + 1, tiles * rows + 1)}) == 1, (tiles, pages)
+        assert scratch(tiles * rows, at - 1) != scratch(tiles * rows, at)

@@ -818,7 +818,7 @@ cudaError_t kv8_split_dispatch(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, 
 // rows: 8192 tokens 26.6 / 26.3 and 16384 tokens 40.8 / 36.0.
 inline bool kv8_is_wide(const w4a8_kv8_cache& c, const w4a8_kv8_attn& a, int R) {
   if (a.pages) return false;
-  const int64_t tiles = (R + 3) / (a.dtype == W4A8_F32 ? 4 : 8);
+  const int64_t rpt = a.dtype == W4A8_F32 ? 4 : 8, tiles = (R + rpt - 1) / rpt;
   return R > kWideRows || (R > 32 && tiles * c.n_seqs * c.n_kv_heads * c.max_pages * c.head_dim >= 1 << 21);
 }
 cudaError_t kv8_wide(const w4a8_kv8_cache&, const w4a8_kv8_attn&, const Kv8Geom&, const Kv8Scratch&, cudaStream_t);
