@@ -247,7 +247,9 @@ w4a8_status w4a8_kv8_check(const w4a8_kv8_cache* c, uint32_t* flags);
  * in order: position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of
  * a draft tree; the same row may come twice); with it n <= 1024, without it n_src >= n (W4A8_ERR_SHAPE).  The new
  * lengths go to len_out (device int32[n_seqs]); len_out == c->len advances the cache, which reads the
- * rows from then on.  A sequence that would pass 64 * max_pages + 63 tokens stays as it was, as does
+ * rows from then on.  Another len_out leaves c->len alone, not the open page: its buffer takes the rows behind the last page
+ * completed, so the cache is right at the lengths in len_out (store them in c->len to go on), and at the old ones
+ * only for sequences that completed no page.  A sequence that would pass 64 * max_pages + 63 tokens stays as it was, as does
  * one with a row out of range; an n beyond that is W4A8_ERR_CAPACITY. */
 w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,
                             int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);

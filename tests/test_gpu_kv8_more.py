@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 import w4a8_verify_gb300 as W
 from oracle import kv8 as O
-from test_gpu_kv8 import _i32, _long_check, _random_cache, _rows
+from test_gpu_kv8 import _check_state, _filled, _i32, _long_check, _np, _random_cache, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,30 @@ def test_outputs_in_any_layout_without_overlap(seq, row, head):
     assert torch.equal(out, want)
     out.fill_(5.0)
     assert (buf == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_what_an_append_with_lengths_apart_leaves(dtype):
+    """At the new lengths every sequence is right; at the old ones those that completed no page, and every whole page."""
+    rng = np.random.default_rng(17)
+    S, H, D = 4, 2, 64
+    lens, n = [10, 60, 127, 128], 20
+    cache, ref = _filled(rng, S, H, D, lens, dtype)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    before = cache.read(_i32([0] * S), 160)
+    after = torch.zeros(S, dtype=torch.int32, device="cuda")
+    cache.append(k, v, len_out=after)
+    assert after.tolist() == [x + n for x in lens] and cache.len.tolist() == lens
+    old = cache.read(_i32([0] * S), 160)
+    for a, b in zip(before, old):
+        assert torch.equal(a[[0, 3]], b[[0, 3]]) and torch.equal(a[2, :64], b[2, :64])
+    for a, b in zip(cache.read(_i32([0] * S), 160, length=after), (0, 1)):
+        for s in range(S):
+            rows = (k, v)[b][s].float()
+            whole = (lens[s] + n) // 64 * 64
+            assert torch.equal(a[s, whole:lens[s] + n], torch.cat([before[b][s, :lens[s]], rows])[whole:])
+    cache.len.copy_(after)
+    for s in range(S):
+        ref.append(s, _np(k)[s], _np(v)[s])
+    _check_state(cache, ref)
+    assert cache.check() == 0
