@@ -220,3 +220,20 @@ def test_what_an_append_with_lengths_apart_leaves(dtype):
         ref.append(s, _np(k)[s], _np(v)[s])
     _check_state(cache, ref)
     assert cache.check() == 0
+
+
+@pytest.mark.parametrize("dtype,n,G,room", [("fp32", 5, 4, 0), ("fp32", 11, 4, 0), ("bf16", 10, 4, 0), ("fp32", 7, 4, 300),
+                                            ("bf16", 9, 5, 300), ("fp32", 31, 4, 0), ("bf16", 11, 8, 300)])
+def test_long_ragged_ranges_of_row_counts_without_divisors(dtype, n, G, room):
+    """One warp to a page and many column blocks, a ring of one page a warp, runs over several segments; with room in the
+    cache behind the sequences; and where that room takes the call to the tcgen05 kernel."""
+    rng = np.random.default_rng(n * G + room)
+    S, H, D = 4, 2, 128
+    lens = [7000, 333, 4095, 6400]
+    c = _random_cache(n, lens, H, D, max_pages=110 + room)
+    q = _rows(rng, S, n, H * G, D, dtype, 2.0)
+    k, v = _rows(rng, S, n, H, D, dtype), _rows(rng, S, n, H, D, dtype)
+    old, new = torch.rand(S, H, c.shape[3], device="cuda"), torch.empty(S, H, c.shape[3], device="cuda")
+    out = c.attention(q, k, v, scale=D ** -0.5, mass=old, mass_out=new)
+    _long_check(c, q, k, v, D ** -0.5, out, range(H), range(S), old, new)
+    assert c.check() == 0
