@@ -237,3 +237,24 @@ def test_long_ragged_ranges_of_row_counts_without_divisors(dtype, n, G, room):
     out = c.attention(q, k, v, scale=D ** -0.5, mass=old, mass_out=new)
     _long_check(c, q, k, v, D ** -0.5, out, range(H), range(S), old, new)
     assert c.check() == 0
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_check_waits_for_its_stream(given):
+    """The status word of a call that is still queued on a stream of its own."""
+    c = _random_cache(8, [500, 77], 2, 64)
+    q = _rows(np.random.default_rng(3), 2, 3, 8, 64, "fp32")
+    counts = _i32([3, 4])                                      # out of range
+    c.attention(q, scale=0.1)
+    assert c.check() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    if given:
+        c.attention(q, scale=0.1, counts=counts, stream=side)
+        assert c.check(stream=side) == W.FLAG_ERR_CAPACITY
+    else:
+        with torch.cuda.stream(side):
+            c.attention(q, scale=0.1, counts=counts)
+            assert c.check() == W.FLAG_ERR_CAPACITY

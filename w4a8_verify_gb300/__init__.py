@@ -476,8 +476,12 @@ class KV8Cache:
             return self._elsewhere(stream, self.reset, ())
         self._run(lib().w4a8_kv8_reset)
 
-    def check(self):
-        """The status word (0 = every call's device state was in range); synchronous."""
+    def check(self, stream=None):
+        """The status word (0 = every call's device state was in range); waits for the calls on the current stream of the
+        cache's device, or on ``stream``."""
+        if stream is not None:
+            return self._elsewhere(stream, self.check, ())
+        self._torch.cuda.current_stream(self.device).synchronize()
         f = _c.c_uint32()
         st = lib().w4a8_kv8_check(self._ref, _c.byref(f))
         if st not in (0, 7):
