@@ -20,9 +20,11 @@
 // fp32 operands are split, q = qh + ql and P = Ph + Pl in f16: hi and lo are neighbouring columns of a tile (four
 // rows to a tile instead of eight), so the accumulator pair of a thread holds both products of one row and adds
 // them there.  Rows of q are scaled by a power of two, to a largest magnitude of at most 2^11; qh is the nearest
-// whole number, so the sums of qh with the codes are whole numbers (times 2^-24) that f32 holds, and the tensor
-// core's truncating additions do not touch them.  (With qh the nearest f16 the logits were off by 3e-7 relative.)
-// P is scaled by 2^7.
+// whole number, so the sums of qh with the codes (64 dims to an accumulator) are whole numbers below 2^24 that f32 holds, and
+// the tensor core's truncating additions do not touch them.  (With qh the nearest f16 the logits were off by 3e-7 relative.)
+// P is scaled by 2^7.  bf16 calls take one f16 term of q (exact: eight bits) and of P (off by 2^-11 at most, in no common
+// direction; the sums l are of P before that rounding): over 64 sequences outputs are 0.1658% off in the 2-norm, of which
+// their own rounding to bf16 (2^-8) is 0.1652%.  A second term of P would double the products with the values.
 // The transposed P fragments are made with movmatrix: no shared memory in the softmax.
 //
 // Work: every (sequence, KV head, block of rows) is a segment of pages.  The pages of all segments, end to end, are
@@ -38,7 +40,7 @@
 //
 // Bound: the codes once from memory when rows are few, the instructions of the conversion and the softmax when they
 // are many.  Measured (join included): one row of 131071 tokens, 8 KV heads of 128, 4 query heads each, bf16, 269 MB:
-// 53.3 us, 5.0 TB/s; 64 sequences of up to 8191 tokens, 646 MB: 117 us cold, 5.6 TB/s; a tree of 16 fp32 rows over 4096 tokens:
+// 53.7 us, 5.0 TB/s; 64 sequences of up to 8191 tokens, 646 MB: 113 us cold, 5.8 TB/s; a tree of 16 fp32 rows over 4096 tokens:
 // 27.7 us, of which 13 remain at 64 tokens (launches, rows, join).
 #pragma once
 #include <type_traits>

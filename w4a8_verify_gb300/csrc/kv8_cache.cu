@@ -65,8 +65,8 @@ constexpr int kVPad = 4;  // bytes between the token rows of a page's value code
 // tail, of a list, unaligned) are read twice.  Key groups of 16 bytes are whole in a thread; value groups (eight tokens of
 // two dims) are gathered from the codes in shared memory.  The CTA of the window's first page reads the old tail, so
 // it alone writes the new one, afterwards.
-// Bound by instructions (20 a value: absmax, rounding, packing, sums; 72% of the issue slots) and by the loads in flight:
-// 32768 bf16 rows of 8 heads of 128, 134 MB in and 67 MB out, 57 us cold (3.5 TB/s) with six CTAs on an SM, 63 with four.
+// Bound by instructions (20 a value: absmax, rounding, packing, sums; 69% of the issue slots) and by the loads in flight:
+// 32768 bf16 rows of 8 heads of 128, 134 MB in and 67 MB out, 58 us cold (3.5 TB/s) with six CTAs on an SM, 63 with four.
 // Four pages a CTA with the next one's loads in flight (120 registers): 10 us more.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 5) k_kv8_append(w4a8_kv8_cache c, w4a8_rows kr, w4a8_rows vr, int n_src,
@@ -305,7 +305,7 @@ __global__ void k_kv8_reset(w4a8_kv8_cache c) {
 // One CTA per (page of the window, KV head, sequence and keys/values): each value s * c with one rounding; positions
 // of the open page come from the tail.  A thread writes eight neighbouring dims of a position, 32 bytes; the codes of
 // value groups (eight tokens of two dims) change places in shared memory.  Bound by the writes: 32768 positions of
-// 8 heads of 128, 67 MB in and 268 MB out, 60 us cold (5.5 TB/s).
+// 8 heads of 128, 67 MB in and 268 MB out, 61 us cold (5.5 TB/s).
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_read(w4a8_kv8_cache c, const int32_t* first, const int32_t* len, int n,
                                                    float* __restrict__ k_out, float* __restrict__ v_out) {

@@ -131,7 +131,7 @@ constexpr int kScorePages = 128;  // pages of one CTA
 // Keys of the scores of one (sequence, new row, KV head) and a range of pages.  Integer dot products of the
 // query codes with the pages' code sums (dp2a: two 16-bit sums by two 8-bit codes); eight lanes share a page, whose sums are
 // read once for the group's queries.  Bound by instructions where rows are many (53% of the issue slots) and by latency
-// where they are few: 16 sequences of 4 rows, 8 heads, up to 511 pages, 15.7 us cold.  Pages are dealt to CTAs by 128, so
+// where they are few: 16 sequences of 4 rows, 8 heads, up to 511 pages, 14.8 us cold.  Pages are dealt to CTAs by 128, so
 // that one row of a long cache fills the GPU.
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(w4a8_kv8_cache c, w4a8_rows qr, const int32_t* counts,
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(w4a8_kv8_cache c, w
 }
 
 // The top_k pages of the scores, a CTA for each (row, KV head), the keys in shared memory: latency of the selection's
-// rounds; 512 lists of 32 of up to 511 pages 12 us cold.
+// rounds; 512 lists of 32 of up to 511 pages 11.5 us cold.
 __global__ void __launch_bounds__(512) k_kv8_pick(w4a8_kv8_cache c, const int32_t* counts, int n, int top_k,
                                                   const uint32_t* __restrict__ keys, int32_t* __restrict__ pages) {
   griddep_enter();

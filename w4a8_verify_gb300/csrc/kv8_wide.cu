@@ -14,13 +14,14 @@
 //             other pages', and nothing is rescaled in tensor memory.
 // fp32 calls split Q and P into f16 hi + lo; the products of P's share an accumulator, those of Q's have one each.  The
 // hi terms are the nearest whole numbers at a largest magnitude of 2^11 (P: scaled by 2^10, with the maximum of its own page),
-// so their sums with the codes are whole numbers below 2^24, which the tensor core's truncating additions leave exact.
+// so their sums with the codes are whole numbers, which the tensor core's truncating additions leave exact up to 2^24: all of
+// P's (64 tokens), and Q's but where 128 dims nearly all agree in sign and size (below 2^25: off by 2^-24 relative).
 // With hi the nearest f16, and Q's lo product in the accumulator of its hi product, outputs were off by 1.8e-6 in the
 // 2-norm at 4096 tokens, against 0.6e-6.
 // Why tcgen05 here: the split kernel converts a page once for every eight columns, and mma.sync tops out at a quarter
 // of the dense rate; with 128 rows a page is 2 x 256 cycles of tensor core against 700 of memory traffic.
-// Measured: 128 rows to each of 8 KV heads of 128, 32768 tokens: 56.0 us bf16, 79.7 us fp32 (0.97 and 1.8 us for a page of a
-// CTA, whose products take a quarter of that); 256 rows with the pages' mass, 32000 tokens, bf16: 91.6 us.  Bound by
+// Measured: 128 rows to each of 8 KV heads of 128, 32768 tokens: 56.7 us bf16, 80.7 us fp32 (0.98 and 1.8 us for a page of a
+// CTA, whose products take a quarter of that); 256 rows with the pages' mass, 32000 tokens, bf16: 92.5 us.  Bound by
 // the latency of the softmax warps (one to a scheduler; more of them leave too few registers for the values).
 #include "kv8_attn.cuh"
 
