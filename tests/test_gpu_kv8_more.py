@@ -258,3 +258,59 @@ def test_check_waits_for_its_stream(given):
         with torch.cuda.stream(side):
             c.attention(q, scale=0.1, counts=counts)
             assert c.check() == W.FLAG_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 64, 16), ("fp32", 128, 15)])
+def test_wide_calls_of_4096_sequences(dtype, D, G):
+    """The most sequences of a call in the tcgen05 kernel: a few checked."""
+    rng = np.random.default_rng(D)
+    S, n, H = 4096, 9, 1
+    lens = [int(x) for x in rng.integers(0, 192, S)]
+    c = _random_cache(11, lens, H, D, max_pages=3)
+    q, k = _rows(rng, S, n, H * G, D, dtype, 2.0), _rows(rng, S, n, H, D, dtype)
+    out = c.attention(q, k, k, scale=0.1)
+    _long_check(c, q, k, k, 0.1, out, [0], [0, 1, 2, 777, S - 2, S - 1])
+    assert c.check() == 0
+
+
+def test_1024_heads():
+    rng = np.random.default_rng(12)
+    S, H, D = 2, 1024, 64
+    cache, ref = W.KV8Cache(S, H, D, 4), O.Cache(S, H, D, 4)
+    k, v = _rows(rng, S, 150, H, D, "fp32"), _rows(rng, S, 150, H, D, "fp32")
+    cache.append(k, v, counts=_i32([150, 70]))
+    for s, c in enumerate((150, 70)):
+        ref.append(s, _np(k)[s, :c], _np(v)[s, :c])
+    q = _rows(rng, S, 2, H, D, "fp32")
+    old, new = torch.rand(S, H, 4, device="cuda"), torch.empty(S, H, 4, device="cuda")
+    out = cache.attention(q, k[:, :2], v[:, :2], scale=0.1, mass=old, mass_out=new)
+    _long_check(cache, q, k[:, :2], v[:, :2], 0.1, out, [0, 1, 511, 1023], [0, 1], old, new)
+    pages = cache.select(q, 1, last_pages=1)
+    assert pages[0].eq(1).all() and pages[1].eq(0).all()
+    table, mass, length = cache.evict(old, 1)
+    best = old[0, :, :2].argmax(dim=1)
+    assert torch.equal(table[0, :, 0], best.int()) and length.tolist() == [86, 70]
+    kk, vv = cache.read(_i32([100, 0]), 50)
+    assert torch.equal(kk[0, 28:50], k[0, 128:150]) and torch.equal(vv[0, 28:50], v[0, 128:150])
+    assert cache.check() == 0
+
+
+def test_the_longest_lists_and_eviction():
+    """16384 pages of one head: read by a list of all of them and without one; eviction to none, some and all."""
+    L, D = 64 * 16384 + 5, 64
+    rng = np.random.default_rng(1)
+    c = _random_cache(12, [L], 1, D, max_pages=16384)
+    q, k = _rows(rng, 1, 1, 2, D, "fp32"), _rows(rng, 1, 1, 1, D, "fp32")
+    pages = c.select(q, 16384)
+    assert torch.equal(pages[0, 0, 0], torch.arange(16384, device="cuda", dtype=torch.int32))
+    for lists in (None, pages):
+        _long_check(c, q, k, k, 0.2, c.attention(q, k, k, scale=0.2, pages=lists), [0], [0], pages=lists)
+    mass = torch.rand(1, 1, 16384, device="cuda")
+    order = mass[0, 0].argsort(descending=True, stable=True)
+    for keep in (0, 1, 100, 8192, 16383, 16384, 20000):
+        table, left, length = c.evict(mass, keep)
+        kept = order[:keep].sort().values
+        held = c.tensors["table"][0, 0]
+        assert torch.equal(table[0, 0, :len(kept)], held[kept]) and torch.equal(left[0, 0, :len(kept)], mass[0, 0, kept])
+        assert sorted(table[0, 0].tolist()) == list(range(16384)) and int(length[0]) == 64 * len(kept) + 5
+    assert c.check() == 0
