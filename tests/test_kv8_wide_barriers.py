@@ -301,3 +301,10 @@ def test_no_product_is_under_way_when_a_wait_has_run_out(fp32, left):
         stopped.steps["tensor"].append(step)
     give_up(stopped, _source(), issued)
     assert not [x for x in stopped.check() if "ends before" in x]
+
+
+def test_tensor_memory_is_taken_when_the_kernel_in_front_is_done():
+    """A CTA may start while the kernel in front runs; if it took tensor memory before that has ended, a CTA of that kernel on
+    the same SM could wait for it while it waits for that kernel."""
+    body = _source().split("k_kv8_wide(w4a8_kv8_cache c")[1]
+    assert 0 < body.index("griddep_enter();") < body.index("tcgen05.alloc")

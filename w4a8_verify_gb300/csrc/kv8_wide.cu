@@ -152,10 +152,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = c.n_seqs;
 
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&bar.code_full[i], 1), mbar_init(&bar.code_empty[i], kConvWarps);
     for (int i = 0; i < 2; ++i) {
@@ -171,6 +167,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv8_wide(w4a8_kv8_cache c, 
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
   griddep_enter();
+  // behind the wait: held while waiting, tensor memory could be what a CTA of the kernel in front still wants on this SM
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   kv8_prefix(c, a, geo, prefix);
   tc_before();
   __syncthreads();
