@@ -209,8 +209,8 @@ int w4a8_matmul_slices(int K, int N);
  * of range makes its sequence (len, counts) or page (table, pages) be left out and sets the
  * status word ctl (w4a8_kv8_check).  n_seqs 1..4096, n_kv_heads 1..1024, head_dim 64 or 128,
  * max_pages 1..16384, n_seqs * n_kv_heads * max_pages < 2^31; else W4A8_ERR_SHAPE.  codes 128-byte,
- * tail, sums and scales 16-byte aligned; else W4A8_ERR_ARG.  Calls that write a cache must be
- * ordered with the other calls on it.
+ * tail, sums and scales 16-byte aligned, every other pointer by its element's size; else W4A8_ERR_ARG.
+ * Calls that write a cache must be ordered with the other calls on it.
  * ---------------------------------------------------------------------------- */
 typedef struct {
   int n_seqs, n_kv_heads, head_dim, max_pages;

@@ -314,3 +314,16 @@ def test_the_longest_lists_and_eviction():
         assert torch.equal(table[0, 0, :len(kept)], held[kept]) and torch.equal(left[0, 0, :len(kept)], mass[0, 0, kept])
         assert sorted(table[0, 0].tolist()) == list(range(16384)) and int(length[0]) == 64 * len(kept) + 5
     assert c.check() == 0
+
+
+@pytest.mark.parametrize("dtype,n", [("fp32", 3), ("bf16", 40)])
+def test_rows_written_over_the_queries(dtype, n):
+    """out is q itself: every kernel that reads the queries is done before they are written."""
+    rng = np.random.default_rng(n)
+    c = _random_cache(14, [3000, 100], 2, 128)
+    q, k = _rows(rng, 2, n, 8, 128, dtype), _rows(rng, 2, n, 2, 128, dtype)
+    pages = c.select(q, 5)
+    for lists in (None, pages):
+        want = c.attention(q, k, k, scale=0.1, pages=lists)
+        mine = q.clone()
+        assert c.attention(mine, k, k, scale=0.1, pages=lists, out=mine) is mine and torch.equal(mine, want)

@@ -179,3 +179,31 @@ def test_the_kernel_of_a_call_goes_by_its_tiles(lib, dtype, rows):
         for pages in (at - 1, at):
             assert len({scratch(n, pages) for n in range((tiles - 1) * rows + 1, tiles * rows + 1)}) == 1, (tiles, pages)
         assert scratch(tiles * rows, at - 1) != scratch(tiles * rows, at)
+
+
+def test_pointers_off_their_alignment_are_refused(lib):
+    """Lengths, counts, lists, masks and masses too: a kernel would fault on them.  (No pointer here is read: every call is
+    refused, by a workspace of no bytes at the latest.)"""
+    if pytest.importorskip("torch").cuda.is_available():
+        pytest.skip("the pointers of an accepted call would be read")
+    c, p, odd = ctypes.byref(_desc(1, 2, 64, 4)), ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100002)
+    rows = W.Rows(0x100000, 4096, 512, 64)
+    r = ctypes.byref(rows)
+    assert lib.w4a8_kv8_append(c, r, r, 0, 4, 4, odd, None, p, None) == 1
+    assert lib.w4a8_kv8_append(c, r, r, 0, 4, 4, None, odd, p, None) == 1
+    assert lib.w4a8_kv8_append(c, r, r, 0, 4, 4, None, None, odd, None) == 1
+    assert lib.w4a8_kv8_read(c, odd, None, 4, p, p, None) == 1 and lib.w4a8_kv8_read(c, p, odd, 4, p, p, None) == 1
+    for args in ((odd, p, p, p), (p, odd, p, p), (p, p, odd, p), (p, p, p, odd)):
+        assert lib.w4a8_kv8_evict(c, args[0], 1, 0, 0, *args[1:], None) == 1
+    for name, value in (("counts", 0x100002), ("mask", 0x100004), ("pages", 0x100001), ("mass", 0x100003), ("mass_out", 0x100002)):
+        a = W.KV8Attn(4, 4, 0, 1.0, rows, rows, rows, rows, top_k=1)
+        assert lib.w4a8_kv8_attention(c, ctypes.byref(a), p, 0, None) == 4
+        if name == "mass":
+            a.mass_out = 0x100000
+        setattr(a, name, value)
+        assert lib.w4a8_kv8_attention(c, ctypes.byref(a), p, 0, None) == 1, name
+    a = W.KV8Attn(4, 4, 0, 1.0, rows)
+    assert lib.w4a8_kv8_select(c, ctypes.byref(a), 1, 0, 0, p, p, 0, None) == 4
+    assert lib.w4a8_kv8_select(c, ctypes.byref(a), 1, 0, 0, odd, p, 0, None) == 1
+    a.counts = 0x100002
+    assert lib.w4a8_kv8_select(c, ctypes.byref(a), 1, 0, 0, p, p, 0, None) == 1

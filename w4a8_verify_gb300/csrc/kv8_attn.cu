@@ -242,7 +242,8 @@ static w4a8_status attend(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, void*
   // rows of out that lie on one another would be written in any order
   if ((c->n_seqs > 1 && !a->out.seq) || (a->n > 1 && !a->out.row) || (a->n_heads > 1 && !a->out.head)) return W4A8_ERR_ARG;
   if (!a->q.data || !a->out.data || !workspace || !aligned(workspace, 256) || !aligned(a->q.data, el) ||
-      !aligned(a->out.data, el) || !aligned(a->k.data, el) || !aligned(a->v.data, el))
+      !aligned(a->out.data, el) || !aligned(a->k.data, el) || !aligned(a->v.data, el) || !aligned(a->counts, 4) ||
+      !aligned(a->mask, 8) || !aligned(a->pages, 4) || !aligned(a->mass, 4) || !aligned(a->mass_out, 4))
     return W4A8_ERR_ARG;
   if (workspace_bytes < p.bytes) return W4A8_ERR_CAPACITY;
   if (rows_overlap(a->out, c->n_seqs, a->n, a->n_heads, c->head_dim)) return W4A8_ERR_ARG;

@@ -422,7 +422,9 @@ W4A8_API w4a8_status w4a8_kv8_append(const w4a8_kv8_cache* c, const w4a8_rows* k
   if (ok != W4A8_OK) return ok;
   if (!k || !v || !k->data || !v->data || !len_out || !kv8_dtype(dtype) || n < 1 || n_src < 1) return W4A8_ERR_ARG;
   if (index ? n > kMaxIndexed : n_src < n) return W4A8_ERR_SHAPE;
-  if (!aligned(k->data, kv8_elem(dtype)) || !aligned(v->data, kv8_elem(dtype))) return W4A8_ERR_ARG;
+  if (!aligned(k->data, kv8_elem(dtype)) || !aligned(v->data, kv8_elem(dtype)) || !aligned(counts, 4) ||
+      !aligned(index, 4) || !aligned(len_out, 4))
+    return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages + kPage - 1) return W4A8_ERR_CAPACITY;
   cudaStream_t st = as_stream(stream);
   const dim3 grid((unsigned)((n + kPage - 1 + kPage - 1) / kPage), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs * 2);
@@ -445,7 +447,8 @@ W4A8_API w4a8_status w4a8_kv8_read(const w4a8_kv8_cache* c, const int32_t* first
                                    float* k_out, float* v_out, void* stream) {
   const w4a8_status ok = kv8_valid(c);
   if (ok != W4A8_OK) return ok;
-  if (!first || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || n < 1) return W4A8_ERR_ARG;
+  if (!first || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(first, 4) || !aligned(len, 4) || n < 1)
+    return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages + kPage - 1) return W4A8_ERR_CAPACITY;
   const dim3 grid((unsigned)((n + kPage - 1 + kPage - 1) / kPage), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs * 2);
   const int32_t* L = len ? len : c->len;

@@ -299,7 +299,7 @@ W4A8_API w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_att
   if (ok == W4A8_OK) ok = kv8_valid(c);
   if (ok != W4A8_OK) return ok;
   if (!a->q.data || !aligned(a->q.data, kv8_elem(a->dtype)) || !pages_out || !workspace || !aligned(workspace, 256) ||
-      top_k < 1 || first_pages < 0 || last_pages < 0)
+      !aligned(pages_out, 4) || !aligned(a->counts, 4) || top_k < 1 || first_pages < 0 || last_pages < 0)
     return W4A8_ERR_ARG;
   if (top_k > kKv8MaxPages) return W4A8_ERR_SHAPE;
   if (workspace_bytes < need) return W4A8_ERR_CAPACITY;
@@ -331,6 +331,7 @@ W4A8_API w4a8_status w4a8_kv8_evict(const w4a8_kv8_cache* c, const float* mass, 
   const w4a8_status ok = kv8_valid(c);
   if (ok != W4A8_OK) return ok;
   if (!mass || !table_out || !mass_out || !len_out || keep < 0 || first_pages < 0 || last_pages < 0) return W4A8_ERR_ARG;
+  if (!aligned(mass, 4) || !aligned(table_out, 4) || !aligned(mass_out, 4) || !aligned(len_out, 4)) return W4A8_ERR_ARG;
   cudaStream_t st = as_stream(stream);
   const bool own = len_out == c->len;
   W4A8_CUDA_TRY(kv8_smem<k_kv8_evict>(kKv8MaxPages * 12));
