@@ -490,7 +490,8 @@ class KV8Cache:
 
     def append(self, k, v, counts=None, index=None, len_out=None, stream=None):
         """Commits rows of k and v, advancing the cache's lengths, or storing the new ones in ``len_out`` instead
-        (w4a8_kv8_append): a sequence that completes a page is then right at its new length alone.  ``index`` [n_seqs][n]: the source row of each new position."""
+        (w4a8_kv8_append): a sequence that completes a page is then right at its new length alone.  ``index``
+        [n_seqs][n]: the source row of each new position."""
         if stream is not None:
             return self._elsewhere(stream, self.append, (k, v, counts, index, len_out))
         S, H, D, _ = self.shape
