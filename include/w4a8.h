@@ -322,6 +322,139 @@ w4a8_status w4a8_kv8_select(const w4a8_kv8_cache* c, const w4a8_kv8_attn* a, int
 w4a8_status w4a8_kv8_evict(const w4a8_kv8_cache* c, const float* mass, int keep, int first_pages, int last_pages,
                            int32_t* table_out, float* mass_out, int32_t* len_out, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Key/value cache in 4 bits (pages in one pool, sequences that may share them)
+ *
+ * One w4a8_kv4_cache holds one layer of n_seqs sequences in buffers the caller owns.  A page of the pool is 64 tokens of
+ * every KV head; table[s][p] is the pool's page with tokens 64 p .. 64 p + 63 of sequence s.  Several sequences may name
+ * the same page (a common prefix); a page that an append writes to must then belong to one sequence alone.
+ * A row of a head is held in groups of 32 dims as whole numbers c times a scale s of eight bits:
+ *   s = absmax / 7 (IEEE), then to the nearest (half to even) of (8 + m) * 2^(e - 18), 0 <= m < 8, 1 <= e, or
+ *       m * 2^-17, at most 240 (larger values are held as 7 * 240);  byte 8 e + m (e = 0 for the small ones)
+ *   c = clamp(rint(x / s), -7, 7);  s == 0 -> c = 0
+ * (a NaN or an infinity among the 32 makes the byte 255, read as NaN, and every c 0).  Tokens are quantised one by
+ * one, as they arrive: there is no open page in another type.  c * s has at most seven significant bits.
+ *
+ * A page of one head is 68 * head_dim bytes (D = head_dim), fields as a warp reads them as m16n8k16 operands:
+ *   codes of the keys, at 0: 16-bit word (((tok/16 * D/64 + dim/64) * 32 + tok%8 * 4 + dim%32/8) * 4 + dim%64/32 * 2
+ *     + dim%8/4) * 2 + dim%2, field dim%4/2 * 2 + tok%16/8
+ *   codes of the values, at 32 D: 16-bit word (((tok/16 * D/64 + dim/64) * 32 + dim%8 * 4 + tok%8/2) * 4 + dim%64/16) * 2
+ *     + tok%2, field dim%16/8 * 2 + tok%16/8
+ *   scales of the keys, at 64 D: byte (tok/16 * 8 + tok%8) * D/16 + tok%16/8 * D/32 + dim/32
+ *   scales of the values, at 66 D: byte ((tok/16 * 4 + tok%8/2) * D/32 + dim/32) * 4 + tok%16/8 * 2 + tok%2
+ * Field f of a word holds c + 8 in its bits 4 f .. 4 f + 3 turned left by two (bits 14, 15 of field 3 and 0, 1).
+ *
+ * Lengths, counts, tables and masks are read on the device when the kernels run, so a captured call can be replayed as
+ * they change.  What they hold is checked there: a value out of range makes its sequence (len, counts) or page (table) be
+ * left out and sets the status word ctl (w4a8_kv4_check).  n_seqs 1..4096, n_kv_heads 1..1024, head_dim 64 or 128,
+ * max_pages 1..16384, n_pages * n_kv_heads and n_seqs * n_kv_heads * max_pages < 2^31; else W4A8_ERR_SHAPE.  pages 128-byte,
+ * every other pointer aligned by its element's size; else W4A8_ERR_ARG.
+ * Calls that write a cache must be ordered with the other calls on it.
+ * ---------------------------------------------------------------------------- */
+typedef struct {
+  int n_seqs, n_kv_heads, head_dim, max_pages, n_pages;
+  uint8_t* pages;   /* [n_pages][n_kv_heads][68 * head_dim] */
+  int32_t* table;   /* [n_seqs][max_pages] */
+  int32_t* len;     /* [n_seqs], 0 .. 64 * max_pages */
+  uint32_t* ctl;    /* [1] status word: W4A8_FLAG_* of the calls since it was cleared */
+} w4a8_kv4_cache;
+
+/* Host.  Bytes of the four buffers of a cache with these dimensions, in the struct's order. */
+w4a8_status w4a8_kv4_bytes(const w4a8_kv4_cache* c, size_t bytes[4]);
+/* Device.  Empties a cache: len = 0, ctl = 0, table[s][p] = s * max_pages + p (modulo n_pages). */
+w4a8_status w4a8_kv4_reset(const w4a8_kv4_cache* c, void* stream);
+/* Host, synchronous (call after the stream has finished).  *flags = the status word; the call returns
+ * W4A8_ERR_DEVICE_FLAG if it is not 0: W4A8_FLAG_ERR_CAPACITY (a length, count or first position out of range, or an append beyond
+ * max_pages), W4A8_FLAG_ERR_TOKEN (a source row out of range), W4A8_FLAG_ERR_TREE (a table entry out of range),
+ * W4A8_FLAG_ERR_TIMEOUT. */
+w4a8_status w4a8_kv4_check(const w4a8_kv4_cache* c, uint32_t* flags);
+
+/* Device.  Commits rows: row j < counts[s] of k and v (n rows, dtype, any order of strides) becomes position len[s] + j of
+ * sequence s.  counts: device int32[n_seqs] in 0..n, NULL = n.  index: device int32 [n_seqs][n], NULL = the rows in order:
+ * position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of a draft tree; the same row may
+ * come twice); with it n <= 1024, without it n_src >= n (W4A8_ERR_SHAPE).  The new lengths go to len_out (device int32[n_seqs]);
+ * len_out == c->len advances the cache, another one leaves c->len alone, and the cache is right at either.  A sequence
+ * that would pass 64 * max_pages tokens stays as it was, as does one with a row out of range; a page whose table entry is out of
+ * range takes no rows.  An n beyond 64 * max_pages is W4A8_ERR_CAPACITY. */
+w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,
+                            int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);
+/* Device.  Positions first[s] .. first[s] + n - 1 of every sequence as the cache holds them (c * s: exact in either type),
+ * positions at or behind len[s] as 0, into k_out and v_out, dtype [n_seqs][n][n_kv_heads][head_dim] contiguous, 16-byte
+ * aligned.  len: NULL = c->len.  A sequence whose length or first position is out of range is read as 0, as is a page whose
+ * table entry is. */
+w4a8_status w4a8_kv4_read(const w4a8_kv4_cache* c, const int32_t* first, const int32_t* len, int n, int dtype,
+                          void* k_out, void* v_out, void* stream);
+
+/* Attention of n new rows per sequence over its cache and the rows themselves. */
+typedef struct {
+  int n;                 /* rows of every sequence, 1..64 */
+  int n_heads;           /* query heads, n_kv_heads * (1..16); head h uses KV head h / (n_heads / n_kv_heads) */
+  int dtype;             /* of q, k, v and out */
+  float scale;           /* logit = scale * q . k */
+  w4a8_rows q, out;      /* [n_seqs][n][n_heads][head_dim] */
+  w4a8_rows k, v;        /* [n_seqs][n][n_kv_heads][head_dim]; both data NULL: the cache alone is read */
+  const int32_t* counts; /* rows of each sequence, 0..n; NULL = n.  Rows behind them: out is left as it was */
+  const uint64_t* mask;  /* [n_seqs][n]: bit j of row i is set where i sees new row j; NULL: j <= i */
+} w4a8_kv4_attn;
+/* Host.  Scratch bytes of w4a8_kv4_attention (the pointers in a are not read, only whether they are NULL). */
+w4a8_status w4a8_kv4_attention_workspace_bytes(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, size_t* bytes);
+/* Device.  out[s][i][h] = sum_t w_t v_t with w = softmax over the committed tokens and the visible new rows; a row that
+ * sees nothing is 0.  Logits, softmax statistics and sums are fp32.  The products with the new rows are plain fp32; those with
+ * the pages use f16 hi/lo pairs of q and of the weights in fp32 calls (about 2^-21 relative) and one f16 factor
+ * each in bf16 calls (2^-11).  A new row has no effect on the rows that do not see it, whatever it holds (NaN and infinities
+ * too), and rows at or behind counts[s] are not read.  The result does not depend on timing; it may depend, in its last
+ * bits, on the other sequences of the call (they share the splits of the long axis).  A page whose table entry is out of range is
+ * left out.  Rows of out must not lie on one another (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one
+ * that runs out sets W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN.  n_seqs * n_kv_heads * B < 2^22 and
+ * times max_pages < 2^31, with B the blocks of at most 128 and at least 4 (fp32) or 8 (bf16) query rows (n * heads of a KV head) a
+ * sequence's rows are cut into; else W4A8_ERR_SHAPE.
+ * workspace: 256-byte aligned, not shared by calls that may overlap.  Its first W4A8_KV4_TICKETS bytes must be zero before its
+ * first use; every call leaves them so, whatever its sizes, and the rest needs no initialisation. */
+#define W4A8_KV4_TICKETS 8192
+w4a8_status w4a8_kv4_attention(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, void* workspace, size_t workspace_bytes,
+                               void* stream);
+/* Device, test-only: w4a8_kv4_attention in which CTA number cta of the kernel over the pages issues none of its copies and
+ * waits are limited to 20 ms, so that its waits run out: ctl gets W4A8_FLAG_ERR_TIMEOUT, the rows that miss its part are NaN,
+ * the others are as ever.  Nothing hangs or faults, no copy is left in flight, and later calls work. */
+w4a8_status w4a8_kv4_attention_inject_timeout(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, void* workspace,
+                                              size_t workspace_bytes, int cta, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Norm and rotary positions of queries and keys, in one pass
+ *
+ *   y = rot(x * r * gain),  r = (mean of the head's squares + eps)^-1/2,
+ * and rot turns pair i of the first rot_dim dims by the angle 2 pi * position[axis[i]] * turns[i] / 2^64, times factor.  The
+ * product is taken in 64-bit whole numbers, whose overflow drops whole turns: the angle is as exact at position
+ * 2^31 as at 1.  A pair is dims (i, i + rot_dim / 2) or, with neighbours, (2 i, 2 i + 1); dims behind rot_dim
+ * are not turned.  One axis is the ordinary rotary position; with several (time, height, width) each frequency takes the
+ * position of its own axis, in any arrangement (blocks of frequencies, by turns).  Everything is fp32 and is rounded once.
+ * ---------------------------------------------------------------------------- */
+/* Host, synchronous.  turns[i] = the fraction inv_freq[i] / (2 pi) modulo 1 in units of 2^-64, rounded from 64-bit floating point
+ * (inv_freq finite: radians for each position). */
+w4a8_status w4a8_rotary_turns(const double* inv_freq, int n, uint64_t* turns);
+typedef struct {
+  int n_seqs, n, n_heads, n_kv_heads, head_dim; /* head_dim a multiple of 16, 16..256 */
+  int rot_dim;            /* a multiple of 16, 0..head_dim */
+  int n_axes;             /* 1..4 */
+  int neighbours;         /* 1: pairs of neighbouring dims; 0: of the two halves of rot_dim */
+  int dtype;              /* of q, k, q_out and k_out */
+  int norm;               /* 1: divide each head by the root of its mean square (eps, gains); 0: do not */
+  float eps, factor;      /* factor: of the turned dims (1 but for stretched contexts) */
+  const uint64_t* turns;  /* device [rot_dim / 2] */
+  const uint8_t* axis;    /* device [rot_dim / 2], below n_axes (others are read as 0); NULL: all 0 */
+  const int32_t* pos;     /* device [n_axes][n_seqs][n]; NULL: the row's number, on every axis */
+  const int32_t* start;   /* device [n_seqs], added to every position of a sequence (e.g. a cache's len); NULL: 0 */
+  const int32_t* counts;  /* device [n_seqs]: rows of each sequence (below 0: 0, above n: n); NULL: n.  Rows behind them: the outputs are
+                             left as they were */
+  const float *q_gain, *k_gain; /* device [head_dim]; NULL: 1 */
+  w4a8_rows q, q_out;     /* [n_seqs][n][n_heads][head_dim] */
+  w4a8_rows k, k_out;     /* [n_seqs][n][n_kv_heads][head_dim]; both data NULL (and n_kv_heads 0): no keys */
+} w4a8_qk_rotary_args;
+/* Device.  q_out may be q itself and k_out k itself, with the same strides; any other way for an output to lie on an input
+ * or on itself is refused where the address ranges cross (W4A8_ERR_ARG), but for rows side by side in one tensor (the
+ * parts of one projection's output: equal seq and row strides, heads that do not meet).  n_seqs * n * (n_heads + n_kv_heads) < 2^31. */
+w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* a, void* stream);
+
 /* ==============================================================================
  * Decoder, session and the GPU-resident speculation loop
  * ============================================================================ */

@@ -71,6 +71,25 @@ class KV8Attn(_c.Structure):
                 ("mass", _vp), ("mass_out", _vp)]
 
 
+class KV4CacheDesc(_c.Structure):
+    _fields_ = [("n_seqs", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("max_pages", _i32), ("n_pages", _i32),
+                ("pages", _vp), ("table", _vp), ("len", _vp), ("ctl", _vp)]
+
+
+class KV4Attn(_c.Structure):
+    _fields_ = [("n", _i32), ("n_heads", _i32), ("dtype", _i32), ("scale", _f32), ("q", Rows), ("out", Rows),
+                ("k", Rows), ("v", Rows), ("counts", _vp), ("mask", _vp)]
+
+
+class QKRotaryArgs(_c.Structure):
+    _fields_ = [("n_seqs", _i32), ("n", _i32), ("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+                ("rot_dim", _i32), ("n_axes", _i32), ("neighbours", _i32), ("dtype", _i32), ("norm", _i32),
+                ("eps", _f32), ("factor", _f32), ("turns", _vp), ("axis", _vp), ("pos", _vp), ("start", _vp),
+                ("counts", _vp), ("q_gain", _vp), ("k_gain", _vp), ("q", Rows), ("q_out", Rows), ("k", Rows),
+                ("k_out", Rows)]
+
+
+KV4_TICKETS = 8192  # bytes of an attention workspace that are zero between calls
 FLAG_TERMINATED, FLAG_ERR_CAPACITY, FLAG_ERR_TOKEN, FLAG_ERR_TREE, FLAG_ERR_TIMEOUT = 1, 2, 4, 8, 16
 T_Q, T_K, T_V, T_O, T_GATE, T_UP, T_DOWN, T_EMBED, T_LM_HEAD = range(9)
 
@@ -104,6 +123,16 @@ _SIGNATURES = {
     "w4a8_kv8_select_workspace_bytes": [_c.POINTER(KV8CacheDesc), _vp, _c.POINTER(_sz)],
     "w4a8_kv8_select": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp],
     "w4a8_kv8_evict": [_c.POINTER(KV8CacheDesc), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
+    "w4a8_kv4_bytes": [_c.POINTER(KV4CacheDesc), _c.POINTER(_sz)],
+    "w4a8_kv4_reset": [_c.POINTER(KV4CacheDesc), _vp],
+    "w4a8_kv4_check": [_c.POINTER(KV4CacheDesc), _c.POINTER(_c.c_uint32)],
+    "w4a8_kv4_append": [_c.POINTER(KV4CacheDesc), _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
+    "w4a8_kv4_read": [_c.POINTER(KV4CacheDesc), _vp, _vp, _i32, _i32, _vp, _vp, _vp],
+    "w4a8_kv4_attention_workspace_bytes": [_c.POINTER(KV4CacheDesc), _vp, _c.POINTER(_sz)],
+    "w4a8_kv4_attention": [_c.POINTER(KV4CacheDesc), _vp, _vp, _sz, _vp],
+    "w4a8_kv4_attention_inject_timeout": [_c.POINTER(KV4CacheDesc), _vp, _vp, _sz, _i32, _vp],
+    "w4a8_rotary_turns": [_vp, _i32, _vp],
+    "w4a8_qk_rotary": [_vp, _vp],
     "w4a8_model_create": [_c.POINTER(ModelDesc), _c.POINTER(_vp)],
     "w4a8_model_load_tensor": [_vp, _i32, _i32, _vp, _vp, _vp],
     "w4a8_model_weight_bytes": [_vp, _c.POINTER(_sz)],
@@ -337,64 +366,45 @@ def w4a8_matmul(a_q, a_s, w_t, s_t, N, y=None, workspace=None, stream=None):
 
 # ------------------------------------------------------------- key/value cache in 8 bits
 
-class KV8Cache:
-    """One layer of ``n_seqs`` sequences' keys and values in 8 bits (w4a8_kv8_cache).
+class _PagedCache:
+    """What the paged caches share: their tensors, checks of arguments, streams and workspaces."""
 
-    Holds the cache's tensors, by name in ``tensors`` (``codes``, ``scales``, ``sums``, ``tail``, ``table``,
-    ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
-    fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
-    stream of the cache's device, or on ``stream`` (outputs and workspaces are then allocated on it, and the memory of
-    the call's tensors is not given to others before it is through with them; work of other streams on them is the
-    caller's to order); device state that is out of range is reported by ``check``.
-
-    A decode step is about ten microseconds on the device, so the calls are written out: arguments are marshalled as
-    packed bytes (w4a8_kv8_attn, w4a8_rows); the workspace sizes of the shapes seen and one workspace for each
-    stream are kept.
-    """
-
-    _NAMES = (("codes", "uint8"), ("scales", "float32"), ("sums", "int16"), ("tail", "float32"), ("table", "int32"),
-              ("len", "int32"), ("ctl", "int32"))
-    _ATTN = struct.Struct("@iiif 4q 4q 4q 4q 3q i 2q")   # w4a8_kv8_attn
     _ROWS = struct.Struct("@4q")                         # w4a8_rows
     _NONE = (0, 0, 0, 0)
 
-    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, device="cuda", tensors=None):
+    def _adopt(self, names, shapes, device, tensors):
+        """Takes the cache's tensors, or makes new ones."""
         import torch
         self._torch = torch
         self._types = {torch.float32: 0, torch.bfloat16: 1}
-        S, H, D, P = self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
-        self.desc = KV8CacheDesc(S, H, D, P)
-        _call("w4a8_kv8_bytes", _c.byref(self.desc), (_sz * 7)())     # refuses dimensions out of range
-        shapes = ((S, H, P, 2, 64 * D), (S, H, P, 2), (S, H, P, D), (S, H, 2, 64, D), (S, H, P), (S,), (1,))
-        own, got = tensors is None, {}
-        for (name, dtype), shape in zip(self._NAMES, shapes):
+        self._name = type(self).__name__
+        got = {}
+        for (name, dtype), shape in zip(names, shapes):
             dtype = getattr(torch, dtype)
-            t = got[name] = torch.empty(shape, dtype=dtype, device=device) if own else tensors[name]
+            t = got[name] = torch.empty(shape, dtype=dtype, device=device) if tensors is None else tensors[name]
             if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-                raise ValueError("KV8Cache: %s must be a contiguous %s tensor of shape %s" % (name, dtype, shape))
+                raise ValueError("%s: %s must be a contiguous %s tensor of shape %s" % (self._name, name, dtype, shape))
         self.tensors = got
-        self.device = got["codes"].device
-        self._dev = got["codes"].get_device()
+        one = next(iter(got.values()))
+        self.device = one.device
+        self._dev = one.get_device()
         if self._dev < 0 or any(t.get_device() != self._dev for t in got.values()):
-            raise ValueError("KV8Cache: the tensors must be on one CUDA device")
-        self.desc = KV8CacheDesc(S, H, D, P, *[t.data_ptr() for t in got.values()])
-        self._ref = _c.byref(self.desc)
+            raise ValueError("%s: the tensors must be on one CUDA device" % self._name)
         self._sizes, self._kept, self._lock, self._streams = {}, {}, threading.Lock(), set()
-        L = lib()
-        self._attention, self._select, self._evict = L.w4a8_kv8_attention, L.w4a8_kv8_select, L.w4a8_kv8_evict
-        self._append, self._read = L.w4a8_kv8_append, L.w4a8_kv8_read
-        if own:
-            self.reset()
+        return [t.data_ptr() for t in got.values()]
 
     @property
     def len(self):
         return self.tensors["len"]
 
+    def _scratch(self, need):
+        return self._torch.empty(need, dtype=self._torch.uint8, device=self.device)
+
     def _elsewhere(self, stream, method, args):
         """The call with ``stream`` as the current one; tensors of other streams are marked as in use on it."""
         torch = self._torch
         if stream.device != self.device:
-            raise ValueError("KV8Cache: the stream is on another device than the cache")
+            raise ValueError(self._name + ": the stream is on another device than the cache")
         with torch.cuda.stream(stream):
             result = method(*args)
         for t in args:
@@ -420,26 +430,26 @@ class KV8Cache:
     def _vec(self, t, name, dtype, shape):
         """Pointer of a contiguous tensor of this device, type and shape."""
         if t.dtype is not dtype or t.shape != shape or t.get_device() != self._dev or not t.is_contiguous():
-            raise ValueError("KV8Cache: %s must be a contiguous %s tensor %s on the cache's device"
-                             % (name, str(dtype)[6:], list(shape)))
+            raise ValueError("%s: %s must be a contiguous %s tensor %s on the cache's device"
+                             % (self._name, name, str(dtype)[6:], list(shape)))
         return t.data_ptr()
 
     def _rows(self, t, name, dtype, shape):
         """The fields of a w4a8_rows for t of that shape, [n_seqs][n][heads][head_dim]."""
         a, b, c, d = t.stride() if t.shape == shape else (0, 0, 0, 0)
         if d != 1 or t.dtype is not dtype or t.get_device() != self._dev:
-            raise ValueError("KV8Cache: %s must be %s %s with unit stride in the last dimension, on the cache's device"
-                             % (name, str(dtype)[6:], list(shape)))
+            raise ValueError("%s: %s must be %s %s with unit stride in the last dimension, on the cache's device"
+                             % (self._name, name, str(dtype)[6:], list(shape)))
         return t.data_ptr(), a, b, c
 
     def _query(self, q):
         """(fields, type number, n, heads) of a tensor of query rows."""
-        S, _, D, _ = self.shape
+        S, D = self.shape[0], self.shape[2]
         shape, dtype = q.shape, q.dtype
         kind = self._types.get(dtype)
         if kind is None or len(shape) != 4 or shape[0] != S or shape[3] != D:
-            raise ValueError("KV8Cache: q must be fp32 or bf16 [%d][n][heads][%d], not %s %s"
-                             % (S, D, str(dtype)[6:], list(shape)))
+            raise ValueError("%s: q must be fp32 or bf16 [%d][n][heads][%d], not %s %s"
+                             % (self._name, S, D, str(dtype)[6:], list(shape)))
         return self._rows(q, "q", dtype, shape), kind, shape[1], shape[2]
 
     def _launch(self, fn, size_fn, key, args, workspace, *more):
@@ -450,7 +460,7 @@ class KV8Cache:
         torch = self._torch
         if workspace is not None:
             if workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError("KV8Cache: the workspace must be contiguous, on the cache's device")
+                raise ValueError(self._name + ": the workspace must be contiguous, on the cache's device")
             return self._run(fn, args, *more, workspace.data_ptr(), workspace.numel() * workspace.element_size())
         need = self._sizes.get(key)
         if need is None:
@@ -458,17 +468,50 @@ class KV8Cache:
             _call(size_fn, self._ref, args, _c.byref(n))
             need = self._sizes[key] = n.value
         if need > 32 << 20 or torch.cuda.current_device() != self._dev or torch._C._cuda_isCurrentStreamCapturing():
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            workspace = self._scratch(need)
             return self._run(fn, args, *more, workspace.data_ptr(), need)
         stream = torch._C._cuda_getCurrentRawStream(self._dev)
         with self._lock:
             ptr, size, _ = self._kept.get(stream, (0, -1, None))
             if size < need:
-                t = torch.empty(need, dtype=torch.uint8, device=self.device)
+                t = self._scratch(need)
                 ptr, size, _ = self._kept[stream] = (t.data_ptr(), need, t)
             status = fn(self._ref, args, *more, ptr, size, stream)
         if status:
             raise W4A8Error(fn.__name__, status)
+
+
+class KV8Cache(_PagedCache):
+    """One layer of ``n_seqs`` sequences' keys and values in 8 bits (w4a8_kv8_cache).
+
+    Holds the cache's tensors, by name in ``tensors`` (``codes``, ``scales``, ``sums``, ``tail``, ``table``,
+    ``len``, ``ctl``: see include/w4a8.h): those given, or new ones of an empty cache.  ``q``, ``k``, ``v`` are
+    fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Asynchronous on the current
+    stream of the cache's device, or on ``stream`` (outputs and workspaces are then allocated on it, and the memory of
+    the call's tensors is not given to others before it is through with them; work of other streams on them is the
+    caller's to order); device state that is out of range is reported by ``check``.
+
+    A decode step is about ten microseconds on the device, so the calls are written out: arguments are marshalled as
+    packed bytes (w4a8_kv8_attn, w4a8_rows); the workspace sizes of the shapes seen and one workspace for each
+    stream are kept.
+    """
+
+    _NAMES = (("codes", "uint8"), ("scales", "float32"), ("sums", "int16"), ("tail", "float32"), ("table", "int32"),
+              ("len", "int32"), ("ctl", "int32"))
+    _ATTN = struct.Struct("@iiif 4q 4q 4q 4q 3q i 2q")   # w4a8_kv8_attn
+
+    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, device="cuda", tensors=None):
+        S, H, D, P = self.shape = (n_seqs, n_kv_heads, head_dim, max_pages)
+        self.desc = KV8CacheDesc(S, H, D, P)
+        _call("w4a8_kv8_bytes", _c.byref(self.desc), (_sz * 7)())     # refuses dimensions out of range
+        shapes = ((S, H, P, 2, 64 * D), (S, H, P, 2), (S, H, P, D), (S, H, 2, 64, D), (S, H, P), (S,), (1,))
+        self.desc = KV8CacheDesc(S, H, D, P, *self._adopt(self._NAMES, shapes, device, tensors))
+        self._ref = _c.byref(self.desc)
+        L = lib()
+        self._attention, self._select, self._evict = L.w4a8_kv8_attention, L.w4a8_kv8_select, L.w4a8_kv8_evict
+        self._append, self._read = L.w4a8_kv8_append, L.w4a8_kv8_read
+        if tensors is None:
+            self.reset()
 
     def reset(self, stream=None):
         """Empties the cache (w4a8_kv8_reset)."""
@@ -591,6 +634,254 @@ class KV8Cache:
             table, mass, length = torch.empty_like(table), torch.empty_like(mass), torch.empty_like(length)
         self._run(self._evict, pm, keep, first_pages, last_pages, table.data_ptr(), mass.data_ptr(), length.data_ptr())
         return table, mass, length
+
+
+# ------------------------------------------------------------- key/value cache in 4 bits
+
+class KV4Cache(_PagedCache):
+    """One layer of ``n_seqs`` sequences' keys and values in 4 bits with a scale for every 32 dims, in a pool of ``n_pages``
+    pages of 64 tokens (w4a8_kv4_cache); ``tensors["table"]`` [n_seqs][max_pages] names each sequence's pages, which
+    sequences may share as long as no append writes to them.
+
+    Holds the cache's tensors, by name in ``tensors`` (``pages``, ``table``, ``len``, ``ctl``: see include/w4a8.h): those given,
+    or new ones of an empty cache, whose sequences own ``max_pages`` pages each where ``n_pages`` is not given.  ``q``, ``k``, ``v``
+    are fp32 or bf16 [n_seqs][n][heads][head_dim] with unit stride in the last dimension.  Streams, workspaces and device
+    state that is out of range: as KV8Cache.
+    """
+
+    _NAMES = (("pages", "uint8"), ("table", "int32"), ("len", "int32"), ("ctl", "int32"))
+    _ATTN = struct.Struct("@iiif 4q 4q 4q 4q 2q")        # w4a8_kv4_attn
+
+    def __init__(self, n_seqs, n_kv_heads, head_dim, max_pages, n_pages=None, device="cuda", tensors=None):
+        if n_pages is None:
+            n_pages = n_seqs * max_pages
+        S, H, D, P, N = self.shape = (n_seqs, n_kv_heads, head_dim, max_pages, n_pages)
+        self.desc = KV4CacheDesc(S, H, D, P, N)
+        _call("w4a8_kv4_bytes", _c.byref(self.desc), (_sz * 4)())     # refuses dimensions out of range
+        shapes = ((N, H, 68 * D), (S, P), (S,), (1,))
+        self.desc = KV4CacheDesc(S, H, D, P, N, *self._adopt(self._NAMES, shapes, device, tensors))
+        self._ref = _c.byref(self.desc)
+        L = lib()
+        self._attention, self._append, self._read = L.w4a8_kv4_attention, L.w4a8_kv4_append, L.w4a8_kv4_read
+        if tensors is None:
+            self.reset()
+
+    def _scratch(self, need):
+        t = super()._scratch(need)
+        t[:KV4_TICKETS].zero_()
+        return t
+
+    def reset(self, stream=None):
+        """Empties the cache: lengths 0, every sequence its own pages as far as the pool goes (w4a8_kv4_reset)."""
+        if stream is not None:
+            return self._elsewhere(stream, self.reset, ())
+        self._run(lib().w4a8_kv4_reset)
+
+    def check(self, stream=None):
+        """The status word (0 = every call's device state was in range); waits for the calls on the current stream of the
+        cache's device, or on ``stream``."""
+        if stream is not None:
+            return self._elsewhere(stream, self.check, ())
+        self._torch.cuda.current_stream(self.device).synchronize()
+        f = _c.c_uint32()
+        st = lib().w4a8_kv4_check(self._ref, _c.byref(f))
+        if st not in (0, 7):
+            raise W4A8Error("w4a8_kv4_check", st)
+        return f.value
+
+    def append(self, k, v, counts=None, index=None, len_out=None, stream=None):
+        """Commits rows of k and v, advancing the cache's lengths, or storing the new ones in ``len_out`` instead
+        (w4a8_kv4_append).  ``index`` [n_seqs][n]: the source row of each new position."""
+        if stream is not None:
+            return self._elsewhere(stream, self.append, (k, v, counts, index, len_out))
+        S, H, D = self.shape[:3]
+        dtype, i32 = k.dtype, self._torch.int32
+        kind = self._types.get(dtype)
+        if kind is None or k.dim() != 4:
+            raise ValueError("KV4Cache: k must be fp32 or bf16 [n_seqs][n][n_kv_heads][head_dim]")
+        n_src = k.shape[1]
+        shape = (S, n_src, H, D)
+        kr = self._ROWS.pack(*self._rows(k, "k", dtype, shape))
+        vr = self._ROWS.pack(*self._rows(v, "v", dtype, shape))
+        n = n_src if index is None else index.shape[1]
+        self._run(self._append, kr, vr, kind, n_src, n, 0 if counts is None else self._vec(counts, "counts", i32, (S,)),
+                  0 if index is None else self._vec(index, "index", i32, (S, n)),
+                  self.desc.len if len_out is None else self._vec(len_out, "len_out", i32, (S,)))
+
+    def read(self, first, n, length=None, dtype=None, stream=None):
+        """Keys and values [n_seqs][n][n_kv_heads][head_dim] of positions first[s].. as held, in fp32 or bf16 (exact in
+        either; fp32 by default) (w4a8_kv4_read)."""
+        if stream is not None:
+            return self._elsewhere(stream, self.read, (first, n, length, dtype))
+        torch = self._torch
+        S, H, D = self.shape[:3]
+        dtype = torch.float32 if dtype is None else dtype
+        kind = self._types.get(dtype)
+        if kind is None:
+            raise ValueError("KV4Cache: dtype must be fp32 or bf16")
+        k = torch.empty((S, n, H, D), dtype=dtype, device=self.device)
+        v = torch.empty_like(k)
+        self._run(self._read, self._vec(first, "first", torch.int32, (S,)),
+                  0 if length is None else self._vec(length, "length", torch.int32, (S,)), n, kind, k.data_ptr(),
+                  v.data_ptr())
+        return k, v
+
+    def attention(self, q, k=None, v=None, scale=1.0, counts=None, mask=None, out=None, workspace=None, stream=None):
+        """Attention of q's rows over the cache and the new rows k, v (w4a8_kv4_attention); returns ``out``, a new tensor if
+        not given.  A ``workspace`` of the caller's needs no initialisation: its first KV4_TICKETS bytes are set to zero by the
+        call (a small launch that the cache's own workspaces do without)."""
+        if stream is not None:
+            return self._elsewhere(stream, self.attention, (q, k, v, scale, counts, mask, out, workspace))
+        if workspace is not None:
+            if workspace.get_device() != self._dev or not workspace.is_contiguous():
+                raise ValueError("KV4Cache: the workspace must be contiguous, on the cache's device")
+            with self._torch.cuda.device(self._dev):
+                workspace.view(-1).view(self._torch.uint8)[:KV4_TICKETS].zero_()
+        torch = self._torch
+        S, H, D = self.shape[:3]
+        qr, kind, n, heads = self._query(q)
+        dtype = q.dtype
+        if k is None and v is None:
+            kr = vr = self._NONE
+        elif k is None or v is None:
+            raise ValueError("KV4Cache: k and v come together")
+        else:
+            kr, vr = self._rows(k, "k", dtype, (S, n, H, D)), self._rows(v, "v", dtype, (S, n, H, D))
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            outr = (out.data_ptr(), n * heads * D, heads * D, D)
+        else:
+            outr = self._rows(out, "out", dtype, (S, n, heads, D))
+        a = self._ATTN.pack(n, heads, kind, scale, *qr, *outr, *kr, *vr,
+                            0 if counts is None else self._vec(counts, "counts", torch.int32, (S,)),
+                            0 if mask is None else self._vec(mask, "mask", torch.int64, (S, n)))
+        self._launch(self._attention, "w4a8_kv4_attention_workspace_bytes", (n, heads, kind, k is None), a, workspace)
+        return out
+
+
+# ------------------------------------------------------- norm and rotation of queries and keys
+
+class Rotary:
+    """Rotary positions of one head size, with the norm of queries and keys in the same pass (w4a8_qk_rotary).
+
+    ``rot_dim``: dims that are turned (all by default).  The frequencies, radians for each position, are ``base`` to the powers
+    -2 i / rot_dim, or ``inv_freq`` [rot_dim / 2] (64-bit values; any stretching of the context is in them).  ``axis``
+    [rot_dim / 2]: for positions of several axes (time, height, width), the axis of each frequency.  ``neighbours``: pairs
+    are dims (2 i, 2 i + 1) instead of (i, i + rot_dim / 2).  ``factor`` multiplies the turned dims.
+    """
+
+    _ARGS = struct.Struct("@10i 2f 7q 16q")              # w4a8_qk_rotary_args
+    _NONE = (0, 0, 0, 0)
+
+    def __init__(self, head_dim, rot_dim=None, base=10000.0, inv_freq=None, axis=None, neighbours=False, factor=1.0,
+                 device="cuda"):
+        import numpy as np
+        import torch
+        self._torch = torch
+        self._types = {torch.float32: 0, torch.bfloat16: 1}
+        rot = head_dim if rot_dim is None else rot_dim
+        if head_dim < 16 or head_dim > 256 or head_dim % 16 or rot < 0 or rot > head_dim or rot % 16:
+            raise ValueError("Rotary: head_dim and rot_dim must be multiples of 16, at most 256 and head_dim")
+        half = rot // 2
+        inv = float(base) ** (-np.arange(half) / max(half, 1)) if inv_freq is None else np.asarray(inv_freq)
+        inv = np.ascontiguousarray(inv, dtype=np.float64)
+        axis = np.zeros(half, np.int64) if axis is None else np.asarray(axis)
+        if inv.shape != (half,) or axis.shape != (half,):
+            raise ValueError("Rotary: inv_freq and axis must have rot_dim / 2 = %d entries" % half)
+        if half and (axis.min() < 0 or axis.max() > 3):
+            raise ValueError("Rotary: at most four axes")
+        turns = np.zeros(half, np.uint64)
+        if half:
+            _call("w4a8_rotary_turns", inv.ctypes.data_as(_vp), half, turns.ctypes.data_as(_vp))
+        self.n_axes = int(axis.max()) + 1 if half else 1
+        self.head_dim, self.rot_dim, self.neighbours, self.factor = head_dim, rot, bool(neighbours), float(factor)
+        self._turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self._axis = torch.from_numpy(axis.astype(np.uint8)).to(device)
+        self.device = self._turns.device
+        self._dev = self._turns.get_device()
+        if self._dev < 0:
+            raise ValueError("Rotary: needs a CUDA device")
+        self._fn = lib().w4a8_qk_rotary
+        self._mine = (self._turns.data_ptr() if half else 0, self._axis.data_ptr() if self.n_axes > 1 else 0)
+
+    def _rows(self, t, name, dtype, shape):
+        a, b, c, d = t.stride() if t.shape == shape else (0, 0, 0, 0)
+        if d != 1 or t.dtype is not dtype or t.get_device() != self._dev:
+            raise ValueError("Rotary: %s must be %s %s with unit stride in the last dimension, on the tables' device"
+                             % (name, str(dtype)[6:], list(shape)))
+        return t.data_ptr(), a, b, c
+
+    def _vec(self, t, name, dtype, shape):
+        if t is None:
+            return 0
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._dev or not t.is_contiguous():
+            raise ValueError("Rotary: %s must be a contiguous %s tensor %s on the tables' device"
+                             % (name, str(dtype)[6:], list(shape)))
+        return t.data_ptr()
+
+    def apply(self, q, k=None, positions=None, start=None, eps=None, q_gain=None, k_gain=None, counts=None, q_out=None,
+              k_out=None, stream=None):
+        """(q, k) turned, in new tensors or in ``q_out`` and ``k_out`` (which may be q and k themselves); q alone where k is not
+        given.  q, k: fp32 or bf16 [n_seqs][n][heads][head_dim], unit stride in the last dimension.  ``positions`` int32
+        [n_axes][n_seqs][n] ([n_seqs][n] does for one axis), the row's number by default; ``start`` int32 [n_seqs] is added to
+        them (e.g. a cache's ``len``).  ``eps``: divide each head by the root of its mean square plus eps, times ``q_gain``,
+        ``k_gain`` (fp32 [head_dim], 1 by default); None: no norm.  ``counts`` int32 [n_seqs]: rows behind them are left as
+        they were in given outputs, and hold anything in new ones."""
+        torch = self._torch
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError("Rotary: the stream is on another device than the tables")
+            args = (q, k, positions, start, eps, q_gain, k_gain, counts, q_out, k_out)
+            with torch.cuda.stream(stream):
+                result = self.apply(*args)
+            for t in args + (self._turns, self._axis):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+            return result
+        shape, dtype, D = q.shape, q.dtype, self.head_dim
+        kind = self._types.get(dtype)
+        if kind is None or len(shape) != 4 or shape[3] != D:
+            raise ValueError("Rotary: q must be fp32 or bf16 [n_seqs][n][heads][%d], not %s %s"
+                             % (D, str(dtype)[6:], list(shape)))
+        S, n, heads, _ = shape
+        qr = self._rows(q, "q", dtype, shape)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dtype, device=self.device)
+            qo = (q_out.data_ptr(), n * heads * D, heads * D, D)
+        else:
+            qo = self._rows(q_out, "q_out", dtype, shape)
+        kv_heads, kr, ko = 0, self._NONE, self._NONE
+        if k is not None:
+            kv_heads = k.shape[2] if k.dim() == 4 else 0
+            kshape = (S, n, kv_heads, D)
+            kr = self._rows(k, "k", dtype, kshape)
+            if k_out is None:
+                k_out = torch.empty(kshape, dtype=dtype, device=self.device)
+                ko = (k_out.data_ptr(), n * kv_heads * D, kv_heads * D, D)
+            else:
+                ko = self._rows(k_out, "k_out", dtype, kshape)
+        elif k_out is not None or k_gain is not None:
+            raise ValueError("Rotary: k_out and k_gain need k")
+        if eps is None and (q_gain is not None or k_gain is not None):
+            raise ValueError("Rotary: gains need eps")
+        i32, f32 = torch.int32, torch.float32
+        pos = 0
+        if positions is not None:
+            pshape = (S, n) if self.n_axes == 1 and positions.dim() == 2 else (self.n_axes, S, n)
+            pos = self._vec(positions, "positions", i32, pshape)
+        a = self._ARGS.pack(S, n, heads, kv_heads, D, self.rot_dim, self.n_axes, self.neighbours, kind, eps is not None,
+                            0.0 if eps is None else eps, self.factor, *self._mine, pos,
+                            self._vec(start, "start", i32, (S,)), self._vec(counts, "counts", i32, (S,)),
+                            self._vec(q_gain, "q_gain", f32, (D,)), self._vec(k_gain, "k_gain", f32, (D,)),
+                            *qr, *qo, *kr, *ko)
+        if torch.cuda.current_device() == self._dev:
+            status = self._fn(a, torch._C._cuda_getCurrentRawStream(self._dev))
+        else:
+            with torch.cuda.device(self._dev):
+                status = self._fn(a, torch._C._cuda_getCurrentRawStream(self._dev))
+        if status:
+            raise W4A8Error("w4a8_qk_rotary", status)
+        return q_out if k is None else (q_out, k_out)
 
 
 # ------------------------------------------------------------------------ model/session

@@ -1,0 +1,772 @@
+// Attention of new rows over the 4-bit key/value cache: the split kernel, its join and its launch.
+//
+// For query head hq of new row i (KV head h = hq / G), over the tokens t that the row sees
+//   l_t = scale q . k_t,  out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x = l log2(e), m = max x
+// in one pass: for each half page the running maximum m, sum l and values O of each row become
+//   m' = max(m, max x),  c = 2^(m - m'),  O = O c + P V,  l = l c + sum P,  P = 2^(x - m'),
+// with m left alone while no x is above m + 8 (P 2^7 keeps its f16 range, and most half pages need no reduction over the lanes).
+//
+// Both products run transposed on the tensor cores (m16n8k16, f16): S^T = K Q^T and O^T = V^T P^T, so the cache is the 16-row
+// operand and the few query rows of a KV head fill 8-column tiles.  A page is stored in the operand's own order (the
+// header documents it): one 16-byte shared-memory load gives a lane the codes of four k-steps.  A 4-bit code under the right
+// exponent is an f16 number, 256 + u or 16 + u, and one fused multiply-add per two codes makes the cached value of it:
+// (256 + u) s - 264 s = (u - 8) s, exact, as 264 s has nine bits, 24 s five and the value seven.  So the scales cost nothing
+// behind the products, and a warp's two column tiles share the conversion.
+//
+// fp32 operands are split, q = qh + ql and P = Ph + Pl in f16: hi and lo are neighbouring columns of a tile (four rows to a
+// tile instead of eight), so the accumulator pair of a thread holds both products of one row and adds them there.
+// Rows of q are scaled by a power of two, to a largest magnitude of at most 2^11; qh is the nearest whole number, so a sum of
+// qh with the codes of one scale (32 dims to an accumulator) is a multiple of the scale's last bit below 2^24 of them: f32
+// holds it, and the tensor core's truncating additions do not touch it.  The groups' sums, and the half pages' values, are
+// added in fp32 outside the tensor core.  bf16 calls take one f16 term of q (exact: eight bits) and of P (2^-11), and add
+// their values up in the tensor core's accumulator: its truncation is 2^-24 of the values for each 16 tokens of a worker.
+//
+// Work: every (sequence, KV head, block of rows) is a segment of pages (one, empty, where there is none).  The pages of
+// all segments, end to end, are cut into equal ranges, one for each warp, so ragged batches balance.  A warp has its own ring of
+// bulk copies (a page each) and waits for nobody.  It begins the first page of a segment with the new rows, in plain fp32,
+// while the copies are on their way.  A segment that lies within one warp's range is finished there; the warps of a CTA add
+// up where they hold the same one; and where several CTAs do, each stores its part, and the one that comes last (a
+// ticket, which it sets back to zero) joins the parts in their order.  One launch: a second one costs more than the join.
+#pragma once
+#include <type_traits>
+
+#include "kv4.cuh"
+#include "mma16.cuh"
+
+namespace w4a8 {
+
+constexpr int kKv4Ctas = 152;             // one per SM of a GB300
+constexpr int kKv4RingBytes = 24 * 8704;  // ring of pages per SM
+constexpr int kKv4MaxWarps = 12;
+constexpr int kKv4WideRows = 128;         // query rows of a segment of a wide call (kv4_wide.cu)
+constexpr float kP4Scale = 128.0f, kP4Slack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
+static_assert(W4A8_KV4_TICKETS >= kKv4Ctas * kKv4MaxWarps * 4, "tickets");
+
+struct Kv4Geom {       // of one call, the same for every kernel of it
+  int n, G, R;         // new rows; query heads per KV head; query rows of a KV head
+  int RB, CB;          // rows of a column block; column blocks
+  int ctas, ng;        // of the kernel over the pages, and its workers in each at most
+  int segments;
+  int tiles;           // wide calls: blocks of 16 new rows
+  int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
+  int withheld;        // CTA whose pages are not copied (w4a8_kv4_attention_inject_timeout), -1: none
+  uint64_t wait_ns;    // limit of the kernels' waits
+};
+struct Kv4Scratch {    // workspace pointers
+  int* ticket;         // [workers] parts of the segment that begins in a worker's range and ends in another's
+  float2* ml;          // [2 workers][RB] maximum, sum of a part: of the workers of a CTA that hold the same segment, at the first
+                       // of them; then, at workers + w, of the one whose worker w went on to another segment
+  float* o;            // [2 workers][RB][D] its values
+};
+
+// Segments of a sequence that have rows: (KV head, column block), and the pages of each (one where there are none).
+__device__ __forceinline__ int kv4_blocks(const Kv4Geom& g, int cnt) { return (cnt * g.G + g.RB - 1) / g.RB; }
+__device__ __forceinline__ int kv4_units(int L) { return max(1, (L + kPage - 1) / kPage); }
+// Pages of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be synchronised after it.
+__device__ __forceinline__ void kv4_prefix(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, int* prefix) {
+  const int S = c.n_seqs;
+  for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    const int L = kv4_len(c, c.len, s), cnt = kv4_count(c, a.counts, s, a.n);
+    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : kv4_units(L) * c.n_kv_heads * kv4_blocks(geo, cnt);
+  }
+  if (threadIdx.x == 0) prefix[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int b = 0; b < S; b += 32) {
+      const int s = b + threadIdx.x;
+      int v = s < S ? prefix[s + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)threadIdx.x >= o) v += x;
+      }
+      if (s < S) prefix[s + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+}
+// The sequence that unit x belongs to.
+__device__ __forceinline__ int kv4_seq_of(const int* prefix, int S, int x) {
+  int lo = 0, hi = S - 1;  // the last sequence whose first unit is at or before x and that has units
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Two f16 numbers of the fields of two words at bits 2..5 (256 + u) or 6..9 (16 + u).
+__device__ __forceinline__ uint32_t kv4_f16_low(uint32_t w) { return (w & 0x003c003cu) | 0x5c005c00u; }
+__device__ __forceinline__ uint32_t kv4_f16_high(uint32_t w) { return (w & 0x03c003c0u) | 0x4c004c00u; }
+__device__ __forceinline__ uint32_t kv4_swap(uint32_t w) { return __byte_perm(w, 0, 0x2301); }
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+constexpr uint32_t kMinus264 = 0xdc20dc20u, kMinus24 = 0xce00ce00u;  // f16 pairs
+// f16 pair of the scale bytes i and j of w
+__device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t w, int i, int j) {
+  return __byte_perm(w, 0, 0x0404 | i << 4 | j << 12) >> 1;
+}
+
+// ---------------------------------------------------------------------------- the split kernel
+
+template <typename T, int D, int NT>
+struct Kv4Split {
+  static constexpr bool SPLIT = sizeof(T) == 4;
+  static constexpr int RPT = SPLIT ? 4 : 8;        // rows of an 8-column tile
+  static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
+  static constexpr int RB = NT * RPT;              // rows of a column block
+  static constexpr int NG = NT == 1 ? 12 : 8;      // workers (warps) of a CTA: what their registers leave room for
+  static constexpr int PAGE = Kv4Page<D>::BYTES;
+  static constexpr int NS = kKv4RingBytes / PAGE / NG;  // ring entries of a worker
+  static constexpr int KS = D / 16, DT = D / 16;
+  static constexpr int THREADS = 32 * NG;
+};
+
+// What a lane knows of one page of its worker's range.
+struct Kv4Unit {
+  int64_t src;  // byte offset in the pool, or -1: nothing to read
+  int seg, u;   // segment; unit inside the segment
+  int valid;    // tokens
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
+    k_kv4_split(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
+  using C = Kv4Split<T, D, NT>;
+  constexpr bool SPLIT = C::SPLIT;
+  constexpr int NC = C::NC, KS = C::KS, DT = C::DT, E = D / 32, RB = C::RB, NG = C::NG;
+  constexpr unsigned FULL = 0xffffffffu;
+  using Vec = std::conditional_t<E == 4, float4, float2>;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ int last_part;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kKv4RingBytes);
+  int* prefix = reinterpret_cast<int*>(full + NG * C::NS);
+
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int H = c.n_kv_heads, S = c.n_seqs;
+
+  for (int i = tid; i < NG * C::NS; i += C::THREADS) mbar_init(&full[i], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  griddep_enter();
+  kv4_prefix(c, a, geo, prefix);
+  __syncthreads();
+
+  const int U = prefix[S];
+  if (U == 0) return;
+  const Kv8Workers wk = kv8_workers(U, geo.ctas, NG);
+  const int worker = blockIdx.x * wk.ng + grp;
+  const bool has = grp < wk.ng && worker < wk.W;
+  const int u0 = has ? worker_begin(worker, wk.W, U) : 0, u1 = has ? worker_begin(worker + 1, wk.W, U) : 0;
+
+  // The lane's unit x (32 units in parallel, so the table's latency is paid once).
+  auto look = [&](int x) -> Kv4Unit {
+    Kv4Unit r{-1, -1, 0, 0};
+    if (x >= u1) return r;
+    const int s = kv4_seq_of(prefix, S, x), cnt = a.counts ? a.counts[s] : a.n, L = c.len[s];
+    const int per = kv4_units(L), q = (x - prefix[s]) / per, blocks = kv4_blocks(geo, cnt);
+    r.u = (x - prefix[s]) % per;
+    r.seg = (s * H + q / blocks) * geo.CB + q % blocks;
+    r.valid = min(kPage, L - r.u * kPage);
+    if (r.valid <= 0) return r;
+    const int phys = kv4_phys(c, s, r.u);
+    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * C::PAGE;
+    return r;
+  };
+
+  uint8_t* ring = sm + (size_t)grp * C::NS * C::PAGE;
+  full += grp * C::NS;
+  Kv4Unit cur = look(u0 + lane), nxt = look(u0 + 32 + lane);
+  const int nu = u1 - u0;
+  int jl = 0;                     // next unit to copy
+  int is = 0, in_ring = 0;        // its ring entry; entries issued and not consumed
+  int cs = 0, cph = 0;            // entry to consume next, and its phase
+  bool ok = true;
+
+  // ---- state of the segment
+  uint32_t qf[NT][KS][2];
+  float O[NT][DT][4], m[NT][NC], l[NT][NC], colfac[NT][NC], collow[NT][NC];
+  int seg = -1, s_cur = 0, h_cur = 0, cb_cur = 0, rows_cur = 0;
+  // the factor of a column, log2(e) scale / (power of two of its row), as hi + lo
+  const double lscale = (double)a.scale * 1.4426950408889634;
+  const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
+  // row (of the column block) of column col of tile x; query rows of the segment's KV head
+  auto row_of = [&](int x, int col) { return x * C::RPT + (SPLIT ? col >> 1 : col); };
+  auto locate = [&](int sg) {
+    seg = sg;
+    cb_cur = sg % geo.CB, h_cur = sg / geo.CB % H, s_cur = sg / geo.CB / H;
+    rows_cur = min(RB, (a.counts ? a.counts[s_cur] : a.n) * geo.G - cb_cur * RB);
+  };
+  auto query = [&](int row) {  // of the column block
+    const int r = cb_cur * RB + row;
+    return static_cast<const T*>(a.q.data) + s_cur * a.q.seq + (r / geo.G) * a.q.row + (h_cur * geo.G + r % geo.G) * a.q.head;
+  };
+  auto output = [&](int sg, int row) {
+    const int cb = sg % geo.CB, h = sg / geo.CB % H, s = sg / geo.CB / H, r = cb * RB + row;
+    return static_cast<T*>(a.out.data) + s * a.out.seq + (r / geo.G) * a.out.row + (h * geo.G + r % geo.G) * a.out.head;
+  };
+
+  auto begin = [&](int sg, int u) {
+    locate(sg);
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[x][d][e] = 0.0f;
+#pragma unroll
+      for (int y = 0; y < NC; ++y) m[x][y] = -INFINITY, l[x][y] = ok ? 0.0f : NAN;
+      const int r = row_of(x, g);
+      float v[KS * 4];
+      if (r < rows_cur) {
+        const T* q = query(r);
+#pragma unroll
+        for (int kp = 0; kp < D / 32; ++kp) {
+          const T* p = q + 32 * kp + 8 * t;
+          if (geo.vec & 1) {
+            uint4 w[sizeof(T) / 2];
+#pragma unroll
+            for (int y = 0; y < (int)sizeof(T) / 2; ++y) w[y] = reinterpret_cast<const uint4*>(p)[y];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) v[8 * kp + y] = kv8_load(reinterpret_cast<const T*>(w) + y);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) v[8 * kp + y] = kv8_load(p + y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < KS * 4; ++y) v[y] = 0.0f;
+      }
+      float am = 0.0f;
+#pragma unroll
+      for (int y = 0; y < KS * 4; ++y) am = max_nan(am, fabsf(v[y]));
+      am = max_nan(am, __shfl_xor_sync(FULL, am, 1));
+      am = max_nan(am, __shfl_xor_sync(FULL, am, 2));
+      const float up = f16_scale(am);
+#pragma unroll
+      for (int y = 0; y < KS; ++y) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e] = v[4 * y + e] * up;
+          if (SPLIT) f[e] = g & 1 ? f[e] - rintf(f[e]) : rintf(f[e]);
+        }
+        qf[x][y][0] = pack_f16(f[0], f[1]);
+        qf[x][y][1] = pack_f16(f[2], f[3]);
+      }
+      // from the lanes of column g to the lanes of accumulator columns 2 t, 2 t + 1
+      const float down = 1.0f / up;
+#pragma unroll
+      for (int y = 0; y < NC; ++y) {
+        const float dn = __shfl_sync(FULL, down, SPLIT ? 8 * t : 4 * (2 * t + y));
+        colfac[x][y] = lhi * dn;
+        collow[x][y] = llo * dn;
+      }
+    }
+    if (u > 0 || !a.k.data) return;
+    // the new rows, one after the other, in plain fp32: a lane has E dims of a key for the dot products, then the values of
+    // its accumulators' dims.  A row that does not see the token is left out of everything, whatever the token holds.
+    const int cnt = a.counts ? a.counts[s_cur] : a.n;
+    const T* kn = static_cast<const T*>(a.k.data) + s_cur * a.k.seq + h_cur * a.k.head + E * lane;
+    const T* vn = static_cast<const T*>(a.v.data) + s_cur * a.v.seq + h_cur * a.v.head + g;
+    const int node0 = cb_cur * RB / geo.G, node1 = (cb_cur * RB + rows_cur - 1) / geo.G;  // the block's nodes
+#pragma unroll 1
+    for (int j = 0; j < cnt; ++j) {
+      if (!a.mask && j > node1) break;
+      float k[E], v[2 * DT];
+#pragma unroll
+      for (int e = 0; e < E; ++e) k[e] = kv8_load(kn + j * a.k.row + e);
+#pragma unroll
+      for (int d = 0; d < 2 * DT; ++d) v[d] = kv8_load(vn + j * a.v.row + 8 * d);
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float dot[C::RPT];
+#pragma unroll
+        for (int r = 0; r < C::RPT; ++r) {
+          dot[r] = 0.0f;
+          if (x * C::RPT + r < rows_cur) {
+            const T* q = query(x * C::RPT + r) + E * lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot[r] = fmaf(kv8_load(q + e), k[e], dot[r]);
+          }
+        }
+        // sums over the lanes; a lane keeps the rows of its half at each step, row lane / (32 / RPT) in the end
+        int w = 16;
+#pragma unroll
+        for (int r = C::RPT / 2; r > 0; r >>= 1, w >>= 1)
+#pragma unroll
+          for (int y = 0; y < r; ++y) {
+            const bool up = lane & w;
+            const float keep = up ? dot[y + r] : dot[y], give = up ? dot[y] : dot[y + r];
+            dot[y] = keep + __shfl_xor_sync(FULL, give, w);
+          }
+#pragma unroll
+        for (int o = 16 / C::RPT; o > 0; o >>= 1) dot[0] += __shfl_xor_sync(FULL, dot[0], o);
+        float s[NC];
+        bool see[NC], high = false;
+#pragma unroll
+        for (int y = 0; y < NC; ++y) {
+          const int row = row_of(x, 2 * t + y);
+          s[y] = __shfl_sync(FULL, dot[0], (32 / C::RPT) * (SPLIT ? t : 2 * t + y)) * lhi;
+          see[y] = row < rows_cur;
+          if (see[y]) {
+            const int node = node0 == node1 ? node0 : (cb_cur * RB + row) / geo.G;
+            see[y] = a.mask ? a.mask[(size_t)s_cur * a.n + node] >> j & 1ull : j <= node;
+          }
+          high = high || (see[y] && s[y] > m[x][y] + kP4Slack);
+        }
+        if (__any_sync(FULL, high)) {
+          float cc[NC];
+#pragma unroll
+          for (int y = 0; y < NC; ++y) {
+            const float mx = see[y] ? fmaxf(m[x][y], s[y]) : m[x][y];
+            cc[y] = mx == -INFINITY ? 1.0f : ex2(m[x][y] - mx);
+            m[x][y] = mx;
+            l[x][y] *= cc[y];
+          }
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[x][d][e] *= cc[(e & 1) * (NC - 1)];
+        }
+#pragma unroll
+        for (int y = 0; y < NC; ++y) {
+          const float p = ex2(s[y] - (m[x][y] == -INFINITY ? 0.0f : m[x][y])) * kP4Scale;
+          if (!see[y]) continue;
+          if (g == 0) l[x][y] += p;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            O[x][d][y] = fmaf(p, v[2 * d], O[x][d][y]);
+            O[x][d][y + 2] = fmaf(p, v[2 * d + 1], O[x][d][y + 2]);
+          }
+        }
+      }
+    }
+  };
+
+  // The worker's part of a segment: with ml and out rows of these; without them the rows of the output.
+  auto flush = [&](float2* ml, float* out) {
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int y = 0; y < NC; ++y) {
+        float sum = l[x][y];
+        sum += __shfl_xor_sync(FULL, sum, 4);
+        sum += __shfl_xor_sync(FULL, sum, 8);
+        sum += __shfl_xor_sync(FULL, sum, 16);
+        const int r = row_of(x, 2 * t + y);
+        if (r >= rows_cur) continue;
+        if (ml) {
+          if (g == 0) ml[r] = make_float2(m[x][y], sum);
+          float* o = out + r * D;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[16 * d + g] = SPLIT ? O[x][d][0] + O[x][d][1] : O[x][d][y];
+            o[16 * d + g + 8] = SPLIT ? O[x][d][2] + O[x][d][3] : O[x][d][y + 2];
+          }
+        } else {
+          T* o = output(seg, r) + g;
+          const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            kv8_store(o + 16 * d, (SPLIT ? O[x][d][0] + O[x][d][1] : O[x][d][y]) * f);
+            kv8_store(o + 16 * d + 8, (SPLIT ? O[x][d][2] + O[x][d][3] : O[x][d][y + 2]) * f);
+          }
+        }
+      }
+  };
+
+  // A page, half of it (32 tokens) at a time: S^T = K Q^T, softmax, O^T += V^T P^T.
+  auto page = [&](const uint8_t* pg, int valid) {
+#pragma unroll 1
+    for (int it = 0; it < 2; ++it) {
+      if (32 * it >= valid) break;
+      float x[NT][2][4];  // two 16-token tiles
+#pragma unroll
+      for (int z = 0; z < NT; ++z)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[z][i][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tile = 2 * it + i;
+        uint32_t sw[2];  // scale bytes of tokens g and g + 8
+        if (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(pg + Kv4Page<D>::KS + (tile * 8 + g) * 8);
+          sw[0] = w.x, sw[1] = w.y;
+        } else {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + Kv4Page<D>::KS + (tile * 8 + g) * 4);
+          sw[0] = w, sw[1] = w >> 16;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 w4 = reinterpret_cast<const uint4*>(pg)[(tile * (D / 64) + j) * 32 + lane];
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            const int grp32 = 2 * j + kh;
+            const uint32_t s0 = kv4_scale_pair(sw[0], grp32, grp32), s1 = kv4_scale_pair(sw[1], grp32, grp32);
+            const uint32_t b0 = mul_h2(s0, kMinus264), b1 = mul_h2(s1, kMinus24);
+            float part[NT][4];
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[z][e] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t wa = w[2 * kh + p], wb = kv4_swap(wa);
+              const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0, b0), fma_h2(kv4_f16_high(wa), s1, b1),
+                                      fma_h2(kv4_f16_low(wb), s0, b0), fma_h2(kv4_f16_high(wb), s1, b1)};
+#pragma unroll
+              for (int z = 0; z < NT; ++z)
+                mma_f16(SPLIT ? part[z] : x[z][i], af, qf[z][2 * grp32 + p][0], qf[z][2 * grp32 + p][1]);
+            }
+            if (SPLIT)
+#pragma unroll
+              for (int z = 0; z < NT; ++z)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[z][i][e] += part[z][e];
+          }
+        }
+      }
+      const int left = valid - 32 * it;  // tokens of this half and on
+      uint32_t pf[NT][2][2];
+#pragma unroll
+      for (int z = 0; z < NT; ++z) {
+        // logits: entry y + 2 e of tile i is row y of the thread, token g + 8 e of the tile
+        if (SPLIT)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[z][i][0] += x[z][i][1], x[z][i][2] += x[z][i][3];  // hi + lo
+        if (left < 32)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = colfac[z][(e & 1) * (NC - 1)] < 0.0f ? INFINITY : -INFINITY;
+        bool high = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int y = 0; y < NC; ++y)
+            high = high || x[z][i][y] * colfac[z][y] > m[z][y] + kP4Slack || x[z][i][y + 2] * colfac[z][y] > m[z][y] + kP4Slack;
+        if (__any_sync(FULL, high)) {
+          float cc[NC];
+#pragma unroll
+          for (int y = 0; y < NC; ++y) {
+            const float f = colfac[z][y];
+            float mx = fmaxf(fmaxf(x[z][0][y] * f, x[z][0][y + 2] * f), fmaxf(x[z][1][y] * f, x[z][1][y + 2] * f));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+            mx = fmaxf(mx, m[z][y]);
+            cc[y] = mx == -INFINITY ? 1.0f : ex2(m[z][y] - mx);
+            m[z][y] = mx;
+            l[z][y] *= cc[y];
+          }
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[z][d][e] *= cc[(e & 1) * (NC - 1)];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int y = 0; y < NC; ++y) {
+            const float base = m[z][y] == -INFINITY ? 0.0f : m[z][y];
+#pragma unroll
+            for (int e = y; e < 4; e += 2) {
+              x[z][i][e] = SPLIT ? ex2(fmaf(x[z][i][e], collow[z][y], fmaf(x[z][i][e], colfac[z][y], -base))) * kP4Scale
+                                 : ex2(fmaf(x[z][i][e], colfac[z][y], 7.0f - base));
+              if (left < 32 && 16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = 0.0f;
+              l[z][y] += x[z][i][e];
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p = x[z][i][2 * e];
+            pf[z][i][e] = movmatrix(SPLIT ? pack_f16(p, p - __half2float(__float2half_rn(p))) : pack_f16(p, x[z][i][2 * e + 1]));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint4 w4[2];
+        uint32_t sw[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tile = 2 * it + i;
+          w4[i] = reinterpret_cast<const uint4*>(pg + Kv4Page<D>::V)[(tile * (D / 64) + j) * 32 + lane];
+          const uint2 w = *reinterpret_cast<const uint2*>(pg + Kv4Page<D>::VS + (tile * 4 + t) * (D / 8) + 8 * j);
+          sw[i][0] = w.x, sw[i][1] = w.y;
+          if (left < 32) {  // tokens that are not there: whatever their bytes hold, scale 0
+            uint32_t keep = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (16 * i + 2 * t + (b & 1) + 8 * (b >> 1) < left) keep |= 255u << (8 * b);
+            sw[i][0] &= keep, sw[i][1] &= keep;
+          }
+        }
+#pragma unroll
+        for (int gh = 0; gh < 2; ++gh) {
+          uint32_t s0[2], s1[2], b0[2], b1[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s0[i] = kv4_scale_pair(sw[i][gh], 0, 1), s1[i] = kv4_scale_pair(sw[i][gh], 2, 3);
+            b0[i] = mul_h2(s0[i], kMinus264), b1[i] = mul_h2(s1[i], kMinus24);
+          }
+#pragma unroll
+          for (int dd = 0; dd < 2; ++dd) {
+            const int d = 4 * j + 2 * gh + dd;
+            float part[NT][4];
+#pragma unroll
+            for (int z = 0; z < NT; ++z)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[z][e] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t wa = gh ? (dd ? w4[i].w : w4[i].z) : (dd ? w4[i].y : w4[i].x), wb = kv4_swap(wa);
+              const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0[i], b0[i]), fma_h2(kv4_f16_low(wb), s0[i], b0[i]),
+                                      fma_h2(kv4_f16_high(wa), s1[i], b1[i]), fma_h2(kv4_f16_high(wb), s1[i], b1[i])};
+#pragma unroll
+              for (int z = 0; z < NT; ++z) mma_f16(SPLIT ? part[z] : O[z][d], af, pf[z][i][0], pf[z][i][1]);
+            }
+            if (SPLIT)
+#pragma unroll
+              for (int z = 0; z < NT; ++z)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[z][d][e] += part[z][e];
+          }
+        }
+      }
+    }
+  };
+
+  // ---- a segment's parts
+  struct Parts {
+    int w0, w1;       // workers of its first and last unit
+    int early, held;  // whether w1 goes on behind it (its part is then stored apart), CTAs that hold the others
+  };
+  auto parts_of = [&](int sg) {
+    const int s = sg / geo.CB / H, h = sg / geo.CB % H, cb = sg % geo.CB;
+    const int per = kv4_units(c.len[s]), blocks = kv4_blocks(geo, a.counts ? a.counts[s] : a.n);
+    const int first = prefix[s] + (h * blocks + cb) * per, end = first + per;
+    Parts p;
+    p.w0 = worker_of(first, wk.W, U), p.w1 = worker_of(end - 1, wk.W, U);
+    p.early = worker_begin(p.w1 + 1, wk.W, U) > end;
+    p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / wk.ng - p.w0 / wk.ng + 1;
+    return p;
+  };
+  // The parts of a segment, the CTAs' in their order, then the early one, to the output: warp `first` of `warps` takes every
+  // warps-th row, B loads in flight.
+  auto join = [&](int sg, const Parts& p, int first, int warps) {
+    const int s = sg / geo.CB / H, cb = sg % geo.CB;
+    const int rows = min(RB, (a.counts ? a.counts[s] : a.n) * geo.G - cb * RB), n = p.held + p.early;
+    auto place = [&](int i) -> size_t {
+      return i < p.held ? (size_t)max(p.w0, (p.w0 / wk.ng + i) * wk.ng) : (size_t)geo.ctas * geo.ng + p.w1;
+    };
+    constexpr int B = 8;
+    for (int r = first; r < rows; r += warps) {
+      float M = -INFINITY, sum = 0.0f, o[E] = {};
+      for (int i0 = 0; i0 < n; i0 += B) {
+        float2 ml[B];
+        Vec v[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          ml[b] = make_float2(-INFINITY, 0.0f);
+          v[b] = {};
+          if (i0 + b < n) {
+            const size_t at = place(i0 + b) * RB + r;
+            ml[b] = __ldcg(ws.ml + at);
+            v[b] = __ldcg(reinterpret_cast<const Vec*>(ws.o + at * D + E * lane));
+          }
+        }
+        float mx = M;
+#pragma unroll
+        for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
+        const float base = mx == -INFINITY ? 0.0f : mx, f = ex2(M - base);
+        M = mx;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const float w = ex2(ml[b].x - base);
+          const float* ve = reinterpret_cast<const float*>(&v[b]);
+          sum = fmaf(ml[b].y, w, sum);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(ve[e], w, o[e]);
+        }
+      }
+      T* out = output(sg, r) + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) kv8_store(out + e, sum == 0.0f ? 0.0f : o[e] / sum);
+    }
+  };
+  // Whether the part that the calling threads have stored (and made visible) was the segment's last.
+  auto is_last = [&](const Parts& p) {
+    __threadfence();
+    if (atomicAdd(ws.ticket + p.w0, 1) != p.held + p.early - 1) return false;
+    ws.ticket[p.w0] = 0;  // for the next call
+    __threadfence();
+    return true;
+  };
+  // The worker's segment ends in front of others of its range.
+  auto finish = [&]() {
+    const Parts p = parts_of(seg);
+    if (p.held == 0) {
+      flush(nullptr, nullptr);
+      return;
+    }
+    const size_t at = ((size_t)geo.ctas * geo.ng + worker) * RB;
+    flush(ws.ml + at, ws.o + at * D);
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) last = is_last(p);
+    if (!__shfl_sync(FULL, last, 0)) return;
+    __threadfence();
+    join(seg, p, 0, 1);
+  };
+
+  // ---- the range
+#pragma unroll 1
+  for (int j = 0, cbase = 0; j < nu; ++j) {
+    if (j - cbase == 32) {
+      cbase += 32;
+      cur = nxt;
+      nxt = look(u0 + cbase + 32 + lane);
+    }
+    // copy ahead as far as the ring and the two batches of units allow
+    while (ok && in_ring < C::NS && jl < nu && jl < cbase + 64) {
+      const int64_t from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
+      ++jl;
+      if (from < 0) continue;
+      if (lane == 0) {
+        mbar_expect_tx(&full[is], C::PAGE);
+        if (geo.withheld != (int)blockIdx.x) bulk_g2s(ring + (size_t)is * C::PAGE, c.pages + from, C::PAGE, &full[is]);
+      }
+      ++in_ring;
+      if (++is == C::NS) is = 0;
+    }
+    const int src = j - cbase;
+    const int64_t from = __shfl_sync(FULL, cur.src, src);
+    const int sg = __shfl_sync(FULL, cur.seg, src), u = __shfl_sync(FULL, cur.u, src), valid = __shfl_sync(FULL, cur.valid, src);
+    if (sg != seg) {
+      if (seg >= 0) finish();
+      begin(sg, u);
+    }
+    if (from < 0 || !ok) continue;
+    ok = __all_sync(FULL, mbar_wait(&full[cs], cph, geo.wait_ns));
+    if (ok) {
+      page(ring + (size_t)cs * C::PAGE, valid);
+    } else {  // a bounded wait expired: the sums from here on are not what they should be, and NaN says so
+      if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int y = 0; y < NC; ++y) l[x][y] = NAN;
+      for (; in_ring > 0; --in_ring) {  // no copy stays in flight (again bounded)
+        (void)mbar_wait(&full[cs], cph, geo.wait_ns);
+        if (++cs == C::NS) cs = 0, cph ^= 1;
+      }
+      continue;
+    }
+    __syncwarp();
+    if (++cs == C::NS) cs = 0, cph ^= 1;
+    --in_ring;
+  }
+  // ---- the workers' last parts, in the ring's place, and of each run of workers on one segment the sum
+  float2* sml = reinterpret_cast<float2*>(sm);                // [NG][RB]
+  int* sseg = reinterpret_cast<int*>(sml + NG * RB);          // [NG], -1: none
+  float* so = reinterpret_cast<float*>(sm) + ((NG * (2 * RB + 1) + 31) & ~31);  // [NG][RB][D]
+  static_assert((((NG * (2 * RB + 1) + 31) & ~31) + NG * RB * D) * 4 <= kKv4RingBytes, "parts");
+  __syncthreads();
+  if (lane == 0) sseg[grp] = seg;
+  if (seg >= 0) flush(sml + grp * RB, so + grp * RB * D);
+  __syncthreads();
+  for (int i0 = 0; i0 < NG;) {
+    const int sg = sseg[i0];
+    int i1 = i0 + 1;
+    while (i1 < NG && sseg[i1] == sg) ++i1;
+    if (sg >= 0) {
+      const Parts p = parts_of(sg);
+      const bool alone = p.held + p.early == 1;
+      const int s = sg / geo.CB / H, cb = sg % geo.CB;
+      const int rows = min(RB, (a.counts ? a.counts[s] : a.n) * geo.G - cb * RB);
+      const size_t at = ((size_t)blockIdx.x * wk.ng + i0) * RB;
+      for (int x = tid; x < rows * (D / 4); x += C::THREADS) {
+        const int r = x / (D / 4), d = x % (D / 4);
+        float M = -INFINITY, L = 0.0f;
+        for (int i = i0; i < i1; ++i) M = fmaxf(M, sml[i * RB + r].x);
+        const float base = M == -INFINITY ? 0.0f : M;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = i0; i < i1; ++i) {
+          const float2 ml = sml[i * RB + r];
+          const float4 o = reinterpret_cast<const float4*>(so + (i * RB + r) * D)[d];
+          const float f = ex2(ml.x - base);
+          L = fmaf(ml.y, f, L);
+          v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+        }
+        if (alone) {
+          T* out = output(sg, r) + 4 * d;
+          kv8_store(out, L == 0.0f ? 0.0f : v.x / L), kv8_store(out + 1, L == 0.0f ? 0.0f : v.y / L);
+          kv8_store(out + 2, L == 0.0f ? 0.0f : v.z / L), kv8_store(out + 3, L == 0.0f ? 0.0f : v.w / L);
+        } else {
+          reinterpret_cast<float4*>(ws.o + (at + r) * D)[d] = v;
+          if (d == 0) ws.ml[at + r] = make_float2(M, L);
+        }
+      }
+      if (!alone) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) last_part = is_last(p);
+        __syncthreads();
+        if (last_part) join(sg, p, grp, NG);
+      }
+    }
+    i0 = i1;
+  }
+}
+
+// ---------------------------------------------------------------------------- launch
+
+inline size_t kv4_split_smem(int S, int entries) { return (size_t)kKv4RingBytes + 8 * (size_t)entries + 4 * ((size_t)S + 1); }
+
+template <typename T, int D, int NT>
+cudaError_t kv4_split_launch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, const Kv4Scratch& ws,
+                             cudaStream_t st) {
+  using C = Kv4Split<T, D, NT>;
+  const size_t most = kv4_split_smem(kKv8MaxSeqs, C::NG * C::NS), smem = kv4_split_smem(c.n_seqs, C::NG * C::NS);
+  cudaError_t e = kv8_smem<k_kv4_split<T, D, NT>>(most);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_kv4_split<T, D, NT>, dim3((unsigned)geo.ctas), dim3(C::THREADS), smem, st, c, a, geo, ws);
+}
+// Column tiles of a warp for R query rows of a KV head: two where one does not hold them (four rows of fp32, eight of bf16).
+inline int kv4_split_tiles(int R, int dtype) { return R > (dtype == W4A8_F32 ? 4 : 8) ? 2 : 1; }
+inline int kv4_split_warps(int R, int dtype) { return kv4_split_tiles(R, dtype) == 1 ? 12 : 8; }
+template <typename T, int D>
+cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, const Kv4Scratch& ws,
+                               cudaStream_t st) {
+  return kv4_split_tiles(geo.R, a.dtype) == 1 ? kv4_split_launch<T, D, 1>(c, a, geo, ws, st)
+                                              : kv4_split_launch<T, D, 2>(c, a, geo, ws, st);
+}
+// one translation unit per head size and element type
+cudaError_t kv4_split_f32_d64(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
+cudaError_t kv4_split_f32_d128(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
+cudaError_t kv4_split_bf16_d64(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
+cudaError_t kv4_split_bf16_d128(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
+
+}  // namespace w4a8

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 
@@ -16,6 +17,7 @@ constexpr int kKv8MaxHeads = 1024;
 constexpr int kKv8MaxPages = 16384;    // a million tokens; the selection keeps a head's scores in shared memory
 constexpr int kKv8MaxRows = 64;        // new rows of one sequence in an attention call (one 64-bit mask)
 constexpr int kKv8MaxGroup = 16;       // query heads per KV head
+constexpr int64_t kMaxDifferences = 1 << 16;  // of strides that do not nest, in a host's check
 
 // Lets a kernel use that much dynamic shared memory: once for each device (a host call of a microsecond).
 template <auto Kern>
@@ -53,6 +55,68 @@ inline size_t kv8_elem(int t) { return t == W4A8_F32 ? 4 : 2; }
 inline bool kv8_vec_rows(const w4a8_rows& r, int dtype) {
   const int64_t e = 16 / (int64_t)kv8_elem(dtype);
   return aligned(r.data, 16) && r.seq % e == 0 && r.row % e == 0 && r.head % e == 0;
+}
+
+// Whether two of the S x n x heads rows of D elements lie on one another.  Strides that nest (each at least the extent of
+// the smaller ones) do not; else a difference of up to two of the indexes is followed by the nearest of the third (more than
+// `most` such differences: taken as overlapping).
+inline bool rows_overlap(const w4a8_rows& r, int S, int n, int heads, int D, int64_t most = INT64_MAX) {
+  using Wide = __int128;
+  struct Axis {
+    Wide stride;
+    int size;
+  } ax[3] = {{r.seq, S}, {r.row, n}, {r.head, heads}};
+  for (Axis& x : ax) x.stride = x.size == 1 ? 0 : x.stride < 0 ? -x.stride : x.stride;
+  std::sort(ax, ax + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  Wide extent = D;
+  bool nested = true;
+  for (const Axis& x : ax) {
+    nested = nested && (x.size == 1 || x.stride >= extent);
+    extent += (Wide)(x.size - 1) * x.stride;
+  }
+  if (nested) return false;
+  if ((int64_t)ax[1].size * ax[2].size > most) return true;
+  for (const Axis& x : ax)
+    if (x.size > 1 && x.stride < D) return true;
+  // a row of other indexes closer than D: i, j the differences in the two wider axes, k in the narrowest
+  for (int i = 0; i < ax[2].size; ++i)
+    for (int j = i ? 1 - ax[1].size : 1; j < ax[1].size; ++j) {
+      const Wide at = i * ax[2].stride + j * ax[1].stride;
+      const Wide k = ax[0].size == 1 ? 0 : at / ax[0].stride;
+      for (Wide y = k - 1; y <= k + 1; ++y) {
+        const Wide d = at - y * ax[0].stride;
+        if (y > -ax[0].size && y < ax[0].size && d > -D && d < D) return true;
+      }
+    }
+  return false;
+}
+
+// Whether the rows of two views, S x n x their heads x D elements of one size, may share memory: not where their address
+// ranges are apart, nor where they are different heads of one tensor whose rows do not lie on one another.
+inline bool rows_meet(const w4a8_rows& x, int heads_x, const w4a8_rows& y, int heads_y, int S, int n, int D, size_t el) {
+  using Wide = __int128;
+  auto range = [&](const w4a8_rows& r, int heads, Wide& lo, Wide& hi) {
+    lo = hi = (Wide)reinterpret_cast<uintptr_t>(r.data);
+    const Wide steps[3] = {(Wide)(S - 1) * r.seq, (Wide)(n - 1) * r.row, (Wide)(heads - 1) * r.head};
+    for (Wide step : steps) (step < 0 ? lo : hi) += step * (Wide)el;
+    hi += (Wide)D * (Wide)el;
+  };
+  Wide a0, a1, b0, b1;
+  range(x, heads_x, a0, a1);
+  range(y, heads_y, b0, b1);
+  if (a1 <= b0 || b1 <= a0) return false;
+  if ((S > 1 && x.seq != y.seq) || (n > 1 && x.row != y.row)) return true;
+  // y's first head is head m of a tensor whose head 0 is x's first
+  const int64_t head = heads_x > 1 ? x.head : y.head;
+  if (heads_x > 1 && heads_y > 1 && x.head != y.head) return true;
+  const Wide d = (Wide)reinterpret_cast<uintptr_t>(y.data) - (Wide)reinterpret_cast<uintptr_t>(x.data);
+  if (!head || d % ((Wide)head * (Wide)el)) return true;
+  const Wide m = d / ((Wide)head * (Wide)el);
+  if (m > -heads_y && m < heads_x) return true;
+  const Wide all = m > 0 ? m + heads_y : heads_x - m;
+  w4a8_rows whole = x;
+  whole.head = head;
+  return all > (Wide)1 << 20 || rows_overlap(whole, S, n, (int)all, D, kMaxDifferences);
 }
 
 // (sequence, KV head) pair index and page addresses: 64-bit, a long cache passes 4 GB

@@ -1,6 +1,4 @@
 // Attention over the 8-bit key/value cache: joining the parts, the pages' mass, and the entry points.
-#include <algorithm>
-
 #include "kv8_attn.cuh"
 
 using namespace w4a8;
@@ -139,38 +137,6 @@ struct Plan {
   Kv8Geom geo;
   size_t segments, prefix, ml, o, rml, ro, fin, page, bytes;  // offsets
 };
-
-// Whether two of the S x n x heads rows of D elements lie on one another.  Strides that nest (each at least the extent of
-// the smaller ones) do not; else a difference of up to two of the indexes is followed by the nearest of the third.
-bool rows_overlap(const w4a8_rows& r, int S, int n, int heads, int D) {
-  using Wide = __int128;
-  struct Axis {
-    Wide stride;
-    int size;
-  } ax[3] = {{r.seq, S}, {r.row, n}, {r.head, heads}};
-  for (Axis& x : ax) x.stride = x.size == 1 ? 0 : x.stride < 0 ? -x.stride : x.stride;
-  std::sort(ax, ax + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
-  Wide extent = D;
-  bool nested = true;
-  for (const Axis& x : ax) {
-    nested = nested && (x.size == 1 || x.stride >= extent);
-    extent += (Wide)(x.size - 1) * x.stride;
-  }
-  if (nested) return false;
-  for (const Axis& x : ax)
-    if (x.size > 1 && x.stride < D) return true;
-  // a row of other indexes closer than D: i, j the differences in the two wider axes, k in the narrowest
-  for (int i = 0; i < ax[2].size; ++i)
-    for (int j = i ? 1 - ax[1].size : 1; j < ax[1].size; ++j) {
-      const Wide at = i * ax[2].stride + j * ax[1].stride;
-      const Wide k = ax[0].size == 1 ? 0 : at / ax[0].stride;
-      for (Wide y = k - 1; y <= k + 1; ++y) {
-        const Wide d = at - y * ax[0].stride;
-        if (y > -ax[0].size && y < ax[0].size && d > -D && d < D) return true;
-      }
-    }
-  return false;
-}
 
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
