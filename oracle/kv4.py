@@ -25,7 +25,7 @@ VALUES = np.array([scale_value(b) for b in range(184)])   # ascending; 183 is 24
 def quantize(x):
     """fp32 [..., D] -> (codes int [..., D], scale bytes int [..., D / 32])."""
     x = np.asarray(x, dtype=np.float32)
-    g = x.reshape(*x.shape[:-1], -1, GROUP)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     finite = np.isfinite(g).all(axis=-1)
     s = (np.abs(np.where(finite[..., None], g, 0)).max(axis=-1) / np.float32(7)).astype(np.float64)
     # the nearest value; halfway between two: the even byte

@@ -113,7 +113,7 @@ def test_append_strides_index_and_len_out(n):
     right at the old lengths and at the new ones."""
     rng = np.random.default_rng(5)
     S, H, D = 2, 3, 64
-    cache, ref = _filled(rng, S, H, D, [60, 127])
+    cache, ref = _filled(rng, S, H, D, [60, 127], P=5)               # room for all of it
     qkv = _rows(rng, S, n, 4 * H, D, "fp32")
     k, v = qkv[:, :, H:2 * H], qkv[:, :, 2 * H:3 * H]
     m = n - 11
@@ -170,12 +170,12 @@ def test_append_special_values(dtype):
 def test_append_leaves_what_is_out_of_range():
     rng = np.random.default_rng(7)
     S, H, D, P = 5, 2, 64, 2
-    cache, ref = _filled(rng, S, H, D, [128, 100, 10, 20, 30], P=P)
+    cache, ref = _filled(rng, S, H, D, [128, 110, 10, 20, 30], P=P)
     x = _rows(rng, S, 20, H, D, "fp32")
     keep = cache.tensors["pages"].clone()
     # full; would pass the end; a count out of range; a source row out of range; fine
     cache.append(x, x, counts=_i32([1, 20, 21, 3, 4]), index=_i32([[0] * 20] * 3 + [[0, 20, 1] + [0] * 17] + [[3, 2, 1, 0] + [0] * 16]))
-    assert cache.len.tolist() == [128, 100, 10, 20, 34]
+    assert cache.len.tolist() == [128, 110, 10, 20, 34]
     assert cache.check() == W.FLAG_ERR_CAPACITY | W.FLAG_ERR_TOKEN
     ref.append(4, _np(x)[4, [3, 2, 1, 0]], _np(x)[4, [3, 2, 1, 0]])
     _check_state(cache, ref)
@@ -224,12 +224,12 @@ def _check_attention(cache, ref, q, k, v, scale, masks, counts=None, mask=None, 
     for s in range(S):
         for h in range(H):
             kh, vh = ref.held(s, h)
-            top = max([0.0] + [np.abs(x).max() for x in (vh, none if vn is None else vn[s, :, h]) if x.size])
-            for i in range(n if counts is None else counts[s]):
+            cnt = n if counts is None else counts[s]
+            top = max([0.0] + [np.abs(x).max() for x in (vh, none if vn is None else vn[s, :cnt, h]) if x.size])
+            for i in range(cnt):
                 for hq in range(h * G, (h + 1) * G):
                     if rows is not None and (s, i, hq) not in rows:
                         continue
-                    cnt = n if counts is None else counts[s]
                     m = masks[s][i] & (1 << cnt) - 1
                     want, B = O.attention(kh, vh, qn[s, i, hq], none if kn is None else kn[s, :, h], none if vn is None else vn[s, :, h], m, scale)
                     d = 2.0 ** -18 * B

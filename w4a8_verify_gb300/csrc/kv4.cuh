@@ -4,7 +4,8 @@
 // A row of 32 dims is c s, c a whole number -7 .. 7 and s = (8 + m) 2^(e - 18) with three bits of m: c s has seven
 // significant bits at most, so it is exact as f16 (the tensor cores' operand) and as bf16 (what a read may return), and no
 // kernel has to carry scales behind its products.  s to the nearest of those numbers costs no error of a code: the
-// largest value is at most 7.44 s, which the code 7 holds as well as any other value its own.
+// largest value is at most 7.4375 s, which the code 7 holds as well as any other value its own (but for scales below
+// 2^-14, whose steps are coarser, and the largest).
 #pragma once
 #include "kv8.cuh"
 

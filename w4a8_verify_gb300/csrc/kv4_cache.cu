@@ -74,8 +74,8 @@ __device__ __forceinline__ void codes(const float (&x)[N], float amax, float s, 
     return;
   }
   constexpr float kMagic = 12582920.0f;
-  const float inv = __fdividef(1.0f, s), half = 0.5f * s, top = 7.0f * kKv4MaxScale;
-  float off = amax > top ? half : 0.0f;
+  const float inv = __fdividef(1.0f, s), half = 0.5f * s, top = 7.0f * s;
+  float off = amax > 7.4375f * s ? half : 0.0f;  // the largest scale and the smallest ones: some are clamped
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float r = fmaf(x[i], inv, kMagic);
