@@ -7,7 +7,8 @@ namespace {
 
 struct Plan {
   Kv4Geom geo;
-  size_t ml, o, bytes;  // offsets
+  bool wide;
+  size_t ml, o, prefix, rml, ro, bytes;  // offsets
 };
 
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -24,18 +25,27 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
   g.n = a->n;
   g.G = a->n_heads / c->n_kv_heads;
   g.R = g.n * g.G;
-  g.RB = kv4_split_tiles(g.R, a->dtype) * (a->dtype == W4A8_F32 ? 4 : 8);
+  p->wide = kv4_is_wide(*c, g.R, a->dtype);
+  g.RB = p->wide ? kKv4WideRows : kv4_split_tiles(g.R, a->dtype) * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
   const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * c->max_pages;
   if (units >= (size_t)1 << 31 || segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.segments = (int)segments;
   g.ctas = (int)(units < (size_t)kKv4Ctas ? units : (size_t)kKv4Ctas);
-  const size_t ng = (units + g.ctas - 1) / g.ctas, most = (size_t)kv4_split_warps(g.R, a->dtype);
+  const size_t ng = (units + g.ctas - 1) / g.ctas, most = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype);
   g.ng = (int)(ng < most ? ng : most);
-  const size_t slots = 2 * (size_t)g.ctas * g.ng;
+  const size_t row = (size_t)g.RB * 4, D = (size_t)c->head_dim;
+  const size_t slots = p->wide ? g.ctas + 2 * segments : 2 * (size_t)g.ctas * g.ng;
   p->ml = W4A8_KV4_TICKETS;
-  p->o = up256(p->ml + slots * g.RB * 8);
-  p->bytes = up256(p->o + slots * g.RB * 4 * c->head_dim);
+  p->o = up256(p->ml + slots * row * 2);
+  p->prefix = p->rml = p->ro = p->bytes = up256(p->o + slots * row * D);
+  if (p->wide) {
+    g.tiles = a->k.data ? (g.n + 15) / 16 : 0;
+    if (segments * (g.tiles ? g.tiles : 1) * 2 >= (size_t)1 << 31) return W4A8_ERR_SHAPE;  // CTAs of the new rows
+    p->rml = up256(p->prefix + ((size_t)c->n_seqs + 1) * 4);
+    p->ro = up256(p->rml + segments * g.tiles * row * 2);
+    p->bytes = up256(p->ro + segments * g.tiles * row * D);
+  }
   return W4A8_OK;
 }
 
@@ -58,13 +68,15 @@ w4a8_status attend(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, void* worksp
       (a->k.data && (rows_meet(a->out, a->n_heads, a->k, H, S, n, D, el) || rows_meet(a->out, a->n_heads, a->v, H, S, n, D, el))))
     return W4A8_ERR_ARG;
   char* base = static_cast<char*>(workspace);
-  const Kv4Scratch ws{reinterpret_cast<int*>(base), reinterpret_cast<float2*>(base + p.ml),
-                      reinterpret_cast<float*>(base + p.o)};
+  const Kv4Scratch ws{reinterpret_cast<int*>(base),          reinterpret_cast<float2*>(base + p.ml),
+                      reinterpret_cast<float*>(base + p.o),  reinterpret_cast<int*>(base + p.prefix),
+                      reinterpret_cast<float2*>(base + p.rml), reinterpret_cast<float*>(base + p.ro)};
   p.geo.vec = (kv8_vec_rows(a->q, a->dtype) ? 1 : 0) | (kv8_vec_rows(a->k, a->dtype) ? 2 : 0) | (kv8_vec_rows(a->v, a->dtype) ? 4 : 0);
   p.geo.withheld = withheld;
   p.geo.wait_ns = wait_ns;
   const bool f32 = a->dtype == W4A8_F32, d64 = D == 64;
-  W4A8_CUDA_TRY((f32 ? d64 ? kv4_split_f32_d64 : kv4_split_f32_d128 : d64 ? kv4_split_bf16_d64 : kv4_split_bf16_d128)(
+  if (p.wide) W4A8_CUDA_TRY(kv4_wide(*c, *a, p.geo, ws, as_stream(stream)));
+  else W4A8_CUDA_TRY((f32 ? d64 ? kv4_split_f32_d64 : kv4_split_f32_d128 : d64 ? kv4_split_bf16_d64 : kv4_split_bf16_d128)(
       *c, *a, p.geo, ws, as_stream(stream)));
   return W4A8_OK;
 }

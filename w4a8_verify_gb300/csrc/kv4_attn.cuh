@@ -57,17 +57,24 @@ struct Kv4Scratch {    // workspace pointers
   float2* ml;          // [2 workers][RB] maximum, sum of a part: of the workers of a CTA that hold the same segment, at the first
                        // of them; then, at workers + w, of the one whose worker w went on to another segment
   float* o;            // [2 workers][RB][D] its values
+  // wide calls: ml and o are [ctas + 2 segments][RB], the part of a (CTA, segment) at CTA + segment, then [segments][RB] of the
+  // parts whose CTA went on to another segment
+  int* prefix;         // [n_seqs + 1] pages of the segments before each sequence
+  float2* rml;         // [segments][tiles][RB] maximum, sum of a block of new rows
+  float* ro;           // [segments][tiles][RB][D] its values
 };
 
 // Segments of a sequence that have rows: (KV head, column block), and the pages of each (one where there are none).
 __device__ __forceinline__ int kv4_blocks(const Kv4Geom& g, int cnt) { return (cnt * g.G + g.RB - 1) / g.RB; }
 __device__ __forceinline__ int kv4_units(int L) { return max(1, (L + kPage - 1) / kPage); }
-// Pages of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be synchronised after it.
-__device__ __forceinline__ void kv4_prefix(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, int* prefix) {
+// Pages (at least `least` each) of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be
+// synchronised after it.
+__device__ __forceinline__ void kv4_prefix(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, int* prefix,
+                                           int least) {
   const int S = c.n_seqs;
   for (int s = threadIdx.x; s < S; s += blockDim.x) {
     const int L = kv4_len(c, c.len, s), cnt = kv4_count(c, a.counts, s, a.n);
-    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : kv4_units(L) * c.n_kv_heads * kv4_blocks(geo, cnt);
+    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : max(least, (L + kPage - 1) / kPage) * c.n_kv_heads * kv4_blocks(geo, cnt);
   }
   if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   griddep_enter();
-  kv4_prefix(c, a, geo, prefix);
+  kv4_prefix(c, a, geo, prefix, 1);
   __syncthreads();
 
   const int U = prefix[S];
@@ -763,6 +770,12 @@ cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, 
   return kv4_split_tiles(geo.R, a.dtype) == 1 ? kv4_split_launch<T, D, 1>(c, a, geo, ws, st)
                                               : kv4_split_launch<T, D, 2>(c, a, geo, ws, st);
 }
+// Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu).
+inline bool kv4_is_wide(const w4a8_kv4_cache& c, int R, int dtype) {
+  (void)c;
+  return R > (dtype == W4A8_F32 ? 16 : 32);
+}
+cudaError_t kv4_wide(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
 // one translation unit per head size and element type
 cudaError_t kv4_split_f32_d64(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
 cudaError_t kv4_split_f32_d128(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
