@@ -89,7 +89,7 @@ class QKRotaryArgs(_c.Structure):
                 ("k_out", Rows)]
 
 
-KV4_TICKETS = 8192  # bytes of an attention workspace that are zero between calls
+KV4_TICKETS = 16384  # bytes of an attention workspace that are zero between calls
 FLAG_TERMINATED, FLAG_ERR_CAPACITY, FLAG_ERR_TOKEN, FLAG_ERR_TREE, FLAG_ERR_TIMEOUT = 1, 2, 4, 8, 16
 T_Q, T_K, T_V, T_O, T_GATE, T_UP, T_DOWN, T_EMBED, T_LM_HEAD = range(9)
 

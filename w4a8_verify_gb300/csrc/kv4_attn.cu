@@ -28,7 +28,7 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
   p->wide = kv4_is_wide(*c, g.R, a->dtype);
   g.RB = p->wide ? kKv4WideRows : kv4_split_tiles(g.R, a->dtype) * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
-  const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * c->max_pages;
+  const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * (p->wide ? c->max_pages : 2 * c->max_pages + 1);
   if (units >= (size_t)1 << 31 || segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.segments = (int)segments;
   g.ctas = (int)(units < (size_t)kKv4Ctas ? units : (size_t)kKv4Ctas);

@@ -21,12 +21,12 @@
 // added in fp32 outside the tensor core.  bf16 calls take one f16 term of q (exact: eight bits) and of P (2^-11), and add
 // their values up in the tensor core's accumulator: its truncation is 2^-24 of the values for each 16 tokens of a worker.
 //
-// Work: every (sequence, KV head, block of rows) is a segment of pages (one, empty, where there is none).  The pages of
-// all segments, end to end, are cut into equal ranges, one for each warp, so ragged batches balance.  A warp has its own ring of
-// bulk copies (a page each) and waits for nobody.  It begins the first page of a segment with the new rows, in plain fp32,
-// while the copies are on their way.  A segment that lies within one warp's range is finished there; the warps of a CTA add
-// up where they hold the same one; and where several CTAs do, each stores its part, and the one that comes last (a
-// ticket, which it sets back to zero) joins the parts in their order.  One launch: a second one costs more than the join.
+// Work: every (sequence, KV head, block of rows) is a segment of units: its new rows, then half pages of 32 tokens (one empty
+// unit where there is nothing).  The units of all segments, end to end, are cut into equal ranges, one for each warp, so ragged
+// batches balance.  A warp has its own ring of bulk copies (half a page each) and waits for nobody.  The new rows are done in
+// plain fp32.  A segment that lies within one warp's range is finished there; the warps of a CTA add up where they hold
+// the same one; and where several CTAs do, each stores its part, and the one that comes last (a ticket, which it sets back
+// to zero) joins the parts in their order.  One launch: a second one costs more than the join.
 #pragma once
 #include <type_traits>
 
@@ -36,8 +36,10 @@
 namespace w4a8 {
 
 constexpr int kKv4Ctas = 152;             // one per SM of a GB300
-constexpr int kKv4RingBytes = 24 * 8704;  // ring of pages per SM
-constexpr int kKv4MaxWarps = 12;
+constexpr int kKv4RingBytes = 24 * 8704;  // ring of half pages per SM
+constexpr int kKv4MaxWarps = 16;
+constexpr int kKv4HalfTokens = 32;        // tokens of a unit
+constexpr int kKv4Lens = 1024;            // sequences whose lengths are kept in shared memory
 constexpr int kKv4WideRows = 128;         // query rows of a segment of a wide call (kv4_wide.cu)
 constexpr float kP4Scale = 128.0f, kP4Slack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
 static_assert(W4A8_KV4_TICKETS >= kKv4Ctas * kKv4MaxWarps * 4, "tickets");
@@ -64,21 +66,22 @@ struct Kv4Scratch {    // workspace pointers
   float* ro;           // [segments][tiles][RB][D] its values
 };
 
-// Segments of a sequence that have rows: (KV head, column block), and the pages of each (one where there are none).
+// Column blocks that hold rows of a sequence of cnt rows.
 __device__ __forceinline__ int kv4_blocks(const Kv4Geom& g, int cnt) { return (cnt * g.G + g.RB - 1) / g.RB; }
-__device__ __forceinline__ int kv4_units(int L) { return max(1, (L + kPage - 1) / kPage); }
-// Pages (at least `least` each) of the segments before each sequence, [n_seqs + 1] in shared memory; the block has to be
-// synchronised after it.
+// Units of the segments before each sequence, [n_seqs + 1] in shared memory, units_of(L) to a segment; lens: the first kKv4Lens
+// lengths (NULL: not wanted).  The block has to be synchronised after it.
+template <typename F>
 __device__ __forceinline__ void kv4_prefix(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, int* prefix,
-                                           int least) {
+                                           int* lens, F units_of) {
   const int S = c.n_seqs;
   for (int s = threadIdx.x; s < S; s += blockDim.x) {
     const int L = kv4_len(c, c.len, s), cnt = kv4_count(c, a.counts, s, a.n);
-    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : max(least, (L + kPage - 1) / kPage) * c.n_kv_heads * kv4_blocks(geo, cnt);
+    prefix[s + 1] = L < 0 || cnt < 0 ? 0 : units_of(L) * c.n_kv_heads * kv4_blocks(geo, cnt);
+    if (lens && s < kKv4Lens) lens[s] = L;
   }
   if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
-  if (threadIdx.x < 32) {
+  if (threadIdx.x < 32 && S > 1) {
     int carry = 0;
     for (int b = 0; b < S; b += 32) {
       const int s = b + threadIdx.x;
@@ -121,7 +124,7 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
 constexpr uint32_t kMinus264 = 0xdc20dc20u, kMinus24 = 0xce00ce00u;  // f16 pairs
 // f16 pair of the scale bytes i and j of w
 __device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t w, int i, int j) {
-  return __byte_perm(w, 0, 0x0404 | i << 4 | j << 12) >> 1;
+  return __byte_perm(w, 0, 0x4040 | i | j << 8) << 7;
 }
 
 // ---------------------------------------------------------------------------- the split kernel
@@ -132,18 +135,19 @@ struct Kv4Split {
   static constexpr int RPT = SPLIT ? 4 : 8;        // rows of an 8-column tile
   static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
   static constexpr int RB = NT * RPT;              // rows of a column block
-  static constexpr int NG = NT == 1 ? 12 : 8;      // workers (warps) of a CTA: what their registers leave room for
-  static constexpr int PAGE = Kv4Page<D>::BYTES;
-  static constexpr int NS = kKv4RingBytes / PAGE / NG;  // ring entries of a worker
-  static constexpr int KS = D / 16, DT = D / 16;
+  static constexpr int NG = NT == 1 ? 16 : 8;      // workers (warps) of a CTA: what their registers leave room for
+  // a ring entry: codes of 32 keys, of 32 values, scales of the keys, of the values
+  static constexpr int V = 16 * D, KS = 32 * D, VS = 33 * D, HALF = 34 * D;
+  static constexpr int NS = kKv4RingBytes / HALF / NG;  // ring entries of a worker
+  static constexpr int STEPS = D / 16;  // k-steps of the first product, 16-dim tiles of the second
   static constexpr int THREADS = 32 * NG;
 };
 
-// What a lane knows of one page of its worker's range.
+// What a lane knows of one unit of its worker's range.
 struct Kv4Unit {
-  int64_t src;  // byte offset in the pool, or -1: nothing to read
-  int seg, u;   // segment; unit inside the segment
-  int valid;    // tokens
+  int64_t src;  // byte offset of the page in the pool (even) + which half, or -1: nothing to read
+  int seg;      // segment
+  int tokens;   // of the half page; -1: the unit of the new rows
 };
 
 template <typename T, int D, int NT>
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     k_kv4_split(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
   using C = Kv4Split<T, D, NT>;
   constexpr bool SPLIT = C::SPLIT;
-  constexpr int NC = C::NC, KS = C::KS, DT = C::DT, E = D / 32, RB = C::RB, NG = C::NG;
+  constexpr int NC = C::NC, KS = C::STEPS, DT = C::STEPS, E = D / 32, RB = C::RB, NG = C::NG;
   constexpr unsigned FULL = 0xffffffffu;
   using Vec = std::conditional_t<E == 4, float4, float2>;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -162,37 +166,47 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int H = c.n_kv_heads, S = c.n_seqs;
+  int* lens = prefix + S + 1;
 
   for (int i = tid; i < NG * C::NS; i += C::THREADS) mbar_init(&full[i], 1);
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   griddep_enter();
-  kv4_prefix(c, a, geo, prefix, 1);
+  const int fresh = a.k.data ? 1 : 0;  // units of the new rows
+  auto units_of = [&](int L) { return max(1, fresh + (L + kKv4HalfTokens - 1) / kKv4HalfTokens); };
+  kv4_prefix(c, a, geo, prefix, lens, units_of);
   __syncthreads();
+  auto len_of = [&](int s) { return s < kKv4Lens ? lens[s] : c.len[s]; };
+  auto count_of = [&](int s) { return a.counts ? a.counts[s] : a.n; };
 
+  // equal ranges of the U units: the first `more` of the W workers have one more than `each`
   const int U = prefix[S];
   if (U == 0) return;
-  const Kv8Workers wk = kv8_workers(U, geo.ctas, NG);
-  const int worker = blockIdx.x * wk.ng + grp;
-  const bool has = grp < wk.ng && worker < wk.W;
-  const int u0 = has ? worker_begin(worker, wk.W, U) : 0, u1 = has ? worker_begin(worker + 1, wk.W, U) : 0;
+  const int ng = min(NG, (U + geo.ctas - 1) / geo.ctas), W = min(U, geo.ctas * ng), each = U / W, more = U % W;
+  auto begin_of = [&](int w) { return w * each + min(w, more); };
+  auto worker_at = [&](int u) {
+    const int x = more * (each + 1);
+    return u < x ? u / (each + 1) : more + (u - x) / each;
+  };
+  const int worker = blockIdx.x * ng + grp;
+  const bool has = grp < ng && worker < W;
+  const int u0 = has ? begin_of(worker) : 0, u1 = has ? begin_of(worker + 1) : 0;
 
   // The lane's unit x (32 units in parallel, so the table's latency is paid once).
   auto look = [&](int x) -> Kv4Unit {
-    Kv4Unit r{-1, -1, 0, 0};
+    Kv4Unit r{-1, -1, 0};
     if (x >= u1) return r;
-    const int s = kv4_seq_of(prefix, S, x), cnt = a.counts ? a.counts[s] : a.n, L = c.len[s];
-    const int per = kv4_units(L), q = (x - prefix[s]) / per, blocks = kv4_blocks(geo, cnt);
-    r.u = (x - prefix[s]) % per;
+    const int s = kv4_seq_of(prefix, S, x), L = len_of(s), blocks = kv4_blocks(geo, count_of(s));
+    const int per = units_of(L), q = (x - prefix[s]) / per, u = (x - prefix[s]) % per - fresh;
     r.seg = (s * H + q / blocks) * geo.CB + q % blocks;
-    r.valid = min(kPage, L - r.u * kPage);
-    if (r.valid <= 0) return r;
-    const int phys = kv4_phys(c, s, r.u);
-    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * C::PAGE;
+    r.tokens = u < 0 ? -1 : max(0, min(kKv4HalfTokens, L - u * kKv4HalfTokens));
+    if (r.tokens <= 0) return r;
+    const int phys = kv4_phys(c, s, u >> 1);
+    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * Kv4Page<D>::BYTES + (u & 1);
     return r;
   };
 
-  uint8_t* ring = sm + (size_t)grp * C::NS * C::PAGE;
+  uint8_t* ring = sm + (size_t)grp * C::NS * C::HALF;
   full += grp * C::NS;
   Kv4Unit cur = look(u0 + lane), nxt = look(u0 + 32 + lane);
   const int nu = u1 - u0;
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   auto locate = [&](int sg) {
     seg = sg;
     cb_cur = sg % geo.CB, h_cur = sg / geo.CB % H, s_cur = sg / geo.CB / H;
-    rows_cur = min(RB, (a.counts ? a.counts[s_cur] : a.n) * geo.G - cb_cur * RB);
+    rows_cur = min(RB, count_of(s_cur) * geo.G - cb_cur * RB);
   };
   auto query = [&](int row) {  // of the column block
     const int r = cb_cur * RB + row;
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     return static_cast<T*>(a.out.data) + s * a.out.seq + (r / geo.G) * a.out.row + (h * geo.G + r % geo.G) * a.out.head;
   };
 
-  auto begin = [&](int sg, int u) {
+  auto begin = [&](int sg) {
     locate(sg);
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -282,10 +296,11 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         collow[x][y] = llo * dn;
       }
     }
-    if (u > 0 || !a.k.data) return;
-    // the new rows, one after the other, in plain fp32: a lane has E dims of a key for the dot products, then the values of
-    // its accumulators' dims.  A row that does not see the token is left out of everything, whatever the token holds.
-    const int cnt = a.counts ? a.counts[s_cur] : a.n;
+  };
+  // The new rows, one after the other, in plain fp32: a lane has E dims of a key for the dot products, then the values of
+  // its accumulators' dims.  A row that does not see the token is left out of everything, whatever the token holds.
+  auto new_rows = [&]() {
+    const int cnt = count_of(s_cur);
     const T* kn = static_cast<const T*>(a.k.data) + s_cur * a.k.seq + h_cur * a.k.head + E * lane;
     const T* vn = static_cast<const T*>(a.v.data) + s_cur * a.v.seq + h_cur * a.v.head + g;
     const int node0 = cb_cur * RB / geo.G, node1 = (cb_cur * RB + rows_cur - 1) / geo.G;  // the block's nodes
@@ -395,168 +410,173 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       }
   };
 
-  // A page, half of it (32 tokens) at a time: S^T = K Q^T, softmax, O^T += V^T P^T.
-  auto page = [&](const uint8_t* pg, int valid) {
-#pragma unroll 1
-    for (int it = 0; it < 2; ++it) {
-      if (32 * it >= valid) break;
-      float x[NT][2][4];  // two 16-token tiles
+  // Half a page: S^T = K Q^T, softmax, O^T += V^T P^T.  The first `left` of its tokens are there.
+  auto half = [&](const uint8_t* pg, int left) {
+    float x[NT][2][4];  // two 16-token tiles
 #pragma unroll
-      for (int z = 0; z < NT; ++z)
+    for (int z = 0; z < NT; ++z)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[z][i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) x[z][i][e] = 0.0f;
+    uint32_t sw[2][2];  // scale bytes of tokens g and g + 8 of the tiles
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(pg + C::KS + (i * 8 + g) * 8);
+        sw[i][0] = w.x, sw[i][1] = w.y;
+      } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + C::KS + (i * 8 + g) * 4);
+        sw[i][0] = w, sw[i][1] = w >> 16;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint32_t w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tile = 2 * it + i;
-        uint32_t sw[2];  // scale bytes of tokens g and g + 8
-        if (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(pg + Kv4Page<D>::KS + (tile * 8 + g) * 8);
-          sw[0] = w.x, sw[1] = w.y;
-        } else {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + Kv4Page<D>::KS + (tile * 8 + g) * 4);
-          sw[0] = w, sw[1] = w >> 16;
+        const uint4 w4 = reinterpret_cast<const uint4*>(pg)[(i * (D / 64) + j) * 32 + lane];
+        w[i][0] = w4.x, w[i][1] = w4.y, w[i][2] = w4.z, w[i][3] = w4.w;
+      }
+#pragma unroll
+      for (int kh = 0; kh < 2; ++kh) {
+        const int gr = 2 * j + kh;
+        float part[NT][2][4];
+        uint32_t s0[2], s1[2], b0[2], b1[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s0[i] = kv4_scale_pair(sw[i][0], gr, gr), s1[i] = kv4_scale_pair(sw[i][1], gr, gr);
+          b0[i] = mul_h2(s0[i], kMinus264), b1[i] = mul_h2(s1[i], kMinus24);
+#pragma unroll
+          for (int z = 0; z < NT; ++z)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[z][i][e] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const uint4 w4 = reinterpret_cast<const uint4*>(pg)[(tile * (D / 64) + j) * 32 + lane];
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            const int grp32 = 2 * j + kh;
-            const uint32_t s0 = kv4_scale_pair(sw[0], grp32, grp32), s1 = kv4_scale_pair(sw[1], grp32, grp32);
-            const uint32_t b0 = mul_h2(s0, kMinus264), b1 = mul_h2(s1, kMinus24);
-            float part[NT][4];
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t wa = w[i][2 * kh + p], wb = kv4_swap(wa);
+            const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0[i], b0[i]), fma_h2(kv4_f16_high(wa), s1[i], b1[i]),
+                                    fma_h2(kv4_f16_low(wb), s0[i], b0[i]), fma_h2(kv4_f16_high(wb), s1[i], b1[i])};
 #pragma unroll
             for (int z = 0; z < NT; ++z)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) part[z][e] = 0.0f;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint32_t wa = w[2 * kh + p], wb = kv4_swap(wa);
-              const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0, b0), fma_h2(kv4_f16_high(wa), s1, b1),
-                                      fma_h2(kv4_f16_low(wb), s0, b0), fma_h2(kv4_f16_high(wb), s1, b1)};
-#pragma unroll
-              for (int z = 0; z < NT; ++z)
-                mma_f16(SPLIT ? part[z] : x[z][i], af, qf[z][2 * grp32 + p][0], qf[z][2 * grp32 + p][1]);
-            }
-            if (SPLIT)
-#pragma unroll
-              for (int z = 0; z < NT; ++z)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[z][i][e] += part[z][e];
+              mma_f16(SPLIT ? part[z][i] : x[z][i], af, qf[z][2 * gr + p][0], qf[z][2 * gr + p][1]);
           }
-        }
-      }
-      const int left = valid - 32 * it;  // tokens of this half and on
-      uint32_t pf[NT][2][2];
-#pragma unroll
-      for (int z = 0; z < NT; ++z) {
-        // logits: entry y + 2 e of tile i is row y of the thread, token g + 8 e of the tile
         if (SPLIT)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) x[z][i][0] += x[z][i][1], x[z][i][2] += x[z][i][3];  // hi + lo
-        if (left < 32)
+          for (int z = 0; z < NT; ++z)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = colfac[z][(e & 1) * (NC - 1)] < 0.0f ? INFINITY : -INFINITY;
-        bool high = false;
+              for (int e = 0; e < 4; ++e) x[z][i][e] += part[z][i][e];
+      }
+    }
+    uint32_t pf[NT][2][2];
+#pragma unroll
+    for (int z = 0; z < NT; ++z) {
+      // logits: entry y + 2 e of tile i is row y of the thread, token g + 8 e of the tile
+      if (SPLIT)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[z][i][0] += x[z][i][1], x[z][i][2] += x[z][i][3];  // hi + lo
+      if (left < 32)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int y = 0; y < NC; ++y)
-            high = high || x[z][i][y] * colfac[z][y] > m[z][y] + kP4Slack || x[z][i][y + 2] * colfac[z][y] > m[z][y] + kP4Slack;
-        if (__any_sync(FULL, high)) {
-          float cc[NC];
+          for (int e = 0; e < 4; ++e)
+            if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = colfac[z][(e & 1) * (NC - 1)] < 0.0f ? INFINITY : -INFINITY;
+      bool high = false;
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
-            const float f = colfac[z][y];
-            float mx = fmaxf(fmaxf(x[z][0][y] * f, x[z][0][y + 2] * f), fmaxf(x[z][1][y] * f, x[z][1][y + 2] * f));
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-            mx = fmaxf(mx, m[z][y]);
-            cc[y] = mx == -INFINITY ? 1.0f : ex2(m[z][y] - mx);
-            m[z][y] = mx;
-            l[z][y] *= cc[y];
-          }
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int d = 0; d < DT; ++d)
+        for (int y = 0; y < NC; ++y)
+          high = high || x[z][i][y] * colfac[z][y] > m[z][y] + kP4Slack || x[z][i][y + 2] * colfac[z][y] > m[z][y] + kP4Slack;
+      if (__any_sync(FULL, high)) {
+        float cc[NC];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) O[z][d][e] *= cc[(e & 1) * (NC - 1)];
+        for (int y = 0; y < NC; ++y) {
+          const float f = colfac[z][y];
+          float mx = fmaxf(fmaxf(x[z][0][y] * f, x[z][0][y + 2] * f), fmaxf(x[z][1][y] * f, x[z][1][y + 2] * f));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+          mx = fmaxf(mx, m[z][y]);
+          cc[y] = mx == -INFINITY ? 1.0f : ex2(m[z][y] - mx);
+          m[z][y] = mx;
+          l[z][y] *= cc[y];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
-            const float base = m[z][y] == -INFINITY ? 0.0f : m[z][y];
+          for (int e = 0; e < 4; ++e) O[z][d][e] *= cc[(e & 1) * (NC - 1)];
+      }
 #pragma unroll
-            for (int e = y; e < 4; e += 2) {
-              x[z][i][e] = SPLIT ? ex2(fmaf(x[z][i][e], collow[z][y], fmaf(x[z][i][e], colfac[z][y], -base))) * kP4Scale
-                                 : ex2(fmaf(x[z][i][e], colfac[z][y], 7.0f - base));
-              if (left < 32 && 16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = 0.0f;
-              l[z][y] += x[z][i][e];
-            }
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int y = 0; y < NC; ++y) {
+          const float base = m[z][y] == -INFINITY ? 0.0f : m[z][y];
+#pragma unroll
+          for (int e = y; e < 4; e += 2) {
+            x[z][i][e] = SPLIT ? ex2(fmaf(x[z][i][e], collow[z][y], fmaf(x[z][i][e], colfac[z][y], -base))) * kP4Scale
+                               : ex2(fmaf(x[z][i][e], colfac[z][y], 7.0f - base));
+            if (left < 32 && 16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = 0.0f;
+            l[z][y] += x[z][i][e];
           }
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p = x[z][i][2 * e];
-            pf[z][i][e] = movmatrix(SPLIT ? pack_f16(p, p - __half2float(__float2half_rn(p))) : pack_f16(p, x[z][i][2 * e + 1]));
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float p = x[z][i][2 * e];
+          pf[z][i][e] = movmatrix(SPLIT ? pack_f16(p, p - __half2float(__float2half_rn(p))) : pack_f16(p, x[z][i][2 * e + 1]));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint32_t w[2][4], vs[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 w4 = reinterpret_cast<const uint4*>(pg + C::V)[(i * (D / 64) + j) * 32 + lane];
+        w[i][0] = w4.x, w[i][1] = w4.y, w[i][2] = w4.z, w[i][3] = w4.w;
+        const uint2 s2 = *reinterpret_cast<const uint2*>(pg + C::VS + (i * 4 + t) * (D / 8) + 8 * j);
+        vs[i][0] = s2.x, vs[i][1] = s2.y;
+        if (left < 32) {  // tokens that are not there: whatever their bytes hold, scale 0
+          uint32_t keep = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (16 * i + 2 * t + (b & 1) + 8 * (b >> 1) < left) keep |= 255u << (8 * b);
+          vs[i][0] &= keep, vs[i][1] &= keep;
         }
       }
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        uint4 w4[2];
-        uint32_t sw[2][2];
+      for (int gh = 0; gh < 2; ++gh) {
+        float part[NT][2][4];
+#pragma unroll
+        for (int z = 0; z < NT; ++z)
+#pragma unroll
+          for (int dd = 0; dd < 2; ++dd)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[z][dd][e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int tile = 2 * it + i;
-          w4[i] = reinterpret_cast<const uint4*>(pg + Kv4Page<D>::V)[(tile * (D / 64) + j) * 32 + lane];
-          const uint2 w = *reinterpret_cast<const uint2*>(pg + Kv4Page<D>::VS + (tile * 4 + t) * (D / 8) + 8 * j);
-          sw[i][0] = w.x, sw[i][1] = w.y;
-          if (left < 32) {  // tokens that are not there: whatever their bytes hold, scale 0
-            uint32_t keep = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (16 * i + 2 * t + (b & 1) + 8 * (b >> 1) < left) keep |= 255u << (8 * b);
-            sw[i][0] &= keep, sw[i][1] &= keep;
-          }
-        }
-#pragma unroll
-        for (int gh = 0; gh < 2; ++gh) {
-          uint32_t s0[2], s1[2], b0[2], b1[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            s0[i] = kv4_scale_pair(sw[i][gh], 0, 1), s1[i] = kv4_scale_pair(sw[i][gh], 2, 3);
-            b0[i] = mul_h2(s0[i], kMinus264), b1[i] = mul_h2(s1[i], kMinus24);
-          }
+          const uint32_t s0 = kv4_scale_pair(vs[i][gh], 0, 1), s1 = kv4_scale_pair(vs[i][gh], 2, 3);
+          const uint32_t b0 = mul_h2(s0, kMinus264), b1 = mul_h2(s1, kMinus24);
 #pragma unroll
           for (int dd = 0; dd < 2; ++dd) {
             const int d = 4 * j + 2 * gh + dd;
-            float part[NT][4];
+            const uint32_t wa = w[i][2 * gh + dd], wb = kv4_swap(wa);
+            const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0, b0), fma_h2(kv4_f16_low(wb), s0, b0),
+                                    fma_h2(kv4_f16_high(wa), s1, b1), fma_h2(kv4_f16_high(wb), s1, b1)};
 #pragma unroll
-            for (int z = 0; z < NT; ++z)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) part[z][e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t wa = gh ? (dd ? w4[i].w : w4[i].z) : (dd ? w4[i].y : w4[i].x), wb = kv4_swap(wa);
-              const uint32_t af[4] = {fma_h2(kv4_f16_low(wa), s0[i], b0[i]), fma_h2(kv4_f16_low(wb), s0[i], b0[i]),
-                                      fma_h2(kv4_f16_high(wa), s1[i], b1[i]), fma_h2(kv4_f16_high(wb), s1[i], b1[i])};
-#pragma unroll
-              for (int z = 0; z < NT; ++z) mma_f16(SPLIT ? part[z] : O[z][d], af, pf[z][i][0], pf[z][i][1]);
-            }
-            if (SPLIT)
-#pragma unroll
-              for (int z = 0; z < NT; ++z)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) O[z][d][e] += part[z][e];
+            for (int z = 0; z < NT; ++z) mma_f16(SPLIT ? part[z][dd] : O[z][d], af, pf[z][i][0], pf[z][i][1]);
           }
         }
+        if (SPLIT)
+#pragma unroll
+          for (int z = 0; z < NT; ++z)
+#pragma unroll
+            for (int dd = 0; dd < 2; ++dd)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) O[z][4 * j + 2 * gh + dd][e] += part[z][dd][e];
       }
     }
   };
@@ -567,62 +587,60 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     int early, held;  // whether w1 goes on behind it (its part is then stored apart), CTAs that hold the others
   };
   auto parts_of = [&](int sg) {
-    const int s = sg / geo.CB / H, h = sg / geo.CB % H, cb = sg % geo.CB;
-    const int per = kv4_units(c.len[s]), blocks = kv4_blocks(geo, a.counts ? a.counts[s] : a.n);
-    const int first = prefix[s] + (h * blocks + cb) * per, end = first + per;
+    const int cb = sg % geo.CB, h = sg / geo.CB % H, s = sg / geo.CB / H;
+    const int per = units_of(len_of(s)), first = prefix[s] + (h * kv4_blocks(geo, count_of(s)) + cb) * per, end = first + per;
     Parts p;
-    p.w0 = worker_of(first, wk.W, U), p.w1 = worker_of(end - 1, wk.W, U);
-    p.early = worker_begin(p.w1 + 1, wk.W, U) > end;
-    p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / wk.ng - p.w0 / wk.ng + 1;
+    p.w0 = worker_at(first), p.w1 = worker_at(end - 1);
+    p.early = begin_of(p.w1 + 1) > end;
+    p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / ng - p.w0 / ng + 1;
     return p;
   };
-  // The parts of a segment, the CTAs' in their order, then the early one, to the output: warp `first` of `warps` takes every
-  // warps-th row, B loads in flight.
-  auto join = [&](int sg, const Parts& p, int first, int warps) {
-    const int s = sg / geo.CB / H, cb = sg % geo.CB;
-    const int rows = min(RB, (a.counts ? a.counts[s] : a.n) * geo.G - cb * RB), n = p.held + p.early;
-    auto place = [&](int i) -> size_t {
-      return i < p.held ? (size_t)max(p.w0, (p.w0 / wk.ng + i) * wk.ng) : (size_t)geo.ctas * geo.ng + p.w1;
-    };
-    constexpr int B = 8;
-    for (int r = first; r < rows; r += warps) {
-      float M = -INFINITY, sum = 0.0f, o[E] = {};
-      for (int i0 = 0; i0 < n; i0 += B) {
-        float2 ml[B];
-        Vec v[B];
+  auto rows_of = [&](int sg) { return min(RB, count_of(sg / geo.CB / H) * geo.G - sg % geo.CB * RB); };
+  // The parts first, first + step, .. of a segment's row, of the CTAs in their order, then the early one: maximum M,
+  // sum, and values of the lane's dims; B loads in flight.
+  auto gather = [&](const Parts& p, int r, int first, int step, float& M, float& sum, float (&o)[E]) {
+    const int n = p.held + p.early;
+    constexpr int B = 6;
+    M = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          ml[b] = make_float2(-INFINITY, 0.0f);
-          v[b] = {};
-          if (i0 + b < n) {
-            const size_t at = place(i0 + b) * RB + r;
-            ml[b] = __ldcg(ws.ml + at);
-            v[b] = __ldcg(reinterpret_cast<const Vec*>(ws.o + at * D + E * lane));
-          }
-        }
-        float mx = M;
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int i0 = first; i0 < n; i0 += B * step) {
+      float2 ml[B];
+      Vec v[B];
 #pragma unroll
-        for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
-        const float base = mx == -INFINITY ? 0.0f : mx, f = ex2(M - base);
-        M = mx;
-        sum *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-          const float w = ex2(ml[b].x - base);
-          const float* ve = reinterpret_cast<const float*>(&v[b]);
-          sum = fmaf(ml[b].y, w, sum);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(ve[e], w, o[e]);
+      for (int b = 0; b < B; ++b) {
+        const int i = i0 + b * step;
+        ml[b] = make_float2(-INFINITY, 0.0f);
+        v[b] = {};
+        if (i < n) {
+          const size_t at = (i < p.held ? (size_t)max(p.w0, (p.w0 / ng + i) * ng) : (size_t)geo.ctas * geo.ng + p.w1) * RB + r;
+          ml[b] = __ldcg(ws.ml + at);
+          v[b] = __ldcg(reinterpret_cast<const Vec*>(ws.o + at * D + E * lane));
         }
       }
-      T* out = output(sg, r) + E * lane;
+      float mx = M;
 #pragma unroll
-      for (int e = 0; e < E; ++e) kv8_store(out + e, sum == 0.0f ? 0.0f : o[e] / sum);
+      for (int b = 0; b < B; ++b) mx = fmaxf(mx, ml[b].x);
+      const float base = mx == -INFINITY ? 0.0f : mx, f = ex2(M - base);
+      M = mx;
+      sum *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const float w = ex2(ml[b].x - base);
+        const float* ve = reinterpret_cast<const float*>(&v[b]);
+        sum = fmaf(ml[b].y, w, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(ve[e], w, o[e]);
+      }
     }
   };
-  // Whether the part that the calling threads have stored (and made visible) was the segment's last.
+  auto store = [&](T* to, float sum, const float (&o)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) kv8_store(to + e, sum == 0.0f ? 0.0f : o[e] / sum);
+  };
+  // Whether the part that the CTA's or the warp's other threads have stored, ordered before this thread, was the segment's last.
   auto is_last = [&](const Parts& p) {
     __threadfence();
     if (atomicAdd(ws.ticket + p.w0, 1) != p.held + p.early - 1) return false;
@@ -639,13 +657,15 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     }
     const size_t at = ((size_t)geo.ctas * geo.ng + worker) * RB;
     flush(ws.ml + at, ws.o + at * D);
-    __threadfence();
     __syncwarp();
     int last = 0;
     if (lane == 0) last = is_last(p);
     if (!__shfl_sync(FULL, last, 0)) return;
-    __threadfence();
-    join(seg, p, 0, 1);
+    for (int r = 0; r < rows_cur; ++r) {
+      float M, sum, o[E];
+      gather(p, r, 0, 1, M, sum, o);
+      store(output(seg, r) + E * lane, sum, o);
+    }
   };
 
   // ---- the range
@@ -662,47 +682,68 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       ++jl;
       if (from < 0) continue;
       if (lane == 0) {
-        mbar_expect_tx(&full[is], C::PAGE);
-        if (geo.withheld != (int)blockIdx.x) bulk_g2s(ring + (size_t)is * C::PAGE, c.pages + from, C::PAGE, &full[is]);
+        mbar_expect_tx(&full[is], C::HALF);
+        if (geo.withheld != (int)blockIdx.x) {
+          const int y = (int)(from & 1);
+          const uint8_t* page = c.pages + (from - y);
+          uint8_t* to = ring + (size_t)is * C::HALF;
+          bulk_g2s(to, page + 16 * D * y, 16 * D, &full[is]);
+          bulk_g2s(to + C::V, page + Kv4Page<D>::V + 16 * D * y, 16 * D, &full[is]);
+          bulk_g2s(to + C::KS, page + Kv4Page<D>::KS + D * y, D, &full[is]);
+          bulk_g2s(to + C::VS, page + Kv4Page<D>::VS + D * y, D, &full[is]);
+        }
       }
       ++in_ring;
       if (++is == C::NS) is = 0;
     }
     const int src = j - cbase;
     const int64_t from = __shfl_sync(FULL, cur.src, src);
-    const int sg = __shfl_sync(FULL, cur.seg, src), u = __shfl_sync(FULL, cur.u, src), valid = __shfl_sync(FULL, cur.valid, src);
+    const int sg = __shfl_sync(FULL, cur.seg, src), tokens = __shfl_sync(FULL, cur.tokens, src);
     if (sg != seg) {
       if (seg >= 0) finish();
-      begin(sg, u);
+      begin(sg);
     }
+    if (tokens < 0 && ok) new_rows();
     if (from < 0 || !ok) continue;
     ok = __all_sync(FULL, mbar_wait(&full[cs], cph, geo.wait_ns));
     if (ok) {
-      page(ring + (size_t)cs * C::PAGE, valid);
-    } else {  // a bounded wait expired: the sums from here on are not what they should be, and NaN says so
-      if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int y = 0; y < NC; ++y) l[x][y] = NAN;
-      for (; in_ring > 0; --in_ring) {  // no copy stays in flight (again bounded)
-        (void)mbar_wait(&full[cs], cph, geo.wait_ns);
-        if (++cs == C::NS) cs = 0, cph ^= 1;
-      }
+      half(ring + (size_t)cs * C::HALF, tokens);
+      __syncwarp();
+      if (++cs == C::NS) cs = 0, cph ^= 1;
+      --in_ring;
       continue;
     }
-    __syncwarp();
-    if (++cs == C::NS) cs = 0, cph ^= 1;
-    --in_ring;
+    // a bounded wait expired: the sums from here on are not what they should be, and NaN says so; no copy stays in flight
+    if (lane == 0) atomicOr(c.ctl, (unsigned)FLAG_ERR_TIMEOUT);
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int y = 0; y < NC; ++y) l[x][y] = NAN;
+    for (; in_ring > 0; --in_ring) {
+      (void)mbar_wait(&full[cs], cph, geo.wait_ns);
+      if (++cs == C::NS) cs = 0, cph ^= 1;
+    }
   }
   // ---- the workers' last parts, in the ring's place, and of each run of workers on one segment the sum
   float2* sml = reinterpret_cast<float2*>(sm);                // [NG][RB]
   int* sseg = reinterpret_cast<int*>(sml + NG * RB);          // [NG], -1: none
-  float* so = reinterpret_cast<float*>(sm) + ((NG * (2 * RB + 1) + 31) & ~31);  // [NG][RB][D]
-  static_assert((((NG * (2 * RB + 1) + 31) & ~31) + NG * RB * D) * 4 <= kKv4RingBytes, "parts");
+  float* sfac = reinterpret_cast<float*>(sseg + NG);          // [NG][RB] factor of a worker's part in its run
+  float* so = reinterpret_cast<float*>(sm) + ((NG * (3 * RB + 1) + 31) & ~31);  // [NG][RB][D]
+  float* jo = so + NG * RB * D;                               // [NG][D], of the join
+  float2* jml = reinterpret_cast<float2*>(jo + NG * D);       // [NG]
+  static_assert((((NG * (3 * RB + 1) + 31) & ~31) + NG * (RB + 1) * D + 2 * NG) * 4 <= kKv4RingBytes, "parts");
   __syncthreads();
   if (lane == 0) sseg[grp] = seg;
   if (seg >= 0) flush(sml + grp * RB, so + grp * RB * D);
+  __syncthreads();
+  for (int x = tid; x < NG * RB; x += C::THREADS) {
+    const int i = x / RB, sg = sseg[i];
+    if (sg < 0 || x % RB >= rows_of(sg)) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int y = 0; y < NG; ++y) M = sseg[y] == sg ? fmaxf(M, sml[y * RB + x % RB].x) : M;
+    sfac[x] = ex2(sml[x].x - (M == -INFINITY ? 0.0f : M));
+  }
   __syncthreads();
   for (int i0 = 0; i0 < NG;) {
     const int sg = sseg[i0];
@@ -711,19 +752,18 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     if (sg >= 0) {
       const Parts p = parts_of(sg);
       const bool alone = p.held + p.early == 1;
-      const int s = sg / geo.CB / H, cb = sg % geo.CB;
-      const int rows = min(RB, (a.counts ? a.counts[s] : a.n) * geo.G - cb * RB);
-      const size_t at = ((size_t)blockIdx.x * wk.ng + i0) * RB;
+      const int rows = rows_of(sg);
+      const size_t at = ((size_t)blockIdx.x * ng + i0) * RB;
       for (int x = tid; x < rows * (D / 4); x += C::THREADS) {
         const int r = x / (D / 4), d = x % (D / 4);
         float M = -INFINITY, L = 0.0f;
-        for (int i = i0; i < i1; ++i) M = fmaxf(M, sml[i * RB + r].x);
-        const float base = M == -INFINITY ? 0.0f : M;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
         for (int i = i0; i < i1; ++i) {
           const float2 ml = sml[i * RB + r];
           const float4 o = reinterpret_cast<const float4*>(so + (i * RB + r) * D)[d];
-          const float f = ex2(ml.x - base);
+          const float f = sfac[i * RB + r];
+          M = fmaxf(M, ml.x);
           L = fmaf(ml.y, f, L);
           v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
         }
@@ -737,11 +777,40 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         }
       }
       if (!alone) {
-        __threadfence();
         __syncthreads();
         if (tid == 0) last_part = is_last(p);
         __syncthreads();
-        if (last_part) join(sg, p, grp, NG);
+        if (last_part) {  // a row to `per` warps, then their sums
+          int per = NG;
+          while (per > 1 && NG / per < rows) per >>= 1;
+          for (int r0 = 0; r0 < rows; r0 += NG / per) {
+            const int r = r0 + grp / per;
+            float M = -INFINITY, sum = 0.0f, o[E] = {};
+            if (r < rows) gather(p, r, grp % per, per, M, sum, o);
+            if (per > 1) {
+              if (lane == 0) jml[grp] = make_float2(M, sum);
+              *reinterpret_cast<Vec*>(jo + grp * D + E * lane) = *reinterpret_cast<Vec*>(o);
+              __syncthreads();
+              if (grp % per == 0) {
+                float top = M;
+                for (int y = 1; y < per; ++y) top = fmaxf(top, jml[grp + y].x);
+                const float base = top == -INFINITY ? 0.0f : top;
+                float f = ex2(M - base);
+                sum *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= f;
+                for (int y = 1; y < per; ++y) {
+                  f = ex2(jml[grp + y].x - base);
+                  sum = fmaf(jml[grp + y].y, f, sum);
+#pragma unroll
+                  for (int e = 0; e < E; ++e) o[e] = fmaf(jo[(grp + y) * D + E * lane + e], f, o[e]);
+                }
+              }
+            }
+            if (r < rows && grp % per == 0) store(output(sg, r) + E * lane, sum, o);
+            if (per > 1) __syncthreads();
+          }
+        }
       }
     }
     i0 = i1;
@@ -750,7 +819,9 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 
 // ---------------------------------------------------------------------------- launch
 
-inline size_t kv4_split_smem(int S, int entries) { return (size_t)kKv4RingBytes + 8 * (size_t)entries + 4 * ((size_t)S + 1); }
+inline size_t kv4_split_smem(int S, int entries) {
+  return (size_t)kKv4RingBytes + 8 * (size_t)entries + 4 * ((size_t)S + 1 + (S < kKv4Lens ? S : kKv4Lens));
+}
 
 template <typename T, int D, int NT>
 cudaError_t kv4_split_launch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, const Kv4Scratch& ws,
@@ -763,7 +834,7 @@ cudaError_t kv4_split_launch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, co
 }
 // Column tiles of a warp for R query rows of a KV head: two where one does not hold them (four rows of fp32, eight of bf16).
 inline int kv4_split_tiles(int R, int dtype) { return R > (dtype == W4A8_F32 ? 4 : 8) ? 2 : 1; }
-inline int kv4_split_warps(int R, int dtype) { return kv4_split_tiles(R, dtype) == 1 ? 12 : 8; }
+inline int kv4_split_warps(int R, int dtype) { return kv4_split_tiles(R, dtype) == 1 ? 16 : 8; }
 template <typename T, int D>
 cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, const Kv4Scratch& ws,
                                cudaStream_t st) {

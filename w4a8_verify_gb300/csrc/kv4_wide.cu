@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  kv4_prefix(c, a, geo, prefix, 0);
+  kv4_prefix(c, a, geo, prefix, nullptr, [](int L) { return (L + kPage - 1) / kPage; });
   tc_before();
   __syncthreads();
   tc_after();

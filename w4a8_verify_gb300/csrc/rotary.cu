@@ -27,32 +27,37 @@ struct RotGeom {
   float inv_dim;
 };
 
+// Eight elements of a row, as they are, and in fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool wide, float (&x)[8]) {
-  if (wide) {
-    uint4 u[sizeof(T) / 2];
+struct Eight {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(u)[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void store(T* p, bool wide) const {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = reinterpret_cast<const T*>(u)[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = kv8_load(reinterpret_cast<const T*>(u) + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = kv8_load(p + i);
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, bool wide, const float (&x)[8]) {
-  if (wide) {
-    uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void set(const float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) kv8_store(reinterpret_cast<T*>(u) + i, x[i]);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) kv8_store(p + i, x[i]);
   }
-}
+};
 
 // Cosine and sine of turn 2^-64 turns.
 __device__ __forceinline__ void unit(uint64_t turn, float& c, float& s) {
@@ -80,34 +85,53 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
   const bool live = sub < D / 16, turned = sub < a.rot_dim / 16, halves = turned && !a.neighbours;
   const int d0 = halves ? 8 * sub : 16 * sub, d1 = halves ? a.rot_dim / 2 + 8 * sub : 16 * sub + 8;
   const int H = a.n_heads + a.n_kv_heads;
+  auto place = [&](int it, bool& on, bool& key) -> int64_t {  // of round it: the lane's head, and its offset from q's or k's data
+    const int h = (seg * geo.iters + it) * HPW + lane / LPH;
+    on = live && h < H && it < geo.iters, key = h >= a.n_heads;
+    const w4a8_rows& in = key ? a.k : a.q;
+    return s * in.seq + j * in.row + (int64_t)(key ? h - a.n_heads : h) * in.head;
+  };
+  Eight<T> x0{}, y0{};  // of the round to come
+  auto fetch = [&](int it) {
+    bool on, key;
+    const int64_t at = place(it, on, key);
+    if (!on) return;
+    const T* p = static_cast<const T*>(key ? a.k.data : a.q.data) + at;
+    x0.load(p + d0, vec >> (int)key & 1);
+    y0.load(p + d1, vec >> (int)key & 1);
+  };
+  fetch(0);
+  // the lanes of a frequency octet share its angles: PER each, then exchanged
+  constexpr int PER = 8 / HPW;
   float c[8], sn[8];
-  if (turned) {
+  {
+    float mc[PER], ms[PER];
     const int64_t start = a.start ? a.start[s] : 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = 8 * sub + e;
+    for (int e = 0; e < PER; ++e) {
+      const int i = 8 * sub + lane / LPH * PER + e;
+      mc[e] = ms[e] = 0.0f;
+      if (!turned) continue;
       int ax = a.axis ? a.axis[i] : 0;
       ax = ax < a.n_axes ? ax : 0;
       const int64_t p = start + (a.pos ? a.pos[((int64_t)ax * a.n_seqs + s) * a.n + j] : j);
-      unit((uint64_t)p * a.turns[i], c[e], sn[e]);
-      c[e] *= a.factor, sn[e] *= a.factor;
+      unit((uint64_t)p * a.turns[i], mc[e], ms[e]);
+      mc[e] *= a.factor, ms[e] *= a.factor;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = __shfl_sync(0xffffffffu, mc[e % PER], e / PER * LPH + sub);
+      sn[e] = __shfl_sync(0xffffffffu, ms[e % PER], e / PER * LPH + sub);
     }
   }
   float gain[16];
   int kind = -1;
   for (int it = 0; it < geo.iters; ++it) {
-    const int h = (seg * geo.iters + it) * HPW + lane / LPH;
-    const bool on = live && h < H, key = h >= a.n_heads;
+    bool on, key;
+    (void)place(it, on, key);
     float x[8], y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.0f;
-    const w4a8_rows& in = key ? a.k : a.q;
-    const int64_t hh = key ? h - a.n_heads : h;
-    if (on) {
-      const T* p = static_cast<const T*>(in.data) + s * in.seq + j * in.row + hh * in.head;
-      load8(p + d0, vec >> (int)key & 1, x);
-      load8(p + d1, vec >> (int)key & 1, y);
-    }
+    x0.get(x), y0.get(y);
+    fetch(it + 1);
     if (a.norm) {
       float sum = 0.0f;
 #pragma unroll
@@ -143,9 +167,12 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
     }
     if (on) {
       const w4a8_rows& out = key ? a.k_out : a.q_out;
-      T* p = static_cast<T*>(out.data) + s * out.seq + j * out.row + hh * out.head;
-      store8(p + d0, vec >> (2 + (int)key) & 1, x);
-      store8(p + d1, vec >> (2 + (int)key) & 1, y);
+      const int h = (seg * geo.iters + it) * HPW + lane / LPH;
+      T* p = static_cast<T*>(out.data) + s * out.seq + j * out.row + (int64_t)(key ? h - a.n_heads : h) * out.head;
+      Eight<T> x1, y1;
+      x1.set(x), y1.set(y);
+      x1.store(p + d0, vec >> (2 + (int)key) & 1);
+      y1.store(p + d1, vec >> (2 + (int)key) & 1);
     }
   }
 }
