@@ -406,7 +406,7 @@ w4a8_status w4a8_kv4_attention_workspace_bytes(const w4a8_kv4_cache* c, const w4
  * bits, on the other sequences of the call (they share the splits of the long axis).  A page whose table entry is out of range is
  * left out.  Rows of out must not lie on one another (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one
  * that runs out sets W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN.  n_seqs * n_kv_heads * B < 2^22 and
- * times 2 max_pages + 1 < 2^31, with B the blocks of at most 128 and at least 4 (fp32) or 8 (bf16) query rows (n * heads of a KV head) a
+ * times max_pages + 1 < 2^31, with B the blocks of at most 128 and at least 4 (fp32) or 8 (bf16) query rows (n * heads of a KV head) a
  * sequence's rows are cut into; else W4A8_ERR_SHAPE.
  * workspace: 256-byte aligned, not shared by calls that may overlap.  Its first W4A8_KV4_TICKETS bytes must be zero before its
  * first use; every call leaves them so, whatever its sizes, and the rest needs no initialisation. */

@@ -28,14 +28,14 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
   p->wide = kv4_is_wide(*c, g.R, a->dtype);
   g.RB = p->wide ? kKv4WideRows : kv4_split_tiles(g.R, a->dtype) * (a->dtype == W4A8_F32 ? 4 : 8);
   g.CB = (g.R + g.RB - 1) / g.RB;
-  const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * (p->wide ? c->max_pages : 2 * c->max_pages + 1);
+  const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * (p->wide ? c->max_pages : c->max_pages + 1);
   if (units >= (size_t)1 << 31 || segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.segments = (int)segments;
   g.ctas = (int)(units < (size_t)kKv4Ctas ? units : (size_t)kKv4Ctas);
-  const size_t ng = (units + g.ctas - 1) / g.ctas, most = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype);
+  const size_t ng = (units + g.ctas - 1) / g.ctas, most = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype) / 2;
   g.ng = (int)(ng < most ? ng : most);
   const size_t row = (size_t)g.RB * 4, D = (size_t)c->head_dim;
-  const size_t slots = p->wide ? g.ctas + 2 * segments : 2 * (size_t)g.ctas * g.ng;
+  const size_t slots = p->wide ? g.ctas + 2 * segments : 5 * (size_t)g.ctas * g.ng;
   p->ml = W4A8_KV4_TICKETS;
   p->o = up256(p->ml + slots * row * 2);
   p->prefix = p->rml = p->ro = p->bytes = up256(p->o + slots * row * D);
@@ -74,6 +74,8 @@ w4a8_status attend(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, void* worksp
   p.geo.vec = (kv8_vec_rows(a->q, a->dtype) ? 1 : 0) | (kv8_vec_rows(a->k, a->dtype) ? 2 : 0) | (kv8_vec_rows(a->v, a->dtype) ? 4 : 0);
   p.geo.withheld = withheld;
   p.geo.wait_ns = wait_ns;
+  const double l = (double)a->scale * 1.4426950408889634;
+  p.geo.lhi = (float)l, p.geo.llo = (float)(l - (double)p.geo.lhi);
   const bool f32 = a->dtype == W4A8_F32, d64 = D == 64;
   if (p.wide) W4A8_CUDA_TRY(kv4_wide(*c, *a, p.geo, ws, as_stream(stream)));
   else W4A8_CUDA_TRY((f32 ? d64 ? kv4_split_f32_d64 : kv4_split_f32_d128 : d64 ? kv4_split_bf16_d64 : kv4_split_bf16_d128)(

@@ -21,11 +21,13 @@
 // added in fp32 outside the tensor core.  bf16 calls take one f16 term of q (exact: eight bits) and of P (2^-11), and add
 // their values up in the tensor core's accumulator: its truncation is 2^-24 of the values for each 16 tokens of a worker.
 //
-// Work: every (sequence, KV head, block of rows) is a segment of units: its new rows, then half pages of 32 tokens (one empty
-// unit where there is nothing).  The units of all segments, end to end, are cut into equal ranges, one for each warp, so ragged
-// batches balance.  A warp has its own ring of bulk copies (half a page each) and waits for nobody.  The new rows are done in
-// plain fp32.  A segment that lies within one warp's range is finished there; the warps of a CTA add up where they hold
-// the same one; and where several CTAs do, each stores its part, and the one that comes last (a ticket, which it sets back
+// Work: every (sequence, KV head, block of rows) is a segment of units: its new rows, then pages (one empty unit where there
+// is nothing).  The units of all segments, end to end, are cut into equal ranges, one for each pair of warps, so ragged batches
+// balance.  A pair has its own ring of whole pages, one bulk copy each (four copies to half a page cost the copy engine
+// 105 us of a served batch of 64 sequences, whole pages 66); a warp takes the page's tokens 0..31 or 32..63, and the one that is
+// done with a ring entry last refills it, so nobody waits for the other.  The new rows are done in plain fp32, every second
+// by either warp.  A segment that lies within one pair's range is finished there; the warps of a CTA add up where they
+// hold the same one; and where several CTAs do, each stores its part, and the one that comes last (a ticket, which it sets back
 // to zero) joins the parts in their order.  One launch: a second one costs more than the join.
 #pragma once
 #include <type_traits>
@@ -36,9 +38,9 @@
 namespace w4a8 {
 
 constexpr int kKv4Ctas = 152;             // one per SM of a GB300
-constexpr int kKv4RingBytes = 24 * 8704;  // ring of half pages per SM
+constexpr int kKv4RingBytes = 24 * 8704;  // ring of pages per SM
 constexpr int kKv4MaxWarps = 16;
-constexpr int kKv4HalfTokens = 32;        // tokens of a unit
+constexpr int kKv4HalfTokens = 32;        // tokens of a page that a warp of a pair takes
 constexpr int kKv4Lens = 1024;            // sequences whose lengths are kept in shared memory
 constexpr int kKv4WideRows = 128;         // query rows of a segment of a wide call (kv4_wide.cu)
 constexpr float kP4Scale = 128.0f, kP4Slack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
@@ -47,18 +49,20 @@ static_assert(W4A8_KV4_TICKETS >= kKv4Ctas * kKv4MaxWarps * 4, "tickets");
 struct Kv4Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a KV head
   int RB, CB;          // rows of a column block; column blocks
-  int ctas, ng;        // of the kernel over the pages, and its workers in each at most
+  int ctas, ng;        // of the kernel over the pages, and its workers (split: pairs of warps) in each at most
   int segments;
   int tiles;           // wide calls: blocks of 16 new rows
   int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
   int withheld;        // CTA whose pages are not copied (w4a8_kv4_attention_inject_timeout), -1: none
   uint64_t wait_ns;    // limit of the kernels' waits
+  float lhi, llo;      // log2(e) scale, as hi + lo
 };
 struct Kv4Scratch {    // workspace pointers
   int* ticket;         // [workers] parts of the segment that begins in a worker's range and ends in another's
-  float2* ml;          // [2 workers][RB] maximum, sum of a part: of the workers of a CTA that hold the same segment, at the first
-                       // of them; then, at workers + w, of the one whose worker w went on to another segment
-  float* o;            // [2 workers][RB][D] its values
+  float2* ml;          // [5 workers][RB] maximum, sum of a part: of the workers of a CTA that hold the same segment, at the first
+                       // of them; then, at workers + 2 w, of the two warps of worker w whose range goes on behind the segment
+                       // that it began with; then, at 3 workers + 2 w, of those of a segment within the range
+  float* o;            // [5 workers][RB][D] its values
   // wide calls: ml and o are [ctas + 2 segments][RB], the part of a (CTA, segment) at CTA + segment, then [segments][RB] of the
   // parts whose CTA went on to another segment
   int* prefix;         // [n_seqs + 1] pages of the segments before each sequence
@@ -107,9 +111,15 @@ __device__ __forceinline__ int kv4_seq_of(const int* prefix, int S, int x) {
   return lo;
 }
 
+// (a & b) | c as one instruction: two immediates would make two of it
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // Two f16 numbers of the fields of two words at bits 2..5 (256 + u) or 6..9 (16 + u).
-__device__ __forceinline__ uint32_t kv4_f16_low(uint32_t w) { return (w & 0x003c003cu) | 0x5c005c00u; }
-__device__ __forceinline__ uint32_t kv4_f16_high(uint32_t w) { return (w & 0x03c003c0u) | 0x4c004c00u; }
+__device__ __forceinline__ uint32_t kv4_f16_low(uint32_t w) { return and_or(w, 0x003c003cu, 0x5c005c00u); }
+__device__ __forceinline__ uint32_t kv4_f16_high(uint32_t w) { return and_or(w, 0x03c003c0u, 0x4c004c00u); }
 __device__ __forceinline__ uint32_t kv4_swap(uint32_t w) { return __byte_perm(w, 0, 0x2301); }
 __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
@@ -135,19 +145,19 @@ struct Kv4Split {
   static constexpr int RPT = SPLIT ? 4 : 8;        // rows of an 8-column tile
   static constexpr int NC = SPLIT ? 1 : 2;         // rows of a thread in a tile
   static constexpr int RB = NT * RPT;              // rows of a column block
-  static constexpr int NG = NT == 1 ? 16 : 8;      // workers (warps) of a CTA: what their registers leave room for
-  // a ring entry: codes of 32 keys, of 32 values, scales of the keys, of the values
-  static constexpr int V = 16 * D, KS = 32 * D, VS = 33 * D, HALF = 34 * D;
-  static constexpr int NS = kKv4RingBytes / HALF / NG;  // ring entries of a worker
+  static constexpr int NG = NT == 1 ? 16 : 8;      // warps of a CTA: what their registers leave room for
+  static constexpr int NP = NG / 2;                // workers: pairs of warps
+  static constexpr int PAGE = Kv4Page<D>::BYTES;   // a ring entry
+  static constexpr int NS = kKv4RingBytes / PAGE / NP;  // ring entries of a pair
   static constexpr int STEPS = D / 16;  // k-steps of the first product, 16-dim tiles of the second
   static constexpr int THREADS = 32 * NG;
 };
 
 // What a lane knows of one unit of its worker's range.
 struct Kv4Unit {
-  int64_t src;  // byte offset of the page in the pool (even) + which half, or -1: nothing to read
+  int64_t src;  // byte offset of the page in the pool, or -1: nothing to read
   int seg;      // segment
-  int tokens;   // of the half page; -1: the unit of the new rows
+  int tokens;   // of the page; -1: the unit of the new rows
 };
 
 template <typename T, int D, int NT>
@@ -155,25 +165,33 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     k_kv4_split(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
   using C = Kv4Split<T, D, NT>;
   constexpr bool SPLIT = C::SPLIT;
-  constexpr int NC = C::NC, KS = C::STEPS, DT = C::STEPS, E = D / 32, RB = C::RB, NG = C::NG;
+  constexpr int NC = C::NC, KS = C::STEPS, DT = C::STEPS, E = D / 32, RB = C::RB, NG = C::NG, NP = C::NP, NS = C::NS;
   constexpr unsigned FULL = 0xffffffffu;
   using Vec = std::conditional_t<E == 4, float4, float2>;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ int last_part;
+  // a segment's parts: workers of its first and last unit; whether the last goes on behind it (its parts are then stored
+  // apart), CTAs that hold the others
+  struct Parts {
+    int seg, w0, w1, early, held;
+  };
+  __shared__ Parts sparts[NG + NP];  // of the warps' last segments; of the segments that ended early in the pairs' ranges
+  __shared__ int joins[NG + NP], n_joins;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kKv4RingBytes);
-  int* prefix = reinterpret_cast<int*>(full + NG * C::NS);
+  unsigned* used = reinterpret_cast<unsigned*>(full + NP * NS);
+  int* prefix = reinterpret_cast<int*>(used + NP * NS);
 
-  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5, pair = grp >> 1, side = grp & 1;
   const int g = lane >> 2, t = lane & 3;
   const int H = c.n_kv_heads, S = c.n_seqs;
   int* lens = prefix + S + 1;
 
-  for (int i = tid; i < NG * C::NS; i += C::THREADS) mbar_init(&full[i], 1);
+  for (int i = tid; i < NP * NS; i += C::THREADS) mbar_init(&full[i], 1), used[i] = 0;
+  if (tid < NG + NP) sparts[tid].seg = -1;
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   griddep_enter();
   const int fresh = a.k.data ? 1 : 0;  // units of the new rows
-  auto units_of = [&](int L) { return max(1, fresh + (L + kKv4HalfTokens - 1) / kKv4HalfTokens); };
+  auto units_of = [&](int L) { return max(1, fresh + (L + kPage - 1) / kPage); };
   kv4_prefix(c, a, geo, prefix, lens, units_of);
   __syncthreads();
   auto len_of = [&](int s) { return s < kKv4Lens ? lens[s] : c.len[s]; };
@@ -182,14 +200,14 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   // equal ranges of the U units: the first `more` of the W workers have one more than `each`
   const int U = prefix[S];
   if (U == 0) return;
-  const int ng = min(NG, (U + geo.ctas - 1) / geo.ctas), W = min(U, geo.ctas * ng), each = U / W, more = U % W;
+  const int ng = min(NP, (U + geo.ctas - 1) / geo.ctas), W = min(U, geo.ctas * ng), each = U / W, more = U % W;
   auto begin_of = [&](int w) { return w * each + min(w, more); };
   auto worker_at = [&](int u) {
     const int x = more * (each + 1);
     return u < x ? u / (each + 1) : more + (u - x) / each;
   };
-  const int worker = blockIdx.x * ng + grp;
-  const bool has = grp < ng && worker < W;
+  const int worker = blockIdx.x * ng + pair;
+  const bool has = pair < ng && worker < W;
   const int u0 = has ? begin_of(worker) : 0, u1 = has ? begin_of(worker + 1) : 0;
 
   // The lane's unit x (32 units in parallel, so the table's latency is paid once).
@@ -199,19 +217,22 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     const int s = kv4_seq_of(prefix, S, x), L = len_of(s), blocks = kv4_blocks(geo, count_of(s));
     const int per = units_of(L), q = (x - prefix[s]) / per, u = (x - prefix[s]) % per - fresh;
     r.seg = (s * H + q / blocks) * geo.CB + q % blocks;
-    r.tokens = u < 0 ? -1 : max(0, min(kKv4HalfTokens, L - u * kKv4HalfTokens));
+    r.tokens = u < 0 ? -1 : max(0, min(kPage, L - u * kPage));
     if (r.tokens <= 0) return r;
-    const int phys = kv4_phys(c, s, u >> 1);
-    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * Kv4Page<D>::BYTES + (u & 1);
+    const int phys = kv4_phys(c, s, u);
+    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * C::PAGE;
     return r;
   };
 
-  uint8_t* ring = sm + (size_t)grp * C::NS * C::HALF;
-  full += grp * C::NS;
-  Kv4Unit cur = look(u0 + lane), nxt = look(u0 + 32 + lane);
+  uint8_t* ring = sm + (size_t)pair * NS * C::PAGE;
+  full += pair * NS;
+  used += pair * NS;
   const int nu = u1 - u0;
+  Kv4Unit cur = look(u0 + lane), nxt{-1, -1, 0};
+  if (nu > 32) nxt = look(u0 + 32 + lane);
   int jl = 0;                     // next unit to copy
-  int is = 0, in_ring = 0;        // its ring entry; entries issued and not consumed
+  int is = 0, in_ring = 0;        // its ring entry; entries asked for and not consumed
+  int asked = 0;                  // pages asked for
   int cs = 0, cph = 0;            // entry to consume next, and its phase
   bool ok = true;
 
@@ -220,8 +241,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   float O[NT][DT][4], m[NT][NC], l[NT][NC], colfac[NT][NC], collow[NT][NC];
   int seg = -1, s_cur = 0, h_cur = 0, cb_cur = 0, rows_cur = 0;
   // the factor of a column, log2(e) scale / (power of two of its row), as hi + lo
-  const double lscale = (double)a.scale * 1.4426950408889634;
-  const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
+  const float lhi = geo.lhi, llo = geo.llo;
   // row (of the column block) of column col of tile x; query rows of the segment's KV head
   auto row_of = [&](int x, int col) { return x * C::RPT + (SPLIT ? col >> 1 : col); };
   auto locate = [&](int sg) {
@@ -297,7 +317,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       }
     }
   };
-  // The new rows, one after the other, in plain fp32: a lane has E dims of a key for the dot products, then the values of
+  // The new rows, a warp's every second, one after the other, in plain fp32: a lane has E dims of a key for the dot products, then the values of
   // its accumulators' dims.  A row that does not see the token is left out of everything, whatever the token holds.
   auto new_rows = [&]() {
     const int cnt = count_of(s_cur);
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     const T* vn = static_cast<const T*>(a.v.data) + s_cur * a.v.seq + h_cur * a.v.head + g;
     const int node0 = cb_cur * RB / geo.G, node1 = (cb_cur * RB + rows_cur - 1) / geo.G;  // the block's nodes
 #pragma unroll 1
-    for (int j = 0; j < cnt; ++j) {
+    for (int j = side; j < cnt; j += 2) {
       if (!a.mask && j > node1) break;
       float k[E], v[2 * DT];
 #pragma unroll
@@ -378,7 +398,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     }
   };
 
-  // The worker's part of a segment: with ml and out rows of these; without them the rows of the output.
+  // The warp's part of its segment.
   auto flush = [&](float2* ml, float* out) {
 #pragma unroll
     for (int x = 0; x < NT; ++x)
@@ -390,28 +410,21 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         sum += __shfl_xor_sync(FULL, sum, 16);
         const int r = row_of(x, 2 * t + y);
         if (r >= rows_cur) continue;
-        if (ml) {
-          if (g == 0) ml[r] = make_float2(m[x][y], sum);
-          float* o = out + r * D;
+        if (g == 0) ml[r] = make_float2(m[x][y], sum);
+        float* o = out + r * D;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            o[16 * d + g] = SPLIT ? O[x][d][0] + O[x][d][1] : O[x][d][y];
-            o[16 * d + g + 8] = SPLIT ? O[x][d][2] + O[x][d][3] : O[x][d][y + 2];
-          }
-        } else {
-          T* o = output(seg, r) + g;
-          const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            kv8_store(o + 16 * d, (SPLIT ? O[x][d][0] + O[x][d][1] : O[x][d][y]) * f);
-            kv8_store(o + 16 * d + 8, (SPLIT ? O[x][d][2] + O[x][d][3] : O[x][d][y + 2]) * f);
-          }
+        for (int d = 0; d < DT; ++d) {
+          o[16 * d + g] = SPLIT ? O[x][d][0] + O[x][d][1] : O[x][d][y];
+          o[16 * d + g + 8] = SPLIT ? O[x][d][2] + O[x][d][3] : O[x][d][y + 2];
         }
       }
   };
 
   // Half a page: S^T = K Q^T, softmax, O^T += V^T P^T.  The first `left` of its tokens are there.
-  auto half = [&](const uint8_t* pg, int left) {
+  auto half = [&](const uint8_t* page, int left) {
+    using P = Kv4Page<D>;
+    const uint8_t *keys = page + side * (16 * D), *values = keys + P::V;
+    const uint8_t *ksc = page + P::KS + side * D, *vsc = page + P::VS + side * D;
     float x[NT][2][4];  // two 16-token tiles
 #pragma unroll
     for (int z = 0; z < NT; ++z)
@@ -423,10 +436,10 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(pg + C::KS + (i * 8 + g) * 8);
+        const uint2 w = *reinterpret_cast<const uint2*>(ksc + (i * 8 + g) * 8);
         sw[i][0] = w.x, sw[i][1] = w.y;
       } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + C::KS + (i * 8 + g) * 4);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(ksc + (i * 8 + g) * 4);
         sw[i][0] = w, sw[i][1] = w >> 16;
       }
     }
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       uint32_t w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 w4 = reinterpret_cast<const uint4*>(pg)[(i * (D / 64) + j) * 32 + lane];
+        const uint4 w4 = reinterpret_cast<const uint4*>(keys)[(i * (D / 64) + j) * 32 + lane];
         w[i][0] = w4.x, w[i][1] = w4.y, w[i][2] = w4.z, w[i][3] = w4.w;
       }
 #pragma unroll
@@ -479,12 +492,14 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       if (SPLIT)
 #pragma unroll
         for (int i = 0; i < 2; ++i) x[z][i][0] += x[z][i][1], x[z][i][2] += x[z][i][3];  // hi + lo
-      if (left < 32)
+      if (left < 32) {
+        __syncwarp();  // a branch: as predicated instructions it would cost every half page its 16 selects
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = colfac[z][(e & 1) * (NC - 1)] < 0.0f ? INFINITY : -INFINITY;
+      }
       bool high = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -519,10 +534,23 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
           for (int e = y; e < 4; e += 2) {
             x[z][i][e] = SPLIT ? ex2(fmaf(x[z][i][e], collow[z][y], fmaf(x[z][i][e], colfac[z][y], -base))) * kP4Scale
                                : ex2(fmaf(x[z][i][e], colfac[z][y], 7.0f - base));
-            if (left < 32 && 16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = 0.0f;
-            l[z][y] += x[z][i][e];
           }
         }
+      }
+      if (left < 32) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int y = 0; y < NC; ++y)
+#pragma unroll
+          for (int e = y; e < 4; e += 2) l[z][y] += x[z][i][e];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float p = x[z][i][2 * e];
@@ -535,11 +563,12 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       uint32_t w[2][4], vs[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 w4 = reinterpret_cast<const uint4*>(pg + C::V)[(i * (D / 64) + j) * 32 + lane];
+        const uint4 w4 = reinterpret_cast<const uint4*>(values)[(i * (D / 64) + j) * 32 + lane];
         w[i][0] = w4.x, w[i][1] = w4.y, w[i][2] = w4.z, w[i][3] = w4.w;
-        const uint2 s2 = *reinterpret_cast<const uint2*>(pg + C::VS + (i * 4 + t) * (D / 8) + 8 * j);
+        const uint2 s2 = *reinterpret_cast<const uint2*>(vsc + (i * 4 + t) * (D / 8) + 8 * j);
         vs[i][0] = s2.x, vs[i][1] = s2.y;
         if (left < 32) {  // tokens that are not there: whatever their bytes hold, scale 0
+          __syncwarp();
           uint32_t keep = 0;
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -582,24 +611,22 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   };
 
   // ---- a segment's parts
-  struct Parts {
-    int w0, w1;       // workers of its first and last unit
-    int early, held;  // whether w1 goes on behind it (its part is then stored apart), CTAs that hold the others
-  };
   auto parts_of = [&](int sg) {
     const int cb = sg % geo.CB, h = sg / geo.CB % H, s = sg / geo.CB / H;
     const int per = units_of(len_of(s)), first = prefix[s] + (h * kv4_blocks(geo, count_of(s)) + cb) * per, end = first + per;
     Parts p;
+    p.seg = sg;
     p.w0 = worker_at(first), p.w1 = worker_at(end - 1);
     p.early = begin_of(p.w1 + 1) > end;
     p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / ng - p.w0 / ng + 1;
     return p;
   };
   auto rows_of = [&](int sg) { return min(RB, count_of(sg / geo.CB / H) * geo.G - sg % geo.CB * RB); };
-  // The parts first, first + step, .. of a segment's row, of the CTAs in their order, then the early one: maximum M,
+  // The parts first, first + step, .. of a segment's row, of the CTAs in their order, then the early ones: maximum M,
   // sum, and values of the lane's dims; B loads in flight.
+  const int slots = geo.ctas * geo.ng;
   auto gather = [&](const Parts& p, int r, int first, int step, float& M, float& sum, float (&o)[E]) {
-    const int n = p.held + p.early;
+    const int n = p.held + 2 * p.early, apart = p.held ? slots : 3 * slots;
     constexpr int B = 6;
     M = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -613,7 +640,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         ml[b] = make_float2(-INFINITY, 0.0f);
         v[b] = {};
         if (i < n) {
-          const size_t at = (i < p.held ? (size_t)max(p.w0, (p.w0 / ng + i) * ng) : (size_t)geo.ctas * geo.ng + p.w1) * RB + r;
+          const size_t at = (size_t)(i < p.held ? max(p.w0, (p.w0 / ng + i) * ng) : apart + 2 * p.w1 + i - p.held) * RB + r;
           ml[b] = __ldcg(ws.ml + at);
           v[b] = __ldcg(reinterpret_cast<const Vec*>(ws.o + at * D + E * lane));
         }
@@ -640,35 +667,32 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 #pragma unroll
     for (int e = 0; e < E; ++e) kv8_store(to + e, sum == 0.0f ? 0.0f : o[e] / sum);
   };
-  // Whether the part that the CTA's or the warp's other threads have stored, ordered before this thread, was the segment's last.
-  auto is_last = [&](const Parts& p) {
-    __threadfence();
-    if (atomicAdd(ws.ticket + p.w0, 1) != p.held + p.early - 1) return false;
-    ws.ticket[p.w0] = 0;  // for the next call
-    __threadfence();
-    return true;
-  };
-  // The worker's segment ends in front of others of its range.
+  // The pair's segment ends in front of others of its range.
   auto finish = [&]() {
     const Parts p = parts_of(seg);
-    if (p.held == 0) {
-      flush(nullptr, nullptr);
+    const size_t at = (size_t)((p.held ? slots : 3 * slots) + 2 * worker + side) * RB;
+    flush(ws.ml + at, ws.o + at * D);
+    if (p.held) {  // joined with the other parts in the end
+      if (side == 0 && lane == 0) sparts[NG + pair] = p;
       return;
     }
-    const size_t at = ((size_t)geo.ctas * geo.ng + worker) * RB;
-    flush(ws.ml + at, ws.o + at * D);
-    __syncwarp();
-    int last = 0;
-    if (lane == 0) last = is_last(p);
-    if (!__shfl_sync(FULL, last, 0)) return;
-    for (int r = 0; r < rows_cur; ++r) {
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); };
+    meet();
+    for (int r = side; r < rows_cur; r += 2) {
       float M, sum, o[E];
       gather(p, r, 0, 1, M, sum, o);
       store(output(seg, r) + E * lane, sum, o);
     }
+    meet();  // the place is free again
   };
 
   // ---- the range
+  // whether the pair's other warp has been here before, and is done with what this one is done with
+  auto second = [&](unsigned* n) {
+    unsigned old;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(old) : "r"(smem_u32(n)) : "memory");
+    return (old & 1u) != 0;
+  };
 #pragma unroll 1
   for (int j = 0, cbase = 0; j < nu; ++j) {
     if (j - cbase == 32) {
@@ -676,25 +700,18 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       cur = nxt;
       nxt = look(u0 + cbase + 32 + lane);
     }
-    // copy ahead as far as the ring and the two batches of units allow
-    while (ok && in_ring < C::NS && jl < nu && jl < cbase + 64) {
+    // copy ahead as far as the ring and the two batches of units allow; the second of the pair to come here fills an entry
+    while (ok && in_ring < NS && jl < nu && jl < cbase + 64) {
       const int64_t from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
       ++jl;
       if (from < 0) continue;
-      if (lane == 0) {
-        mbar_expect_tx(&full[is], C::HALF);
-        if (geo.withheld != (int)blockIdx.x) {
-          const int y = (int)(from & 1);
-          const uint8_t* page = c.pages + (from - y);
-          uint8_t* to = ring + (size_t)is * C::HALF;
-          bulk_g2s(to, page + 16 * D * y, 16 * D, &full[is]);
-          bulk_g2s(to + C::V, page + Kv4Page<D>::V + 16 * D * y, 16 * D, &full[is]);
-          bulk_g2s(to + C::KS, page + Kv4Page<D>::KS + D * y, D, &full[is]);
-          bulk_g2s(to + C::VS, page + Kv4Page<D>::VS + D * y, D, &full[is]);
-        }
+      if (lane == 0 && (asked < NS ? side == 0 : second(&used[is]))) {
+        mbar_expect_tx(&full[is], C::PAGE);
+        if (geo.withheld != (int)blockIdx.x) bulk_g2s(ring + (size_t)is * C::PAGE, c.pages + from, C::PAGE, &full[is]);
       }
+      ++asked;
       ++in_ring;
-      if (++is == C::NS) is = 0;
+      if (++is == NS) is = 0;
     }
     const int src = j - cbase;
     const int64_t from = __shfl_sync(FULL, cur.src, src);
@@ -707,9 +724,10 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     if (from < 0 || !ok) continue;
     ok = __all_sync(FULL, mbar_wait(&full[cs], cph, geo.wait_ns));
     if (ok) {
-      half(ring + (size_t)cs * C::HALF, tokens);
+      const int left = tokens - side * kKv4HalfTokens;
+      if (left > 0) half(ring + (size_t)cs * C::PAGE, left);
       __syncwarp();
-      if (++cs == C::NS) cs = 0, cph ^= 1;
+      if (++cs == NS) cs = 0, cph ^= 1;
       --in_ring;
       continue;
     }
@@ -721,113 +739,144 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       for (int y = 0; y < NC; ++y) l[x][y] = NAN;
     for (; in_ring > 0; --in_ring) {
       (void)mbar_wait(&full[cs], cph, geo.wait_ns);
-      if (++cs == C::NS) cs = 0, cph ^= 1;
+      if (++cs == NS) cs = 0, cph ^= 1;
     }
   }
-  // ---- the workers' last parts, in the ring's place, and of each run of workers on one segment the sum
+  // ---- the warps' last parts, in the ring's place, and of each run of warps on one segment the sum
   float2* sml = reinterpret_cast<float2*>(sm);                // [NG][RB]
-  int* sseg = reinterpret_cast<int*>(sml + NG * RB);          // [NG], -1: none
-  float* sfac = reinterpret_cast<float*>(sseg + NG);          // [NG][RB] factor of a worker's part in its run
-  float* so = reinterpret_cast<float*>(sm) + ((NG * (3 * RB + 1) + 31) & ~31);  // [NG][RB][D]
+  float* sfac = reinterpret_cast<float*>(sml + NG * RB);      // [NG][RB] factor of a warp's part in its run
+  float* so = sfac + NG * RB;                                 // [NG][RB][D]
   float* jo = so + NG * RB * D;                               // [NG][D], of the join
   float2* jml = reinterpret_cast<float2*>(jo + NG * D);       // [NG]
-  static_assert((((NG * (3 * RB + 1) + 31) & ~31) + NG * (RB + 1) * D + 2 * NG) * 4 <= kKv4RingBytes, "parts");
+  static_assert((NG * RB * (3 + D) + NG * D + 2 * NG) * 4 <= kKv4RingBytes, "parts");
+  if (seg >= 0) {
+    const Parts p = parts_of(seg);
+    if (lane == 0) sparts[grp] = p;
+  }
   __syncthreads();
-  if (lane == 0) sseg[grp] = seg;
   if (seg >= 0) flush(sml + grp * RB, so + grp * RB * D);
   __syncthreads();
-  for (int x = tid; x < NG * RB; x += C::THREADS) {
-    const int i = x / RB, sg = sseg[i];
-    if (sg < 0 || x % RB >= rows_of(sg)) continue;
+  const int mine = lane < NG ? sparts[lane].seg : -1, before = __shfl_up_sync(FULL, mine, 1);
+  const unsigned heads = __ballot_sync(FULL, mine >= 0 && (lane == 0 || mine != before));  // first warps of the runs
+  const unsigned warps = __ballot_sync(FULL, mine >= 0);  // warps with a part: the first ones
+  const int busy = __popc(warps);
+  auto run_end = [&](int i) {  // of the run that begins with warp i
+    const unsigned later = heads & (0xfffffffeu << i);
+    return later ? __ffs(later) - 1 : busy;
+  };
+  for (int x = tid; x < busy * RB; x += C::THREADS) {
+    const int i = x / RB, i0 = 31 - __clz(heads & (0xffffffffu >> (31 - i))), i1 = run_end(i0);
+    if (x % RB >= rows_of(sparts[i].seg)) continue;
     float M = -INFINITY;
-#pragma unroll
-    for (int y = 0; y < NG; ++y) M = sseg[y] == sg ? fmaxf(M, sml[y * RB + x % RB].x) : M;
+    for (int y = i0; y < i1; ++y) M = fmaxf(M, sml[y * RB + x % RB].x);
     sfac[x] = ex2(sml[x].x - (M == -INFINITY ? 0.0f : M));
   }
   __syncthreads();
-  for (int i0 = 0; i0 < NG;) {
-    const int sg = sseg[i0];
-    int i1 = i0 + 1;
-    while (i1 < NG && sseg[i1] == sg) ++i1;
-    if (sg >= 0) {
-      const Parts p = parts_of(sg);
-      const bool alone = p.held + p.early == 1;
-      const int rows = rows_of(sg);
-      const size_t at = ((size_t)blockIdx.x * ng + i0) * RB;
-      for (int x = tid; x < rows * (D / 4); x += C::THREADS) {
-        const int r = x / (D / 4), d = x % (D / 4);
-        float M = -INFINITY, L = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int x = tid; x < __popc(heads) * (RB * D / 4); x += C::THREADS) {
+    unsigned rest = heads;
+    for (int k = x / (RB * D / 4); k > 0; --k) rest &= rest - 1;
+    const int i0 = __ffs(rest) - 1, i1 = run_end(i0), r = x / (D / 4) % RB, d = x % (D / 4);
+    const Parts& p = sparts[i0];
+    if (r >= rows_of(p.seg)) continue;
+    float M = -INFINITY, L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int i = i0; i < i1; ++i) {
-          const float2 ml = sml[i * RB + r];
-          const float4 o = reinterpret_cast<const float4*>(so + (i * RB + r) * D)[d];
-          const float f = sfac[i * RB + r];
-          M = fmaxf(M, ml.x);
-          L = fmaf(ml.y, f, L);
-          v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
-        }
-        if (alone) {
-          T* out = output(sg, r) + 4 * d;
-          kv8_store(out, L == 0.0f ? 0.0f : v.x / L), kv8_store(out + 1, L == 0.0f ? 0.0f : v.y / L);
-          kv8_store(out + 2, L == 0.0f ? 0.0f : v.z / L), kv8_store(out + 3, L == 0.0f ? 0.0f : v.w / L);
-        } else {
-          reinterpret_cast<float4*>(ws.o + (at + r) * D)[d] = v;
-          if (d == 0) ws.ml[at + r] = make_float2(M, L);
-        }
-      }
-      if (!alone) {
-        __syncthreads();
-        if (tid == 0) last_part = is_last(p);
-        __syncthreads();
-        if (last_part) {  // a row to `per` warps, then their sums
-          int per = NG;
-          while (per > 1 && NG / per < rows) per >>= 1;
-          for (int r0 = 0; r0 < rows; r0 += NG / per) {
-            const int r = r0 + grp / per;
-            float M = -INFINITY, sum = 0.0f, o[E] = {};
-            if (r < rows) gather(p, r, grp % per, per, M, sum, o);
-            if (per > 1) {
-              if (lane == 0) jml[grp] = make_float2(M, sum);
-              *reinterpret_cast<Vec*>(jo + grp * D + E * lane) = *reinterpret_cast<Vec*>(o);
-              __syncthreads();
-              if (grp % per == 0) {
-                float top = M;
-                for (int y = 1; y < per; ++y) top = fmaxf(top, jml[grp + y].x);
-                const float base = top == -INFINITY ? 0.0f : top;
-                float f = ex2(M - base);
-                sum *= f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] *= f;
-                for (int y = 1; y < per; ++y) {
-                  f = ex2(jml[grp + y].x - base);
-                  sum = fmaf(jml[grp + y].y, f, sum);
-#pragma unroll
-                  for (int e = 0; e < E; ++e) o[e] = fmaf(jo[(grp + y) * D + E * lane + e], f, o[e]);
-                }
-              }
-            }
-            if (r < rows && grp % per == 0) store(output(sg, r) + E * lane, sum, o);
-            if (per > 1) __syncthreads();
-          }
-        }
+    for (int i = i0; i < i1; ++i) {
+      const float2 ml = sml[i * RB + r];
+      const float4 o = reinterpret_cast<const float4*>(so + (i * RB + r) * D)[d];
+      const float f = sfac[i * RB + r];
+      M = fmaxf(M, ml.x);
+      L = fmaf(ml.y, f, L);
+      v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+    }
+    if (p.held + p.early == 1) {  // the only part
+      T* out = output(p.seg, r) + 4 * d;
+      kv8_store(out, L == 0.0f ? 0.0f : v.x / L), kv8_store(out + 1, L == 0.0f ? 0.0f : v.y / L);
+      kv8_store(out + 2, L == 0.0f ? 0.0f : v.z / L), kv8_store(out + 3, L == 0.0f ? 0.0f : v.w / L);
+    } else {
+      const size_t at = (size_t)(blockIdx.x * ng + i0 / 2) * RB + r;
+      reinterpret_cast<float4*>(ws.o + at * D)[d] = v;
+      if (d == 0) ws.ml[at] = make_float2(M, L);
+    }
+  }
+  // the parts that other CTAs' are joined with: a ticket each, and the CTA that draws a segment's last joins it
+  __syncthreads();
+  if (grp == 0) {
+    const bool part = lane < NG ? heads >> lane & 1u : lane < NG + NP && sparts[lane].seg >= 0;
+    bool last = false;
+    if (part) {
+      const Parts& p = sparts[lane];
+      const int all = p.held + p.early;
+      if (all > 1) {
+        int old;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(ws.ticket + p.w0) : "memory");
+        last = old == all - 1;
+        if (last) ws.ticket[p.w0] = 0;  // for the next call
       }
     }
-    i0 = i1;
+    const unsigned which = __ballot_sync(FULL, last);
+    if (last) joins[__popc(which & ((1u << lane) - 1))] = lane;
+    if (lane == 0) n_joins = __popc(which);
+  }
+  __syncthreads();
+  // Warps of a row: by the number of its parts, so that the order of a sum does not depend on which CTA draws what.
+  const int rows = min(RB, geo.R);
+  auto split_of = [&](const Parts& p) {
+    int per = 1;
+    while (per * 6 < p.held + 2 * p.early && 2 * per * rows <= NG) per *= 2;
+    return per;
+  };
+  for (int x = grp; x < n_joins * rows; x += NG) {
+    const Parts p = sparts[joins[x / rows]];
+    const int r = x % rows;
+    if (split_of(p) > 1 || r >= rows_of(p.seg)) continue;
+    float M, sum, o[E];
+    gather(p, r, 0, 1, M, sum, o);
+    store(output(p.seg, r) + E * lane, sum, o);
+  }
+  for (int k = 0; k < n_joins; ++k) {
+    const Parts p = sparts[joins[k]];
+    const int per = split_of(p), r = grp / per;  // NG / per >= rows
+    if (per == 1) continue;
+    const bool on = r < rows_of(p.seg);
+    float M, sum, o[E];
+    if (on) {
+      gather(p, r, grp % per, per, M, sum, o);
+      if (lane == 0) jml[grp] = make_float2(M, sum);
+      *reinterpret_cast<Vec*>(jo + grp * D + E * lane) = *reinterpret_cast<Vec*>(o);
+    }
+    __syncthreads();
+    if (on && grp % per == 0) {
+      float top = M;
+      for (int y = 1; y < per; ++y) top = fmaxf(top, jml[grp + y].x);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float f = ex2(M - base);
+      sum *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      for (int y = 1; y < per; ++y) {
+        f = ex2(jml[grp + y].x - base);
+        sum = fmaf(jml[grp + y].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(jo[(grp + y) * D + E * lane + e], f, o[e]);
+      }
+      store(output(p.seg, r) + E * lane, sum, o);
+    }
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------- launch
 
 inline size_t kv4_split_smem(int S, int entries) {
-  return (size_t)kKv4RingBytes + 8 * (size_t)entries + 4 * ((size_t)S + 1 + (S < kKv4Lens ? S : kKv4Lens));
+  return (size_t)kKv4RingBytes + 12 * (size_t)entries + 4 * ((size_t)S + 1 + (S < kKv4Lens ? S : kKv4Lens));
 }
 
 template <typename T, int D, int NT>
 cudaError_t kv4_split_launch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo, const Kv4Scratch& ws,
                              cudaStream_t st) {
   using C = Kv4Split<T, D, NT>;
-  const size_t most = kv4_split_smem(kKv8MaxSeqs, C::NG * C::NS), smem = kv4_split_smem(c.n_seqs, C::NG * C::NS);
+  const size_t most = kv4_split_smem(kKv8MaxSeqs, C::NP * C::NS), smem = kv4_split_smem(c.n_seqs, C::NP * C::NS);
   cudaError_t e = kv8_smem<k_kv4_split<T, D, NT>>(most);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_kv4_split<T, D, NT>, dim3((unsigned)geo.ctas), dim3(C::THREADS), smem, st, c, a, geo, ws);

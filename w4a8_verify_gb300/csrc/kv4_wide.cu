@@ -326,8 +326,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
     Turn<kFac> fb;
     int n = 0, runs = 0, freed = 0;  // pages and runs done; S buffers released to the products (page n needs n + 1 of them)
     // the logit's factor is not negative (Q takes the scale's sign), so the largest logit is the largest S
-    const double lscale = fabs((double)a.scale) * 1.4426950408889634;
-    const float lhi = (float)lscale, llo = (float)(lscale - (double)lhi);
+    const float lhi = fabsf(geo.lhi), llo = a.scale < 0.0f ? -geo.llo : geo.llo;
     for (int x = u0; x < u1 && ok;) {
       const Run r = run_at(x);
       const int rows = rows_of(r);
