@@ -137,6 +137,12 @@ __device__ __forceinline__ uint32_t kv4_scale_pair(uint32_t w, int i, int j) {
   return __byte_perm(w, 0, 0x4040 | i | j << 8) << 7;
 }
 
+// A pair of half h of w
+__device__ __forceinline__ uint32_t twice(uint32_t w, int h) {
+  const __half2 p = *reinterpret_cast<const __half2*>(&w), r = h ? __high2half2(p) : __low2half2(p);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // ---------------------------------------------------------------------------- the split kernel
 
 template <typename T, int D, int NT>
@@ -155,9 +161,8 @@ struct Kv4Split {
 
 // What a lane knows of one unit of its worker's range.
 struct Kv4Unit {
-  int64_t src;  // byte offset of the page in the pool, or -1: nothing to read
-  int seg;      // segment
-  int tokens;   // of the page; -1: the unit of the new rows
+  int page;  // number of the (page, head) in the pool, or -1: nothing to read
+  int what;  // segment, and in the low seven bits the tokens of the page plus 1; 0 there: the unit of the new rows
 };
 
 template <typename T, int D, int NT>
@@ -212,15 +217,15 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 
   // The lane's unit x (32 units in parallel, so the table's latency is paid once).
   auto look = [&](int x) -> Kv4Unit {
-    Kv4Unit r{-1, -1, 0};
+    Kv4Unit r{-1, 0};
     if (x >= u1) return r;
     const int s = kv4_seq_of(prefix, S, x), L = len_of(s), blocks = kv4_blocks(geo, count_of(s));
     const int per = units_of(L), q = (x - prefix[s]) / per, u = (x - prefix[s]) % per - fresh;
-    r.seg = (s * H + q / blocks) * geo.CB + q % blocks;
-    r.tokens = u < 0 ? -1 : max(0, min(kPage, L - u * kPage));
-    if (r.tokens <= 0) return r;
+    const int tokens = u < 0 ? -1 : max(0, min(kPage, L - u * kPage));
+    r.what = ((s * H + q / blocks) * geo.CB + q % blocks) << 7 | (tokens + 1);
+    if (tokens <= 0) return r;
     const int phys = kv4_phys(c, s, u);
-    if (phys >= 0) r.src = ((int64_t)phys * H + q / blocks) * C::PAGE;
+    if (phys >= 0) r.page = phys * H + q / blocks;
     return r;
   };
 
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   full += pair * NS;
   used += pair * NS;
   const int nu = u1 - u0;
-  Kv4Unit cur = look(u0 + lane), nxt{-1, -1, 0};
+  Kv4Unit cur = look(u0 + lane), nxt{-1, 0};
   if (nu > 32) nxt = look(u0 + 32 + lane);
   int jl = 0;                     // next unit to copy
   int is = 0, in_ring = 0;        // its ring entry; entries asked for and not consumed
@@ -238,10 +243,11 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 
   // ---- state of the segment
   uint32_t qf[NT][KS][2];
-  float O[NT][DT][4], m[NT][NC], l[NT][NC], colfac[NT][NC], collow[NT][NC];
+  // m and most: the row's maximum, and the product S that would pass it by the slack (the factors are not negative)
+  float O[NT][DT][4], m[NT][NC], most[NT][NC], l[NT][NC], colfac[NT][NC], collow[NT][NC];
   int seg = -1, s_cur = 0, h_cur = 0, cb_cur = 0, rows_cur = 0;
-  // the factor of a column, log2(e) scale / (power of two of its row), as hi + lo
-  const float lhi = geo.lhi, llo = geo.llo;
+  // the factor of a column, log2(e) |scale| / (power of two of its row), as hi + lo; q takes the scale's sign
+  const float lhi = fabsf(geo.lhi), llo = a.scale < 0.0f ? -geo.llo : geo.llo;
   // row (of the column block) of column col of tile x; query rows of the segment's KV head
   auto row_of = [&](int x, int col) { return x * C::RPT + (SPLIT ? col >> 1 : col); };
   auto locate = [&](int sg) {
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) O[x][d][e] = 0.0f;
 #pragma unroll
-      for (int y = 0; y < NC; ++y) m[x][y] = -INFINITY, l[x][y] = ok ? 0.0f : NAN;
+      for (int y = 0; y < NC; ++y) m[x][y] = most[x][y] = -INFINITY, l[x][y] = ok ? 0.0f : NAN;
       const int r = row_of(x, g);
       float v[KS * 4];
       if (r < rows_cur) {
@@ -295,13 +301,13 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       for (int y = 0; y < KS * 4; ++y) am = max_nan(am, fabsf(v[y]));
       am = max_nan(am, __shfl_xor_sync(FULL, am, 1));
       am = max_nan(am, __shfl_xor_sync(FULL, am, 2));
-      const float up = f16_scale(am);
+      const float up = f16_scale(am), sup = a.scale < 0.0f ? -up : up;
 #pragma unroll
       for (int y = 0; y < KS; ++y) {
         float f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          f[e] = v[4 * y + e] * up;
+          f[e] = v[4 * y + e] * sup;
           if (SPLIT) f[e] = g & 1 ? f[e] - rintf(f[e]) : rintf(f[e]);
         }
         qf[x][y][0] = pack_f16(f[0], f[1]);
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
           const int row = row_of(x, 2 * t + y);
-          s[y] = __shfl_sync(FULL, dot[0], (32 / C::RPT) * (SPLIT ? t : 2 * t + y)) * lhi;
+          s[y] = __shfl_sync(FULL, dot[0], (32 / C::RPT) * (SPLIT ? t : 2 * t + y)) * geo.lhi;
           see[y] = row < rows_cur;
           if (see[y]) {
             const int node = node0 == node1 ? node0 : (cb_cur * RB + row) / geo.G;
@@ -376,6 +382,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
             const float mx = see[y] ? fmaxf(m[x][y], s[y]) : m[x][y];
             cc[y] = mx == -INFINITY ? 1.0f : ex2(m[x][y] - mx);
             m[x][y] = mx;
+            most[x][y] = __fdividef(mx + kP4Slack, colfac[x][y]);
             l[x][y] *= cc[y];
           }
 #pragma unroll
@@ -432,16 +439,20 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[z][i][e] = 0.0f;
-    uint32_t sw[2][2];  // scale bytes of tokens g and g + 8 of the tiles
+    // scales of tokens g and g + 8 of the tiles as f16 pairs: of groups 0 and 2, of groups 1 and 3 (D = 64: of group 0 of
+    // either token, of group 1)
+    uint32_t sc[2][2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      uint32_t w[2];
       if (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(ksc + (i * 8 + g) * 8);
-        sw[i][0] = w.x, sw[i][1] = w.y;
+        const uint2 w2 = *reinterpret_cast<const uint2*>(ksc + (i * 8 + g) * 8);
+        w[0] = w2.x, w[1] = w2.y;
       } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(ksc + (i * 8 + g) * 4);
-        sw[i][0] = w, sw[i][1] = w >> 16;
+        w[0] = w[1] = *reinterpret_cast<const uint32_t*>(ksc + (i * 8 + g) * 4);
       }
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y) sc[i][y][0] = w[y] << 7 & 0x7f807f80u, sc[i][y][1] = w[y] >> 1 & 0x7f807f80u;
     }
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
@@ -458,7 +469,8 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         uint32_t s0[2], s1[2], b0[2], b1[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          s0[i] = kv4_scale_pair(sw[i][0], gr, gr), s1[i] = kv4_scale_pair(sw[i][1], gr, gr);
+          s0[i] = D == 128 ? twice(sc[i][0][kh], j) : twice(sc[i][0][kh], 0);
+          s1[i] = D == 128 ? twice(sc[i][1][kh], j) : twice(sc[i][0][kh], 1);
           b0[i] = mul_h2(s0[i], kMinus264), b1[i] = mul_h2(s1[i], kMinus24);
 #pragma unroll
           for (int z = 0; z < NT; ++z)
@@ -498,26 +510,27 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = colfac[z][(e & 1) * (NC - 1)] < 0.0f ? INFINITY : -INFINITY;
+            if (16 * i + g + 8 * (e >> 1) >= left) x[z][i][e] = -INFINITY;
       }
       bool high = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int y = 0; y < NC; ++y)
-          high = high || x[z][i][y] * colfac[z][y] > m[z][y] + kP4Slack || x[z][i][y + 2] * colfac[z][y] > m[z][y] + kP4Slack;
+          high = high || x[z][i][y] > most[z][y] || x[z][i][y + 2] > most[z][y];
       if (__any_sync(FULL, high)) {
         float cc[NC];
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
           const float f = colfac[z][y];
-          float mx = fmaxf(fmaxf(x[z][0][y] * f, x[z][0][y + 2] * f), fmaxf(x[z][1][y] * f, x[z][1][y + 2] * f));
+          float mx = fmaxf(fmaxf(x[z][0][y], x[z][0][y + 2]), fmaxf(x[z][1][y], x[z][1][y + 2])) * f;
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
           mx = fmaxf(mx, m[z][y]);
           cc[y] = mx == -INFINITY ? 1.0f : ex2(m[z][y] - mx);
           m[z][y] = mx;
+          most[z][y] = __fdividef(mx + kP4Slack, f);
           l[z][y] *= cc[y];
         }
 #pragma unroll
@@ -702,20 +715,19 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     }
     // copy ahead as far as the ring and the two batches of units allow; the second of the pair to come here fills an entry
     while (ok && in_ring < NS && jl < nu && jl < cbase + 64) {
-      const int64_t from = __shfl_sync(FULL, jl < cbase + 32 ? cur.src : nxt.src, (jl - cbase) & 31);
+      const int from = __shfl_sync(FULL, jl < cbase + 32 ? cur.page : nxt.page, (jl - cbase) & 31);
       ++jl;
       if (from < 0) continue;
       if (lane == 0 && (asked < NS ? side == 0 : second(&used[is]))) {
         mbar_expect_tx(&full[is], C::PAGE);
-        if (geo.withheld != (int)blockIdx.x) bulk_g2s(ring + (size_t)is * C::PAGE, c.pages + from, C::PAGE, &full[is]);
+        if (geo.withheld != (int)blockIdx.x) bulk_g2s(ring + is * C::PAGE, c.pages + (size_t)from * C::PAGE, C::PAGE, &full[is]);
       }
       ++asked;
       ++in_ring;
       if (++is == NS) is = 0;
     }
-    const int src = j - cbase;
-    const int64_t from = __shfl_sync(FULL, cur.src, src);
-    const int sg = __shfl_sync(FULL, cur.seg, src), tokens = __shfl_sync(FULL, cur.tokens, src);
+    const int from = __shfl_sync(FULL, cur.page, j - cbase), what = __shfl_sync(FULL, cur.what, j - cbase);
+    const int sg = what >> 7, tokens = (what & 127) - 1;
     if (sg != seg) {
       if (seg >= 0) finish();
       begin(sg);
@@ -725,7 +737,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     ok = __all_sync(FULL, mbar_wait(&full[cs], cph, geo.wait_ns));
     if (ok) {
       const int left = tokens - side * kKv4HalfTokens;
-      if (left > 0) half(ring + (size_t)cs * C::PAGE, left);
+      if (left > 0) half(ring + cs * C::PAGE, left);
       __syncwarp();
       if (++cs == NS) cs = 0, cph ^= 1;
       --in_ring;
