@@ -100,4 +100,11 @@ __device__ __forceinline__ uint32_t kv4_unturn(uint32_t two) {
   return (two >> 2 & 0x3fff3fffu) | (two << 14 & 0xc000c000u);
 }
 
+// (a & b) | c as one instruction: two immediates would make two of it
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 }  // namespace w4a8

@@ -111,12 +111,6 @@ __device__ __forceinline__ int kv4_seq_of(const int* prefix, int S, int x) {
   return lo;
 }
 
-// (a & b) | c as one instruction: two immediates would make two of it
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
 // Two f16 numbers of the fields of two words at bits 2..5 (256 + u) or 6..9 (16 + u).
 __device__ __forceinline__ uint32_t kv4_f16_low(uint32_t w) { return and_or(w, 0x003c003cu, 0x5c005c00u); }
 __device__ __forceinline__ uint32_t kv4_f16_high(uint32_t w) { return and_or(w, 0x03c003c0u, 0x4c004c00u); }

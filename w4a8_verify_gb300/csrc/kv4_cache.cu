@@ -41,50 +41,54 @@ __device__ bool append_index_ok(const w4a8_kv4_cache& c, const int32_t* index, i
   return ok;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int wide, float (&x)[8]) {
-  if (wide) {
-    uint4 u[sizeof(T) / 2];
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = kv8_load(reinterpret_cast<const T*>(u) + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = kv8_load(p + i);
-  }
-}
+// Largest magnitude of N vectors of eight elements; NaN where one is among them.
 template <int N>
-__device__ __forceinline__ float largest(const float (&x)[N]) {
+__device__ __forceinline__ float largest(const Eight<float> (&x)[N]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = max_nan(m, fabsf(x[i]));
+  for (int i = 0; i < 8 * N; ++i) m = max_nan(m, fabsf(reinterpret_cast<const float*>(x)[i]));
   return m;
 }
-// Codes + 8 (in the low four bits; others are not cleared) of N values of a group of largest magnitude amax at scale s:
-// rint of the IEEE quotient without a division.  f = rint(x fl(1 / s)) is the nearest whole number or, close to a half,
-// its neighbour; x - f s is exact (f s has seven bits), so comparing it with s / 2 decides: x and s / 2 odd multiples
-// are a unit of x apart at least, which the quotient's rounding keeps on its side.  Adding 1.5 2^23 + 8 makes a whole
-// number in the low bits, ties to even.
 template <int N>
-__device__ __forceinline__ void codes(const float (&x)[N], float amax, float s, uint32_t (&u)[N]) {
+__device__ __forceinline__ float largest(const Eight<__nv_bfloat16> (&x)[N]) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(x);
+  __nv_bfloat162 m = __habs2(p[0]);
+#pragma unroll
+  for (int i = 1; i < 4 * N; ++i) m = __hmax2_nan(m, __habs2(p[i]));
+  return max_nan(__low2float(m), __high2float(m));
+}
+
+// Codes are held as the bits of the fp32 number 1.5 2^23 + 8 + code: adding that constant makes a whole number, ties to
+// even, in the low bits.  A word of eight fields is then a sum of products (kFields takes the constant's bits out).
+constexpr float kMagic = 12582920.0f;
+constexpr uint32_t kMagicBits = 0x4b400000u, kFields = 0u - kMagicBits * 0x11111111u;
+
+// Scale of a group, its byte, and the codes of N of its values.
+//
+// fp32: rint of the IEEE quotient without a division.  f = rint(x fl(1 / s)) is the nearest whole number or, close to a half,
+// its neighbour; x - f s is exact (f s has seven bits), so comparing it with s / 2 decides: x and s / 2 odd multiples
+// are a unit of x apart at least, which the quotient's rounding keeps on its side.
+template <int N>
+__device__ __forceinline__ uint32_t quantise(const Eight<float> (&v)[N], float amax, uint32_t (&u)[8 * N]) {
+  const float* x = reinterpret_cast<const float*>(v);
+  uint32_t byte;
+  const float s = kv4_scale(amax, byte);
   if (!(s > 0.0f)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = 8;
-    return;
+    for (int i = 0; i < 8 * N; ++i) u[i] = kMagicBits + 8;
+    return byte;
   }
-  constexpr float kMagic = 12582920.0f;
   const float inv = __fdividef(1.0f, s), half = 0.5f * s, top = 7.0f * s;
   float off = amax > 7.4375f * s ? half : 0.0f;  // the largest scale and the smallest ones: some are clamped
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 8 * N; ++i) {
     const float r = fmaf(x[i], inv, kMagic);
     off = fmaxf(off, fabsf(fmaf(-__fadd_rn(r, -kMagic), s, x[i])));
     u[i] = __float_as_uint(r);
   }
   if (off >= half) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 8 * N; ++i) {
       const float y = fminf(fmaxf(x[i], -top), top);
       const float r = fmaf(y, inv, kMagic), f = __fadd_rn(r, -kMagic);
       const float d = fmaf(-f, s, y);
@@ -92,6 +96,43 @@ __device__ __forceinline__ void codes(const float (&x)[N], float amax, float s, 
       u[i] = __float_as_uint(over ? __fadd_rn(r, copysignf(1.0f, d)) : r);
     }
   }
+  return byte;
+}
+// bf16: a value of eight bits over a scale of four is exactly half way between two codes (one value in a hundred is), or
+// 2^-9 of itself away from there and more.  So both neighbours of a half are found, by factors 2^-20 below and above 1 / s, and
+// the even one is taken; elsewhere they are the same.  The scale, to four bits, of a largest magnitude over 7 likewise.
+template <int N>
+__device__ __forceinline__ uint32_t quantise(const Eight<__nv_bfloat16> (&v)[N], float amax, uint32_t (&u)[8 * N]) {
+  constexpr float kBelow = 0.99999904632568359375f, kAbove = 1.00000095367431640625f;  // 1 -+ 2^-20
+  float s;
+  uint32_t byte;
+  if (amax > 5e-4f && amax < 1670.0f) {  // normal scales below the largest: 7 2^-14, 7 240
+    const uint32_t a = (__float_as_uint(amax * (kBelow / 7.0f)) + 0x80000u) >> 20;
+    const uint32_t b = (__float_as_uint(amax * (kAbove / 7.0f)) + 0x80000u) >> 20, t = a & 1u ? b : a;
+    byte = t - (112u << 3);
+    s = __uint_as_float(t << 20);
+  } else {
+    s = kv4_scale(amax, byte);
+  }
+  if (!(s > 0.0f)) {
+#pragma unroll
+    for (int i = 0; i < 8 * N; ++i) u[i] = kMagicBits + 8;
+    return byte;
+  }
+  float x[8 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i].get(*reinterpret_cast<float(*)[8]>(x + 8 * i));
+  if (amax > 7.4375f * s) {  // the largest scale and the smallest ones: some are clamped
+#pragma unroll
+    for (int i = 0; i < 8 * N; ++i) x[i] = fminf(fmaxf(x[i], -7.0f * s), 7.0f * s);
+  }
+  const float inv = __fdividef(1.0f, s), below = inv * kBelow, above = inv * kAbove;
+#pragma unroll
+  for (int i = 0; i < 8 * N; ++i) {
+    const uint32_t a = __float_as_uint(fmaf(x[i], below, kMagic)), b = __float_as_uint(fmaf(x[i], above, kMagic));
+    u[i] = a & 1u ? b : a;
+  }
+  return byte;
 }
 
 // Keys: lane (g, t) has tokens g and g + 8, dims 8 t .. 8 t + 7 of each group: two words of the page order, whole.
@@ -100,16 +141,15 @@ __device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const
   const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
   uint32_t scale[2][D / 32];
   const uint32_t keep = kv4_turn((is_new[0] ? 0u : 0x0f0f0f0fu) | (is_new[1] ? 0u : 0xf0f0f0f0u));
-  float x[D / 32][2][8];  // every load on its way
+  Eight<T> x[D / 32][2][1];  // every load on its way
 #pragma unroll
   for (int k = 0; k < D / 32; ++k)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (is_new[i]) {
-        load8(row[i] + 32 * k + 8 * t, wide, x[k][i]);
+        x[k][i][0].load(row[i] + 32 * k + 8 * t, wide);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][i][e] = 0.0f;
+        x[k][i][0] = Eight<T>{};
       }
     }
 #pragma unroll
@@ -123,15 +163,15 @@ __device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const
         float m = largest(x[2 * j + kh][i]);
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        codes(x[2 * j + kh][i], m, kv4_scale(m, scale[i][2 * j + kh]), u[i]);
+        scale[i][2 * j + kh] = quantise(x[2 * j + kh][i], m, u[i]);
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        uint32_t nat = 0;
+        uint32_t nat = kFields;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) nat |= (u[i][4 * p + e] & 15u) << (16 * (e & 1) + 8 * (e >> 1) + 4 * i);
+          for (int i = 0; i < 2; ++i) nat += u[i][4 * p + e] * (1u << (16 * (e & 1) + 8 * (e >> 1) + 4 * i));
         w[2 * kh + p] = kv4_turn(nat);
       }
     }
@@ -146,10 +186,14 @@ __device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const
   if (t == 0) {
     uint8_t* to = page + Kv4Page<D>::KS + (tile * 8 + g) * (D / 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (is_new[i])
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) to[i * (D / 32) + k] = (uint8_t)scale[i][k];
+    for (int i = 0; i < 2; ++i) {
+      if (!is_new[i]) continue;
+      if (D == 128) {
+        *reinterpret_cast<uint32_t*>(to + 4 * i) = scale[i][0] | scale[i][1] << 8 | scale[i][D / 32 - 2] << 16 | scale[i][D / 32 - 1] << 24;
+      } else {
+        *reinterpret_cast<uint16_t*>(to + 2 * i) = (uint16_t)(scale[i][0] | scale[i][1] << 8);
+      }
+    }
   }
 }
 
@@ -160,29 +204,28 @@ __device__ __forceinline__ void put_values(uint8_t* page, int tile, const T* con
   const int lane = threadIdx.x & 31, i = lane & 3, t = lane >> 2 & 3, j = lane >> 4;
   const bool mine = j < D / 64;
   const int dt = 4 * j + i;
-  float x[4][16];
+  Eight<T> x[4][2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    float(&a)[8] = *reinterpret_cast<float(*)[8]>(&x[k][0]);
-    float(&b)[8] = *reinterpret_cast<float(*)[8]>(&x[k][8]);
     if (mine && is_new[k]) {
-      load8(row[k] + 16 * dt, wide, a);
-      load8(row[k] + 16 * dt + 8, wide, b);
+      x[k][0].load(row[k] + 16 * dt, wide);
+      x[k][1].load(row[k] + 16 * dt + 8, wide);
     } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[k][e] = 0.0f;
+      x[k][0] = x[k][1] = Eight<T>{};
     }
   }
-  uint32_t nat[8] = {}, bytes[4], kept = 0;
+  uint32_t nat[8], bytes[4], kept = 0;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) nat[g] = kFields;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {  // token 2 t + (k & 1) + 8 (k >> 1)
     float m = largest(x[k]);
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
     uint32_t u[16];
-    codes(x[k], m, kv4_scale(m, bytes[k]), u);
+    bytes[k] = quantise(x[k], m, u);
     if (!is_new[k]) kept |= 0x0f0fu << (16 * (k & 1) + 4 * (k >> 1));
 #pragma unroll
-    for (int e = 0; e < 16; ++e) nat[e & 7] |= (u[e] & 15u) << (16 * (k & 1) + 8 * (e >> 3) + 4 * (k >> 1));
+    for (int e = 0; e < 16; ++e) nat[e & 7] += u[e] * (1u << (16 * (k & 1) + 8 * (e >> 3) + 4 * (k >> 1)));
   }
   if (!mine || !(is_new[0] || is_new[1] || is_new[2] || is_new[3])) return;
   kept = kv4_turn(kept);
@@ -232,8 +275,7 @@ __device__ __forceinline__ void append_tile(const w4a8_kv4_cache& c, const Sourc
   }
 }
 
-// Many rows: one CTA per (four tiles, head, sequence), a warp per tile of keys or values.  Bound by instructions (about 15
-// a value) and the loads in flight.
+// Many rows: one CTA per (four tiles, head, sequence), a warp per tile of keys or values.  TODO
 template <typename T, int D>
 __global__ void __launch_bounds__(kBigThreads) k_kv4_append(w4a8_kv4_cache c, Source k, Source v, int n_src, int n,
                                                             const int32_t* counts, const int32_t* index, int32_t* len_out,
@@ -290,13 +332,18 @@ __global__ void k_kv4_reset(w4a8_kv4_cache c) {
 __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  uint4 u[sizeof(T) / 2];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) kv8_store(reinterpret_cast<T*>(u) + i, x[i]);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+// The values of the 4-bit fields at bit `at` of two 16-bit halves, times s: neighbours lo, hi of a vector.  A field below the
+// leading bit of 128 (bf16) or 16 (fp32) is a number; c s and, in fp32, 24 s are exact.
+__device__ __forceinline__ void put_pair(Eight<__nv_bfloat16>& x, int pair, uint32_t w, int at, float s) {
+  uint32_t v = and_or(w >> at, 0x000f000fu, 0x43004300u);
+  const __nv_bfloat162 c = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f));
+  reinterpret_cast<__nv_bfloat162*>(x.u)[pair] = __hmul2(c, __float2bfloat162_rn(s));
+}
+__device__ __forceinline__ void put_pair(Eight<float>& x, int pair, uint32_t w, int at, float s) {
+  const uint32_t a = at <= 19 ? w << (19 - at) : w >> (at - 19), b = at + 16 <= 19 ? w << (3 - at) : w >> (at - 3 < 0 ? 0 : at - 3);
+  float* f = reinterpret_cast<float*>(x.u) + 2 * pair;
+  f[0] = fmaf(__uint_as_float(and_or(a, 0x00780000u, 0x41800000u)), s, -24.0f * s);
+  f[1] = fmaf(__uint_as_float(and_or(b, 0x00780000u, 0x41800000u)), s, -24.0f * s);
 }
 
 // One CTA per (four tiles, head, sequence), a warp per tile of keys or values, in the lanes of the append.
@@ -319,10 +366,10 @@ __global__ void __launch_bounds__(256) k_kv4_read(w4a8_kv4_cache c, const int32_
   int phys = -1;
   if (p0 < L) phys = kv4_phys(c, s, (int)(tile >> 2));
   T* out = (val ? v_out : k_out) + ((size_t)s * n * H + h) * D;
-  auto put = [&](int64_t pos, int d, const float (&x)[8]) {
+  auto put = [&](int64_t pos, int d, const Eight<T>& x) {
     if (pos < f || pos >= stop) return;
-    const float zero[8] = {};
-    store8(out + (size_t)(pos - f) * H * D + d, phys >= 0 && pos < L ? x : zero);
+    const Eight<T> zero{};
+    (phys >= 0 && pos < L ? x : zero).store(out + (size_t)(pos - f) * H * D + d, true);
   };
   const uint8_t* page = kv4_page<D>(c, phys < 0 ? 0 : phys, h);
   const int tl = (int)(tile & 3);
@@ -345,12 +392,9 @@ __global__ void __launch_bounds__(256) k_kv4_read(w4a8_kv4_cache c, const int32_
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float s0 = scale_value(b[i][2 * j + kh]);
-          float x[8];
+          Eight<T> x;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t u = (e < 4 ? n0 : n1) >> (16 * (e & 1) + 8 * (e >> 1 & 1) + 4 * i) & 15u;
-            x[e] = (float)((int)u - 8) * s0;
-          }
+          for (int e = 0; e < 4; ++e) put_pair(x, e, e < 2 ? n0 : n1, 8 * (e & 1) + 4 * i, s0);
           put(p0 + g + 8 * i, 32 * (2 * j + kh) + 8 * t, x);
         }
       }
@@ -369,9 +413,10 @@ __global__ void __launch_bounds__(256) k_kv4_read(w4a8_kv4_cache c, const int32_
       const float s0 = scale_value(sc >> (8 * k) & 255u);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        float x[8];
+        Eight<T> x;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) x[g] = (float)((int)(w[g] >> (16 * (k & 1) + 8 * q + 4 * (k >> 1)) & 15u) - 8) * s0;
+        for (int g = 0; g < 4; ++g)
+          put_pair(x, g, __byte_perm(w[2 * g], w[2 * g + 1], k & 1 ? 0x7632 : 0x5410), 8 * q + 4 * (k >> 1), s0);
         put(p0 + 2 * t + (k & 1) + 8 * (k >> 1), 16 * dt + 8 * q, x);
       }
     }

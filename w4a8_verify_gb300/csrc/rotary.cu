@@ -27,38 +27,6 @@ struct RotGeom {
   float inv_dim;
 };
 
-// Eight elements of a row, as they are, and in fp32.
-template <typename T>
-struct Eight {
-  uint4 u[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, bool wide) {
-    if (wide) {
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(u)[i] = p[i];
-    }
-  }
-  __device__ __forceinline__ void store(T* p, bool wide) const {
-    if (wide) {
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = reinterpret_cast<const T*>(u)[i];
-    }
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = kv8_load(reinterpret_cast<const T*>(u) + i);
-  }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) kv8_store(reinterpret_cast<T*>(u) + i, x[i]);
-  }
-};
-
 // Cosine and sine of turn 2^-64 turns.
 __device__ __forceinline__ void unit(uint64_t turn, float& c, float& s) {
   const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
