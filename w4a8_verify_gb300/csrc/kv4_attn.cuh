@@ -632,9 +632,9 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   // The parts first, first + step, .. of a segment's row, of the CTAs in their order, then the early ones: maximum M,
   // sum, and values of the lane's dims; B loads in flight.
   const int slots = geo.ctas * geo.ng;
+  constexpr int B = NT == 1 ? 10 : 16;
   auto gather = [&](const Parts& p, int r, int first, int step, float& M, float& sum, float (&o)[E]) {
     const int n = p.held + 2 * p.early, apart = p.held ? slots : 3 * slots;
-    constexpr int B = 6;
     M = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   const int rows = min(RB, geo.R);
   auto split_of = [&](const Parts& p) {
     int per = 1;
-    while (per * 6 < p.held + 2 * p.early && 2 * per * rows <= NG) per *= 2;
+    while (per * B < p.held + 2 * p.early && 2 * per * rows <= NG) per *= 2;
     return per;
   };
   for (int x = grp; x < n_joins * rows; x += NG) {
@@ -896,10 +896,16 @@ cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, 
   return kv4_split_tiles(geo.R, a.dtype) == 1 ? kv4_split_launch<T, D, 1>(c, a, geo, ws, st)
                                               : kv4_split_launch<T, D, 2>(c, a, geo, ws, st);
 }
-// Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu).
+// Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu): a tile of it takes 128 rows at one price, the split
+// kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  With few (sequence, KV head) pairs the parts of a segment are
+// many, and bf16 blocks of 9 to 16 rows are slow to join.  Measured (us, split / wide), heads of 128:
+//   fp32,   8 pairs, 32000 tokens:  16 rows 45 / 80,  32 rows 71 / 81,  48 rows 99 / 82;  4096:  32 rows 31 / 32,  48 rows 38 / 33
+//   fp32, 128 pairs, to 4096:  16 rows 68 / 94,  20 rows 107 / 97,  32 rows 188 / 100
+//   bf16,   8 pairs, 32000:  8 rows 29 / 51,  12 rows 45 / 51,  20 rows 55 / 52;  4096:  8 rows 18 / 26,  12 rows 29 / 26,  16 rows 34 / 26
+//   bf16, 128 pairs, to 4096:  12 rows 57 / 71,  16 rows 64 / 74,  20 rows 101 / 74
 inline bool kv4_is_wide(const w4a8_kv4_cache& c, int R, int dtype) {
-  (void)c;
-  return R > (dtype == W4A8_F32 ? 16 : 32);
+  const bool few = (int64_t)c.n_seqs * c.n_kv_heads <= 32;
+  return R > (few ? dtype == W4A8_F32 ? 32 : 8 : 16);
 }
 cudaError_t kv4_wide(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
 // one translation unit per head size and element type
