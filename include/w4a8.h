@@ -332,7 +332,8 @@ w4a8_status w4a8_kv8_evict(const w4a8_kv8_cache* c, const float* mass, int keep,
  *   s = absmax / 7 (IEEE), then to the nearest (half to even) of (8 + m) * 2^(e - 18), 0 <= m < 8, 1 <= e, or
  *       m * 2^-17, at most 240 (larger values are held as 7 * 240);  byte 8 e + m (e = 0 for the small ones)
  *   c = clamp(rint(x / s), -7, 7);  s == 0 -> c = 0
- * (a NaN or an infinity among the 32 makes the byte 255, read as NaN, and every c 0).  Tokens are quantised one by
+ * (a NaN or an infinity among the 32 makes the byte 255, read as NaN, and every c 0; bytes 184 .. 254 are not written, and
+ * what holds them may come out as NaN).  Tokens are quantised one by
  * one, as they arrive: there is no open page in another type.  c * s has at most seven significant bits.
  *
  * A page of one head is 68 * head_dim bytes (D = head_dim), fields as a warp reads them as m16n8k16 operands:
@@ -373,7 +374,8 @@ w4a8_status w4a8_kv4_check(const w4a8_kv4_cache* c, uint32_t* flags);
  * sequence s.  counts: device int32[n_seqs] in 0..n, NULL = n.  index: device int32 [n_seqs][n], NULL = the rows in order:
  * position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of a draft tree; the same row may
  * come twice); with it n <= 1024, without it n_src >= n (W4A8_ERR_SHAPE).  The new lengths go to len_out (device int32[n_seqs]);
- * len_out == c->len advances the cache, another one leaves c->len alone, and the cache is right at either.  A sequence
+ * len_out == c->len advances the cache, another one leaves c->len alone, and the cache is right at either; on counts, index,
+ * the rest of the cache's buffers or a part of c->len it is refused (W4A8_ERR_ARG).  A sequence
  * that would pass 64 * max_pages tokens stays as it was, as does one with a row out of range; a page whose table entry is out of
  * range takes no rows.  An n beyond 64 * max_pages is W4A8_ERR_CAPACITY. */
 w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,

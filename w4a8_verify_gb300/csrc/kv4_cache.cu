@@ -462,6 +462,15 @@ W4A8_API w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k
   if (!aligned(k->data, kv8_elem(dtype)) || !aligned(v->data, kv8_elem(dtype)) || !aligned(counts, 4) ||
       !aligned(index, 4) || !aligned(len_out, 4))
     return W4A8_ERR_ARG;
+  // new lengths on what other CTAs of the call still read (they may take the place of the old ones)
+  const size_t S4 = 4 * (size_t)c->n_seqs;
+  auto on = [&](const void* p, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(len_out);
+    return p && x < y + S4 && y < x + bytes;
+  };
+  if (on(counts, S4) || on(index, S4 * n) || on(c->table, S4 * c->max_pages) || on(c->ctl, 4) ||
+      (len_out != c->len && on(c->len, S4)))
+    return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages) return W4A8_ERR_CAPACITY;
   cudaStream_t st = as_stream(stream);
   const bool own = len_out == c->len, f32 = dtype == W4A8_F32, d64 = c->head_dim == 64;
