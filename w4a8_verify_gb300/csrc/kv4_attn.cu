@@ -31,7 +31,14 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
   const size_t segments = (size_t)c->n_seqs * c->n_kv_heads * g.CB, units = segments * (p->wide ? c->max_pages : c->max_pages + 1);
   if (units >= (size_t)1 << 31 || segments >= (size_t)1 << 22) return W4A8_ERR_SHAPE;
   g.segments = (int)segments;
-  g.ctas = (int)(units < (size_t)kKv4Ctas ? units : (size_t)kKv4Ctas);
+  size_t most_ctas = kKv4Ctas;
+  if (p->wide && a->k.data) {  // a few CTAs for the new rows get SMs of their own, a sixth of them at most
+    g.tiles = (g.n + kKv4RowTile - 1) / kKv4RowTile;
+    const int64_t blocks = kv4_rows_blocks(*c, g);
+    if (blocks >= (int64_t)1 << 31) return W4A8_ERR_SHAPE;
+    if (blocks <= kKv4Ctas / 6) g.folded = (int)blocks, most_ctas -= g.folded;
+  }
+  g.ctas = (int)(units < most_ctas ? units : most_ctas);
   const size_t ng = (units + g.ctas - 1) / g.ctas, most = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype) / 2;
   g.ng = (int)(ng < most ? ng : most);
   const size_t row = (size_t)g.RB * 4, D = (size_t)c->head_dim;
@@ -40,8 +47,6 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
   p->o = up256(p->ml + slots * row * 2);
   p->prefix = p->rml = p->ro = p->bytes = up256(p->o + slots * row * D);
   if (p->wide) {
-    g.tiles = a->k.data ? (g.n + 15) / 16 : 0;
-    if (segments * (g.tiles ? g.tiles : 1) * 2 >= (size_t)1 << 31) return W4A8_ERR_SHAPE;  // CTAs of the new rows
     p->rml = up256(p->prefix + ((size_t)c->n_seqs + 1) * 4);
     p->ro = up256(p->rml + segments * g.tiles * row * 2);
     p->bytes = up256(p->ro + segments * g.tiles * row * D);

@@ -43,6 +43,7 @@ constexpr int kKv4MaxWarps = 16;
 constexpr int kKv4HalfTokens = 32;        // tokens of a page that a warp of a pair takes
 constexpr int kKv4Lens = 1024;            // sequences whose lengths are kept in shared memory
 constexpr int kKv4WideRows = 128;         // query rows of a segment of a wide call (kv4_wide.cu)
+constexpr int kKv4RowTile = 16, kKv4RowsRows = 64;  // new rows and query rows of a CTA of those that do the new rows of a wide call
 constexpr float kP4Scale = 128.0f, kP4Slack = 8.0f;  // scale of P; how far (log2) a logit may pass the row's maximum
 static_assert(W4A8_KV4_TICKETS >= kKv4Ctas * kKv4MaxWarps * 4, "tickets");
 
@@ -52,6 +53,7 @@ struct Kv4Geom {       // of one call, the same for every kernel of it
   int ctas, ng;        // of the kernel over the pages, and its workers (split: pairs of warps) in each at most
   int segments;
   int tiles;           // wide calls: blocks of 16 new rows
+  int folded;          // CTAs behind the others of the kernel over the pages, for the new rows; 0: those are a kernel of their own
   int vec;             // rows may be read 16 bytes at a time: bit 0 q, bit 1 k, bit 2 v
   int withheld;        // CTA whose pages are not copied (w4a8_kv4_attention_inject_timeout), -1: none
   uint64_t wait_ns;    // limit of the kernels' waits
@@ -70,6 +72,10 @@ struct Kv4Scratch {    // workspace pointers
   float* ro;           // [segments][tiles][RB][D] its values
 };
 
+// CTAs that do the new rows of a wide call.
+inline int64_t kv4_rows_blocks(const w4a8_kv4_cache& c, const Kv4Geom& g) {
+  return (int64_t)((g.R + kKv4RowsRows - 1) / kKv4RowsRows) * g.tiles * c.n_seqs * c.n_kv_heads;
+}
 // Column blocks that hold rows of a sequence of cnt rows.
 __device__ __forceinline__ int kv4_blocks(const Kv4Geom& g, int cnt) { return (cnt * g.G + g.RB - 1) / g.RB; }
 // Units of the segments before each sequence, [n_seqs + 1] in shared memory, units_of(L) to a segment; lens: the first kKv4Lens

@@ -62,12 +62,176 @@ struct Bars {
 };
 static_assert(sizeof(Bars) + 4 <= 256, "barriers");
 
+// The new rows of wide calls: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
+// holds the logits of two rows and two tokens, then D / 8 values of the two rows.  Rows 32 apart and tokens 8 apart
+// belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice.  Plain fp32.
+// A few of them are CTAs of the wide kernel's own grid, which then leaves them SMs (a tree of 16 rows: 33 us as a kernel of
+// its own behind, 22.5 us so); many are a kernel behind it, whose CTAs start as SMs become free: it reads (from L2) what the wide
+// kernel waited for before it let this one start, so the wait for that kernel comes last, for the join that follows.
+constexpr int kRowsThreads = 256, kRT = 8 * kKv4RowsRows / kRowsThreads;  // kRT rows of a thread
+template <int D>
+struct RowsSmem {
+  float q[kKv4RowsRows][D + 4], k[kKv4RowTile][D + 4], v[kKv4RowTile][D], p[kKv4RowsRows][kKv4RowTile + 4];
+  uint32_t see[kKv4RowsRows];
+};
+// whether x holds for one of the first kRowsThreads threads, which meet here
+__device__ __forceinline__ bool rows_any(bool x) {
+  unsigned r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((unsigned)x), "n"(kRowsThreads)
+      : "memory");
+  return r != 0;
+}
+// Block `number` of the call's; the CTA's first kRowsThreads threads.
+template <typename T, int D>
+__device__ __forceinline__ void rows_block(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4Geom& geo,
+                                           const Kv4Scratch& ws, uint8_t* shared, int number) {
+  RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(shared);
+  constexpr int V = D / 8;  // vectors of eight elements in a row
+  const int tid = threadIdx.x, rg = tid >> 3, tg = tid & 7;
+  const int blocks = (a.n * geo.G + kKv4RowsRows - 1) / kKv4RowsRows, x = number / blocks;
+  const int fresh = x % geo.tiles, pair = x / geo.tiles;
+  const struct { int s, h; } sg = {pair / c.n_kv_heads, pair % c.n_kv_heads};
+  const int L = __ldcg(c.len + sg.s), cnt = a.counts ? __ldcg(a.counts + sg.s) : a.n;
+  const int first = number % blocks * kKv4RowsRows;
+  auto slot = [&](int r) {  // of row first + r of the KV head
+    return (((size_t)pair * geo.CB + (first + r) / geo.RB) * geo.tiles + fresh) * geo.RB + (first + r) % geo.RB;
+  };
+  int nv = 0, rows = 0;
+  if (L >= 0 && L <= kPage * c.max_pages && cnt > 0 && cnt <= a.n) {
+    nv = min(kKv4RowTile, cnt - fresh * kKv4RowTile);
+    rows = min(kKv4RowsRows, cnt * geo.G - first);
+  }
+  if (nv > 0 && rows > 0) {  // the same for the whole block
+    const T* kn = static_cast<const T*>(a.k.data) + sg.s * a.k.seq + sg.h * a.k.head + (int64_t)fresh * kKv4RowTile * a.k.row;
+    const T* vn = static_cast<const T*>(a.v.data) + sg.s * a.v.seq + sg.h * a.v.head + (int64_t)fresh * kKv4RowTile * a.v.row;
+    // eight elements of a row of T; all of a loop's rows on their way
+    auto load8 = [&](const T* p, int vec, float (&e)[8]) {
+      if (vec) {
+        uint4 w[sizeof(T) / 2];
+#pragma unroll
+        for (int y = 0; y < (int)sizeof(T) / 2; ++y) w[y] = __ldcg(reinterpret_cast<const uint4*>(p) + y);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = kv8_load(reinterpret_cast<const T*>(w) + y);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = kv8_float(__ldcg(p + y));
+      }
+    };
+    bool bad = false;  // a value that is not finite
+#pragma unroll
+    for (int y = tid; y < 2 * kKv4RowTile * V; y += kRowsThreads) {
+      const int t = y / V % kKv4RowTile, d = y % V * 8;
+      const bool val = y >= kKv4RowTile * V;
+      float e[8] = {};
+      if (t < nv) {
+        load8(val ? vn + (int64_t)t * a.v.row + d : kn + (int64_t)t * a.k.row + d, geo.vec & (val ? 4 : 2), e);
+      }
+      float* to = val ? &sm.v[t][d] : &sm.k[t][d];
+      *reinterpret_cast<float4*>(to) = *reinterpret_cast<float4*>(e);
+      *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<float4*>(e + 4);
+#pragma unroll
+      for (int z = 0; z < 8; ++z) bad = bad || (val && !(fabsf(e[z]) <= 3.402823466e38f));
+    }
+#pragma unroll 4
+    for (int y = tid; y < kKv4RowsRows * V; y += kRowsThreads) {
+      const int r = y / V, d = y % V * 8, rr = first + min(r, rows - 1);
+      float e[8];
+      load8(static_cast<const T*>(a.q.data) + sg.s * a.q.seq + (rr / geo.G) * a.q.row +
+                (sg.h * geo.G + rr % geo.G) * a.q.head + d, geo.vec & 1, e);
+      *reinterpret_cast<float4*>(&sm.q[r][d]) = *reinterpret_cast<float4*>(e);
+      *reinterpret_cast<float4*>(&sm.q[r][d + 4]) = *reinterpret_cast<float4*>(e + 4);
+    }
+    if (tid < kKv4RowsRows) {  // tokens that a row sees
+      const int node = (first + min(tid, rows - 1)) / geo.G;
+      const uint64_t mask = a.mask ? __ldcg(a.mask + (size_t)sg.s * a.n + node) : (node >= 63 ? ~0ull : (1ull << (node + 1)) - 1ull);
+      sm.see[tid] = (uint32_t)(mask >> (fresh * kKv4RowTile)) & ((1u << nv) - 1u);
+    }
+    bad = rows_any(bad);
+    float s[kRT][2] = {};
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 k[2], q[kRT];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.k[8 * j + tg][d]);
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[kKv4RowsRows / kRT * i + rg][d]);
+#pragma unroll
+      for (int i = 0; i < kRT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
+    }
+    const float qscale = a.scale * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      const int r = kKv4RowsRows / kRT * i + rg;
+      const uint32_t see = sm.see[r] >> tg;
+      const float s0 = see & 1u ? s[i][0] * qscale : -INFINITY, s1 = see & 256u ? s[i][1] * qscale : -INFINITY;
+      float m = fmaxf(s0, s1);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.0f : m;
+      const float p0 = see & 1u ? ex2(s0 - base) : 0.0f, p1 = see & 256u ? ex2(s1 - base) : 0.0f;
+      float l = p0 + p1;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      sm.p[r][tg] = p0, sm.p[r][8 + tg] = p1;
+      if (tg == 0 && r < rows) ws.rml[slot(r)] = make_float2(m, l);
+    }
+    __syncwarp();  // a row's weights come from the lanes that read them
+    float4 o[kRT][D / 32] = {};
+#pragma unroll 1
+    for (int t = 0; t < kKv4RowTile; t += 4) {
+      float p[kRT][4];
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(&sm.p[kKv4RowsRows / kRT * i + rg][t]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float4 v[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = *reinterpret_cast<const float4*>(&sm.v[t + y][32 * e + 4 * tg]);
+#pragma unroll
+        for (int i = 0; i < kRT; ++i) {
+          if (bad && !(sm.see[kKv4RowsRows / kRT * i + rg] >> (t + y) & 1u)) continue;  // 0 times it would not be 0
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            o[i][e].x = fmaf(p[i][y], v[e].x, o[i][e].x), o[i][e].y = fmaf(p[i][y], v[e].y, o[i][e].y);
+            o[i][e].z = fmaf(p[i][y], v[e].z, o[i][e].z), o[i][e].w = fmaf(p[i][y], v[e].w, o[i][e].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRT; ++i)
+      if (kKv4RowsRows / kRT * i + rg < rows)
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          *reinterpret_cast<float4*>(ws.ro + slot(kKv4RowsRows / kRT * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
+  }
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowsThreads, 3) k_kv4_rows(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
+  griddep_launch();
+  extern __shared__ __align__(16) uint8_t sm_raw[];
+  rows_block<T, D>(c, a, geo, ws, sm_raw, blockIdx.x);
+  // the grid has not ended before the kernel in front has; only one CTA keeps its place for that
+  if (blockIdx.x == 0) griddep_wait();
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
   using C = Wide<T, D>;
   constexpr int NQ = C::NQ, NO = C::NO;
   constexpr unsigned FULL = 0xffffffffu;
   extern __shared__ __align__(16) uint8_t sm_raw[];
+  if ((int)blockIdx.x >= geo.ctas) {  // a block of new rows
+    griddep_enter();
+    if (threadIdx.x < kRowsThreads) rows_block<T, D>(c, a, geo, ws, sm_raw, blockIdx.x - geo.ctas);
+    return;
+  }
   uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);  // swizzle atoms start at multiples of 1024
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::sBar + sizeof(Bars));
   Bars& bar = *reinterpret_cast<Bars*>(sm + C::sBar);
@@ -241,6 +405,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
             const uint2 s = *reinterpret_cast<const uint2*>(from + Kv4Page<D>::VS + (t16 * 4 + t) * (D / 8) + 8 * j);
             sw[i][0] = s.x, sw[i][1] = s.y;
             if (tokens < kPage) {
+              __syncwarp();
               uint32_t keep = 0;
 #pragma unroll
               for (int b = 0; b < 4; ++b)
@@ -406,9 +571,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
           for (int y = 0; y < 2; ++y) {
             uint32_t v[32];
             tc_load32(sa + 32 * y, v);
+            if (tokens < kPage) {
+              __syncwarp();  // a branch: as predicated instructions it would cost every page its selects
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (tokens == kPage || 32 * y + e < tokens) mx = fmaxf(mx, __uint_as_float(v[e]));
+              for (int e = 0; e < 32; ++e)
+                if (32 * y + e >= tokens) v[e] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
           }
           if (mx * colfac > m) {
             f = ex2(m - mx * colfac);
@@ -437,26 +607,38 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
                   v[16 * z + e] = __float_as_uint(__uint_as_float(v[16 * z + e]) + __uint_as_float(w[e]));
               }
             }
-            // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
+            if (part) {
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * y + e >= tokens) v[e] = __float_as_uint(-INFINITY);
+            }
             float sum[2] = {0.0f, 0.0f}, top[2] = {mx, mx};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float s = __uint_as_float(v[e]);
+              top[e & 1] = fmaxf(top[e & 1], s);
+              v[e] = __float_as_uint(NQ == 2 ? ex2(fmaf(s, collow, fmaf(s, colfac, -base))) * C::PSCALE
+                                             : ex2(fmaf(s, colfac, 7.0f - base)));
+            }
+            if (part) {  // a factor of 0 makes NaN of what is not there
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * y + e >= tokens) v[e] = 0;
+            }
+            // register 4 t + 2 ks + h8 holds tokens 16 ks + 8 h8 + 2 t + {0, 1} of the 32: the values' chunk order
 #pragma unroll
             for (int z = 0; z < 16; ++z) {
               const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
-              float e[2];
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const float s = __uint_as_float(v[tok + w]);
-                if (!part || 32 * y + tok + w < tokens) top[w] = fmaxf(top[w], s);
-                e[w] = NQ == 2 ? ex2(fmaf(s, collow, fmaf(s, colfac, -base))) * C::PSCALE : ex2(fmaf(s, colfac, 7.0f - base));
-                if (part && 32 * y + tok + w >= tokens) e[w] = 0.0f;
-                sum[w] += e[w];
-              }
+              const float e0 = __uint_as_float(v[tok]), e1 = __uint_as_float(v[tok + 1]);
+              sum[0] += e0, sum[1] += e1;
               if (NQ == 2) {
-                const float w0 = whole(e[0]), w1 = whole(e[1]);
+                const float w0 = whole(e0), w1 = whole(e1);
                 hi[z] = pack_f16(w0, w1);
-                lo[z] = pack_f16(e[0] - w0, e[1] - w1);
+                lo[z] = pack_f16(e0 - w0, e1 - w1);
               } else {
-                hi[z] = pack_f16(e[0], e[1]);
+                hi[z] = pack_f16(e0, e1);
               }
             }
             mx = fmaxf(top[0], top[1]);
@@ -560,149 +742,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
   }
 }
 
-// The new rows of wide calls: 64 query rows by 16 tokens to a CTA of 256 threads, both products in registers: a thread
-// holds the logits of two rows and two tokens, then D / 8 values of the two rows.  Rows 32 apart and tokens 8 apart
-// belong to a thread, so that the lanes' 16-byte reads of neighbouring (padded) rows meet no bank twice.  Plain fp32.
-// Launched behind the wide kernel and run beside it where an SM has room: it reads (from L2) what that kernel waited for
-// before it let this one start, so the wait for that kernel comes last, for the join that follows.
-constexpr int kRowTile = 16;  // new rows of one part
-constexpr int kRowsThreads = 256, kRowsRows = 64, kRT = 8 * kRowsRows / kRowsThreads;  // kRT rows of a thread
-template <int D>
-struct RowsSmem {
-  float q[kRowsRows][D + 4], k[kRowTile][D + 4], v[kRowTile][D], p[kRowsRows][kRowTile + 4];
-  uint32_t see[kRowsRows];
-};
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowsThreads, 3) k_kv4_rows(w4a8_kv4_cache c, w4a8_kv4_attn a, Kv4Geom geo, Kv4Scratch ws) {
-  griddep_launch();
-  extern __shared__ __align__(16) uint8_t sm_raw[];
-  RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>(sm_raw);
-  constexpr int V = D / 8;  // vectors of eight elements in a row
-  const int tid = threadIdx.x, rg = tid >> 3, tg = tid & 7;
-  const int blocks = (a.n * geo.G + kRowsRows - 1) / kRowsRows, x = blockIdx.x / blocks;
-  const int fresh = x % geo.tiles, pair = x / geo.tiles;
-  const struct { int s, h; } sg = {pair / c.n_kv_heads, pair % c.n_kv_heads};
-  const int L = __ldcg(c.len + sg.s), cnt = a.counts ? __ldcg(a.counts + sg.s) : a.n;
-  const int first = blockIdx.x % blocks * kRowsRows;
-  auto slot = [&](int r) {  // of row first + r of the KV head
-    return (((size_t)pair * geo.CB + (first + r) / geo.RB) * geo.tiles + fresh) * geo.RB + (first + r) % geo.RB;
-  };
-  int nv = 0, rows = 0;
-  if (L >= 0 && L <= kPage * c.max_pages && cnt > 0 && cnt <= a.n) {
-    nv = min(kRowTile, cnt - fresh * kRowTile);
-    rows = min(kRowsRows, cnt * geo.G - first);
-  }
-  if (nv > 0 && rows > 0) {  // the same for the whole block
-    const T* kn = static_cast<const T*>(a.k.data) + sg.s * a.k.seq + sg.h * a.k.head + (int64_t)fresh * kRowTile * a.k.row;
-    const T* vn = static_cast<const T*>(a.v.data) + sg.s * a.v.seq + sg.h * a.v.head + (int64_t)fresh * kRowTile * a.v.row;
-    // eight elements of a row of T; all of a loop's rows on their way
-    auto load8 = [&](const T* p, int vec, float (&e)[8]) {
-      if (vec) {
-        uint4 w[sizeof(T) / 2];
-#pragma unroll
-        for (int y = 0; y < (int)sizeof(T) / 2; ++y) w[y] = __ldcg(reinterpret_cast<const uint4*>(p) + y);
-#pragma unroll
-        for (int y = 0; y < 8; ++y) e[y] = kv8_load(reinterpret_cast<const T*>(w) + y);
-      } else {
-#pragma unroll
-        for (int y = 0; y < 8; ++y) e[y] = kv8_float(__ldcg(p + y));
-      }
-    };
-    bool bad = false;  // a value that is not finite
-#pragma unroll
-    for (int y = tid; y < 2 * kRowTile * V; y += kRowsThreads) {
-      const int t = y / V % kRowTile, d = y % V * 8;
-      const bool val = y >= kRowTile * V;
-      float e[8] = {};
-      if (t < nv) {
-        load8(val ? vn + (int64_t)t * a.v.row + d : kn + (int64_t)t * a.k.row + d, geo.vec & (val ? 4 : 2), e);
-      }
-      float* to = val ? &sm.v[t][d] : &sm.k[t][d];
-      *reinterpret_cast<float4*>(to) = *reinterpret_cast<float4*>(e);
-      *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<float4*>(e + 4);
-#pragma unroll
-      for (int z = 0; z < 8; ++z) bad = bad || (val && !(fabsf(e[z]) <= 3.402823466e38f));
-    }
-#pragma unroll 4
-    for (int y = tid; y < kRowsRows * V; y += kRowsThreads) {
-      const int r = y / V, d = y % V * 8, rr = first + min(r, rows - 1);
-      float e[8];
-      load8(static_cast<const T*>(a.q.data) + sg.s * a.q.seq + (rr / geo.G) * a.q.row +
-                (sg.h * geo.G + rr % geo.G) * a.q.head + d, geo.vec & 1, e);
-      *reinterpret_cast<float4*>(&sm.q[r][d]) = *reinterpret_cast<float4*>(e);
-      *reinterpret_cast<float4*>(&sm.q[r][d + 4]) = *reinterpret_cast<float4*>(e + 4);
-    }
-    if (tid < kRowsRows) {  // tokens that a row sees
-      const int node = (first + min(tid, rows - 1)) / geo.G;
-      const uint64_t mask = a.mask ? __ldcg(a.mask + (size_t)sg.s * a.n + node) : (node >= 63 ? ~0ull : (1ull << (node + 1)) - 1ull);
-      sm.see[tid] = (uint32_t)(mask >> (fresh * kRowTile)) & ((1u << nv) - 1u);
-    }
-    bad = __syncthreads_or(bad);
-    float s[kRT][2] = {};
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      float4 k[2], q[kRT];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.k[8 * j + tg][d]);
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[kRowsRows / kRT * i + rg][d]);
-#pragma unroll
-      for (int i = 0; i < kRT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          s[i][j] = fmaf(q[i].w, k[j].w, fmaf(q[i].z, k[j].z, fmaf(q[i].y, k[j].y, fmaf(q[i].x, k[j].x, s[i][j]))));
-    }
-    const float qscale = a.scale * 1.4426950408889634f;
-#pragma unroll
-    for (int i = 0; i < kRT; ++i) {
-      const int r = kRowsRows / kRT * i + rg;
-      const uint32_t see = sm.see[r] >> tg;
-      const float s0 = see & 1u ? s[i][0] * qscale : -INFINITY, s1 = see & 256u ? s[i][1] * qscale : -INFINITY;
-      float m = fmaxf(s0, s1);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float base = m == -INFINITY ? 0.0f : m;
-      const float p0 = see & 1u ? ex2(s0 - base) : 0.0f, p1 = see & 256u ? ex2(s1 - base) : 0.0f;
-      float l = p0 + p1;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      sm.p[r][tg] = p0, sm.p[r][8 + tg] = p1;
-      if (tg == 0 && r < rows) ws.rml[slot(r)] = make_float2(m, l);
-    }
-    __syncwarp();  // a row's weights come from the lanes that read them
-    float4 o[kRT][D / 32] = {};
-#pragma unroll 1
-    for (int t = 0; t < kRowTile; t += 4) {
-      float p[kRT][4];
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(&sm.p[kRowsRows / kRT * i + rg][t]);
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        float4 v[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) v[e] = *reinterpret_cast<const float4*>(&sm.v[t + y][32 * e + 4 * tg]);
-#pragma unroll
-        for (int i = 0; i < kRT; ++i) {
-          if (bad && !(sm.see[kRowsRows / kRT * i + rg] >> (t + y) & 1u)) continue;  // 0 times it would not be 0
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            o[i][e].x = fmaf(p[i][y], v[e].x, o[i][e].x), o[i][e].y = fmaf(p[i][y], v[e].y, o[i][e].y);
-            o[i][e].z = fmaf(p[i][y], v[e].z, o[i][e].z), o[i][e].w = fmaf(p[i][y], v[e].w, o[i][e].w);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRT; ++i)
-      if (kRowsRows / kRT * i + rg < rows)
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          *reinterpret_cast<float4*>(ws.ro + slot(kRowsRows / kRT * i + rg) * D + 32 * e + 4 * tg) = o[i][e];
-  }
-  // the grid has not ended before the kernel in front has; only one CTA keeps its place for that
-  if (blockIdx.x == 0) griddep_wait();
-}
-
 // The parts of a segment's rows, the CTAs in their order, then the blocks of new rows: RPC rows to a CTA, a warp takes
 // every (kJoinWarps / RPC)th part of its row, B loads in flight; then the warps' sums.  No parts: zero.  The
 // sum of a part that is not there, where a CTA's wait ran out, is NaN, and so is the row.
@@ -735,7 +774,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv4_join(w4a8_kv4_cache c, 
       early = worker_begin(w1 + 1, wk.W, U) > u1;
       held = w1 - early - c0 + 1;
     }
-    const int blocks = held + early, parts = blocks + (a.k.data ? (cnt + kRowTile - 1) / kRowTile : 0);
+    const int blocks = held + early, parts = blocks + (a.k.data ? (cnt + kKv4RowTile - 1) / kKv4RowTile : 0);
     // place of part p: of the CTAs, the early one, the new rows (those beyond the early one: another array)
     auto place = [&](int p) -> int64_t {
       if (p < held) return ((int64_t)c0 + p + seg) * geo.RB + rb;
@@ -805,13 +844,13 @@ cudaError_t wide_run(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, const Kv4G
   const size_t smem = 1024 + C::sPrefix + 4 * ((size_t)c.n_seqs + 1);
   cudaError_t e = kv8_smem<k_kv4_wide<T, D>>(1024 + C::sPrefix + 4 * (kKv8MaxSeqs + 1));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_kv4_wide<T, D>, dim3((unsigned)geo.ctas), dim3(kWideThreads), smem, st, c, a, geo, ws);
+  static_assert(sizeof(RowsSmem<D>) <= C::sPrefix, "new rows");
+  e = launch_pdl(k_kv4_wide<T, D>, dim3((unsigned)(geo.ctas + geo.folded)), dim3(kWideThreads), smem, st, c, a, geo, ws);
   if (e != cudaSuccess) return e;
-  if (geo.tiles) {
+  if (geo.tiles && !geo.folded) {
     e = kv8_smem<k_kv4_rows<T, D>>(sizeof(RowsSmem<D>));
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (geo.R + kRowsRows - 1) / kRowsRows;
-    e = launch_pdl(k_kv4_rows<T, D>, dim3((unsigned)(blocks * geo.tiles * c.n_seqs * c.n_kv_heads)), dim3(kRowsThreads),
+    e = launch_pdl(k_kv4_rows<T, D>, dim3((unsigned)kv4_rows_blocks(c, geo)), dim3(kRowsThreads),
                    sizeof(RowsSmem<D>), st, c, a, geo, ws);
     if (e != cudaSuccess) return e;
   }
