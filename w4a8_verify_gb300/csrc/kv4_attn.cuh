@@ -903,15 +903,18 @@ cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, 
                                               : kv4_split_launch<T, D, 2>(c, a, geo, ws, st);
 }
 // Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu): a tile of it takes 128 rows at one price, the split
-// kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  With few (sequence, KV head) pairs the parts of a segment are
-// many, and bf16 blocks of 9 to 16 rows are slow to join.  Measured (us, split / wide), heads of 128:
-//   fp32,   8 pairs, 32000 tokens:  16 rows 45 / 80,  32 rows 71 / 81,  48 rows 99 / 82;  4096:  32 rows 31 / 32,  48 rows 38 / 33
-//   fp32, 128 pairs, to 4096:  16 rows 68 / 94,  20 rows 107 / 97,  32 rows 188 / 100
-//   bf16,   8 pairs, 32000:  8 rows 29 / 51,  12 rows 45 / 51,  20 rows 55 / 52;  4096:  8 rows 18 / 26,  12 rows 29 / 26,  16 rows 34 / 26
-//   bf16, 128 pairs, to 4096:  12 rows 57 / 71,  16 rows 64 / 74,  20 rows 101 / 74
+// kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  Short caches of few (sequence, KV head) pairs are bound by
+// latency, where the wide kernel with the new rows in its own grid is the shorter way; otherwise the blocks count.  Measured
+// (us, split / wide; pairs x tokens, heads of 128):
+//   fp32,   8 x 4096:    8 rows 20 / 20,  12 rows 24 / 21,  16 rows 25 / 21,  32 rows 32 / 21
+//   fp32,   8 x 32000:  16 rows 44 / 66,  24 rows 57 / 66,  32 rows 72 / 66;   8 x 131071:  24 rows 174 / 225,  32 rows 221 / 225
+//   fp32, 128 x to 4096:  12 rows 64 / 87,  16 rows 70 / 90,  20 rows 109 / 92
+//   bf16,   8 x 4096:    8 rows 18 / 17,  12 rows 30 / 18;   8 x 32000:  8 rows 28 / 43,  12 rows 45 / 45,  16 rows 50 / 45
+//   bf16,   8 x 131071: 16 rows 90 / 139,  20 rows 125 / 140,  32 rows 134 / 141;   128 x to 4096:  16 rows 66 / 78,  20 rows 103 / 78
 inline bool kv4_is_wide(const w4a8_kv4_cache& c, int R, int dtype) {
-  const bool few = (int64_t)c.n_seqs * c.n_kv_heads <= 32;
-  return R > (few ? dtype == W4A8_F32 ? 32 : 8 : 16);
+  const int64_t pairs = (int64_t)c.n_seqs * c.n_kv_heads, pages = pairs * c.max_pages;
+  if (pairs <= kKv4Ctas / 6 && pages <= (dtype == W4A8_F32 ? 512 : 4096)) return R > 8;
+  return R > (dtype == W4A8_F32 && pairs <= 16 ? 24 : 16);
 }
 cudaError_t kv4_wide(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
 // one translation unit per head size and element type
