@@ -5,6 +5,8 @@
 // on its own, in registers: four lanes (keys) or two (values) hold it, and exchange nothing but its largest magnitude.
 #include "kv4.cuh"
 
+#include <type_traits>
+
 using namespace w4a8;
 
 namespace {
@@ -137,7 +139,7 @@ __device__ __forceinline__ uint32_t quantise(const Eight<__nv_bfloat16> (&v)[N],
 
 // Keys: lane (g, t) has tokens g and g + 8, dims 8 t .. 8 t + 7 of each group: two words of the page order, whole.
 template <typename T, int D>
-__device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const (&row)[2], const bool (&is_new)[2], int wide) {
+__device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const (&row)[2], const bool (&is_new)[2], bool wide) {
   const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
   uint32_t scale[2][D / 32];
   const uint32_t keep = kv4_turn((is_new[0] ? 0u : 0x0f0f0f0fu) | (is_new[1] ? 0u : 0xf0f0f0f0u));
@@ -200,7 +202,7 @@ __device__ __forceinline__ void put_keys(uint8_t* page, int tile, const T* const
 // Values: lane (j, t, i) has the tokens 2 t, 2 t + 1 and those plus 8, dims 16 (4 j + i) .. + 15: eight words of the page
 // order, whole; neighbouring i make 16 bytes, those of a store instruction 64.
 template <typename T, int D>
-__device__ __forceinline__ void put_values(uint8_t* page, int tile, const T* const (&row)[4], const bool (&is_new)[4], int wide) {
+__device__ __forceinline__ void put_values(uint8_t* page, int tile, const T* const (&row)[4], const bool (&is_new)[4], bool wide) {
   const int lane = threadIdx.x & 31, i = lane & 3, t = lane >> 2 & 3, j = lane >> 4;
   const bool mine = j < D / 64;
   const int dt = 4 * j + i;
@@ -249,7 +251,7 @@ __device__ __forceinline__ void put_values(uint8_t* page, int tile, const T* con
 }
 
 // Tile `tile` (of sequence s, counted from its first token) of one head takes its new rows [L, end).
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __device__ __forceinline__ void append_tile(const w4a8_kv4_cache& c, const Source& src, bool val, int s, int h, int tile, int L,
                                             int end, int n, const int32_t* index) {
   const int lane = threadIdx.x & 31, p0 = tile * kTile;
@@ -266,17 +268,17 @@ __device__ __forceinline__ void append_tile(const w4a8_kv4_cache& c, const Sourc
     bool is_new[2];
     const T* r[2];
     for (int i = 0; i < 2; ++i) r[i] = row(p0 + (lane >> 2) + 8 * i, is_new[i]);
-    put_keys<T, D>(page, tile & 3, r, is_new, src.wide);
+    put_keys<T, D>(page, tile & 3, r, is_new, WIDE || src.wide);
   } else {
     bool is_new[4];
     const T* r[4];
     for (int i = 0; i < 4; ++i) r[i] = row(p0 + 2 * (lane >> 2 & 3) + (i & 1) + 8 * (i >> 1), is_new[i]);
-    put_values<T, D>(page, tile & 3, r, is_new, src.wide);
+    put_values<T, D>(page, tile & 3, r, is_new, WIDE || src.wide);
   }
 }
 
 // Many rows: one CTA per (four tiles, head, sequence), a warp per tile of keys or values.  TODO
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kBigThreads) k_kv4_append(w4a8_kv4_cache c, Source k, Source v, int n_src, int n,
                                                             const int32_t* counts, const int32_t* index, int32_t* len_out,
                                                             bool store_len) {
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kBigThreads) k_kv4_append(w4a8_kv4_cache c, So
   if (end <= L) return;
   const int64_t tile = (int64_t)(L / kTile & ~3) + blockIdx.x * 4 + (warp & 3);  // a CTA's tiles are of one page
   if (tile < L / kTile || tile * kTile >= end) return;
-  append_tile<T, D>(c, warp >> 2 ? v : k, warp >> 2, s, h, (int)tile, L, end, n, index);
+  append_tile<T, D, WIDE>(c, warp >> 2 ? v : k, warp >> 2, s, h, (int)tile, L, end, n, index);
 }
 // A few rows (decode steps, accepted paths): one CTA per sequence takes all heads and then stores the length, so the call is one
 // launch.  Bound by latency: length, table, rows and old words one after the other.
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_kv4_append_few(w4a8_kv4_cache
   const int tiles = end > L ? (end - 1) / kTile - L / kTile + 1 : 0;
   for (int x = threadIdx.x >> 5; x < tiles * 2 * c.n_kv_heads; x += kSmallThreads / 32) {
     const int h = (x >> 1) % c.n_kv_heads, tile = L / kTile + (x >> 1) / c.n_kv_heads;
-    append_tile<T, D>(c, x & 1 ? v : k, x & 1, s, h, tile, L, end, n, index);
+    append_tile<T, D, false>(c, x & 1 ? v : k, x & 1, s, h, tile, L, end, n, index);
   }
   __syncthreads();  // every warp has read the old length
   if (threadIdx.x == 0 && (end >= 0 || len_out != c.len)) len_out[s] = end >= 0 ? end : c.len[s];
@@ -487,8 +489,16 @@ W4A8_API w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k
   auto run = [&](auto kern) {
     return launch_pdl(kern, grid, dim3(kBigThreads), 0, st, *c, ks, vs, n_src, n, counts, index, len_out, !own);
   };
-  W4A8_CUDA_TRY(f32 ? (d64 ? run(k_kv4_append<float, 64>) : run(k_kv4_append<float, 128>))
-                    : (d64 ? run(k_kv4_append<__nv_bfloat16, 64>) : run(k_kv4_append<__nv_bfloat16, 128>)));
+  auto typed = [&](auto t, auto all) {
+    using T = decltype(t);
+    constexpr bool WIDE = decltype(all)::value;
+    return d64 ? run(k_kv4_append<T, 64, WIDE>) : run(k_kv4_append<T, 128, WIDE>);
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  const bool all = ks.wide && vs.wide;
+  if (f32) W4A8_CUDA_TRY(all ? typed(float{}, yes) : typed(float{}, no));
+  else W4A8_CUDA_TRY(all ? typed(__nv_bfloat16{}, yes) : typed(__nv_bfloat16{}, no));
   if (own)
     W4A8_CUDA_TRY(launch_pdl(k_kv4_append_len, dim3((unsigned)c->n_seqs), dim3(index ? 128 : 32), 0, st, *c, n_src, n,
                              counts, index));

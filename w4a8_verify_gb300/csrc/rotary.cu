@@ -9,11 +9,14 @@
 // bits, and what is left of it, at most an eighth of a turn, goes to the sine and cosine as fp32.  (fp32 angles are off by
 // 2^-5 at position 2^19.)
 //
-// Bound by memory once rows are many: each value is read and written once.  Few tokens: the heads of a token are dealt to
-// several warps, each with the angles once more.
+// Bound by memory once rows are many: each value is read and written once (32768 tokens of 40 heads of 128 in bf16: 108 us,
+// 91% of the copy rate; the rows of a warp's next round are on their way while it works on one, and 32 warps an SM do
+// that: two rounds ahead with 16 warps took 164 us, the gains in registers with 24 warps 132).  Few tokens: the heads of a
+// token are dealt to several warps, each with the angles once more; 5 us for 256 tokens, bound by latency.
 #include "kv8.cuh"
 
 #include <cmath>
+#include <type_traits>
 
 using namespace w4a8;
 
@@ -40,9 +43,10 @@ __device__ __forceinline__ void unit(uint64_t turn, float& c, float& s) {
   if (quarter & 2u) s = -s;
 }
 
-// LPH lanes to a head (a power of two, D / 16 of them used); vec: 16-byte access to q, k, q_out, k_out (bits 0 to 3).
-template <typename T, int LPH>
-__global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a, RotGeom geo, int vec) {
+// LPH lanes to a head (a power of two, D / 16 of them used); vec: 16-byte access to q, k, q_out, k_out, q_gain, k_gain (bits 0 to 5);
+// WIDE: to all of them, known at compile time (with the other ways in the code bf16 does not fit 64 registers: 134 us for 108).
+template <typename T, int LPH, bool WIDE>
+__global__ void __launch_bounds__(kRotThreads, WIDE && sizeof(T) == 2 ? 4 : 3) k_qk_rotary(w4a8_qk_rotary_args a, RotGeom geo, int vec) {
   griddep_enter();
   constexpr int HPW = 32 / LPH;
   const int lane = threadIdx.x & 31, sub = lane % LPH, D = a.head_dim;
@@ -65,8 +69,8 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
     const int64_t at = place(it, on, key);
     if (!on) return;
     const T* p = static_cast<const T*>(key ? a.k.data : a.q.data) + at;
-    x0.load(p + d0, vec >> (int)key & 1);
-    y0.load(p + d1, vec >> (int)key & 1);
+    x0.load(p + d0, WIDE || (vec >> (int)key & 1));
+    y0.load(p + d1, WIDE || (vec >> (int)key & 1));
   };
   fetch(0);
   // the lanes of a frequency octet share its angles: PER each, then exchanged
@@ -92,8 +96,6 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
       sn[e] = __shfl_sync(0xffffffffu, ms[e % PER], e / PER * LPH + sub);
     }
   }
-  float gain[16];
-  int kind = -1;
   for (int it = 0; it < geo.iters; ++it) {
     bool on, key;
     (void)place(it, on, key);
@@ -107,14 +109,24 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       const float r = __frsqrt_rn(fmaf(sum, geo.inv_dim, a.eps));
-      if (on && kind != (int)key) {
-        kind = key;
-        const float* g = key ? a.k_gain : a.q_gain;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gain[e] = g ? g[d0 + e] : 1.0f, gain[8 + e] = g ? g[d1 + e] : 1.0f;
+      for (int e = 0; e < 8; ++e) x[e] *= r, y[e] *= r;
+      const float* g = key ? a.k_gain : a.q_gain;
+      if (g && live) {  // from L1: in registers they would cost a third of the warps
+        float u[8], v[8];
+        if (WIDE || (vec >> (4 + (int)key) & 1)) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(u + e) = *reinterpret_cast<const float4*>(g + d0 + e);
+            *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(g + d1 + e);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = g[d0 + e], v[e] = g[d1 + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= u[e], y[e] *= v[e];
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * r * gain[e], y[e] = y[e] * r * gain[8 + e];
     }
     if (halves) {
 #pragma unroll
@@ -139,8 +151,8 @@ __global__ void __launch_bounds__(kRotThreads) k_qk_rotary(w4a8_qk_rotary_args a
       T* p = static_cast<T*>(out.data) + s * out.seq + j * out.row + (int64_t)(key ? h - a.n_heads : h) * out.head;
       Eight<T> x1, y1;
       x1.set(x), y1.set(y);
-      x1.store(p + d0, vec >> (2 + (int)key) & 1);
-      y1.store(p + d1, vec >> (2 + (int)key) & 1);
+      x1.store(p + d0, WIDE || (vec >> (2 + (int)key) & 1));
+      y1.store(p + d1, WIDE || (vec >> (2 + (int)key) & 1));
     }
   }
 }
@@ -188,8 +200,9 @@ W4A8_API w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* arg, void* stream
                (!same_rows(a.k, a.k_out, S, n, Hk) && rows_meet(a.k_out, Hk, a.k, Hk, S, n, D, el)) ||
                rows_meet(a.k_out, Hk, a.q, Hq, S, n, D, el) || rows_meet(a.q_out, Hq, a.k, Hk, S, n, D, el)))
     return W4A8_ERR_ARG;
-  auto wide = [&](const w4a8_rows& r) { return r.data && kv8_vec_rows(r, a.dtype) ? 1 : 0; };
-  const int vec = wide(a.q) | wide(a.k) << 1 | wide(a.q_out) << 2 | wide(a.k_out) << 3;
+  auto wide = [&](const w4a8_rows& r) { return !r.data || kv8_vec_rows(r, a.dtype) ? 1 : 0; };
+  const int vec = wide(a.q) | wide(a.k) << 1 | wide(a.q_out) << 2 | wide(a.k_out) << 3 |
+                  (aligned(a.q_gain, 16) ? 16 : 0) | (aligned(a.k_gain, 16) ? 32 : 0);
   const int lph = D <= 64 ? 4 : D <= 128 ? 8 : 16;
   const int rounds = (Hq + Hk + 32 / lph - 1) / (32 / lph);
   const int64_t tokens = (int64_t)S * n;
@@ -207,9 +220,14 @@ W4A8_API w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* arg, void* stream
   auto run = [&](auto four, auto eight, auto sixteen) {
     return launch_pdl(lph == 4 ? four : lph == 8 ? eight : sixteen, grid, dim3(kRotThreads), 0, st, a, geo, vec);
   };
-  if (a.dtype == W4A8_F32)
-    W4A8_CUDA_TRY(run(k_qk_rotary<float, 4>, k_qk_rotary<float, 8>, k_qk_rotary<float, 16>));
-  else
-    W4A8_CUDA_TRY(run(k_qk_rotary<__nv_bfloat16, 4>, k_qk_rotary<__nv_bfloat16, 8>, k_qk_rotary<__nv_bfloat16, 16>));
+  auto typed = [&](auto t, auto all) {
+    using T = decltype(t);
+    constexpr bool WIDE = decltype(all)::value;
+    return run(k_qk_rotary<T, 4, WIDE>, k_qk_rotary<T, 8, WIDE>, k_qk_rotary<T, 16, WIDE>);
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (a.dtype == W4A8_F32) W4A8_CUDA_TRY(vec == 63 ? typed(float{}, yes) : typed(float{}, no));
+  else W4A8_CUDA_TRY(vec == 63 ? typed(__nv_bfloat16{}, yes) : typed(__nv_bfloat16{}, no));
   return W4A8_OK;
 }
