@@ -240,3 +240,69 @@ def test_new_lengths_on_what_the_call_reads_are_refused():
     for counts, index, out in ((0x50000, None, 0x50000), (0x50000, None, 0x5000c), (None, 0x50000, 0x503fc), (None, None, 0x20010),
                                (None, None, 0x30004), (None, None, 0x40000 - 4), (0x30000, None, 0x30000)):
         assert call(counts, index, out) == 1, (counts, index, out)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_new_rows_in_the_grid_of_the_wide_kernel(D, dtype):
+    """A few blocks of new rows are CTAs behind those of the pages: ragged counts, strides that are not of 16 bytes, no new
+    rows at all, a cache of length zero, and copies that are withheld from the first CTA."""
+    _need_gpu()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    S, H, G, n = 3, 2, 4, 13
+    lens = torch.tensor([260, 0, 70], dtype=torch.int32, device="cuda")
+    cache, held = _cache(g, S, H, D, lens, dtype)
+    rows = _randn(g, (S, n, H * (G + 2), D + 1), dtype)[..., 1:]
+    q, k, v = rows[:, :, :H * G], rows[:, :, H * G:H * G + H], rows[:, :, H * G + H:]
+    counts = torch.tensor([n, n - 1, 5], dtype=torch.int32, device="cuda")
+    out = torch.full((S, n, H * G, D), 7.0, dtype=TYPES[dtype], device="cuda")
+    cache.attention(q, k, v, scale=0.1, counts=counts, out=out)
+    _check(cache, held, q, k, v, 0.1, counts, out)
+    assert (out[torch.arange(n, device="cuda") >= counts[:, None]] == 7).all()
+    alone = cache.attention(q, scale=0.1)
+    _check(cache, held, q, None, None, 0.1, None, alone)
+    assert (alone[1] == 0).all() and cache.check() == 0
+    real = cache._attention
+    want = cache.attention(q, k, v, scale=0.1)
+    try:
+        cache._attention = lambda c, a, w, b, st: W.lib().w4a8_kv4_attention_inject_timeout(c, a, w, b, 0, st)
+        got = cache.attention(q, k, v, scale=0.1)
+        assert cache.check() == W.FLAG_ERR_TIMEOUT
+    finally:
+        cache._attention = real
+    bad = torch.isnan(got).any(-1)
+    assert bad.any() and not bad.all() and torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+    cache.tensors["ctl"].zero_()
+    assert torch.equal(cache.attention(q, k, v, scale=0.1), want) and cache.check() == 0
+
+
+@gpu
+def test_two_captured_graphs_with_one_memory_pool():
+    """The workspace of a captured call is set up by the call: a second graph that is given the first one's memory, and replays of
+    both in turn, do not meet what the other left."""
+    _need_gpu()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    S, H, G, D = 2, 4, 4, 128
+    lens = torch.tensor([1500, 333], dtype=torch.int32, device="cuda")
+    cache, _ = _cache(g, S, H, D, lens, "fp32")
+    work, graphs, pool = [], [], None
+    for n in (1, 2, 12):
+        q, k, v = (_randn(g, (S, n, h, D), "fp32") for h in (H * G, H, H))
+        want = cache.attention(q, k, v, scale=0.1)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        out = torch.empty_like(want)
+        with torch.cuda.graph(graph, pool=pool):
+            cache.attention(q, k, v, scale=0.1, out=out)
+        pool = pool or graph.pool()
+        graphs.append(graph)
+        work.append((q, k, v, out, want))
+    for i in (0, 1, 2, 1, 0, 0, 2, 1):
+        work[i][3].fill_(0)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(work[i][3], work[i][4]), i
+    assert cache.check() == 0

@@ -38,11 +38,10 @@ w4a8_status plan_of(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, Plan* p) {
     if (blocks >= (int64_t)1 << 31) return W4A8_ERR_SHAPE;
     if (blocks <= kKv4Ctas / 6) g.folded = (int)blocks, most_ctas -= g.folded;
   }
-  g.ctas = (int)(units < most_ctas ? units : most_ctas);
-  const size_t ng = (units + g.ctas - 1) / g.ctas, most = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype) / 2;
-  g.ng = (int)(ng < most ? ng : most);
+  const size_t workers = p->wide ? 1 : (size_t)kv4_split_warps(g.R, a->dtype) / 2, ctas = (units + workers - 1) / workers;
+  g.ctas = (int)(ctas < most_ctas ? ctas : most_ctas);
   const size_t row = (size_t)g.RB * 4, D = (size_t)c->head_dim;
-  const size_t slots = p->wide ? g.ctas + 2 * segments : 5 * (size_t)g.ctas * g.ng;
+  const size_t slots = p->wide ? g.ctas + 2 * segments : 5 * g.ctas * workers;
   p->ml = W4A8_KV4_TICKETS;
   p->o = up256(p->ml + slots * row * 2);
   p->prefix = p->rml = p->ro = p->bytes = up256(p->o + slots * row * D);

@@ -23,8 +23,9 @@
 //
 // Work: every (sequence, KV head, block of rows) is a segment of units: its new rows, then pages (one empty unit where there
 // is nothing).  The units of all segments, end to end, are cut into equal ranges, one for each pair of warps, so ragged batches
-// balance.  A pair has its own ring of whole pages, one bulk copy each (four copies to half a page cost the copy engine
-// 105 us of a served batch of 64 sequences, whole pages 66); a warp takes the page's tokens 0..31 or 32..63, and the one that is
+// balance.  Few units go to few CTAs, a pair each (129 units of one row to 17 CTAs instead of 129: 12 us for 21, the parts that are
+// left to join are an eighth).  A pair has its own ring of whole pages, one bulk copy each (four copies to half a page, the
+// arithmetic left out, took 105 us of a served batch of 64 sequences, whole pages 88); a warp takes the page's tokens 0..31 or 32..63, and the one that is
 // done with a ring entry last refills it, so nobody waits for the other.  The new rows are done in plain fp32, every second
 // by either warp.  A segment that lies within one pair's range is finished there; the warps of a CTA add up where they
 // hold the same one; and where several CTAs do, each stores its part, and the one that comes last (a ticket, which it sets back
@@ -50,7 +51,7 @@ static_assert(W4A8_KV4_TICKETS >= kKv4Ctas * kKv4MaxWarps * 4, "tickets");
 struct Kv4Geom {       // of one call, the same for every kernel of it
   int n, G, R;         // new rows; query heads per KV head; query rows of a KV head
   int RB, CB;          // rows of a column block; column blocks
-  int ctas, ng;        // of the kernel over the pages, and its workers (split: pairs of warps) in each at most
+  int ctas;            // of the kernel over the pages
   int segments;
   int tiles;           // wide calls: blocks of 16 new rows
   int folded;          // CTAs behind the others of the kernel over the pages, for the new rows; 0: those are a kernel of their own
@@ -205,14 +206,14 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
   // equal ranges of the U units: the first `more` of the W workers have one more than `each`
   const int U = prefix[S];
   if (U == 0) return;
-  const int ng = min(NP, (U + geo.ctas - 1) / geo.ctas), W = min(U, geo.ctas * ng), each = U / W, more = U % W;
+  const int W = min(U, geo.ctas * NP), each = U / W, more = U % W;
   auto begin_of = [&](int w) { return w * each + min(w, more); };
   auto worker_at = [&](int u) {
     const int x = more * (each + 1);
     return u < x ? u / (each + 1) : more + (u - x) / each;
   };
-  const int worker = blockIdx.x * ng + pair;
-  const bool has = pair < ng && worker < W;
+  const int worker = blockIdx.x * NP + pair;
+  const bool has = worker < W;
   const int u0 = has ? begin_of(worker) : 0, u1 = has ? begin_of(worker + 1) : 0;
 
   // The lane's unit x (32 units in parallel, so the table's latency is paid once).
@@ -631,13 +632,13 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     p.seg = sg;
     p.w0 = worker_at(first), p.w1 = worker_at(end - 1);
     p.early = begin_of(p.w1 + 1) > end;
-    p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / ng - p.w0 / ng + 1;
+    p.held = p.w1 - p.early < p.w0 ? 0 : (p.w1 - p.early) / NP - p.w0 / NP + 1;
     return p;
   };
   auto rows_of = [&](int sg) { return min(RB, count_of(sg / geo.CB / H) * geo.G - sg % geo.CB * RB); };
   // The parts first, first + step, .. of a segment's row, of the CTAs in their order, then the early ones: maximum M,
   // sum, and values of the lane's dims; B loads in flight.
-  const int slots = geo.ctas * geo.ng;
+  const int slots = geo.ctas * NP;
   constexpr int B = NT == 1 ? 10 : 16;
   auto gather = [&](const Parts& p, int r, int first, int step, float& M, float& sum, float (&o)[E]) {
     const int n = p.held + 2 * p.early, apart = p.held ? slots : 3 * slots;
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
         ml[b] = make_float2(-INFINITY, 0.0f);
         v[b] = {};
         if (i < n) {
-          const size_t at = (size_t)(i < p.held ? max(p.w0, (p.w0 / ng + i) * ng) : apart + 2 * p.w1 + i - p.held) * RB + r;
+          const size_t at = (size_t)(i < p.held ? max(p.w0, (p.w0 / NP + i) * NP) : apart + 2 * p.w1 + i - p.held) * RB + r;
           ml[b] = __ldcg(ws.ml + at);
           v[b] = __ldcg(reinterpret_cast<const Vec*>(ws.o + at * D + E * lane));
         }
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
       kv8_store(out, L == 0.0f ? 0.0f : v.x / L), kv8_store(out + 1, L == 0.0f ? 0.0f : v.y / L);
       kv8_store(out + 2, L == 0.0f ? 0.0f : v.z / L), kv8_store(out + 3, L == 0.0f ? 0.0f : v.w / L);
     } else {
-      const size_t at = (size_t)(blockIdx.x * ng + i0 / 2) * RB + r;
+      const size_t at = (size_t)(blockIdx.x * NP + i0 / 2) * RB + r;
       reinterpret_cast<float4*>(ws.o + at * D)[d] = v;
       if (d == 0) ws.ml[at] = make_float2(M, L);
     }
@@ -905,16 +906,17 @@ cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, 
 // Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu): a tile of it takes 128 rows at one price, the split
 // kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  Short caches of few (sequence, KV head) pairs are bound by
 // latency, where the wide kernel with the new rows in its own grid is the shorter way; otherwise the blocks count.  Measured
-// (us, split / wide; pairs x tokens, heads of 128):
-//   fp32,   8 x 4096:    8 rows 20 / 20,  12 rows 24 / 21,  16 rows 25 / 21,  32 rows 32 / 21
-//   fp32,   8 x 32000:  16 rows 44 / 66,  24 rows 57 / 66,  32 rows 72 / 66;   8 x 131071:  24 rows 174 / 225,  32 rows 221 / 225
-//   fp32, 128 x to 4096:  12 rows 64 / 87,  16 rows 70 / 90,  20 rows 109 / 92
-//   bf16,   8 x 4096:    8 rows 18 / 17,  12 rows 30 / 18;   8 x 32000:  8 rows 28 / 43,  12 rows 45 / 45,  16 rows 50 / 45
-//   bf16,   8 x 131071: 16 rows 90 / 139,  20 rows 125 / 140,  32 rows 134 / 141;   128 x to 4096:  16 rows 66 / 78,  20 rows 103 / 78
+// (us, split / wide; pairs x tokens, heads of 128 unless said):
+//   fp32, 8 x 4096:  8 rows 18 / 20,  12 rows 21 / 21,  16 rows 23 / 21,  32 rows 31 / 21;  4 x 4096 of 64:  16 rows 15 / 18,  24 rows 19 / 19
+//   fp32, 8 x 16000:  16 rows 30 / 39,  24 rows 38 / 40,  32 rows 46 / 40;  8 x 32000:  24 rows 55 / 66,  32 rows 69 / 66
+//   fp32, 128 x to 4096:  12 rows 63 / 87,  16 rows 69 / 90,  20 rows 108 / 92
+//   bf16, 8 x 4096:  8 rows 15 / 17,  12 rows 26 / 18;  8 x 16000:  8 rows 23 / 28,  12 rows 34 / 29,  16 rows 38 / 29
+//   bf16, 8 x 32000:  12 rows 40 / 45,  16 rows 42 / 45,  20 rows 51 / 45;   128 x to 4096:  16 rows 65 / 78,  20 rows 103 / 79
 inline bool kv4_is_wide(const w4a8_kv4_cache& c, int R, int dtype) {
   const int64_t pairs = (int64_t)c.n_seqs * c.n_kv_heads, pages = pairs * c.max_pages;
-  if (pairs <= kKv4Ctas / 6 && pages <= (dtype == W4A8_F32 ? 512 : 4096)) return R > 8;
-  return R > (dtype == W4A8_F32 && pairs <= 16 ? 24 : 16);
+  const bool f32 = dtype == W4A8_F32;
+  if (pairs <= kKv4Ctas / 6 && pages <= (f32 ? 512 : 2048)) return R > (f32 && c.head_dim == 64 ? 16 : 8);
+  return R > (f32 && pairs <= 16 ? 24 : 16);
 }
 cudaError_t kv4_wide(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
 // one translation unit per head size and element type
