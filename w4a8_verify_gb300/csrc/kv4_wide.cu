@@ -19,6 +19,23 @@
 namespace w4a8 {
 namespace {
 
+// Two fp32 numbers in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Warp roles.  Softmax and value warps sit where their number modulo 4 names the tensor-memory lanes they may touch.
 constexpr int kSoftWarps = 4, kSumWarps = 8, kConvWarps = 4;
 constexpr int kSum0 = kSoftWarps, kConv0 = kSum0 + kSumWarps, kMmaWarp = kConv0 + kConvWarps, kCopyWarp = kMmaWarp + 1;
@@ -613,13 +630,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
               for (int e = 0; e < 32; ++e)
                 if (32 * y + e >= tokens) v[e] = __float_as_uint(-INFINITY);
             }
-            float sum[2] = {0.0f, 0.0f}, top[2] = {mx, mx};
+            float2 sum = make_float2(0.0f, 0.0f);
+            float top[2] = {mx, mx};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float s = __uint_as_float(v[e]);
-              top[e & 1] = fmaxf(top[e & 1], s);
-              v[e] = __float_as_uint(NQ == 2 ? ex2(fmaf(s, collow, fmaf(s, colfac, -base))) * C::PSCALE
-                                             : ex2(fmaf(s, colfac, 7.0f - base)));
+            for (int e = 0; e < 32; e += 2) {
+              const float2 s = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              top[0] = fmaxf(top[0], s.x), top[1] = fmaxf(top[1], s.y);
+              const float off = NQ == 2 ? -base : 7.0f - base;
+              float2 y = fma2(s, make_float2(colfac, colfac), make_float2(off, off));
+              if (NQ == 2) y = fma2(s, make_float2(collow, collow), y);
+              v[e] = __float_as_uint(NQ == 2 ? ex2(y.x) * C::PSCALE : ex2(y.x));
+              v[e + 1] = __float_as_uint(NQ == 2 ? ex2(y.y) * C::PSCALE : ex2(y.y));
             }
             if (part) {  // a factor of 0 makes NaN of what is not there
               __syncwarp();
@@ -632,7 +653,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
             for (int z = 0; z < 16; ++z) {
               const int tok = (z >> 1 & 1) * 16 + (z & 1) * 8 + (z >> 2) * 2;
               const float e0 = __uint_as_float(v[tok]), e1 = __uint_as_float(v[tok + 1]);
-              sum[0] += e0, sum[1] += e1;
+              sum = add2(sum, make_float2(e0, e1));
               if (NQ == 2) {
                 const float w0 = whole(e0), w1 = whole(e1);
                 hi[z] = pack_f16(w0, w1);
@@ -642,7 +663,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
               }
             }
             mx = fmaxf(top[0], top[1]);
-            ps += sum[0] + sum[1];
+            ps += sum.x + sum.y;
             tc_store16(mine + C::cP + b.i % C::NP * NQ * (kPage / 2) + 16 * y, hi);
             if (NQ == 2) tc_store16(mine + C::cP + kPage / 2 + 16 * y, lo);
           }
@@ -707,7 +728,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
           uint32_t v[16];
           tc_load16(mine + ob.i * D + d, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) O[d + e] += __uint_as_float(v[e]);
+          for (int e = 0; e < 16; e += 2) {
+            const float2 o = add2(make_float2(O[d + e], O[d + e + 1]), make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+            O[d + e] = o.x, O[d + e + 1] = o.y;
+          }
         }
         tc_before();
         __syncwarp();
