@@ -375,7 +375,7 @@ w4a8_status w4a8_kv4_check(const w4a8_kv4_cache* c, uint32_t* flags);
  * position len[s] + j takes source row index[s][j] in 0..n_src-1 (e.g. the accepted path of a draft tree; the same row may
  * come twice); with it n <= 1024, without it n_src >= n (W4A8_ERR_SHAPE).  The new lengths go to len_out (device int32[n_seqs]);
  * len_out == c->len advances the cache, another one leaves c->len alone, and the cache is right at either; on counts, index,
- * the rest of the cache's buffers or a part of c->len it is refused (W4A8_ERR_ARG).  A sequence
+ * the rest of the cache's buffers or a part of c->len it is refused (W4A8_ERR_ARG), as are rows of k or v on it or on the pages.  A sequence
  * that would pass 64 * max_pages tokens stays as it was, as does one with a row out of range; a page whose table entry is out of
  * range takes no rows.  An n beyond 64 * max_pages is W4A8_ERR_CAPACITY. */
 w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k, const w4a8_rows* v, int dtype, int n_src,

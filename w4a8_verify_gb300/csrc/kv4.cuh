@@ -39,6 +39,8 @@ inline w4a8_status kv4_valid(const w4a8_kv4_cache* c) {
   return W4A8_OK;
 }
 
+inline size_t kv4_pool_bytes(const w4a8_kv4_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * 68 * (size_t)c.head_dim; }
+
 // Committed length of sequence s, or -1 (and the status bit) where it is out of range.
 __device__ __forceinline__ int kv4_len(const w4a8_kv4_cache& c, const int32_t* len, int s) {
   const int L = __ldcg(len + s);  // from L2: a kernel that starts early reads it before it waits for the last one

@@ -434,7 +434,7 @@ W4A8_API w4a8_status w4a8_kv4_bytes(const w4a8_kv4_cache* c, size_t bytes[4]) {
   const w4a8_status st = kv4_dims(c);
   if (st != W4A8_OK) return st;
   if (!bytes) return W4A8_ERR_ARG;
-  bytes[0] = (size_t)c->n_pages * c->n_kv_heads * 68 * (size_t)c->head_dim;
+  bytes[0] = kv4_pool_bytes(*c);
   bytes[1] = (size_t)c->n_seqs * c->max_pages * 4;
   bytes[2] = (size_t)c->n_seqs * 4;
   bytes[3] = 4;
@@ -467,14 +467,16 @@ W4A8_API w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k
   if (!aligned(k->data, kv8_elem(dtype)) || !aligned(v->data, kv8_elem(dtype)) || !aligned(counts, 4) ||
       !aligned(index, 4) || !aligned(len_out, 4))
     return W4A8_ERR_ARG;
-  // new lengths on what other CTAs of the call still read (they may take the place of the old ones)
-  const size_t S4 = 4 * (size_t)c->n_seqs;
-  auto on = [&](const void* p, size_t bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(len_out);
-    return p && x < y + S4 && y < x + bytes;
+  // new lengths on what the call writes, or other CTAs of it still read (they may take the place of the old ones); rows on what it writes
+  const size_t S4 = 4 * (size_t)c->n_seqs, pool = kv4_pool_bytes(*c);
+  auto on = [&](const void* p, size_t bytes) { return bytes_meet(p, bytes, len_out, S4); };
+  auto written = [&](const w4a8_rows& r) {
+    const size_t el = kv8_elem(dtype);
+    return rows_touch(r, c->n_kv_heads, c->n_seqs, n_src, c->head_dim, el, len_out, S4) ||
+           rows_touch(r, c->n_kv_heads, c->n_seqs, n_src, c->head_dim, el, c->pages, pool);
   };
-  if (on(counts, S4) || on(index, S4 * n) || on(c->table, S4 * c->max_pages) || on(c->ctl, 4) ||
-      (len_out != c->len && on(c->len, S4)))
+  if (on(counts, S4) || on(index, S4 * n) || on(c->table, S4 * c->max_pages) || on(c->ctl, 4) || on(c->pages, pool) ||
+      (len_out != c->len && on(c->len, S4)) || written(*k) || written(*v))
     return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages) return W4A8_ERR_CAPACITY;
   cudaStream_t st = as_stream(stream);

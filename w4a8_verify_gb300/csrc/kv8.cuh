@@ -119,6 +119,39 @@ inline bool rows_meet(const w4a8_rows& x, int heads_x, const w4a8_rows& y, int h
   return all > (Wide)1 << 20 || rows_overlap(whole, S, n, (int)all, D, kMaxDifferences);
 }
 
+// Whether the a bytes at p and the b bytes at q share one (NULL: no).
+inline bool bytes_meet(const void* p, size_t a, const void* q, size_t b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+  return p && q && x < y + b && y < x + a;
+}
+// Whether one of the S x n x heads rows of D elements of el bytes lies on the bytes at p (NULL: no).  Where the address ranges
+// cross, the first row behind p - D el is looked for along the longest axis, for each pair of the others' indexes (more than
+// kMaxDifferences pairs: taken as touching).
+inline bool rows_touch(const w4a8_rows& r, int heads, int S, int n, int D, size_t el, const void* p, size_t bytes) {
+  using Wide = __int128;
+  struct Axis {
+    Wide stride;
+    int size;
+  } ax[3] = {{(Wide)r.seq * (Wide)el, S}, {(Wide)r.row * (Wide)el, n}, {(Wide)r.head * (Wide)el, heads}};
+  const Wide row = (Wide)D * (Wide)el, lo = (Wide)reinterpret_cast<uintptr_t>(p), hi = lo + (Wide)bytes;
+  Wide base = (Wide)reinterpret_cast<uintptr_t>(r.data), extent = row;
+  for (Axis& x : ax) {  // from the lowest row on, upwards
+    const Wide all = (x.size - 1) * x.stride;
+    if (all < 0) base += all, x.stride = -x.stride;
+    extent += all < 0 ? -all : all;
+  }
+  if (!p || !r.data || base + extent <= lo || hi <= base) return false;
+  std::sort(ax, ax + 3, [](const Axis& x, const Axis& y) { return x.size > y.size; });
+  if ((int64_t)ax[1].size * ax[2].size > kMaxDifferences) return true;
+  for (int i = 0; i < ax[1].size; ++i)
+    for (int j = 0; j < ax[2].size; ++j) {
+      const Wide at = base + i * ax[1].stride + j * ax[2].stride, d = lo - row - at;
+      const Wide k = d < 0 ? 0 : ax[0].stride ? d / ax[0].stride + 1 : ax[0].size;
+      if (k < ax[0].size && at + k * ax[0].stride < hi) return true;
+    }
+  return false;
+}
+
 // (sequence, KV head) pair index and page addresses: 64-bit, a long cache passes 4 GB
 __device__ __forceinline__ size_t kv8_pair(const w4a8_kv8_cache& c, int s, int h) { return (size_t)s * c.n_kv_heads + h; }
 __device__ __forceinline__ size_t kv8_page(const w4a8_kv8_cache& c, size_t pair, int phys) {
