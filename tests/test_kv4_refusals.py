@@ -64,3 +64,22 @@ def test_only_rows_that_lie_there_are_refused(lib):
         assert status == (ARG if touch else 4), (data, strides, touch)
         seen[touch] += 1
     assert min(seen) > 40
+
+
+def _attn(out, n=2, heads=4, counts=None, mask=None, strides=None):
+    at = lambda base, h: W.Rows(base, n * h * D, h * D, D)  # noqa: E731
+    q, k, v = at(0x10000000, heads), at(0x18000000, H), at(0x1c000000, H)
+    return W.KV4Attn(n, heads, 0, 0.1, q, W.Rows(out, *(strides or (n * heads * D, heads * D, D))), k, v, counts, mask)
+
+
+def test_attention_output_on_what_it_reads(lib):
+    ws, need = 0x40000000, ctypes.c_size_t()
+    assert lib.w4a8_kv4_attention_workspace_bytes(DESC, ctypes.byref(_attn(0x20000000)), ctypes.byref(need)) == 0
+    counts, mask, n, heads = 0x50000000, 0x60000000, 2, 4
+    call = lambda a, b=need.value: lib.w4a8_kv4_attention(DESC, ctypes.byref(a), ws, b, None)  # noqa: E731
+    end = 4 * (S * n * heads * D - 1)                                # bytes to the output's last element
+    for at, size in ((PAGES, POOL), (TABLE, 4 * S * P), (LEN, 4 * S), (CTL, 4), (counts, 4 * S), (mask, 8 * S * n), (ws, need.value)):
+        for out in (at, at + size - 4, at - end):
+            assert call(_attn(out, counts=counts, mask=mask)) == ARG, hex(out)
+        # one row of many on it, the others around
+        assert call(_attn(at + size - 4 - 3 * (1 << 20) * 4, counts=counts, mask=mask, strides=(1 << 20, 1 << 16, 1 << 10))) == ARG

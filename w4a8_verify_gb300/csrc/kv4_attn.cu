@@ -71,6 +71,10 @@ w4a8_status attend(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, void* worksp
   if (rows_overlap(a->out, S, n, a->n_heads, D, kMaxDifferences) || rows_meet(a->out, a->n_heads, a->q, a->n_heads, S, n, D, el) ||
       (a->k.data && (rows_meet(a->out, a->n_heads, a->k, H, S, n, D, el) || rows_meet(a->out, a->n_heads, a->v, H, S, n, D, el))))
     return W4A8_ERR_ARG;
+  auto on = [&](const void* at, size_t bytes) { return rows_touch(a->out, a->n_heads, S, n, D, el, at, bytes); };
+  if (on(c->pages, kv4_pool_bytes(*c)) || on(c->table, 4 * (size_t)S * c->max_pages) || on(c->len, 4 * (size_t)S) || on(c->ctl, 4) ||
+      on(a->counts, 4 * (size_t)S) || on(a->mask, 8 * (size_t)S * n) || on(workspace, p.bytes))
+    return W4A8_ERR_ARG;
   char* base = static_cast<char*>(workspace);
   const Kv4Scratch ws{reinterpret_cast<int*>(base),          reinterpret_cast<float2*>(base + p.ml),
                       reinterpret_cast<float*>(base + p.o),  reinterpret_cast<int*>(base + p.prefix),
