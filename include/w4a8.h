@@ -454,7 +454,8 @@ typedef struct {
 } w4a8_qk_rotary_args;
 /* Device.  q_out may be q itself and k_out k itself, with the same strides; any other way for an output to lie on an input
  * or on itself is refused where the address ranges cross (W4A8_ERR_ARG), but for rows side by side in one tensor (the
- * parts of one projection's output: equal seq and row strides, heads that do not meet).  n_seqs * n * (n_heads + n_kv_heads) < 2^31. */
+ * parts of one projection's output: equal seq and row strides, heads that do not meet); rows of an output on the tables,
+ * positions, counts or gains are refused likewise.  n_seqs * n * (n_heads + n_kv_heads) < 2^31. */
 w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* a, void* stream);
 
 /* ==============================================================================

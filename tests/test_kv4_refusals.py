@@ -83,3 +83,19 @@ def test_attention_output_on_what_it_reads(lib):
             assert call(_attn(out, counts=counts, mask=mask)) == ARG, hex(out)
         # one row of many on it, the others around
         assert call(_attn(at + size - 4 - 3 * (1 << 20) * 4, counts=counts, mask=mask, strides=(1 << 20, 1 << 16, 1 << 10))) == ARG
+
+
+def test_rotation_outputs_on_its_tables(lib):
+    S, n, Hq, Hk, D, axes = 2, 3, 4, 2, 64, 3
+    names = (("turns", 8 * 32), ("axis", 32), ("pos", 4 * axes * S * n), ("start", 4 * S), ("counts", 4 * S), ("q_gain", 4 * D),
+             ("k_gain", 4 * D))
+    at = {name: 0x100000 * (i + 1) for i, (name, _) in enumerate(names)}
+    rows = lambda base, h: W.Rows(base, n * h * D, h * D, D)  # noqa: E731
+    for name, size in names:
+        for out, h in (("q_out", Hq), ("k_out", Hk)):
+            end = 4 * (S * n * h * D - 1)
+            for place in (at[name], at[name] + (size - 1) // 4 * 4, at[name] - end):
+                a = W.QKRotaryArgs(S, n, Hq, Hk, D, D, axes, 0, 0, 1, 1e-6, 1.0, *at.values(), rows(0x10000000, Hq),
+                                   rows(0x20000000, Hq), rows(0x30000000, Hk), rows(0x40000000, Hk))
+                getattr(a, out).data = place
+                assert lib.w4a8_qk_rotary(ctypes.byref(a), None) == ARG, (name, out, hex(place))

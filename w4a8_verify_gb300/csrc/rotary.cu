@@ -200,6 +200,13 @@ W4A8_API w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* arg, void* stream
                (!same_rows(a.k, a.k_out, S, n, Hk) && rows_meet(a.k_out, Hk, a.k, Hk, S, n, D, el)) ||
                rows_meet(a.k_out, Hk, a.q, Hq, S, n, D, el) || rows_meet(a.q_out, Hq, a.k, Hk, S, n, D, el)))
     return W4A8_ERR_ARG;
+  const size_t half = (size_t)a.rot_dim / 2, places = 4 * (size_t)S * n * a.n_axes, gain = 4 * (size_t)D;
+  auto on = [&](const w4a8_rows& out, int heads) {  // what other warps of the call still read
+    const auto at = [&](const void* p, size_t bytes) { return rows_touch(out, heads, S, n, D, el, p, bytes); };
+    return at(a.turns, 8 * half) || at(a.axis, half) || at(a.pos, places) || at(a.start, 4 * (size_t)S) ||
+           at(a.counts, 4 * (size_t)S) || at(a.q_gain, gain) || at(a.k_gain, gain);
+  };
+  if (on(a.q_out, Hq) || (keys && on(a.k_out, Hk))) return W4A8_ERR_ARG;
   auto wide = [&](const w4a8_rows& r) { return !r.data || kv8_vec_rows(r, a.dtype) ? 1 : 0; };
   const int vec = wide(a.q) | wide(a.k) << 1 | wide(a.q_out) << 2 | wide(a.k_out) << 3 |
                   (aligned(a.q_gain, 16) ? 16 : 0) | (aligned(a.k_gain, 16) ? 32 : 0);
