@@ -382,7 +382,7 @@ w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k, const w
                             int n, const int32_t* counts, const int32_t* index, int32_t* len_out, void* stream);
 /* Device.  Positions first[s] .. first[s] + n - 1 of every sequence as the cache holds them (c * s: exact in either type),
  * positions at or behind len[s] as 0, into k_out and v_out, dtype [n_seqs][n][n_kv_heads][head_dim] contiguous, 16-byte
- * aligned.  len: NULL = c->len.  A sequence whose length or first position is out of range is read as 0, as is a page whose
+ * aligned, on nothing that the call reads nor on one another (W4A8_ERR_ARG).  len: NULL = c->len.  A sequence whose length or first position is out of range is read as 0, as is a page whose
  * table entry is. */
 w4a8_status w4a8_kv4_read(const w4a8_kv4_cache* c, const int32_t* first, const int32_t* len, int n, int dtype,
                           void* k_out, void* v_out, void* stream);

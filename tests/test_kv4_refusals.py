@@ -99,3 +99,12 @@ def test_rotation_outputs_on_its_tables(lib):
                                    rows(0x20000000, Hq), rows(0x30000000, Hk), rows(0x40000000, Hk))
                 getattr(a, out).data = place
                 assert lib.w4a8_qk_rotary(ctypes.byref(a), None) == ARG, (name, out, hex(place))
+
+
+def test_read_outputs_on_what_it_reads(lib):
+    n, far, first, length = 64, 0x70000000, 0x50000000, 0x60000000
+    bytes_ = S * n * H * D * 2
+    call = lambda k, v: lib.w4a8_kv4_read(DESC, first, length, n, 1, k, v, None)  # noqa: E731
+    for at, size in ((PAGES, POOL), (TABLE, 4 * S * P), (LEN, 4 * S), (CTL, 4), (first, 4 * S), (length, 4 * S), (far, bytes_)):
+        for out in (at, at + size - 16 if size > 16 else at, at - bytes_ + 16):
+            assert call(out, far) == ARG and call(far, out) == ARG, hex(out)

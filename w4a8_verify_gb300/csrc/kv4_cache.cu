@@ -518,6 +518,12 @@ W4A8_API w4a8_status w4a8_kv4_read(const w4a8_kv4_cache* c, const int32_t* first
       n < 1 || !kv8_dtype(dtype))
     return W4A8_ERR_ARG;
   if (n > kPage * c->max_pages) return W4A8_ERR_CAPACITY;
+  const size_t S4 = 4 * (size_t)c->n_seqs, bytes = (size_t)c->n_seqs * n * c->n_kv_heads * c->head_dim * kv8_elem(dtype);
+  for (const void* out : {k_out, v_out})  // on one another, or on what other CTAs still read
+    if (bytes_meet(out, bytes, c->pages, kv4_pool_bytes(*c)) || bytes_meet(out, bytes, c->table, S4 * c->max_pages) ||
+        bytes_meet(out, bytes, c->len, S4) || bytes_meet(out, bytes, c->ctl, 4) || bytes_meet(out, bytes, first, S4) ||
+        bytes_meet(out, bytes, len, S4) || bytes_meet(k_out, bytes, v_out, bytes))
+      return W4A8_ERR_ARG;
   const dim3 grid((unsigned)((n + kPage - 1 + kPage - 1) / kPage), (unsigned)c->n_kv_heads, (unsigned)c->n_seqs);
   const int32_t* L = len ? len : c->len;
   cudaStream_t st = as_stream(stream);
