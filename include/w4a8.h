@@ -362,7 +362,8 @@ typedef struct {
 
 /* Host.  Bytes of the four buffers of a cache with these dimensions, in the struct's order. */
 w4a8_status w4a8_kv4_bytes(const w4a8_kv4_cache* c, size_t bytes[4]);
-/* Device.  Empties a cache: len = 0, ctl = 0, table[s][p] = s * max_pages + p (modulo n_pages). */
+/* Device.  Empties a cache: len = 0, ctl = 0, table[s][p] = s * max_pages + p, or -1 (out of range) where the pool has no such
+ * page: the caller of a smaller pool names its pages in the table. */
 w4a8_status w4a8_kv4_reset(const w4a8_kv4_cache* c, void* stream);
 /* Host, synchronous (call after the stream has finished).  *flags = the status word; the call returns
  * W4A8_ERR_DEVICE_FLAG if it is not 0: W4A8_FLAG_ERR_CAPACITY (a length, count or first position out of range, or an append beyond

@@ -672,7 +672,8 @@ class KV4Cache(_PagedCache):
         return t
 
     def reset(self, stream=None):
-        """Empties the cache: lengths 0, every sequence its own pages as far as the pool goes (w4a8_kv4_reset)."""
+        """Empties the cache: lengths 0, every sequence its own pages as far as the pool goes and no page (-1) behind that
+        (w4a8_kv4_reset)."""
         if stream is not None:
             return self._elsewhere(stream, self.reset, ())
         self._run(lib().w4a8_kv4_reset)

@@ -329,7 +329,7 @@ __global__ void k_kv4_append_len(w4a8_kv4_cache c, int n_src, int n, const int32
 __global__ void k_kv4_reset(w4a8_kv4_cache c) {
   griddep_enter();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < (int64_t)c.n_seqs * c.max_pages) c.table[i] = (int)(i % c.n_pages);
+  if (i < (int64_t)c.n_seqs * c.max_pages) c.table[i] = i < c.n_pages ? (int)i : -1;  // no page for two sequences
   if (i < c.n_seqs) c.len[i] = 0;
   if (i == 0) *c.ctl = 0;
 }
