@@ -407,8 +407,9 @@ w4a8_status w4a8_kv4_attention_workspace_bytes(const w4a8_kv4_cache* c, const w4
  * each in bf16 calls (2^-11).  A new row has no effect on the rows that do not see it, whatever it holds (NaN and infinities
  * too), and rows at or behind counts[s] are not read.  The result does not depend on timing; it may depend, in its last
  * bits, on the other sequences of the call (they share the splits of the long axis).  A page whose table entry is out of range is
- * left out.  Rows of out must not lie on one another or on anything that the call reads, the workspace too (W4A8_ERR_ARG).  The kernels' waits are bounded (2 s): one
- * that runs out sets W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN.  n_seqs * n_kv_heads * B < 2^22 and
+ * left out.  Rows of out must not lie on one another or on anything that the call reads, the workspace too (W4A8_ERR_ARG).  The
+ * kernels' waits are bounded (2 s): one that runs out sets W4A8_FLAG_ERR_TIMEOUT, and the rows whose sums miss a part are NaN;
+ * copies that may still be under way then get 2 s more, all together.  n_seqs * n_kv_heads * B < 2^22 and
  * times max_pages + 1 < 2^31, with B the blocks of at most 128 and at least 4 (fp32) or 8 (bf16) query rows (n * heads of a KV head) a
  * sequence's rows are cut into; else W4A8_ERR_SHAPE.
  * workspace: 256-byte aligned, not shared by calls that may overlap.  Its first W4A8_KV4_TICKETS bytes must be zero before its

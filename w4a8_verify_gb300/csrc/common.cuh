@@ -121,6 +121,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, uint64
     if ((it & 255u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
+// Several waits, one behind the other, within one limit: a copy that was under way before the first has all of it.
+struct WaitsWithin {
+  uint64_t t0, limit_ns;
+  __device__ explicit WaitsWithin(uint64_t limit) : t0(globaltimer_ns()), limit_ns(limit) {}
+  __device__ bool wait(uint64_t* bar, unsigned parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t gone = globaltimer_ns() - t0;
+    return mbar_wait(bar, parity, gone < limit_ns ? limit_ns - gone : 0);
+  }
+};
 // TMA tiled copy of one 4-D box (coordinates innermost first) of `map` into shared memory;
 // its bytes complete on bar.  x must keep the box start 16-byte aligned.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,

@@ -749,8 +749,9 @@ __global__ void __launch_bounds__(Kv4Split<T, D, NT>::THREADS, 1)
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int y = 0; y < NC; ++y) l[x][y] = NAN;
+    const WaitsWithin drain(geo.wait_ns);
     for (; in_ring > 0; --in_ring) {
-      (void)mbar_wait(&full[cs], cph, geo.wait_ns);
+      (void)drain.wait(&full[cs], cph);
       if (++cs == NS) cs = 0, cph ^= 1;
     }
   }

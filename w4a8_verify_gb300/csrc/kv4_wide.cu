@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_kv4_wide(w4a8_kv4_cache c, 
       x += r.pages;
     }
     // no copy in flight when the CTA ends
-    for (int i = max(0, n - kRing); i < n; ++i)
-      (void)mbar_wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1), geo.wait_ns);
-    if ((geo.vec & 1) && runs > 0) (void)mbar_wait(&bar.q_full, (unsigned)(runs - 1) & 1, geo.wait_ns);
+    const WaitsWithin drain(geo.wait_ns);
+    for (int i = max(0, n - kRing); i < n; ++i) (void)drain.wait(&bar.code_full[i % kRing], (unsigned)(i / kRing & 1));
+    if ((geo.vec & 1) && runs > 0) (void)drain.wait(&bar.q_full, (unsigned)(runs - 1) & 1);
   } else if (warp >= kConv0 && warp < kMmaWarp) {
     // the first half of the warps takes the keys, the second the values
     constexpr int kHalf = kConvWarps / 2;
