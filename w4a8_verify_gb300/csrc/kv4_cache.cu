@@ -14,7 +14,7 @@ namespace {
 constexpr int kTile = 16;                // tokens of a tile
 constexpr int kMaxIndexed = 1024;        // rows of an append that takes its source rows from a list
 constexpr int kBigThreads = 256;         // four tiles of keys, four of values
-constexpr int kSmallThreads = 512, kSmallRows = 16;
+constexpr int kSmallThreads = 512;
 
 struct Source {                          // new rows of one of keys and values
   w4a8_rows rows;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kBigThreads) k_kv4_append(w4a8_kv4_cache c, So
   append_tile<T, D, WIDE>(c, warp >> 2 ? v : k, warp >> 2, s, h, (int)tile, L, end, n, index);
 }
 // A few rows (decode steps, accepted paths): one CTA per sequence takes all heads and then stores the length, so the call is one
-// launch.  Bound by latency: length, table, rows and old words one after the other.
+// launch.  Bound by latency: length, table, rows and old words one after the other, for each round of the CTA's warps over its tiles.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSmallThreads) k_kv4_append_few(w4a8_kv4_cache c, Source k, Source v, int n_src, int n,
                                                                   const int32_t* counts, const int32_t* index, int32_t* len_out) {
@@ -313,6 +313,19 @@ __global__ void __launch_bounds__(kSmallThreads) k_kv4_append_few(w4a8_kv4_cache
   }
   __syncthreads();  // every warp has read the old length
   if (threadIdx.x == 0 && (end >= 0 || len_out != c.len)) len_out[s] = end >= 0 ? end : c.len[s];
+}
+
+// Whether a call of up to 16 rows is k_kv4_append_few's: where a warp has one tile (one launch instead of two), or the heads of
+// all sequences are so many that their CTAs would queue.  R rounds of a warp cost about 2 + 4 R us whatever the sequences,
+// k_kv4_append and the lengths behind it 6 us and 1 for every 85 (fp32) to 150 (bf16) heads.  Measured (us, heads of 128, sequences
+// x heads, few / many; caches of 50 to 300 tokens that advance):
+//   fp32, 1 row:   1 x 8  6.5 / 6.1,  64 x 8  6.8 / 11.2,  16 x 16  10.5 / 7.3,  64 x 16  10.5 / 18.1,  1 x 32  17.5 / 6.3,  1 x 1024  477 / 17
+//   fp32, 8 rows:  16 x 4  6.7 / 7.2,  1 x 8  10.7 / 6.7,  64 x 8  10.9 / 12.6,  64 x 16  18.2 / 19.2,  256 x 16  34 / 61
+//   bf16, 8 rows:  16 x 4  7.0 / 7.8,  1 x 8  10.9 / 7.3,  64 x 8  11.3 / 11.2,  64 x 16  19.6 / 15.7,  256 x 16  37 / 45
+inline bool append_few(const w4a8_kv4_cache& c, int n) {
+  if (n > kTile) return false;
+  const int tiles = 2 * c.n_kv_heads * (n > 1 ? 2 : 1), warps = kSmallThreads / 32, rounds = (tiles + warps - 1) / warps;
+  return rounds == 1 || c.n_seqs * c.n_kv_heads >= 256 * rounds;
 }
 
 // The new lengths of an append that advances its own cache: behind the kernel whose CTAs all read the old ones.
@@ -482,7 +495,7 @@ W4A8_API w4a8_status w4a8_kv4_append(const w4a8_kv4_cache* c, const w4a8_rows* k
   cudaStream_t st = as_stream(stream);
   const bool own = len_out == c->len, f32 = dtype == W4A8_F32, d64 = c->head_dim == 64;
   const Source ks{*k, kv8_vec_rows(*k, dtype)}, vs{*v, kv8_vec_rows(*v, dtype)};
-  if (n <= kSmallRows) {
+  if (append_few(*c, n)) {
     auto run = [&](auto kern) {
       return launch_pdl(kern, dim3((unsigned)c->n_seqs), dim3(kSmallThreads), 0, st, *c, ks, vs, n_src, n, counts, index, len_out);
     };
