@@ -904,18 +904,31 @@ cudaError_t kv4_split_dispatch(const w4a8_kv4_cache& c, const w4a8_kv4_attn& a, 
                                               : kv4_split_launch<T, D, 2>(c, a, geo, ws, st);
 }
 // Calls whose KV heads have many query rows run on tcgen05 (kv4_wide.cu): a tile of it takes 128 rows at one price, the split
-// kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  Short caches of few (sequence, KV head) pairs are bound by
-// latency, where the wide kernel with the new rows in its own grid is the shorter way; otherwise the blocks count.  Measured
-// (us, split / wide; pairs x tokens, heads of 128 unless said):
-//   fp32, 8 x 4096:  8 rows 18 / 20,  12 rows 21 / 21,  16 rows 23 / 21,  32 rows 31 / 21;  4 x 4096 of 64:  16 rows 15 / 18,  24 rows 19 / 19
-//   fp32, 8 x 16000:  16 rows 30 / 39,  24 rows 38 / 40,  32 rows 46 / 40;  8 x 32000:  24 rows 55 / 66,  32 rows 69 / 66
+// kernel's price goes by blocks of 8 (fp32) or 16 (bf16) rows.  Few pages of few (sequence, KV head) pairs are bound by
+// latency, where the wide kernel with the new rows in its own grid is the shorter way; otherwise the blocks count.  The pages are those
+// that the cache has room for: the host does not know its lengths.  Measured on full caches (us, split / wide; pairs x tokens,
+// heads of 128 unless said), on both sides of the limits: 640 pages for 9 to 16 rows of fp32, 1100 for 17 to 24, 2600 for bf16:
+//   fp32, 8 x 4096 (512):  8 rows 18 / 20,  12 rows 21 / 21,  16 rows 23 / 21,  32 rows 31 / 21
+//   fp32, 8 x 5000 (632):  12 rows 22.9 / 22.1,  16 rows 23.5 / 22.3;   8 x 6000 (752):  12 rows 23.8 / 24.1,  16 rows 25.8 / 24.4
+//   fp32, 8 x 7000 (880):  12 rows 20.2 / 25.6,  16 rows 22.0 / 26.0,  20 rows 28.8 / 26.2;   8 x 8192 (1024):  16 rows 26 / 27,  24 rows 31 / 28
+//   fp32, 4 x 12000 (752):  12 rows 22 / 25,  16 rows 25 / 26,  20 rows 28 / 26;   24 x 1500 (576):  12 rows 20 / 22,  16 rows 22 / 23,  20 rows 27 / 23
+//   fp32, 24 x 3000 (1128):  20 rows 21 / 23;   8 x 16000 (2000):  16 rows 30 / 39,  24 rows 38 / 40,  32 rows 46 / 40;  8 x 32000:  24 rows 55 / 66,  32 rows 69 / 66
 //   fp32, 128 x to 4096:  12 rows 63 / 87,  16 rows 69 / 90,  20 rows 108 / 92
-//   bf16, 8 x 4096:  8 rows 15 / 17,  12 rows 26 / 18;  8 x 16000:  8 rows 23 / 28,  12 rows 34 / 29,  16 rows 38 / 29
-//   bf16, 8 x 32000:  12 rows 40 / 45,  16 rows 42 / 45,  20 rows 51 / 45;   128 x to 4096:  16 rows 65 / 78,  20 rows 103 / 79
+//   bf16, 8 x 4096:  8 rows 15 / 17,  12 rows 26 / 18;  8 x 16000 (2000):  8 rows 23 / 28,  12 rows 34 / 29,  16 rows 38 / 29
+//   bf16, 8 x 20000 (2504):  12 rows 35 / 32,  16 rows 39 / 32;   8 x 24000 (3000):  12 rows 37 / 35,  16 rows 40 / 35;   of 64:  16 rows 30 / 33,  24 rows 35 / 34
+//   bf16, 16 x 12000 (3008):  12 rows 34 / 35,  16 rows 35 / 35,  20 rows 39 / 36
+//   bf16, 8 x 28000 (3500):  12 rows 38 / 40,  16 rows 41 / 40;   8 x 32000 (4000):  12 rows 40 / 45,  16 rows 42 / 45,  20 rows 51 / 45
+//   bf16, 128 x to 4096:  16 rows 65 / 78,  20 rows 103 / 79
+// fp32 heads of 64, whose split kernel has half the conversions, from 17 rows on up to 128 pages, else as behind the limits:
+//   2 x 4096 (128):  14 rows 15 / 15,  21 rows 17 / 16;   2 x 6000 (188):  24 rows 18 / 23;   4 x 4096 (256):  16 rows 16 / 18,  24 rows 20 / 19,  32 rows 20 / 19
+//   4 x 8192 (512):  24 rows 21 / 22,  32 rows 21 / 22;   24 x 1500 (576):  24 rows 20 / 21;   8 x 16000 (2000):  24 rows 29 / 35
+// Up to about 1000 tokens the wide kernel is the shorter way for 4 to 8 rows too (8 heads: fp32 8 rows over 300 tokens 14.6 / 11.9, over 1000
+// 15.1 / 13.4; bf16 13.5 / 11.1 and 14.5 / 12.7, 4 rows 12.1 / 11.0 and 12.6 / 12.5), over 2000 no more (bf16 8 rows 14.7 / 14.7):
+// the rule does not go there.
 inline bool kv4_is_wide(const w4a8_kv4_cache& c, int R, int dtype) {
   const int64_t pairs = (int64_t)c.n_seqs * c.n_kv_heads, pages = pairs * c.max_pages;
-  const bool f32 = dtype == W4A8_F32;
-  if (pairs <= kKv4Ctas / 6 && pages <= (f32 ? 512 : 2048)) return R > (f32 && c.head_dim == 64 ? 16 : 8);
+  const bool f32 = dtype == W4A8_F32, d64 = c.head_dim == 64;
+  if (pairs <= kKv4Ctas / 6 && pages <= (!f32 ? 2600 : d64 ? 128 : 1100)) return R > (f32 && (d64 || pages > 640) ? 16 : 8);
   return R > (f32 && pairs <= 16 ? 24 : 16);
 }
 cudaError_t kv4_wide(const w4a8_kv4_cache&, const w4a8_kv4_attn&, const Kv4Geom&, const Kv4Scratch&, cudaStream_t);
