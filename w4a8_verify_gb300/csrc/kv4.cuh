@@ -11,7 +11,6 @@
 
 namespace w4a8 {
 
-constexpr int kKv4Group = 32;                // dims of a scale
 constexpr float kKv4MaxScale = 240.0f;       // 264 s, the offset of a code in f16, stays finite
 constexpr int kKv4Nan = 255;                 // scale byte of a group with a value that is not finite
 constexpr int kKv4MaxRows = 64;              // new rows of one sequence in an attention call (one 64-bit mask)
