@@ -402,8 +402,8 @@ typedef struct {
 /* Host.  Scratch bytes of w4a8_kv4_attention (the pointers in a are not read, only whether they are NULL). */
 w4a8_status w4a8_kv4_attention_workspace_bytes(const w4a8_kv4_cache* c, const w4a8_kv4_attn* a, size_t* bytes);
 /* Device.  out[s][i][h] = sum_t w_t v_t with w = softmax over the committed tokens and the visible new rows; a row that
- * sees nothing is 0.  Logits, softmax statistics and sums are fp32.  The products with the new rows are plain fp32; those with
- * the pages use f16 hi/lo pairs of q and of the weights in fp32 calls (about 2^-21 relative) and one f16 factor
+ * sees nothing is 0.  Logits, softmax statistics and sums are fp32 (logits beyond 2^20, whose own rounding is more than 2^-4, may come
+ * out as NaN).  The products with the new rows are plain fp32; those with the pages use f16 hi/lo pairs of q and of the weights in fp32 calls (about 2^-21 relative) and one f16 factor
  * each in bf16 calls (2^-11).  A new row has no effect on the rows that do not see it, whatever it holds (NaN and infinities
  * too), and rows at or behind counts[s] are not read.  The result does not depend on timing; it may depend, in its last
  * bits, on the other sequences of the call (they share the splits of the long axis).  A page whose table entry is out of range is

@@ -729,7 +729,7 @@ class KV4Cache(_PagedCache):
 
     def attention(self, q, k=None, v=None, scale=1.0, counts=None, mask=None, out=None, workspace=None, stream=None):
         """Attention of q's rows over the cache and the new rows k, v (w4a8_kv4_attention); returns ``out``, a new tensor if
-        not given.  A ``workspace`` of the caller's needs no initialisation: its first KV4_TICKETS bytes are set to zero by the
+        not given, whose rows behind the counts and of sequences that are left out hold anything.  A ``workspace`` of the caller's needs no initialisation: its first KV4_TICKETS bytes are set to zero by the
         call (a small launch that the cache's own workspaces do without)."""
         if stream is not None:
             return self._elsewhere(stream, self.attention, (q, k, v, scale, counts, mask, out, workspace))

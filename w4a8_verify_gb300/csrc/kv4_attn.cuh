@@ -18,7 +18,7 @@
 // Rows of q are scaled by a power of two, to a largest magnitude of at most 2^11; qh is the nearest whole number, so a sum of
 // qh with the codes of one scale (32 dims to an accumulator) is a multiple of the scale's last bit below 2^24 of them: f32
 // holds it, and the tensor core's truncating additions do not touch it.  The groups' sums are added in fp32 outside the tensor core.
-// bf16 calls take one f16 term of q (exact: eight bits) and of P (2^-11).  In either type the values of a half page are added up
+// bf16 calls take one f16 term of q (exact: eight bits) and of P (2^-11, an eighth of their outputs' own rounding).  In either type the values of a half page are added up
 // in fp32 outside the tensor core, whose additions are truncated: left in its accumulator, every 16 tokens took up to 2^-23 of the
 // sum (0.6% of the values of a warp that went through 16384 pages; 1 to 2% of a call's time).
 //

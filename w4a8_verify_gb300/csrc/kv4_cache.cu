@@ -280,7 +280,7 @@ __device__ __forceinline__ void append_tile(const w4a8_kv4_cache& c, const Sourc
 // Many rows: one CTA per (four tiles, head, sequence), a warp per tile of keys or values.  WIDE: rows are read 16 bytes
 // at a time, known at compile time.  Bound by instructions, 19 a value (conversion, two roundings and a choice, packing), and
 // by fetching them: 24600 bf16 rows of 8 heads of 128, keys and values, 40 us, 3.2 TB/s (a correction pass behind one rounding
-// took 35 a value and 85 us).
+// took 35 a value and 85 us).  fp32 rows, 95 registers: by latency, 16 warps an SM (57 us, 4.0 TB/s).
 template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kBigThreads) k_kv4_append(w4a8_kv4_cache c, Source k, Source v, int n_src, int n,
                                                             const int32_t* counts, const int32_t* index, int32_t* len_out,

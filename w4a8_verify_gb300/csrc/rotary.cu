@@ -214,7 +214,7 @@ W4A8_API w4a8_status w4a8_qk_rotary(const w4a8_qk_rotary_args* arg, void* stream
   const int rounds = (Hq + Hk + 32 / lph - 1) / (32 / lph);
   const int64_t tokens = (int64_t)S * n;
   // Head rounds of a warp: all of a token's where there are warps enough for the SMs without splitting, else so many that
-  // each of 152 x 16 warps has one task.
+  // each of 152 x 16 warps has one task (an SM holds 24, and 32 of the wide bf16 kernel).
   constexpr int64_t kWarps = 152 * 16;
   const int64_t most = (tokens * rounds + kWarps - 1) / kWarps;
   RotGeom geo;
