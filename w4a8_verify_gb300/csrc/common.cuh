@@ -128,7 +128,7 @@ struct WaitsWithin {
   __device__ bool wait(uint64_t* bar, unsigned parity) const {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t gone = globaltimer_ns() - t0;
-    return mbar_wait(bar, parity, gone < limit_ns ? limit_ns - gone : 0);
+    return gone < limit_ns && mbar_wait(bar, parity, limit_ns - gone);
   }
 };
 // TMA tiled copy of one 4-D box (coordinates innermost first) of `map` into shared memory;
